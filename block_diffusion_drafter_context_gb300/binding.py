@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char, c_double, c_float, c_int, c_size_t, c_ulonglong, c_void_p
+from ctypes import POINTER, c_char, c_double, c_float, c_int, c_longlong, c_size_t, c_ulonglong, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdflash.so")
 
@@ -28,6 +28,7 @@ EXPORTS = (
     "dflash_get_block_size", "dflash_debug_e4m3_to_bf16", "dflash_debug_gemm_scratch_bytes", "dflash_debug_gemm",
     "dflash_debug_gemm_plan", "dflash_set_gemm_pairs", "dflash_fp8_weights_to_bf16",
     "dflash_debug_gemm_pair_clusters", "dflash_set_fused_topk",
+    "dflash_target_workspace_bytes", "dflash_append_kv", "dflash_cache_attention", "dflash_token_logprobs",
 )
 
 
@@ -60,6 +61,10 @@ class dflash_weights(ctypes.Structure):
 class dflash_kv(ctypes.Structure):
     _fields_ = [("k_cache", c_void_p), ("v_cache", c_void_p), ("page_table", c_void_p),
                 ("num_pages", c_int), ("max_pages", c_int)]
+
+
+class dflash_heads(ctypes.Structure):
+    _fields_ = [(n, c_int) for n in ("dtype", "n_q_heads", "n_kv_heads", "head_dim")]
 
 
 class dflash_kernel_stat(ctypes.Structure):
@@ -113,6 +118,12 @@ def load(path: str = LIB_PATH):
         "dflash_debug_gemm_scratch_bytes": (c_size_t, []),
         "dflash_debug_gemm": (i, [vp, vp, i, vp, i, i, i, vp, vp, c_size_t, i, vp]),
         "dflash_debug_gemm_plan": (i, [i, i, i, i, i, i, i, i, i, i, vp]),
+        "dflash_target_workspace_bytes": (c_size_t, [POINTER(dflash_heads), i, i]),
+        "dflash_append_kv": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, vp, c_float, c_float,
+                                 vp, i, vp, i, vp, vp, c_size_t, vp]),
+        "dflash_cache_attention": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, i, vp, i, i, i,
+                                       c_float, vp, vp, vp, c_size_t, vp]),
+        "dflash_token_logprobs": (i, [vp, i, i, i, c_longlong, vp, c_float, i, vp, vp, vp, vp, vp, vp]),
         "dflash_last_error": (ctypes.c_char_p, []),
         "dflash_topk16_noalloc": (i, [vp, i, i, vp, vp, vp]),
     }
@@ -144,6 +155,28 @@ def _stream(s):
         import torch
         return torch.cuda.current_stream().cuda_stream
     return s if isinstance(s, int) else s.cuda_stream
+
+
+class on_device:
+    """``with on_device(dev):`` - dev the current CUDA device of the block; no
+    device call when it already is."""
+    __slots__ = ("want", "old")
+
+    def __init__(self, device):
+        self.want = device.index
+
+    def __enter__(self):
+        import torch
+        old = torch.cuda.current_device()
+        self.old = None
+        if self.want is not None and old != self.want:
+            torch.cuda.set_device(self.want)
+            self.old = old
+
+    def __exit__(self, *exc):
+        if self.old is not None:
+            import torch
+            torch.cuda.set_device(self.old)
 
 
 # ---------------------------------------------------------------- C names
@@ -290,6 +323,34 @@ def dflash_topk16_noalloc(logits, rows, vocab, topk_ids, topk_logits, stream=Non
     """Top-16 per row with the library's fixed scratch array (no device allocation)."""
     return _check(load().dflash_topk16_noalloc(_p(logits), rows, vocab, _p(topk_ids), _p(topk_logits),
                                                _stream(stream)))
+
+
+def dflash_target_workspace_bytes(heads: dflash_heads, max_batch: int, max_new: int) -> int:
+    n = load().dflash_target_workspace_bytes(ctypes.byref(heads), max_batch, max_new)
+    if n == 0:
+        raise DflashError(-1, dflash_last_error())
+    return n
+
+
+def dflash_append_kv(heads: dflash_heads, kv: dflash_kv, layer, qkv, row_stride, g_q, g_k, eps, rope_base, cu_new,
+                     total_new, ctx_len, batch, q_out, workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_append_kv(ctypes.byref(heads), ctypes.byref(kv), layer, _p(qkv), row_stride, _p(g_q),
+                                          _p(g_k), eps, rope_base, _p(cu_new), total_new, _p(ctx_len), batch,
+                                          _p(q_out), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_cache_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_stride, cu_new, total_new, ctx_len, batch,
+                           max_new, window, scale, out, lse, workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_cache_attention(ctypes.byref(heads), ctypes.byref(kv), layer, _p(q), q_stride,
+                                                _p(cu_new), total_new, _p(ctx_len), batch, max_new, window, scale,
+                                                _p(out), _p(lse), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_token_logprobs(logits, dtype, rows, vocab, row_stride, token_ids, temperature, n_top, logprob, entropy,
+                          rank, top_ids, top_logprobs, stream=None):
+    return _check(load().dflash_token_logprobs(_p(logits), dtype, rows, vocab, row_stride, _p(token_ids), temperature,
+                                               n_top, _p(logprob), _p(entropy), _p(rank), _p(top_ids),
+                                               _p(top_logprobs), _stream(stream)))
 
 
 def dflash_last_error() -> str:

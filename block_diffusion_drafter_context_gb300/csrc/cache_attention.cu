@@ -1,0 +1,854 @@
+// Causal attention of the newest 1..16 tokens of each request over its paged
+// cache, which already holds their own keys and values
+// (dflash_cache_attention): decode steps and verification passes.
+//
+// For query head q of token i (position p = ctx + i) and its kv head's keys:
+//   s_t = scale q.k_t over p - window < t <= p,
+//   out = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m),  lse = m + log sum.
+// One pass over the pages with a running maximum and sum; a kv head's pages
+// are read once for all its g query heads and all new tokens (rows r = i g +
+// query head, R = n g of them).  At 2 d bf16 values a token and 4 d R
+// operations on them the pass is bound by HBM, and the work is the flat list
+// of pages over (request, kv head, row tile), cut into equal runs, one
+// persistent CTA each, so that ragged batches and a single long request both
+// fill the GPU.  A (request, kv head, row tile) cut by a run boundary leaves
+// (max, sum, O) partials, and the last contributor to arrive joins them in
+// contributor order: the same bits on every call.
+#include "common.cuh"
+#include "target.h"
+
+#include <math.h>
+
+namespace dflash {
+namespace {
+
+constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 8.f;        // a row's maximum is moved when it grows by more than 2^8
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+constexpr int MAX_CTAS = 512;              // CTAs of a launch at most (workspace partials)
+constexpr int MAX_TILE_ROWS = 32;
+constexpr int PART_FLOATS = MAX_TILE_ROWS * (128 + 2);   // one partial at most
+constexpr size_t HEADER_BYTES = 256;
+constexpr size_t PART_BYTES = static_cast<size_t>(MAX_CTAS) * 2 * PART_FLOATS * sizeof(float);
+
+struct Params {
+  const void *q;
+  long long ldq;
+  void *out;
+  float *lse;
+  const void *k, *v;                       // this layer (fp32 path; the bf16 path goes through tensor maps)
+  const int32_t *page_table, *cu_new, *ctx_len;
+  int max_pages, num_pages;
+  int B, nkv, g, total, max_new, window;
+  int tiles;                               // row tiles of a (request, kv head) at most: counter stride
+  int min_chunks;
+  float scale_log2;
+  int *counters;
+  float *partials;
+  int *status;
+};
+
+// One request's place: rows row0 .. row0+n-1, ctx tokens before them, pages
+// p0 .. p0+np-1 hold every position any of its tokens sees.
+struct Req {
+  int row0, n, ctx, p0, np;
+};
+
+__device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
+  Req r;
+  r.row0 = p.cu_new[b];
+  const long long n = static_cast<long long>(p.cu_new[b + 1]) - r.row0;
+  r.ctx = p.ctx_len[b];
+  const bool ok = r.row0 >= 0 && n >= 0 && n <= p.max_new && r.row0 + n <= p.total && r.ctx >= 0 &&
+                  r.ctx + n <= static_cast<long long>(p.max_pages) * PAGE;
+  if (!ok && tell) report(p.status, DFLASH_ERR_DEVICE);
+  r.n = ok ? static_cast<int>(n) : 0;
+  r.p0 = 0;
+  r.np = 0;
+  if (r.n > 0) {
+    const int lo = p.window > 0 ? max(0, r.ctx - p.window + 1) : 0;
+    r.p0 = lo / PAGE;
+    r.np = (r.ctx + r.n - 1) / PAGE - r.p0 + 1;
+  }
+  return r;
+}
+
+// the runs: CTA c of G takes list positions [run_lo(c), run_lo(c + 1))
+__device__ __forceinline__ long long run_lo(int c, long long total, int G) {
+  return static_cast<long long>(c) * total / G;
+}
+__device__ __forceinline__ int run_owner(long long x, long long total, int G) {
+  return static_cast<int>(((x + 1) * G + total - 1) / total) - 1;
+}
+
+// What the consumers need to know of a chunk, written by the producer beside
+// the chunk's data.
+struct Chunk {
+  int b, h, rt, page;        // request, kv head, row tile, page of the request
+  int row0, n, ctx, flags;   // FIRST / LAST of this CTA's part, BAD page, WHOLE: no other CTA has a part
+  int cf, cl, slot0, pad;    // contributors cf..cl, and whether cf's part is its first
+};
+enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
+
+// ------------------------------------------------------------------ bf16, up to 32 rows per tile: warp MMAs
+// A tile of MT x 16 query rows per (request, kv head) on mma.sync: with so few
+// rows the tensor work is a fraction of the HBM time whichever way it is
+// issued, and register accumulators keep a page's path short.  Warp 0
+// produces: K page as 128-byte-swizzled 64-column halves, V^T page, and for a
+// new tile its query rows, into a ring of NST stages.  Warps 1-4 each take 16
+// tokens of every page with a maximum, sum and O of their own (no exchange
+// per page) and meet when the tile ends, in the last page's stage.
+template <int D, int MT>
+struct Shape {
+  static constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;
+  static constexpr int ROWS = MT * 16, QP = D * 2 + 16, QB = ROWS * QP;    // query rows, padded pitch
+  static constexpr int NST = D == 64 ? 6 : MT == 1 ? 3 : 5;
+  static constexpr int CTAS = MT == 1 ? 2 : 1;                             // per SM
+  static constexpr int SMEM = 1024 + NST * (STAGE + QB) + 1024;
+};
+
+struct __align__(16) Ctrl {
+  uint64_t full[6], empty[6], cons;
+  long long lo, total;
+  int n_mine, G, b, h, rt, k;              // the run's first chunk: page k of (b, h, rt)
+  int abort_flag, merge;
+  Chunk chunk[6];
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
+    decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using S = Shape<D, MT>;
+  constexpr int NST = S::NST, KB = S::KB, ROWS = S::ROWS, NT = D / 8, KS = D / 16;
+  static_assert(sizeof(Ctrl) <= 1024 && S::SMEM <= 232448 / S::CTAS, "shared memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t *sQ = base + NST * S::STAGE;
+  Ctrl *ct = reinterpret_cast<Ctrl *>(sQ + NST * S::QB);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&ct->full[i], 1);
+      mbar_init(&ct->empty[i], 4);
+    }
+    mbar_init(&ct->cons, 4);
+    ct->abort_flag = 0;
+    fence_mbar_init();
+  }
+  volatile int *abort_flag = &ct->abort_flag;
+  auto tiles_of = [&](const Req &r) { return (r.n * p.g + ROWS - 1) / ROWS; };
+  pdl_start();
+  if (warp == 0) {
+    // Lane i sums the chunks of a contiguous slice of the requests; a warp
+    // scan gives the list length and the slice holding this CTA's start.
+    const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Req r = request(p, b, blockIdx.x == 0);
+      sum += static_cast<long long>(r.np) * tiles_of(r);
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    const long long total = __shfl_sync(0xffffffffu, inc, 31) * p.nkv;
+    const long long want = (total + p.min_chunks - 1) / p.min_chunks;
+    const int G = static_cast<int>(want < static_cast<long long>(gridDim.x) ? (want < 1 ? 1 : want) : gridDim.x);
+    const int c = blockIdx.x;
+    const long long lo = c < G ? run_lo(c, total, G) : 0, hi = c < G ? run_lo(c + 1, total, G) : 0;
+    const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
+    if (lane == 0) {
+      ct->n_mine = static_cast<int>(hi - lo);
+      ct->lo = lo;
+      ct->total = total;
+      ct->G = G;
+    }
+    if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
+      long long pre = ex;
+      for (int b = b0; b < b1; ++b) {
+        const Req r = request(p, b, false);
+        const long long item = r.np, head = item * tiles_of(r), span = head * p.nkv;
+        if (lo < pre + span) {
+          const long long off = lo - pre;
+          ct->b = b;
+          ct->h = static_cast<int>(off / head);
+          ct->rt = static_cast<int>(off % head / item);
+          ct->k = static_cast<int>(off % item);
+          break;
+        }
+        pre += span;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = ct->n_mine;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (the whole warp walks)
+    if (n == 0) return;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
+    const uint64_t pol = policy_evict_first();
+    const long long total = ct->total;
+    const int G = ct->G;
+    int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
+    long long x = ct->lo;
+    Req r = request(p, b, false);
+    int issued = 0;
+    bool ok = true;
+    for (int i = 0; i < n; ++i, ++x) {
+      const int st = i % NST;
+      ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / NST) & 1) ^ 1), abort_flag, WAIT_NS);
+      ok = !__any_sync(0xffffffffu, !ok);
+      if (!ok) break;
+      const bool first = i == 0 || k == 0, last = i == n - 1 || k == r.np - 1;
+      const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
+      const bool bad = page < 0 || page >= p.num_pages;
+      const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
+      if (lane == 0) {
+        if (bad) report(p.status, DFLASH_ERR_DEVICE);
+        const long long start = x - k, end = start + r.np;
+        const int cf = run_owner(start, total, G), cl = run_owner(end - 1, total, G);
+        Chunk c;
+        c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+        c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (cf == cl ? WHOLE : 0);
+        c.cf = cf, c.cl = cl, c.slot0 = run_lo(cf, total, G) == start, c.pad = i - k <= 0 ? 0 : 1;
+        ct->chunk[st] = c;
+        mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * 2);
+      }
+      __syncwarp();
+      if (lane < live) {
+        const int row = rt * ROWS + lane, i_new = row / p.g;
+        bulk_load(sQ + st * S::QB + lane * S::QP,
+                  q + static_cast<size_t>(r.row0 + i_new) * p.ldq + static_cast<size_t>(h * p.g + row % p.g) * D, D * 2,
+                  &ct->full[st]);
+      }
+      if (lane == 0 && !bad) {
+        uint8_t *dk = base + st * S::STAGE;
+        const int rowk = (page * p.nkv + h) * PAGE, rowv = (page * p.nkv + h) * D;
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half)
+          tma_load_2d_hint(dk + half * (PAGE * 128), &tmK, &ct->full[st], half * 64, rowk, pol);
+        tma_load_2d_hint(dk + KB, &tmV, &ct->full[st], 0, rowv, pol);
+      }
+      issued = i + 1;
+      if (++k == r.np) {
+        k = 0;
+        if (++rt == tiles_of(r)) {
+          rt = 0;
+          if (++h == p.nkv && i + 1 < n) {
+            h = 0;
+            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+            while (r.np == 0 && b + 1 < p.B);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      report(p.status, DFLASH_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // every issued copy lands before the shared memory goes away
+    for (int i = max(0, issued - NST); i < issued; ++i)
+      mbar_wait(&ct->full[i % NST], static_cast<uint32_t>((i / NST) & 1), nullptr, WAIT_NS);
+    return;
+  }
+  // -------------------------------------------------------------- consumers
+  const int cw = warp - 1, ctid = threadIdx.x - 32;
+  uint32_t cphase = 0;
+  auto waitw = [&](uint64_t *bar, uint32_t par) -> bool {   // warp-uniform bounded wait
+    const bool ok = mbar_wait(bar, par, abort_flag, WAIT_NS);
+    return !__any_sync(0xffffffffu, !ok);
+  };
+  auto csync = [&]() -> bool {   // the four consumer warps meet
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ct->cons);
+    const bool ok = waitw(&ct->cons, cphase & 1);
+    ++cphase;
+    return ok;
+  };
+  uint32_t qf[MT][KS][4];
+  float o[MT][NT][4], m[MT][2], l[MT][2];
+  int top[MT][2];                             // the last position a row sees
+  bool ok = true;
+  for (int i = 0; i < n && ok; ++i) {
+    const int st = i % NST;
+    ok = waitw(&ct->full[st], static_cast<uint32_t>((i / NST) & 1));
+    if (!ok) break;
+    const Chunk c = ct->chunk[st];
+    uint8_t *stage = base + st * S::STAGE;
+    if (c.flags & FIRST) {
+      const uint32_t qa = smem_u32(sQ + st * S::QB) + ((lane & 7) + (lane & 8)) * S::QP + (lane >> 4) * 16;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+          ldmatrix_x4(qa + mt * 16 * S::QP + kk * 32, qf[mt][kk][0], qf[mt][kk][1], qf[mt][kk][2], qf[mt][kk][3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // rows past the tile's are zeros, whatever the slot held: they have
+          // a say in when the warp moves its maxima
+          if (c.rt * ROWS + mt * 16 + e * 8 + (lane >> 2) >= c.n * p.g)
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) qf[mt][kk][e] = qf[mt][kk][2 + e] = 0u;
+          m[mt][e] = -INFINITY;
+          l[mt][e] = 0.f;
+          top[mt][e] = c.ctx + min(c.n - 1, (c.rt * ROWS + mt * 16 + e * 8 + (lane >> 2)) / p.g);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
+      }
+    }
+    const int t0 = c.page * PAGE + cw * 16;   // this warp's 16 positions
+    const int newest = c.ctx + c.n - 1, oldest = p.window > 0 ? c.ctx - p.window + 1 : 0;
+    if (!(c.flags & BAD) && t0 <= newest && t0 + 15 >= oldest) {
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.f;
+      const int ktok = cw * 16 + (lane >> 4) * 8 + (lane & 7);
+      const uint32_t ka = smem_u32(stage) + ktok * 128;
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        uint32_t b0, b1, b2, b3;
+        const int ch = (kk & 3) * 2 + ((lane >> 3) & 1);
+        ldmatrix_x4(ka + (kk >> 2) * (PAGE * 128) + ((ch ^ (ktok & 7)) << 4), b0, b1, b2, b3);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(s[mt][0], qf[mt][kk], b0, b1);
+          mma_bf16_16816(s[mt][1], qf[mt][kk], b2, b3);
+        }
+      }
+      // positions a row does not see (whatever their slots hold)
+      const bool edge = t0 + 15 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+      if (edge) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = t0 + t * 8 + (lane & 3) * 2 + (e & 1), hi = top[mt][e >> 1];
+              if (pos > hi || (p.window > 0 && pos <= hi - p.window)) s[mt][t][e] = -INFINITY;
+            }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(fmaxf(s[mt][0][2 * e] * p.scale_log2, s[mt][0][2 * e + 1] * p.scale_log2),
+                          fmaxf(s[mt][1][2 * e] * p.scale_log2, s[mt][1][2 * e + 1] * p.scale_log2));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+          mx[e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        }
+        const bool need = mx[0] > m[mt][0] + RESCALE_LOG2 || mx[1] > m[mt][1] + RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, need)) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[mt][e], mx[e]);
+            f[e] = mn == -INFINITY ? 1.f : fast_exp2(m[mt][e] - mn);
+            m[mt][e] = mn;
+            l[mt][e] *= f[e];
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][t][e] *= f[e >> 1];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float nm = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
+          const float p0 = fast_exp2(fmaf(s[mt][0][2 * e], p.scale_log2, nm));
+          const float p1 = fast_exp2(fmaf(s[mt][0][2 * e + 1], p.scale_log2, nm));
+          const float p2 = fast_exp2(fmaf(s[mt][1][2 * e], p.scale_log2, nm));
+          const float p3 = fast_exp2(fmaf(s[mt][1][2 * e + 1], p.scale_log2, nm));
+          l[mt][e] += (p0 + p1) + (p2 + p3);
+          pa[mt][e] = pack_bf16(p0, p1);
+          pa[mt][2 + e] = pack_bf16(p2, p3);
+        }
+      }
+      // slots past the newest token may hold anything: their V becomes 0
+      const bool stale = t0 + 15 > newest;
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (stale) {
+        const int pos = t0 + (lane & 3) * 2;
+        keep0 = pos + 1 <= newest ? 0xffffffffu : pos <= newest ? 0xffffu : 0u;
+        keep1 = pos + 9 <= newest ? 0xffffffffu : pos + 8 <= newest ? 0xffffu : 0u;
+      }
+      const uint32_t va = smem_u32(stage + KB);
+      const int dr = (lane >> 4) * 8 + (lane & 7), vch = cw * 2 + ((lane >> 3) & 1);
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4(va + (t * 8 + dr) * 128 + ((vch ^ (dr & 7)) << 4), b0, b1, b2, b3);
+        if (stale) b0 &= keep0, b1 &= keep1, b2 &= keep0, b3 &= keep1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma_bf16_16816(o[mt][t], pa[mt], b0, b1);
+          mma_bf16_16816(o[mt][t + 1], pa[mt], b2, b3);
+        }
+      }
+    }
+    if (!(c.flags & LAST)) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->empty[st]);
+      continue;
+    }
+    // ---- the end of this CTA's part of the tile: the four warps' shares are
+    // joined in the stage this chunk occupied, 16 rows at a time.  O is laid
+    // out [warp][row][D] with the columns XORed by the row (no bank conflicts).
+    const bool whole = c.flags & WHOLE;
+    float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.pad) * PART_FLOATS;
+    const int rows = min(ROWS, c.n * p.g - c.rt * ROWS);
+    float *so = reinterpret_cast<float *>(stage);
+    float *sm = reinterpret_cast<float *>(sQ + st * S::QB);   // [4][16] maxima, then sums (the Q slot is consumed)
+    static_assert(S::QB >= 4 * 16 * 2 * 4 && S::STAGE == 4 * 16 * D * 4, "join scratch");
+#pragma unroll
+    for (int mt = 0; mt < MT && ok; ++mt) {
+      ok = csync();   // every warp has read the stage (and the previous 16 rows' sums)
+      if (!ok) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float s = l[mt][e];
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        const int row = (lane >> 2) + e * 8;
+        if ((lane & 3) == 0) {
+          sm[cw * 16 + row] = m[mt][e];
+          sm[64 + cw * 16 + row] = s;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const int col = (t * 8 + (lane & 3) * 2) ^ ((row & 7) << 3);
+          *reinterpret_cast<float2 *>(so + (cw * 16 + row) * D + col) = make_float2(o[mt][t][2 * e], o[mt][t][2 * e + 1]);
+        }
+      }
+      ok = csync();
+      if (!ok) break;
+      for (int e = ctid; e < 16 * (D / 4); e += 128) {
+        const int row = e / (D / 4), c4 = (e % (D / 4)) * 4, r = mt * 16 + row;
+        if (r >= rows) break;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w * 16 + row]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float mw = sm[w * 16 + row], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+          const float4 v = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * D + (c4 ^ ((row & 7) << 3)));
+          L = fmaf(f, sm[64 + w * 16 + row], L);
+          acc.x = fmaf(f, v.x, acc.x);
+          acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z);
+          acc.w = fmaf(f, v.w, acc.w);
+        }
+        if (whole) {
+          const int row_g = c.rt * ROWS + r, tok = c.row0 + row_g / p.g, hq = c.h * p.g + row_g % p.g;
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                     (static_cast<size_t>(tok) * (p.nkv * p.g) + hq) * D + c4) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+          if (p.lse && c4 == 0)
+            p.lse[static_cast<size_t>(tok) * (p.nkv * p.g) + hq] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+        } else {
+          __stcg(reinterpret_cast<float4 *>(part + r * D + c4), acc);
+          if (c4 == 0) {
+            __stcg(part + ROWS * D + r, M);
+            __stcg(part + ROWS * D + ROWS + r, L);
+          }
+        }
+      }
+    }
+    if (!ok) break;
+    if (!whole) {
+      __threadfence();
+      if (!(ok = csync())) break;
+      if (ctid == 0) {
+        int *ctr = p.counters + (static_cast<size_t>(c.b) * p.nkv + c.h) * p.tiles + c.rt;
+        const int old = atomicAdd(ctr, 1), done = old == c.cl - c.cf;
+        if (done) atomicExch(ctr, 0);
+        __threadfence();
+        ct->merge = done;
+      }
+      if (!(ok = csync())) break;
+      if (ct->merge) {
+        auto src = [&](int cc) -> const float * {
+          return p.partials + (static_cast<size_t>(cc) * 2 + (cc > c.cf || c.slot0 ? 0 : 1)) * PART_FLOATS;
+        };
+        for (int e = ctid; e < rows * (D / 4); e += 128) {
+          const int r = e / (D / 4), c4 = (e % (D / 4)) * 4;
+          float M = -INFINITY, L = 0.f;
+#pragma unroll 8
+          for (int cc = c.cf; cc <= c.cl; ++cc) M = fmaxf(M, __ldcg(src(cc) + ROWS * D + r));
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int cc = c.cf; cc <= c.cl; ++cc) {
+            const float *pp = src(cc);
+            const float mw = __ldcg(pp + ROWS * D + r), lw = __ldcg(pp + ROWS * D + ROWS + r);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp + r * D + c4));
+            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+            L = fmaf(f, lw, L);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
+          }
+          const int row_g = c.rt * ROWS + r, tok = c.row0 + row_g / p.g, hq = c.h * p.g + row_g % p.g;
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                     (static_cast<size_t>(tok) * (p.nkv * p.g) + hq) * D + c4) =
+              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+          if (p.lse && c4 == 0)
+            p.lse[static_cast<size_t>(tok) * (p.nkv * p.g) + hq] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+        }
+      }
+    } else if (!(ok = csync())) {   // the join's reads of the stage are done
+      break;
+    }
+    fence_proxy_async_smem();   // the stage was written by plain stores: before the next bulk copy into it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ct->empty[st]);
+  }
+  if (!ok) {
+    report(p.status, DFLASH_ERR_TIMEOUT);
+    *abort_flag = 1;
+  }
+}
+
+// ------------------------------------------------------------------ fp32
+// CUDA cores (tensor-core formats would round the inputs).  One CTA takes a
+// share of the pages of a tile of 8 query rows of one (request, kv head):
+// thread t scores token t % 64 for rows 4 (t / 64) .., then sums column t
+// (of D) of P V for all 8 rows, so a K or V value read from shared memory
+// serves 4 or 8 rows.  Shares are joined by the last CTA to arrive.
+constexpr int F_ROWS = 8, F_THREADS = 128;
+
+template <int D>
+__global__ void __launch_bounds__(F_THREADS) decode_f32_kernel(const Params p) {
+  constexpr int KP = D + 4, VP = PAGE + 4, NC = D == 128 ? 1 : 2;   // NC threads share a column at D = 64
+  extern __shared__ float4 smem4[];
+  float *sk = reinterpret_cast<float *>(smem4);      // [2][64][KP]
+  float *sv = sk + 2 * PAGE * KP;                    // [2][D][VP]
+  float *sq = sv + 2 * D * VP;                       // [8][D]
+  float *sp = sq + F_ROWS * D;                       // [8][64] scores, then probabilities
+  float *st = sp + F_ROWS * PAGE;                    // [3][8] maximum, sum, factor
+  __shared__ int last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_start();
+  const int rt = blockIdx.x % p.tiles, h = blockIdx.x / p.tiles % p.nkv, b = blockIdx.x / (p.tiles * p.nkv);
+  const Req r = request(p, b, blockIdx.y == 0 && rt == 0 && h == 0 && tid == 0);
+  const int rows = min(F_ROWS, r.n * p.g - rt * F_ROWS);
+  if (rows <= 0) return;
+  const int k0 = static_cast<int>(static_cast<long long>(blockIdx.y) * r.np / gridDim.y);
+  const int k1 = static_cast<int>(static_cast<long long>(blockIdx.y + 1) * r.np / gridDim.y);
+  const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
+  const float *q = static_cast<const float *>(p.q);
+  auto page_of = [&](int k) {
+    const int pg = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
+    return pg >= 0 && pg < p.num_pages ? pg : -1;
+  };
+  auto load = [&](int k, int buf) {   // 16-byte asynchronous copies, rows at a padded pitch
+    const int pg = page_of(k);
+    if (pg >= 0) {
+      const float *gk = kc + (static_cast<size_t>(pg) * p.nkv + h) * PAGE * D;
+      const float *gv = vc + (static_cast<size_t>(pg) * p.nkv + h) * PAGE * D;
+      for (int e = tid; e < PAGE * D / 4; e += F_THREADS) {
+        const uint32_t dk = smem_u32(sk + buf * PAGE * KP + (e / (D / 4)) * KP + (e % (D / 4)) * 4);
+        const uint32_t dv = smem_u32(sv + buf * D * VP + (e / (PAGE / 4)) * VP + (e % (PAGE / 4)) * 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk), "l"(gk + 4 * e) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dv), "l"(gv + 4 * e) : "memory");
+      }
+    } else if (tid == 0) {
+      report(p.status, DFLASH_ERR_DEVICE);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (k0 < k1) load(k0, 0);
+  for (int e = tid; e < F_ROWS * D; e += F_THREADS) {
+    const int row = rt * F_ROWS + e / D;
+    sq[e] = e / D < rows ? q[static_cast<size_t>(r.row0 + row / p.g) * p.ldq +
+                             static_cast<size_t>(h * p.g + row % p.g) * D + e % D]
+                         : 0.f;
+  }
+  if (tid < F_ROWS) {
+    st[tid] = -INFINITY;
+    st[8 + tid] = 0.f;
+  }
+  float acc[F_ROWS];
+#pragma unroll
+  for (int i = 0; i < F_ROWS; ++i) acc[i] = 0.f;
+  const int tok = tid % PAGE, rg = (tid / PAGE) * 4;       // scores: token, rows rg .. rg + 3
+  const int col = tid % D, part_t = NC == 2 ? (tid / D) * (PAGE / 2) : 0;
+  const int newest = r.ctx + r.n - 1;
+  for (int k = k0; k < k1; ++k) {
+    const int buf = (k - k0) & 1;
+    if (k + 1 < k1) {
+      load(k + 1, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    const bool have = page_of(k) >= 0;
+    const float *kr = sk + buf * PAGE * KP + tok * KP;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (have) {
+#pragma unroll 8
+      for (int c = 0; c < D; c += 4) {
+        const float4 kv = *reinterpret_cast<const float4 *>(kr + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 qv = *reinterpret_cast<const float4 *>(sq + (rg + i) * D + c);
+          s[i] = fmaf(kv.x, qv.x, s[i]);
+          s[i] = fmaf(kv.y, qv.y, s[i]);
+          s[i] = fmaf(kv.z, qv.z, s[i]);
+          s[i] = fmaf(kv.w, qv.w, s[i]);
+        }
+      }
+    }
+    const int pos = (r.p0 + k) * PAGE + tok;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int hi = r.ctx + min(r.n - 1, (rt * F_ROWS + rg + i) / p.g);
+      const bool see = have && pos <= hi && (p.window <= 0 || pos > hi - p.window);
+      sp[(rg + i) * PAGE + tok] = see ? s[i] * p.scale_log2 : -INFINITY;
+    }
+    __syncthreads();
+    // running maximum and sum: warp w serves rows 2 w, 2 w + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = warp * 2 + i;
+      const float a = sp[row * PAGE + lane], c = sp[row * PAGE + 32 + lane];
+      const float mo = st[row], mn = fmaxf(mo, warp_max(fmaxf(a, c)));
+      const float nm = mn == -INFINITY ? 0.f : -mn;
+      const float pa = exp2f(a + nm), pc = exp2f(c + nm), f = mn == -INFINITY ? 1.f : exp2f(mo - mn);
+      const float sum = warp_sum(pa + pc);
+      sp[row * PAGE + lane] = pa;
+      sp[row * PAGE + 32 + lane] = pc;
+      __syncwarp();
+      if (lane == 0) {
+        st[row] = mn;
+        st[8 + row] = st[8 + row] * f + sum;
+        st[16 + row] = f;
+      }
+    }
+    __syncthreads();
+    if (have) {
+      const float *vr = sv + buf * D * VP + col * VP + part_t;
+      const int left = newest - (r.p0 + k) * PAGE - part_t;   // slots past the newest token may hold anything
+#pragma unroll
+      for (int i = 0; i < F_ROWS; ++i) acc[i] *= st[16 + i];
+#pragma unroll 4
+      for (int c = 0; c < PAGE / NC; c += 4) {
+        float4 vv = *reinterpret_cast<const float4 *>(vr + c);
+        if (left < PAGE) {
+          if (c > left) vv.x = 0.f;
+          if (c + 1 > left) vv.y = 0.f;
+          if (c + 2 > left) vv.z = 0.f;
+          if (c + 3 > left) vv.w = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < F_ROWS; ++i) {
+          const float4 pv = *reinterpret_cast<const float4 *>(sp + i * PAGE + part_t + c);
+          acc[i] = fmaf(pv.x, vv.x, acc[i]);
+          acc[i] = fmaf(pv.y, vv.y, acc[i]);
+          acc[i] = fmaf(pv.z, vv.z, acc[i]);
+          acc[i] = fmaf(pv.w, vv.w, acc[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < F_ROWS; ++i) acc[i] *= st[16 + i];
+    }
+    __syncthreads();
+  }
+  if (NC == 2) {   // the two halves of a column's tokens
+    __syncthreads();
+    if (tid >= D)
+#pragma unroll
+      for (int i = 0; i < F_ROWS; ++i) sk[i * D + col] = acc[i];
+    __syncthreads();
+    if (tid < D)
+#pragma unroll
+      for (int i = 0; i < F_ROWS; ++i) acc[i] += sk[i * D + col];
+  }
+  __syncthreads();
+  const bool writer = tid < D;
+  auto write = [&](int i, float o, float M, float L) {
+    const int row = rt * F_ROWS + i, t = r.row0 + row / p.g, hq = h * p.g + row % p.g;
+    const size_t at = static_cast<size_t>(t) * (p.nkv * p.g) + hq;
+    static_cast<float *>(p.out)[at * D + col] = L > 0.f ? o / L : 0.f;
+    if (p.lse && col == 0) p.lse[at] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+  };
+  if (gridDim.y == 1) {
+    if (writer)
+#pragma unroll
+      for (int i = 0; i < F_ROWS; ++i)
+        if (i < rows) write(i, acc[i], st[i], st[8 + i]);
+    return;
+  }
+  constexpr int FP = F_ROWS * (D + 2);
+  float *part = p.partials + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * FP;
+  if (writer)
+#pragma unroll
+    for (int i = 0; i < F_ROWS; ++i) __stcg(part + i * D + col, acc[i]);
+  if (tid < F_ROWS) {
+    __stcg(part + F_ROWS * D + tid, st[tid]);
+    __stcg(part + F_ROWS * D + F_ROWS + tid, st[8 + tid]);
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    int *ctr = p.counters + blockIdx.x;
+    const int old = atomicAdd(ctr, 1);
+    last = old == static_cast<int>(gridDim.y) - 1;
+    if (last) atomicExch(ctr, 0);
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last || !writer) return;
+  const float *all = p.partials + static_cast<size_t>(blockIdx.x) * gridDim.y * FP;
+  for (int i = 0; i < rows; ++i) {
+    float M = -INFINITY, L = 0.f, o = 0.f;
+    for (int y = 0; y < static_cast<int>(gridDim.y); ++y) M = fmaxf(M, __ldcg(all + y * FP + F_ROWS * D + i));
+    for (int y = 0; y < static_cast<int>(gridDim.y); ++y) {
+      const float *pp = all + y * FP;
+      const float mw = __ldcg(pp + F_ROWS * D + i), f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+      L = fmaf(f, __ldcg(pp + F_ROWS * D + F_ROWS + i), L);
+      o = fmaf(f, __ldcg(pp + i * D + col), o);
+    }
+    write(i, o, M, L);
+  }
+}
+
+// ------------------------------------------------------------------ host
+int row_tiles(const dflash_heads &h, int max_new, int tile_rows) {
+  return (max_new * (h.n_q_heads / h.n_kv_heads) + tile_rows - 1) / tile_rows;
+}
+
+// rows of a tile: 16 where the call's rows fit, else 32
+int tile_rows_bf16(const dflash_heads &h, int max_new) {
+  return max_new * (h.n_q_heads / h.n_kv_heads) <= 16 ? 16 : 32;
+}
+
+template <int D, int MT>
+int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sms, cudaStream_t s) {
+  using S = Shape<D, MT>;
+  auto *kernel = decode_kernel<D, MT>;
+  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
+                         "cache_attention shared memory"))
+    return e;
+  const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
+  CUtensorMap tk, tv;
+  if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
+  if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
+  p.min_chunks = 2;
+  launch_pdl(kernel, dim3(min(sms * S::CTAS, MAX_CTAS)), dim3(160), S::SMEM, s, tk, tv, p);
+  return cuda_check(cudaGetLastError(), "cache_attention launch");
+}
+
+template <int D>
+int launch_f32(const Params &p, int sms, cudaStream_t s) {
+  constexpr int SMEM = (2 * PAGE * (D + 4) + 2 * D * (PAGE + 4) + F_ROWS * D + F_ROWS * PAGE + 24) * 4;
+  auto *kernel = decode_f32_kernel<D>;
+  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM),
+                         "cache_attention shared memory"))
+    return e;
+  // few (request, kv head, row tile)s: their pages split over several CTAs
+  const long long items = static_cast<long long>(p.B) * p.nkv * p.tiles;
+  const long long cap = static_cast<long long>(PART_BYTES / (F_ROWS * (D + 2) * 4)) / items;
+  long long split = (3LL * sms + items - 1) / items;
+  split = split > (p.max_pages + 1) / 2 ? (p.max_pages + 1) / 2 : split;
+  split = split > cap ? cap : split;
+  split = split < 1 ? 1 : split;
+  launch_pdl(kernel, dim3(static_cast<unsigned>(items), static_cast<unsigned>(split)), dim3(F_THREADS), SMEM, s, p);
+  return cuda_check(cudaGetLastError(), "cache_attention launch");
+}
+
+// counters: one per (request, kv head, row tile), of the narrowest tile any path uses
+size_t counter_count(const dflash_heads &h, int batch, int max_new) {
+  return static_cast<size_t>(batch) * h.n_kv_heads * row_tiles(h, max_new, F_ROWS);
+}
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+DFLASH_API size_t dflash_target_workspace_bytes(const dflash_heads *hs, int max_batch, int max_new) {
+  if (check_heads("target_workspace_bytes", hs)) return 0;
+  if (max_batch < 1 || max_batch > DFLASH_MAX_BATCH || max_new < 1 || max_new > TARGET_MAX_NEW) {
+    set_error(DFLASH_ERR_ARG, "target_workspace_bytes: max_batch must be 1..%d and max_new 1..%d", DFLASH_MAX_BATCH,
+              TARGET_MAX_NEW);
+    return 0;
+  }
+  return HEADER_BYTES + PART_BYTES + (counter_count(*hs, max_batch, max_new) * sizeof(int) + 255) / 256 * 256;
+}
+
+DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q,
+                                      long long q_stride, const int32_t *cu_new, int total_new,
+                                      const int32_t *ctx_len, int batch, int max_new, int window, float scale,
+                                      void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                      dflash_stream_t stream) {
+  const char *who = "cache_attention";
+  if (int e = check_heads(who, hs)) return e;
+  if (max_new < 1 || max_new > TARGET_MAX_NEW)
+    return set_error(DFLASH_ERR_ARG, "cache_attention: max_new must be 1..%d", TARGET_MAX_NEW);
+  const int nq = hs->n_q_heads, nkv = hs->n_kv_heads, d = hs->head_dim;
+  const size_t need = HEADER_BYTES + PART_BYTES + counter_count(*hs, batch > 0 ? batch : 0, max_new) * sizeof(int);
+  if (int e = check_target(who, hs, kv, layer, q, q_stride, nq * d, cu_new, total_new, ctx_len, batch, workspace,
+                           workspace_bytes, need))
+    return e;
+  if (total_new > 0 && !out) return set_error(DFLASH_ERR_ARG, "cache_attention: null out");
+  if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(DFLASH_ERR_ALIGN, "cache_attention: out not 16-byte aligned");
+  if (window < 0 || !(scale > 0.f) || !(scale < 3.0e38f))
+    return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0 and scale positive and finite");
+  if (batch == 0 || total_new == 0) return DFLASH_OK;
+  int sms = 0;
+  if (int e = device_sms(&sms)) return e;
+  const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
+  Params p = {};
+  p.q = q;
+  p.ldq = q_stride;
+  p.out = out;
+  p.lse = lse;
+  p.k = static_cast<const char *>(kv->k_cache) + off;
+  p.v = static_cast<const char *>(kv->v_cache) + off;
+  p.page_table = kv->page_table;
+  p.cu_new = cu_new;
+  p.ctx_len = ctx_len;
+  p.max_pages = kv->max_pages;
+  p.num_pages = kv->num_pages;
+  p.B = batch;
+  p.nkv = nkv;
+  p.g = nq / nkv;
+  p.total = total_new;
+  p.max_new = max_new;
+  p.window = window;
+  p.scale_log2 = scale * LOG2E_F;
+  p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + HEADER_BYTES);
+  p.counters = reinterpret_cast<int *>(static_cast<char *>(workspace) + HEADER_BYTES + PART_BYTES);
+  p.status = static_cast<int *>(workspace);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (hs->dtype == DFLASH_F32) {
+    p.tiles = row_tiles(*hs, max_new, F_ROWS);
+    return d == 64 ? launch_f32<64>(p, sms, s) : launch_f32<128>(p, sms, s);
+  }
+  const int tr = tile_rows_bf16(*hs, max_new);
+  p.tiles = row_tiles(*hs, max_new, tr);
+  if (tr == 16)
+    return d == 64 ? launch_decode<64, 1>(*hs, *kv, p, sms, s) : launch_decode<128, 1>(*hs, *kv, p, sms, s);
+  return d == 64 ? launch_decode<64, 2>(*hs, *kv, p, sms, s) : launch_decode<128, 2>(*hs, *kv, p, sms, s);
+}
+
+}  // extern "C"

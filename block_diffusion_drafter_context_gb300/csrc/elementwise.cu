@@ -14,6 +14,7 @@
 // written as bf16 high + low halves (split activations).
 #include "common.cuh"
 #include "internal.h"
+#include "rope.cuh"
 
 #include <math.h>
 
@@ -74,24 +75,6 @@ __device__ __forceinline__ float4 scale4(float4 a, float r, float4 g) {
   return make_float4(a.x * r * g.x, a.y * r * g.y, a.z * r * g.z, a.w * r * g.w);
 }
 __device__ __forceinline__ float dot4(float4 a) { return a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w; }
-
-// cos / sin of pos * theta_i, theta_i = hi + lo (host-computed in fp64), all
-// in fp32 (this GPU's fp64 rate is a small fraction of fp32's): the product
-// pos * hi is split exactly into prod + err by one FMA, whole turns are
-// removed from prod with 2 pi in three parts (Cody-Waite: 6.28125 has few
-// significant bits; the rest in two fp32 terms), and the small terms are
-// added back.  Angle error below 4e-7 rad for positions up to 2^17.
-__device__ __forceinline__ void rope_cs(int pos, float th_hi, float th_lo, float &c, float &s) {
-  const float p = static_cast<float>(pos);        // exact below 2^24
-  const float prod = p * th_hi;
-  const float err = fmaf(p, th_hi, -prod);        // p * th_hi = prod + err exactly
-  const float tail = fmaf(p, th_lo, err);
-  const float k = rintf(prod * 0.15915494309189535f);   // whole turns
-  float r = fmaf(-k, 6.28125f, prod);
-  r = fmaf(-k, 1.9353072e-3f, r);
-  r = fmaf(-k, 1.0253132e-11f, r);
-  sincosf(r + tail, &s, &c);
-}
 
 // ------------------------------------------------------------------ embed
 // x[b*S+j] = E[id] (fp32 residual stream); u = RMSNorm(x) (activation dtype);
@@ -242,31 +225,6 @@ __global__ void __launch_bounds__(ROW_THREADS) feature_norm_kernel(const float *
 }
 
 // ------------------------------------------------------------------ q/k norm + rope
-struct RopeArgs {
-  float th_hi[64], th_lo[64];
-};
-
-// This lane's angles theta_{lane + 32 i}, i < N, from the parameter table.
-// Kernel parameters indexed by lane serialise the constant bank (one access
-// per distinct address, each a possible miss); uniform reads broadcast, so
-// the warp walks the table uniformly and each lane keeps its entries.
-template <int N>
-__device__ __forceinline__ void lane_thetas(const RopeArgs &rp, int lane, float (&hi)[N], float (&lo)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) hi[i] = lo[i] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float h = rp.th_hi[k + 32 * i], l = rp.th_lo[k + 32 * i];
-      if (lane == k) {
-        hi[i] = h;
-        lo[i] = l;
-      }
-    }
-  }
-}
-
 // 16 consecutive values with vector stores (dst 16-byte aligned).
 __device__ __forceinline__ void store16(float *dst, const float (&x)[16]) {
 #pragma unroll
@@ -619,16 +577,6 @@ int run(const Launch &lc, const char *name, F f) {
   ProfScope ps(lc, name, -1.0, -1.0);
   f();
   return cuda_check(cudaGetLastError(), name);
-}
-
-RopeArgs rope_table(int d, float base) {
-  RopeArgs r = {};
-  for (int i = 0; i < d / 2 && i < 64; ++i) {
-    const double th = pow(static_cast<double>(base), -2.0 * i / d);
-    r.th_hi[i] = static_cast<float>(th);
-    r.th_lo[i] = static_cast<float>(th - static_cast<double>(r.th_hi[i]));
-  }
-  return r;
 }
 
 int check_row(int H) {

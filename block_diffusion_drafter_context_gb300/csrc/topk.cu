@@ -14,49 +14,15 @@
 // chunks merge in the CTA that finishes a row last (per-row counter).
 #include "common.cuh"
 #include "internal.h"
+#include "top16.cuh"
 
 #include <mutex>
 
 namespace dflash {
 namespace {
 
-constexpr int K = 16;
+constexpr int K = TOP_K;
 constexpr int WARPS = 8;
-
-
-// Warp-wide sorted list in lanes 0..15 (descending).  Insert key k (uniform).
-__device__ __forceinline__ void insert(uint64_t &list, uint64_t k, int lane) {
-  const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-  if (lane < K) list = (list > k) ? list : ((lane == 0 || up > k) ? k : up);
-}
-
-// Offer one key per lane; inserts every key that beats the current 16th.
-__device__ __forceinline__ void offer(uint64_t &list, uint64_t &thr, uint64_t key, int lane) {
-  unsigned m = __ballot_sync(0xffffffffu, key > thr);
-  while (m) {
-    const int src = __ffs(m) - 1;
-    const uint64_t k = __shfl_sync(0xffffffffu, key, src);
-    insert(list, k, lane);
-    thr = __shfl_sync(0xffffffffu, list, K - 1);
-    m &= ~(1u << src);
-    m &= __ballot_sync(0xffffffffu, key > thr);
-  }
-}
-
-// The 16th largest of the 32 lanes' values (a warp-wide descending bitonic
-// sort; every lane gets the result).
-__device__ __forceinline__ float warp_16th_largest(float v, int lane) {
-#pragma unroll
-  for (int k = 2; k <= 32; k <<= 1) {
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      const float o = __shfl_xor_sync(0xffffffffu, v, j);
-      const bool up = ((lane & k) == 0) == ((lane & j) == 0);   // this lane keeps the larger
-      v = up ? fmaxf(v, o) : fminf(v, o);
-    }
-  }
-  return __shfl_sync(0xffffffffu, v, K - 1);
-}
 
 // The end of a row's selection: this CTA's warp lists merged in shared
 // memory; a row cut into chunks leaves its chunk's 16 keys in `part` and the

@@ -190,6 +190,30 @@ class PagedKV:
         self.struct = B.dflash_kv(self.k.data_ptr(), self.v.data_ptr(), self.page_table.data_ptr(),
                                   self.num_pages, self.max_pages)
 
+    @classmethod
+    def from_tensors(cls, k, v, page_table):
+        """A cache over pools the caller already has: k [L][num_pages][n_kv][64][d]
+        and v [L][num_pages][n_kv][d][64] of one dtype (bf16 or fp32), page_table
+        int32 [batch][max_pages], all contiguous on one CUDA device."""
+        torch = _torch()
+        if k.dim() != 5 or v.dim() != 5 or page_table.dim() != 2:
+            raise ValueError("k and v must have 5 dimensions, page_table 2")
+        L, pages, nkv, page, d = k.shape
+        if page != 64 or v.shape != (L, pages, nkv, d, page):
+            raise ValueError(f"k is [L][pages][n_kv][64][d] and v [L][pages][n_kv][d][64]: got {tuple(k.shape)} and "
+                             f"{tuple(v.shape)}")
+        if k.dtype not in (torch.bfloat16, torch.float32) or v.dtype != k.dtype or page_table.dtype != torch.int32:
+            raise ValueError("k and v must both be bf16 or both fp32, page_table int32")
+        if not (k.is_contiguous() and v.is_contiguous() and page_table.is_contiguous()):
+            raise ValueError("k, v and page_table must be contiguous")
+        if not k.is_cuda or v.device != k.device or page_table.device != k.device:
+            raise ValueError("k, v and page_table must be on one CUDA device")
+        kv = cls.__new__(cls)
+        kv.k, kv.v, kv.page_table = k, v, page_table
+        kv.num_pages, kv.max_pages = int(pages), int(page_table.shape[1])
+        kv.struct = B.dflash_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), kv.num_pages, kv.max_pages)
+        return kv
+
     def fill_from_templates(self, tk: np.ndarray, tv: np.ndarray, page_map: np.ndarray):
         """Set a drawn cache state: pool page p of layer l takes template page
         page_map[l, p] of tk / tv ([L][T][nkv][page][d]); V is stored

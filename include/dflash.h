@@ -10,6 +10,13 @@
  * and the sampling modes of the same steps:
  *   dflash_sample_path      a draft drawn over the path scores at a temperature
  *   dflash_verify_rejection rejection sampling against target logits (lossless)
+ * and, on the same paged-cache layout, the operators of the target model's pass
+ * over the drafted tokens (no context handle; any model and layer):
+ *   dflash_append_kv        q / k norm, rotation, K and V into the paged cache
+ *   dflash_cache_attention  causal attention of the newest 1..16 tokens of
+ *                           each request over its cache
+ *   dflash_token_logprobs   log probability, entropy, rank and top
+ *                           alternatives of given tokens
  * Engine options ([DF2] table of inference engines): the block size S may be
  * changed between steps (dflash_set_block_size), and the drafter's weights
  * may be FP8 (dflash_config.weight_fp8, "draft quantization").
@@ -428,6 +435,112 @@ DFLASH_API int dflash_debug_e4m3_to_bf16(const void *codes, int n, void *out, df
  * start of each call: calls that overlap on the GPU race. */
 DFLASH_API int dflash_topk16_noalloc(const float *logits, int rows, int vocab, int32_t *topk_ids,
                                      float *topk_logits, dflash_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * Operators of the target model's side of a step.  The target is any
+ * decoder whose paged cache has the layout of dflash_kv (its own n_layers;
+ * `layer` picks one).  A step appends the K and V of the tokens to be
+ * verified (dflash_append_kv) and attends over the cache with them in it
+ * (dflash_cache_attention), layer by layer; ctx_len stays the number of
+ * tokens *before* them, so that rejected tokens need no undoing: the next
+ * step's tokens overwrite their slots.
+ *
+ * Ragged batches: request b owns rows cu_new[b] .. cu_new[b+1]-1 of the
+ * token-major buffers, at positions ctx_len[b] ...  A request may have no
+ * new tokens.  Rows from cu_new[batch] to total_new (the padding of a
+ * captured batch) are neither read nor written. */
+
+/* Heads of one attention layer. */
+typedef struct dflash_heads {
+  int dtype;             /* DFLASH_BF16 or DFLASH_F32: cache, q and outputs   */
+  int n_q_heads;         /* nq                                               */
+  int n_kv_heads;        /* nkv, divides nq, nq/nkv <= 8                     */
+  int head_dim;          /* d: 64 or 128                                     */
+} dflash_heads;
+
+/* Bytes of workspace for the two calls below with at most max_batch requests
+ * (1..DFLASH_MAX_BATCH) of at most max_new (1..16) new tokens; 0 for bad
+ * arguments.  Zero-filled once after allocation, and again after a call on
+ * it reported DFLASH_ERR_TIMEOUT.  Layers and steps share one workspace as
+ * long as their calls are ordered on one stream; two captured graphs that
+ * may replay at the same time need one each.  Host-only. */
+DFLASH_API size_t dflash_target_workspace_bytes(const dflash_heads *hs, int max_batch, int max_new);
+
+/* Per-head RMSNorm of q and k (optional), rotation of q and k, K and V
+ * appended to layer `layer` of the cache:
+ *   y = g * x / sqrt(mean(x^2) + eps)            (g_q, g_k: both or neither)
+ *   (y_i, y_{i+d/2}) rotated by pos * rope_base^(-2i/d)
+ * in fp32, rounded once to dtype; V is copied.
+ *   qkv:       device [total_new][row_stride] (dtype): q heads, k heads, v heads
+ *              (the first (nq+2nkv)*d elements of a row); row_stride in
+ *              elements, >= (nq+2nkv)*d, a multiple of 16 bytes.
+ *   g_q, g_k:  device fp32 [d], or both NULL: no norm.
+ *   rope_base: > 1, or 0: no rotation.
+ *   cu_new:    device int32 [batch+1]; cu_new[batch] <= total_new.  Any number
+ *              of new tokens per request (a prompt, a block, one token).
+ *   ctx_len:   device int32 [batch], tokens cached before the new ones.
+ *   q_out:     device [total_new][nq*d] (dtype) out, not overlapping qkv; NULL:
+ *              the q heads are not read.
+ *   kv->max_pages <= 2^18 (positions below 2^24).
+ * A token whose position has no valid page (or whose request's cu_new or
+ * ctx_len is out of range) is not appended and is reported as
+ * DFLASH_ERR_DEVICE in the status word of `workspace` (at least 256 bytes;
+ * usually the one dflash_cache_attention uses). */
+DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
+                     long long row_stride, const float *g_q, const float *g_k, float eps, float rope_base,
+                     const int32_t *cu_new, int total_new, const int32_t *ctx_len, int batch, void *q_out,
+                     void *workspace, size_t workspace_bytes, dflash_stream_t stream);
+
+/* Attention of the newest tokens of each request over its paged cache, which
+ * already holds their own K and V.  Token i of request b, at position
+ * p = ctx_len[b] + i, sees positions max(0, p - window + 1) .. p:
+ *   s_t = scale * q.k_t,  out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),
+ *   lse = m + log(sum_t exp(s_t - m)),  m = max_t s_t.
+ * One new token per request is a decode step, up to 16 a verification pass.
+ *   q:        device [total_new][q_stride] (dtype), the first nq*d elements of
+ *             a row; q_stride in elements, a multiple of 16 bytes.
+ *   cu_new:   device int32 [batch+1]; at most max_new (1..16) per request.
+ *   window:   0: every position up to p; > 0: the last `window` of them.
+ *   scale:    positive and finite, e.g. 1/sqrt(d).
+ *   out:      device [total_new][nq*d] (dtype) out.
+ *   lse:      device fp32 [total_new][nq] out, or NULL.
+ * Cache slots past a request's newest token may hold anything (NaN too).
+ * A page index outside [0, num_pages) drops that page's positions and is
+ * reported as DFLASH_ERR_DEVICE; a token left without any gets out = 0 and
+ * lse = -inf.  A request whose cu_new or ctx_len is out of range (or that has
+ * more than max_new tokens) is reported the same way and left unwritten.
+ * The same inputs give the same bits on every call. */
+DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q,
+                           long long q_stride, const int32_t *cu_new, int total_new, const int32_t *ctx_len,
+                           int batch, int max_new, int window, float scale, void *out, float *lse,
+                           void *workspace, size_t workspace_bytes, dflash_stream_t stream);
+
+/* Log probabilities of given tokens, with entropy, rank and the most probable
+ * alternatives; e.g. of a step's committed tokens under the target logits
+ * they were verified with.  Per row, y = logits / temperature:
+ *   logprob = y[token] - lse(y),  entropy = -sum_v p_v log p_v,
+ *   rank = number of entries before the token in the order (logit
+ *   descending, id ascending): 0 for the most probable token;
+ *   top_ids / top_logprobs: the first n_top entries of that order.
+ *   logits:    device [rows][row_stride] of dtype (DFLASH_BF16 or DFLASH_F32),
+ *              the first vocab elements of a row; any row_stride >= vocab.
+ *   token_ids: device int32 [rows].  A negative id (the -1 padding of
+ *              `committed`) skips the row: its logits are not read, logprob,
+ *              entropy and top_logprobs are 0, rank and top_ids -1.  An id
+ *              >= vocab gives logprob NaN and rank -1.
+ *   temperature: 1e-4 .. 1e4.   rows: up to 2^27.
+ *   n_top:     0..16, <= vocab.
+ *   logprob, entropy: device fp32 [rows] out; rank: device int32 [rows] out;
+ *   top_ids: device int32 [rows][n_top] out, top_logprobs: device fp32
+ *   [rows][n_top] out (both may be NULL when n_top is 0).
+ * -inf logits have probability 0; a row of nothing else gives logprob and
+ * top_logprobs -inf and entropy 0.  A NaN or +inf logit makes the row's
+ * logprob, entropy and top_logprobs NaN (and its rank and top_ids
+ * unspecified, the ids within the vocabulary).  Sums are fp32; no workspace. */
+DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, int rows, int vocab, long long row_stride,
+                          const int32_t *token_ids, float temperature, int n_top, float *logprob,
+                          float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
+                          dflash_stream_t stream);
 
 /* Message for the last non-zero return on this thread. */
 DFLASH_API const char *dflash_last_error(void);
