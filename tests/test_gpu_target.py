@@ -287,13 +287,15 @@ def rows_of(kind, rows, V, rng):
         x[np.arange(rows), rng.integers(0, V, rows)] = 60.0
     elif kind == "far":
         x += 5e4
+    elif kind == "ascending":      # every logit is above all before it
+        x.sort(axis=1)
     return x
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,V,pad", [(1, 1, 0), (3, 17, 0), (4, 1000, 3), (2, 4097, 1), (5, 40001, 0), (2, 9000, 7),
                                         (700, 300, 0)])
-@pytest.mark.parametrize("kind", ["normal", "masked", "lowest", "ties", "equal", "peaked", "far"])
+@pytest.mark.parametrize("kind", ["normal", "masked", "lowest", "ties", "equal", "peaked", "far", "ascending"])
 def test_logprobs_match_oracle(dtype, rows, V, pad, kind):
     import torch
     from block_diffusion_drafter_context_gb300.target import token_logprobs
