@@ -14,81 +14,10 @@
 // fill the GPU.  A (request, kv head, row tile) cut by a run boundary leaves
 // (max, sum, O) partials, and the last contributor to arrive joins them in
 // contributor order: the same bits on every call.
-#include "common.cuh"
-#include "target.h"
-
-#include <math.h>
+#include "cache_attention.cuh"
 
 namespace dflash {
 namespace {
-
-constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
-constexpr float RESCALE_LOG2 = 8.f;        // a row's maximum is moved when it grows by more than 2^8
-constexpr unsigned long long WAIT_NS = 2000000000ull;
-constexpr int MAX_CTAS = 512;              // CTAs of a launch at most (workspace partials)
-constexpr int MAX_TILE_ROWS = 32;
-constexpr int PART_FLOATS = MAX_TILE_ROWS * (128 + 2);   // one partial at most
-constexpr size_t HEADER_BYTES = 256;
-constexpr size_t PART_BYTES = static_cast<size_t>(MAX_CTAS) * 2 * PART_FLOATS * sizeof(float);
-
-struct Params {
-  const void *q;
-  long long ldq;
-  void *out;
-  float *lse;
-  const void *k, *v;                       // this layer (fp32 path; the bf16 path goes through tensor maps)
-  const int32_t *page_table, *cu_new, *ctx_len;
-  int max_pages, num_pages;
-  int B, nkv, g, total, max_new, window;
-  int tiles;                               // row tiles of a (request, kv head) at most: counter stride
-  int min_chunks;
-  float scale_log2;
-  int *counters;
-  float *partials;
-  int *status;
-};
-
-// One request's place: rows row0 .. row0+n-1, ctx tokens before them, pages
-// p0 .. p0+np-1 hold every position any of its tokens sees.
-struct Req {
-  int row0, n, ctx, p0, np;
-};
-
-__device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
-  Req r;
-  r.row0 = p.cu_new[b];
-  const long long n = static_cast<long long>(p.cu_new[b + 1]) - r.row0;
-  r.ctx = p.ctx_len[b];
-  const bool ok = r.row0 >= 0 && n >= 0 && n <= p.max_new && r.row0 + n <= p.total && r.ctx >= 0 &&
-                  r.ctx + n <= static_cast<long long>(p.max_pages) * PAGE;
-  if (!ok && tell) report(p.status, DFLASH_ERR_DEVICE);
-  r.n = ok ? static_cast<int>(n) : 0;
-  r.p0 = 0;
-  r.np = 0;
-  if (r.n > 0) {
-    const int lo = p.window > 0 ? max(0, r.ctx - p.window + 1) : 0;
-    r.p0 = lo / PAGE;
-    r.np = (r.ctx + r.n - 1) / PAGE - r.p0 + 1;
-  }
-  return r;
-}
-
-// the runs: CTA c of G takes list positions [run_lo(c), run_lo(c + 1))
-__device__ __forceinline__ long long run_lo(int c, long long total, int G) {
-  return static_cast<long long>(c) * total / G;
-}
-__device__ __forceinline__ int run_owner(long long x, long long total, int G) {
-  return static_cast<int>(((x + 1) * G + total - 1) / total) - 1;
-}
-
-// What the consumers need to know of a chunk, written by the producer beside
-// the chunk's data.
-struct Chunk {
-  int b, h, rt, page;        // request, kv head, row tile, page of the request
-  int row0, n, ctx, flags;   // FIRST / LAST of this CTA's part, BAD page, WHOLE: no other CTA has a part
-  int cf, cl, slot0, pad;    // contributors cf..cl, and whether cf's part is its first
-};
-enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 
 // ------------------------------------------------------------------ bf16, up to 32 rows per tile: warp MMAs
 // A tile of MT x 16 query rows per (request, kv head) on mma.sync: with so few
@@ -105,6 +34,7 @@ struct Shape {
   static constexpr int NST = D == 64 ? 6 : MT == 1 ? 3 : 5;
   static constexpr int CTAS = MT == 1 ? 2 : 1;                             // per SM
   static constexpr int SMEM = 1024 + NST * (STAGE + QB) + 1024;
+  static constexpr int PART = ROWS * (D + 2);                              // floats of a partial
 };
 
 struct __align__(16) Ctrl {
@@ -212,7 +142,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         Chunk c;
         c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (cf == cl ? WHOLE : 0);
-        c.cf = cf, c.cl = cl, c.slot0 = run_lo(cf, total, G) == start, c.pad = i - k <= 0 ? 0 : 1;
+        c.cf = cf, c.cl = cl, c.slot0 = run_lo(cf, total, G) == start, c.slot = i - k <= 0 ? 0 : 1;
+        c.nrow0 = c.nn = c.nh = c.pad = 0;
         ct->chunk[st] = c;
         mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * 2);
       }
@@ -406,7 +337,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     // joined in the stage this chunk occupied, 16 rows at a time.  O is laid
     // out [warp][row][D] with the columns XORed by the row (no bank conflicts).
     const bool whole = c.flags & WHOLE;
-    float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.pad) * PART_FLOATS;
+    float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * S::PART;
     const int rows = min(ROWS, c.n * p.g - c.rt * ROWS);
     float *so = reinterpret_cast<float *>(stage);
     float *sm = reinterpret_cast<float *>(sQ + st * S::QB);   // [4][16] maxima, then sums (the Q slot is consumed)
@@ -479,37 +410,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         ct->merge = done;
       }
       if (!(ok = csync())) break;
-      if (ct->merge) {
-        auto src = [&](int cc) -> const float * {
-          return p.partials + (static_cast<size_t>(cc) * 2 + (cc > c.cf || c.slot0 ? 0 : 1)) * PART_FLOATS;
-        };
-        for (int e = ctid; e < rows * (D / 4); e += 128) {
-          const int r = e / (D / 4), c4 = (e % (D / 4)) * 4;
-          float M = -INFINITY, L = 0.f;
-#pragma unroll 8
-          for (int cc = c.cf; cc <= c.cl; ++cc) M = fmaxf(M, __ldcg(src(cc) + ROWS * D + r));
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int cc = c.cf; cc <= c.cl; ++cc) {
-            const float *pp = src(cc);
-            const float mw = __ldcg(pp + ROWS * D + r), lw = __ldcg(pp + ROWS * D + ROWS + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp + r * D + c4));
-            const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-            L = fmaf(f, lw, L);
-            acc.x = fmaf(f, v.x, acc.x);
-            acc.y = fmaf(f, v.y, acc.y);
-            acc.z = fmaf(f, v.z, acc.z);
-            acc.w = fmaf(f, v.w, acc.w);
-          }
-          const int row_g = c.rt * ROWS + r, tok = c.row0 + row_g / p.g, hq = c.h * p.g + row_g % p.g;
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                     (static_cast<size_t>(tok) * (p.nkv * p.g) + hq) * D + c4) =
-              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          if (p.lse && c4 == 0)
-            p.lse[static_cast<size_t>(tok) * (p.nkv * p.g) + hq] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
-        }
-      }
+      if (ct->merge) join_parts<D>(p, c, S::PART, ROWS, rows, c.rt * ROWS, ctid, 128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
     }
@@ -751,7 +652,8 @@ int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sm
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
   if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
   p.min_chunks = 2;
-  launch_pdl(kernel, dim3(min(sms * S::CTAS, MAX_CTAS)), dim3(160), S::SMEM, s, tk, tv, p);
+  const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
+  launch_pdl(kernel, dim3(min(sms * S::CTAS, most)), dim3(160), S::SMEM, s, tk, tv, p);
   return cuda_check(cudaGetLastError(), "cache_attention launch");
 }
 
@@ -843,6 +745,10 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   if (hs->dtype == DFLASH_F32) {
     p.tiles = row_tiles(*hs, max_new, F_ROWS);
     return d == 64 ? launch_f32<64>(p, sms, s) : launch_f32<128>(p, sms, s);
+  }
+  if (d == 128 && max_new * p.g > 32) {
+    p.tiles = 1;
+    return launch_verify(*hs, *kv, p, sms, s);
   }
   const int tr = tile_rows_bf16(*hs, max_new);
   p.tiles = row_tiles(*hs, max_new, tr);

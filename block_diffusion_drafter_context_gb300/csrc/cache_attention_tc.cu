@@ -1,0 +1,530 @@
+// The verification form of dflash_cache_attention: 33..128 query rows per
+// (request, kv head), head_dim 128, bf16, on the 5th-generation tensor cores.
+//
+// At 80 rows (5 heads x 16 tokens) a 64-token page is 2.6 MFLOP of products on
+// 32 KB: 0.55 PFLOP/s at HBM speed, past what warp-level MMAs reach, so S = Q
+// K^T and O += P V are tcgen05.mma with M = 128 rows (the tile's, padded), S
+// and O in tensor memory, and Q and P as A operands from tensor memory too:
+// the shared memory then holds nothing but a 6-page K / V^T ring.  One
+// persistent CTA per SM with a warp per duty:
+//   warp 0     walks the CTA's run of pages and feeds the ring by TMA;
+//   warp 1     issues S = Q K^T (N = 64, K = 128) into one of three buffers;
+//   warps 2-5  one tensor-memory lane (= query row) per thread: mask, online
+//              softmax in the exp2 domain, P back to tensor memory in bf16;
+//              O is rescaled only when a row's maximum grows by 2^8; the next
+//              tile's query rows are written a tile ahead;
+//   warp 6     issues O += P V (N = 128, K = the page's tokens rounded to 16).
+// Row r of a tile is token r / g, query head r % g of the group.
+#include "cache_attention.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int D = 128, MROWS = 128;
+constexpr int ST = 6, NSB = 3;                           // ring depth, S buffers
+constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;         // K page as two halves of [64][64], then V^T [128][64]
+constexpr int SMEM = 1024 + ST * STAGE + 1024;
+constexpr int NTHR = 224;
+constexpr int PART = MROWS * (D + 2);
+constexpr uint32_t TMEM_COLS = 512, O_COL = 256, P_COL = 384;   // S at 0, 64, 128; P: two buffers of 32 columns
+__device__ __forceinline__ uint32_t q_col(int buf) { return buf ? 448u : 192u; }   // Q: 64 columns each
+
+struct __align__(16) Ctrl {
+  uint64_t full[ST], empty[ST], sfull[NSB], sempty[NSB], pfull[2], pdone[2], qfull[2], oempty, cons, drain;
+  long long lo, total;
+  int n_mine, G, b, h, k;                                // the run's first page: k of (b, h)
+  uint32_t tmem;
+  int abort_flag, merge;
+  Chunk chunk[ST];
+};
+static_assert(sizeof(Ctrl) <= 1024 && SMEM <= 232448, "shared memory");
+
+__global__ void __launch_bounds__(NTHR, 1)
+    verify_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Ctrl *ct = reinterpret_cast<Ctrl *>(ring + ST * STAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = p.g, nact = (g * p.max_new + 31) / 32;   // softmax warps with query rows
+  volatile int *abort_flag = &ct->abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&ct->full[i], 1);
+      mbar_init(&ct->empty[i], 1);
+    }
+    for (int i = 0; i < NSB; ++i) {
+      mbar_init(&ct->sfull[i], 1);
+      mbar_init(&ct->sempty[i], nact);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ct->pfull[i], nact);
+      mbar_init(&ct->pdone[i], 1);
+      mbar_init(&ct->qfull[i], nact);
+    }
+    mbar_init(&ct->oempty, nact);
+    mbar_init(&ct->cons, nact);
+    mbar_init(&ct->drain, 2);   // both MMA issuers
+    ct->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ct->tmem, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ct->tmem;
+  if (warp >= 2 && warp <= 5) {
+    // P and Q rows that no lane writes enter the products too: zeros
+    const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    const uint32_t lz = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll
+    for (int c = 0; c < 64; c += 16) {
+      tmem_st16_nw(lz + P_COL + c, z);
+      tmem_st16_nw(lz + q_col(0) + c, z);
+      tmem_st16_nw(lz + q_col(1) + c, z);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+  }
+  pdl_start();
+  if (warp == 0) {
+    // Lane i sums the pages of a contiguous slice of the requests; a warp
+    // scan gives the list length and the slice holding this CTA's start.
+    const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += request(p, b, blockIdx.x == 0).np;
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    const long long total = __shfl_sync(0xffffffffu, inc, 31) * p.nkv;
+    const long long want = (total + p.min_chunks - 1) / p.min_chunks;
+    const int G = static_cast<int>(want < static_cast<long long>(gridDim.x) ? (want < 1 ? 1 : want) : gridDim.x);
+    const int c = blockIdx.x;
+    const long long lo = c < G ? run_lo(c, total, G) : 0, hi = c < G ? run_lo(c + 1, total, G) : 0;
+    const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
+    if (lane == 0) {
+      ct->n_mine = static_cast<int>(hi - lo);
+      ct->lo = lo;
+      ct->total = total;
+      ct->G = G;
+    }
+    if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
+      long long pre = ex;
+      for (int b = b0; b < b1; ++b) {
+        const long long np = request(p, b, false).np, span = np * p.nkv;
+        if (lo < pre + span) {
+          ct->b = b;
+          ct->h = static_cast<int>((lo - pre) / np);
+          ct->k = static_cast<int>((lo - pre) % np);
+          break;
+        }
+        pre += span;
+      }
+    }
+  }
+  __syncthreads();
+  const int n = ct->n_mine;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (n > 0) {
+      const uint64_t pol = policy_evict_first();
+      const long long total = ct->total;
+      const int G = ct->G;
+      int b = ct->b, h = ct->h, k = ct->k, issued = 0;
+      long long x = ct->lo;
+      Req r = request(p, b, false), nr = r;   // this tile's request, and the next tile's
+      int nb = b, nh = h;
+      bool ok = true, fresh = true;
+      for (int i = 0; i < n; ++i, ++x) {
+        const int st = i % ST;
+        if (fresh) {   // the tile after this one, if the run reaches it
+          nb = b, nh = h + 1, nr = r;
+          if (n - i <= r.np - k) {
+            nr.n = 0;
+          } else if (nh == p.nkv) {
+            nh = 0;
+            do nr = request(p, ++nb, false);
+            while (nr.np == 0 && nb + 1 < p.B);
+          }
+        }
+        ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
+        ok = !__any_sync(0xffffffffu, !ok);
+        if (!ok) break;
+        const bool last = i == n - 1 || k == r.np - 1;
+        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
+        const bool bad = page < 0 || page >= p.num_pages;
+        if (lane == 0) {
+          if (bad) report(p.status, DFLASH_ERR_DEVICE);
+          const long long start = x - k, end = start + r.np;
+          Chunk c;
+          c.b = b, c.h = h, c.rt = 0, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+          c.cf = run_owner(start, total, G), c.cl = run_owner(end - 1, total, G);
+          c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (c.cf == c.cl ? WHOLE : 0);
+          c.slot0 = run_lo(c.cf, total, G) == start, c.slot = i - k <= 0 ? 0 : 1;
+          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = 0;
+          ct->chunk[st] = c;
+          mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
+          if (!bad) {
+            uint8_t *dk = ring + st * STAGE;
+            const int rowk = (page * p.nkv + h) * PAGE, rowv = (page * p.nkv + h) * D;
+            tma_load_2d_hint(dk, &tmK, &ct->full[st], 0, rowk, pol);
+            tma_load_2d_hint(dk + KB / 2, &tmK, &ct->full[st], 64, rowk, pol);
+            tma_load_2d_hint(dk + KB, &tmV, &ct->full[st], 0, rowv, pol);
+          }
+        }
+        __syncwarp();
+        issued = i + 1;
+        fresh = false;
+        if (++k == r.np) {
+          k = 0;
+          b = nb, h = nh, r = nr;
+          fresh = true;
+        }
+      }
+      if (!ok && lane == 0) {
+        report(p.status, DFLASH_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // every issued copy lands before the shared memory goes away
+      for (int i = max(0, issued - ST); i < issued; ++i)
+        mbar_wait(&ct->full[i % ST], static_cast<uint32_t>((i / ST) & 1), nullptr, WAIT_NS);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ QK issuer
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(MROWS, PAGE);
+      int seg = -1;
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int st = i % ST, sb = i % NSB;
+        ok = mbar_wait(&ct->full[st], static_cast<uint32_t>((i / ST) & 1), abort_flag, WAIT_NS);
+        if (!ok) break;
+        const int flags = ct->chunk[st].flags;
+        if (flags & FIRST) {
+          ++seg;
+          ok = mbar_wait(&ct->qfull[seg & 1], static_cast<uint32_t>((seg >> 1) & 1), abort_flag, WAIT_NS);
+        }
+        ok = ok && mbar_wait(&ct->sempty[sb], static_cast<uint32_t>(((i / NSB) & 1) ^ 1), abort_flag, WAIT_NS);
+        if (!ok) break;
+        tc_fence_after();
+        if (!(flags & BAD)) {
+          const uint32_t k0 = smem_u32(ring + st * STAGE), qa = tmem + q_col(seg & 1);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)   // 16 dims = 8 columns of Q per k-step
+            umma_bf16_ts(tmem + sb * PAGE, qa + static_cast<uint32_t>(kk * 8),
+                         sdesc_k_sw128(k0 + (kk >> 2) * (KB / 2) + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&ct->sfull[sb]);
+      }
+      if (!ok) {
+        report(p.status, DFLASH_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      umma_commit(&ct->drain);   // every issued MMA retires before TMEM is released
+      mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ PV issuer
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(MROWS, D);
+      int seg = -1;
+      bool ok = true, started = false;   // started: O holds something of this tile
+      for (int i = 0; i < n && ok; ++i) {
+        const int st = i % ST, pb = i & 1;
+        ok = mbar_wait(&ct->full[st], static_cast<uint32_t>((i / ST) & 1), abort_flag, WAIT_NS) &&
+             mbar_wait(&ct->pfull[pb], static_cast<uint32_t>((i >> 1) & 1), abort_flag, WAIT_NS);
+        if (!ok) break;
+        const Chunk &c = ct->chunk[st];
+        if (c.flags & FIRST) {
+          started = false;
+          if (++seg > 0) ok = mbar_wait(&ct->oempty, static_cast<uint32_t>((seg - 1) & 1), abort_flag, WAIT_NS);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        // only the 16-token steps that hold tokens of the request
+        const int left = c.ctx + c.n - c.page * PAGE, steps = (c.flags & BAD) ? 0 : (min(left, PAGE) + 15) / 16;
+        const uint32_t pt = tmem + P_COL + static_cast<uint32_t>(pb * 32), v0 = smem_u32(ring + st * STAGE + KB);
+#pragma unroll
+        for (int kk = 0; kk < PAGE / 16; ++kk)
+          if (kk < steps)
+            umma_bf16_ts(tmem + O_COL, pt + static_cast<uint32_t>(kk * 8), sdesc_k_sw128(v0 + kk * 32), idesc,
+                         (kk > 0 || started) ? 1u : 0u);
+        started = started || steps > 0;
+        umma_commit(&ct->pdone[pb]);
+        umma_commit(&ct->empty[st]);   // PV is the last reader of the stage
+      }
+      if (!ok) {
+        report(p.status, DFLASH_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      umma_commit(&ct->drain);
+      mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
+    }
+  } else if ((warp & 3) < nact && n > 0) {
+    // ------------------------------------------------------------ softmax
+    const int quad = warp & 3, row = quad * 32 + lane, tid = row;   // TMEM lane = query row
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int tok = row / g, head = row % g;
+    uint32_t cphase = 0;
+    int seg = -1;
+    bool ok = true;
+    float m = -INFINITY, l = 0.f;   // maximum (scaled, log2) and sum of this row
+    auto waitw = [&](uint64_t *bar, uint32_t par) -> bool {   // warp-uniform bounded wait
+      const bool done = mbar_wait(bar, par, abort_flag, WAIT_NS);
+      return !__any_sync(0xffffffffu, !done);
+    };
+    auto csync = [&]() -> bool {   // the softmax warps meet
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->cons);
+      const bool done = waitw(&ct->cons, cphase & 1);
+      ++cphase;
+      return done;
+    };
+    // this lane's query row of a tile into Q buffer qb: column c holds dims 2c and 2c + 1
+    auto write_q = [&](int row0, int nn, int h, int qb) {
+      const bool live = tok < nn;
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                         static_cast<size_t>(row0 + (live ? tok : 0)) * p.ldq +
+                                                         static_cast<size_t>(h * g + head) * D);
+      uint4 u[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        uint32_t w[16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          w[4 * t] = u[4 * c4 + t].x;
+          w[4 * t + 1] = u[4 * c4 + t].y;
+          w[4 * t + 2] = u[4 * c4 + t].z;
+          w[4 * t + 3] = u[4 * c4 + t].w;
+        }
+        tmem_st16_nw(lane_base + q_col(qb) + static_cast<uint32_t>(16 * c4), w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->qfull[qb]);
+    };
+    for (int i = 0; i < n && ok; ++i) {
+      const int st = i % ST, sb = i % NSB;
+      if (!(ok = waitw(&ct->full[st], static_cast<uint32_t>((i / ST) & 1)))) break;
+      const Chunk c = ct->chunk[st];
+      const bool first = c.flags & FIRST, last = c.flags & LAST;
+      if (first) {
+        ++seg;
+        if (i == 0) write_q(c.row0, c.n, c.h, 0);   // the others were written a tile ahead
+        m = -INFINITY;
+        l = 0.f;
+      }
+      if (!(ok = waitw(&ct->sfull[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;
+      tc_fence_after();
+      float x[PAGE];
+      {
+        uint32_t r[4][16];   // the four loads in flight together
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tmem_ld16_nw(lane_base + sb * PAGE + 16 * t, r[t]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          tmem_regs_ready(r[t]);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[16 * t + e] = __uint_as_float(r[t][e]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->sempty[sb]);
+      // positions this row does not see (whatever their slots hold)
+      const int t0 = c.page * PAGE, newest = c.ctx + c.n - 1;
+      const bool edge = (c.flags & BAD) || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+      if (edge) {
+        const int top = c.ctx + min(c.n - 1, tok);
+        const int hi = (c.flags & BAD) ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
+#pragma unroll
+        for (int e = 0; e < PAGE; ++e)
+          if (e > hi || e < lo) x[e] = -INFINITY;
+      }
+      float mx;
+      {
+        float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
+#pragma unroll
+        for (int e = 4; e < PAGE; e += 4) {
+          a0 = fmaxf(a0, x[e]);
+          a1 = fmaxf(a1, x[e + 1]);
+          a2 = fmaxf(a2, x[e + 2]);
+          a3 = fmaxf(a3, x[e + 3]);
+        }
+        mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.scale_log2;
+      }
+      if (first) {
+        m = mx;
+      } else {
+        const bool need = mx > m + RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, need)) {   // O holds pages up to i - 1: wait for that PV, rescale in TMEM
+          if (!(ok = waitw(&ct->pdone[(i - 1) & 1], static_cast<uint32_t>(((i - 1) >> 1) & 1)))) break;
+          tc_fence_after();
+          const float f = need ? fast_exp2(m - mx) : 1.f;
+#pragma unroll
+          for (int c0 = 0; c0 < D / 16; c0 += 4) {
+            uint32_t ov[4][16];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) tmem_ld16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              tmem_regs_ready(ov[u]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[u][e] = __float_as_uint(__uint_as_float(ov[u][e]) * f);
+              tmem_st16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          if (need) {
+            l *= f;
+            m = mx;
+          }
+        }
+      }
+      const float nm = m == -INFINITY ? 0.f : -m;
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+      for (int e = 0; e < PAGE; e += 4) {
+        x[e] = fast_exp2(fmaf(x[e], p.scale_log2, nm));
+        x[e + 1] = fast_exp2(fmaf(x[e + 1], p.scale_log2, nm));
+        x[e + 2] = fast_exp2(fmaf(x[e + 2], p.scale_log2, nm));
+        x[e + 3] = fast_exp2(fmaf(x[e + 3], p.scale_log2, nm));
+        s0 += x[e];
+        s1 += x[e + 1];
+        s2 += x[e + 2];
+        s3 += x[e + 3];
+      }
+      l += (s0 + s1) + (s2 + s3);
+      // P buffer i & 1 was last read by the PV of page i - 2
+      if (i >= 2 && !(ok = waitw(&ct->pdone[i & 1], static_cast<uint32_t>(((i - 2) >> 1) & 1)))) break;
+      tc_fence_after();
+      {
+        uint32_t w0[16], w1[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          w0[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+          w1[j] = pack_bf16(x[32 + 2 * j], x[32 + 2 * j + 1]);
+        }
+        const uint32_t pcol = lane_base + P_COL + static_cast<uint32_t>((i & 1) * 32);
+        tmem_st16_nw(pcol, w0);
+        tmem_st16_nw(pcol + 16, w1);
+        tmem_wait_st();
+      }
+      // slots past the newest token may hold anything: in the 16-token step
+      // that the PV reads with them, V becomes 0
+      const int held = newest - t0 + 1;
+      if (held < PAGE && (held & 15) && !(c.flags & BAD)) {
+        uint8_t *v = ring + st * STAGE + KB;
+        for (int dr = tid; dr < D; dr += nact * 32)
+          for (int e = held; e & 15; ++e)
+            *reinterpret_cast<uint16_t *>(v + dr * 128 + (((e >> 3) ^ (dr & 7)) << 4) + (e & 7) * 2) = 0;
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->pfull[i & 1]);
+      // the next tile's query rows into the other buffer: it held the previous
+      // tile's, whose products all completed before this warp read their scores
+      if (first && c.nn > 0) write_q(c.nrow0, c.nn, c.nh, (seg + 1) & 1);
+      if (!last) continue;
+
+      // ---- the end of this CTA's part of the tile
+      if (!(ok = waitw(&ct->pdone[i & 1], static_cast<uint32_t>((i >> 1) & 1)))) break;
+      tc_fence_after();
+      const bool whole = c.flags & WHOLE, live = tok < c.n;
+      const int rows = c.n * g;
+      const size_t at = static_cast<size_t>(c.row0 + (live ? tok : 0)) * (p.nkv * g) + c.h * g + head;
+      float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * PART;
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int c0 = 0; c0 < D / 16; c0 += 4) {
+        uint32_t ov[4][16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tmem_ld16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          tmem_regs_ready(ov[u]);
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(ov[u][e]) : 0.f;   // l 0: O was never written
+          if (!live) continue;
+          if (whole) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = l > 0.f ? pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + (c0 + u) * 16);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(part + row * D + (c0 + u) * 16);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) __stcg(dst + t, make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ct->oempty);   // the next tile may overwrite O
+      if (whole) {
+        if (live && p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * LN2_F : -INFINITY;
+        continue;
+      }
+      if (live) {
+        __stcg(part + MROWS * D + row, m);
+        __stcg(part + MROWS * D + MROWS + row, l);
+      }
+      __threadfence();
+      if (!(ok = csync())) break;
+      if (tid == 0) {
+        int *ctr = p.counters + static_cast<size_t>(c.b) * p.nkv + c.h;
+        const int old = atomicAdd(ctr, 1), done = old == c.cl - c.cf;
+        if (done) atomicExch(ctr, 0);
+        __threadfence();
+        ct->merge = done;
+      }
+      if (!(ok = csync())) break;
+      if (ct->merge) join_parts<D>(p, c, PART, MROWS, rows, 0, tid, nact * 32);
+    }
+    if (!ok) {
+      report(p.status, DFLASH_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  // all duties done: TMEM and the ring are free
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+}  // namespace
+
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sms, cudaStream_t s) {
+  if (int e = cuda_check(cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM),
+                         "cache_attention shared memory"))
+    return e;
+  const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
+  CUtensorMap tk, tv;
+  if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
+  if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
+  p.min_chunks = 4;
+  const int most = static_cast<int>(PART_TOTAL / (2 * PART));
+  launch_pdl(verify_kernel, dim3(sms < most ? sms : most), dim3(NTHR), SMEM, s, tk, tv, p);
+  return cuda_check(cudaGetLastError(), "cache_attention launch");
+}
+
+}  // namespace dflash
