@@ -19,6 +19,7 @@ namespace {
 
 constexpr int TT = 16;        // tokens per CTA
 constexpr int THREADS = 256;
+constexpr int MAX_HPC = 4;    // kv heads per CTA
 
 struct AppendArgs {
   const void *qkv;
@@ -33,161 +34,210 @@ struct AppendArgs {
   int *status;
 };
 
-// 8 consecutive values of a row
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 4 consecutive values of a row, as they lie in memory and as fp32
+template <typename T> struct Four;
+template <> struct Four<float> {
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(const uint4 &u, float *x) {
+    x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
   }
-}
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-  *reinterpret_cast<uint4 *>(p) =
-      make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
+  static __device__ __forceinline__ uint4 pack(const float *x) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+template <> struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void unpack(const uint2 &u, float *x) {
+    x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint2 pack(const float *x) {
+    return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  }
+};
 
-// The last b < B with cu[b] <= t, searched 32 ways by the whole warp: one
-// dependent load for batches up to 32, two up to 1024.
-__device__ __forceinline__ int request_of(const int32_t *cu, int B, int t, int lane) {
-  int lo = 0, n = B;   // the answer is in [lo, lo + n)
-  while (n > 1) {
+// The last b < B with cu[b] <= t, for both of a warp's tokens at once.  Up to
+// 256 requests every entry is loaded side by side (one dependent load, where a
+// binary search takes eight); more are searched 32 ways first.
+__device__ __forceinline__ void requests_of(const int32_t *cu, int B, int t0, int t1, int lane, int &b0, int &b1) {
+  int base = 0, n = B;
+  while (n > 256) {   // the answers are in [base, base + n); t0 <= t1 lie in one tile
     const int step = (n + 31) / 32, i = lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, i < n && cu[lo + i] <= t);
-    const int k = m ? 31 - __clz(m) : 0;
-    lo += k * step;
-    n = min(step, n - k * step);
+    const unsigned m0 = __ballot_sync(0xffffffffu, i < n && cu[base + i] <= t0);
+    const unsigned m1 = __ballot_sync(0xffffffffu, i < n && cu[base + i] <= t1);
+    const int k0 = m0 ? 31 - __clz(m0) : 0, k1 = m1 ? 31 - __clz(m1) : 0;
+    base += k0 * step;
+    const int m = min(n - k0 * step, (k1 - k0 + 1) * step);
+    if (m >= n) break;   // the two answers lie far apart (many empty requests)
+    n = m;
   }
-  return lo;
+  int c0 = 0, c1 = 0;
+  for (int i = lane; i < n; i += 32) {
+    const int v = cu[base + i];
+    c0 += v <= t0;
+    c1 += v <= t1;
+  }
+  b0 = base + max(__reduce_add_sync(0xffffffffu, c0) - 1, 0);
+  b1 = base + max(__reduce_add_sync(0xffffffffu, c1) - 1, 0);
 }
 
-// CTA (token tile, group of kv heads).  A row (one head of one token) is
-// D / 8 lanes with 16 bytes of bf16 (or 32 of fp32) each, the pair
-// (i, i + D/2) D/16 lanes apart.  The rotation of the tile's tokens is
-// tabulated once per CTA and shared by its heads.  V rows pass through
-// shared memory, so that a d-row's consecutive slots are written together.
+// CTA (16 tokens, up to 4 kv heads with their q heads).  A row (one head of
+// one token) is D / 8 lanes; lane l holds values 4l..4l+3 of both halves, so
+// that the rotation's pairs are its own (with 8 consecutive values per lane
+// the exchange and the rotation table made shared memory the bound: 159 us
+// for 23 040 prompt tokens of 32 + 16 heads).  The first rows' loads and the V rows' copies into shared
+// memory do not depend on where the tokens belong, so they are under way
+// while each token's request, page and rotation are looked up (three
+// dependent loads).  The rotation of the tile's tokens is tabulated once and
+// shared by the heads.  V leaves transposed.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, const RopeArgs rp) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, HALF = D / 2, ROWS = (THREADS / 32) * RPW;
-  __shared__ __align__(16) float2 cs[TT][HALF];
-  __shared__ __align__(16) T vt[TT][D];
+  constexpr int LPR = D / 8, HALF = D / 2, ROWS = THREADS / LPR, V16 = 16 / sizeof(T);
+  using F = Four<T>;
+  __shared__ __align__(16) float2 cs[TT][HALF];      // pairs 4l + 2q, 4l + 2q + 1 as float4 number q LPR + l
+  __shared__ __align__(16) T vt[MAX_HPC][TT][D + V16];
   __shared__ int s_page[TT], s_pos[TT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * TT, h0 = blockIdx.y * a.hpc, nh = min(a.hpc, a.nkv - h0);
+  const int rows = min(TT, a.total - t0);              // rows of the buffer; the batch may end before
+  const int sh = rows > 8 ? 4 : rows > 4 ? 3 : rows > 2 ? 2 : rows > 1 ? 1 : 0;   // a power of two of tokens
+  const int nqh = a.q_out ? nh * a.g : 0, items = (nqh + nh) << sh;               // rows (head, token): q heads, then k
+  const int slot = threadIdx.x / LPR, l = threadIdx.x % LPR;                      // this thread's row of a pass, its lane in it
   float th_hi[HALF / 32], th_lo[HALF / 32];
-  lane_thetas(rp, lane, th_hi, th_lo);
+  if (a.rotate) lane_thetas(rp, lane, th_hi, th_lo);
   pdl_start();
-  const int total = min(a.total, a.cu_new[a.B]);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (a.cu_new[a.B] > a.total || a.cu_new[a.B] < 0))
+  const T *src = static_cast<const T *>(a.qkv) + static_cast<size_t>(t0) * a.ld;
+  for (int e = threadIdx.x; e < nh * rows * (D / V16); e += THREADS) {
+    const int c = (e % (D / V16)) * V16, hj = e / (D / V16), h = hj / rows, j = hj - h * rows;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&vt[h][j][c])),
+                 "l"(src + j * a.ld + static_cast<size_t>(a.nq + a.nkv + h0 + h) * D + c)
+                 : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  constexpr int U = 4;   // rows in flight per thread
+  typename F::Raw raw[U][2];
+  auto load = [&](int it0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int it = it0 + u * ROWS, j = it & ((1 << sh) - 1), hh = it >> sh;
+      if (it < items && j < rows) {
+        const T *row = src + j * a.ld + static_cast<size_t>(hh < nqh ? h0 * a.g + hh : a.nq + h0 + hh - nqh) * D + 4 * l;
+        raw[u][0] = *reinterpret_cast<const typename F::Raw *>(row);
+        raw[u][1] = *reinterpret_cast<const typename F::Raw *>(row + HALF);
+      }
+    }
+  };
+  load(slot);
+  // ---- where the tokens go: warp w looks up tokens w and w + 8
+  const int end = a.cu_new[a.B], total = min(a.total, end), nt = min(TT, total - t0);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (end > a.total || end < 0))
     report(a.status, DFLASH_ERR_DEVICE);
-  const int nt = min(TT, total - t0);
-  if (nt <= 0) return;
-  for (int j = warp; j < nt; j += THREADS / 32) {
-    const int t = t0 + j, b = request_of(a.cu_new, a.B, t, lane);
-    const int first = a.cu_new[b], c = a.ctx_len[b];
-    const long long pos = static_cast<long long>(c) + t - first;
-    const bool in = first >= 0 && first <= t && c >= 0 && pos < static_cast<long long>(a.max_pages) * PAGE;
-    const int pg = in ? a.page_table[static_cast<size_t>(b) * a.max_pages + pos / PAGE] : -1;
-    const bool ok = pg >= 0 && pg < a.num_pages;
-    const int p = in ? static_cast<int>(pos) : 0;
-    if (lane == 0) {
-      if (!ok) report(a.status, DFLASH_ERR_DEVICE);
-      s_page[j] = ok ? pg : -1;
-      s_pos[j] = p;
+  {
+    int bb[2];
+    requests_of(a.cu_new, a.B, t0 + warp, t0 + warp + 8, lane, bb[0], bb[1]);
+    int pos[2], pg[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = t0 + warp + 8 * k, first = a.cu_new[bb[k]], c = a.ctx_len[bb[k]];
+      const long long at = static_cast<long long>(c) + t - first;
+      const bool in = first >= 0 && first <= t && c >= 0 && at < static_cast<long long>(a.max_pages) * PAGE;
+      pos[k] = in ? static_cast<int>(at) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < HALF / 32; ++i) {
-      float co = 1.f, si = 0.f;
-      if (a.rotate) rope_cs(p, th_hi[i], th_lo[i], co, si);
-      cs[j][lane + 32 * i] = make_float2(co, si);
+    for (int k = 0; k < 2; ++k)
+      pg[k] = pos[k] >= 0 && warp + 8 * k < nt ? a.page_table[static_cast<size_t>(bb[k]) * a.max_pages + pos[k] / PAGE] : -1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = warp + 8 * k;
+      if (j >= nt) continue;
+      const bool ok = pg[k] >= 0 && pg[k] < a.num_pages;
+      if (lane == 0) {
+        if (!ok) report(a.status, DFLASH_ERR_DEVICE);
+        s_page[j] = ok ? pg[k] : -1;
+        s_pos[j] = max(pos[k], 0);
+      }
+#pragma unroll
+      for (int i = 0; i < HALF / 32; ++i) {
+        float co = 1.f, si = 0.f;
+        if (a.rotate) rope_cs(max(pos[k], 0), th_hi[i], th_lo[i], co, si);
+        const int pair = lane + 32 * i;
+        cs[j][((pair >> 1 & 1) * LPR + (pair >> 2)) * 2 + (pair & 1)] = make_float2(co, si);
+      }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
-  const T *src = static_cast<const T *>(a.qkv) + static_cast<size_t>(t0) * a.ld;
-  const int slot = threadIdx.x / LPR, l8 = (threadIdx.x % LPR) * 8;   // this thread's row of a pass, its 8 columns
-  // ---- q heads of the group, then its k heads: rows (head, token)
-  const int nqh = a.q_out ? nh * a.g : 0, items = (nqh + nh) * nt;
+  if (nt <= 0) return;
   float gq[8], gk[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    gq[i] = a.g_q ? a.g_q[l8 + i] : 1.f;
-    gk[i] = a.g_k ? a.g_k[l8 + i] : 1.f;
+    const int c = (i >> 2) * HALF + 4 * l + (i & 3);
+    gq[i] = a.g_q ? a.g_q[c] : 1.f;
+    gk[i] = a.g_k ? a.g_k[c] : 1.f;
   }
-  constexpr int U = 4;   // rows in flight per thread
-  for (int it0 = slot; it0 - slot < items; it0 += ROWS * U) {
-    float x[U][8];
+  // ---- v heads, transposed into [d][slot] pages.  Consecutive lanes take a
+  // d-row's consecutive slots: what costs here is the number of sectors each
+  // store instruction touches (lanes along d took 7 times as long)
+  {
+    const int pg = s_page[0], sl = s_pos[0] % PAGE;
+    const bool packed = nt == TT && pg >= 0 && s_page[TT - 1] == pg && sl % V16 == 0 && s_pos[TT - 1] % PAGE == sl + TT - 1;
+    T *vc = static_cast<T *>(a.v);
+    if (packed) {   // the tile is 16 slots of one page, on 16-byte boundaries
+      constexpr int GR = TT / V16;
+      for (int e = threadIdx.x; e < nh * D * GR; e += THREADS) {
+        const int grp = e % GR, d = e / GR % D, h = e / (GR * D);
+        __align__(16) T w[V16];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int it = it0 + u * ROWS;
-      if (it < items) {
-        const int j = it % nt, hh = it / nt;
-        const size_t col = static_cast<size_t>(hh < nqh ? h0 * a.g + hh : a.nq + h0 + hh - nqh) * D + l8;
-        load8(src + j * a.ld + col, x[u]);
+        for (int i = 0; i < V16; ++i) w[i] = vt[h][grp * V16 + i][d];
+        *reinterpret_cast<uint4 *>(vc + ((static_cast<size_t>(pg) * a.nkv + h0 + h) * D + d) * PAGE + sl + grp * V16) =
+            *reinterpret_cast<const uint4 *>(w);
+      }
+    } else {
+      for (int e = threadIdx.x; e < nh * D << sh; e += THREADS) {
+        const int j = e & ((1 << sh) - 1), d = (e >> sh) % D, h = (e >> sh) / D;
+        if (j < nt && s_page[j] >= 0)
+          vc[((static_cast<size_t>(s_page[j]) * a.nkv + h0 + h) * D + d) * PAGE + s_pos[j] % PAGE] = vt[h][j][d];
       }
     }
+  }
+  // ---- q and k heads
+  for (int it0 = slot; it0 - slot < items; it0 += ROWS * U) {   // uniform trip count
+    if (it0 != slot) load(it0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int it = it0 + u * ROWS;
-      const bool live = it < items;
-      const int j = live ? it % nt : 0, hh = live ? it / nt : 0;
-      const bool isq = hh < nqh;
+      if (it0 - slot + u * ROWS >= items) break;   // uniform
+      const int it = it0 + u * ROWS, j = it & ((1 << sh) - 1), hh = it >> sh;
+      const bool live = it < items && j < nt, isq = hh < nqh;
+      float x[8], y[8];
+      F::unpack(raw[u][0], x);
+      F::unpack(raw[u][1], x + 4);
       if (a.g_q) {
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = rsqrtf(ss / D + a.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] *= r * (isq ? gq[i] : gk[i]);
+        for (int i = 0; i < 8; ++i) x[i] *= r * (isq ? gq[i] : gk[i]);
       }
-      const float4 *c4 = reinterpret_cast<const float4 *>(&cs[j][l8 % HALF]);
-      const float sign = l8 < HALF ? -1.f : 1.f;
-      float y[8];
+      const float4 *c4 = reinterpret_cast<const float4 *>(cs[live ? j : 0]);
+      const float4 ca = c4[l], cb = c4[LPR + l];
+      const float co[4] = {ca.x, ca.z, cb.x, cb.z}, si[4] = {ca.y, ca.w, cb.y, cb.w};
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float4 c = c4[i / 2];
-        const float o0 = __shfl_xor_sync(0xffffffffu, x[u][i], LPR / 2);
-        const float o1 = __shfl_xor_sync(0xffffffffu, x[u][i + 1], LPR / 2);
-        y[i] = fmaf(sign * c.y, o0, x[u][i] * c.x);
-        y[i + 1] = fmaf(sign * c.w, o1, x[u][i + 1] * c.z);
+      for (int i = 0; i < 4; ++i) {
+        y[i] = fmaf(-si[i], x[4 + i], x[i] * co[i]);
+        y[4 + i] = fmaf(si[i], x[i], x[4 + i] * co[i]);
       }
-      if (live) {
-        if (isq) {
-          store8(static_cast<T *>(a.q_out) + (static_cast<size_t>(t0 + j) * a.nq + h0 * a.g + hh) * D + l8, y);
-        } else if (s_page[j] >= 0) {
-          store8(static_cast<T *>(a.k) +
-                     ((static_cast<size_t>(s_page[j]) * a.nkv + h0 + hh - nqh) * PAGE + s_pos[j] % PAGE) * D + l8,
-                 y);
-        }
+      T *dst = nullptr;
+      if (live && isq)
+        dst = static_cast<T *>(a.q_out) + (static_cast<size_t>(t0 + j) * a.nq + h0 * a.g + hh) * D;
+      else if (live && s_page[j] >= 0)
+        dst = static_cast<T *>(a.k) + ((static_cast<size_t>(s_page[j]) * a.nkv + h0 + hh - nqh) * PAGE + s_pos[j] % PAGE) * D;
+      if (dst) {
+        *reinterpret_cast<typename F::Raw *>(dst + 4 * l) = F::pack(y);
+        *reinterpret_cast<typename F::Raw *>(dst + HALF + 4 * l) = F::pack(y + 4);
       }
-    }
-  }
-  // ---- v heads, transposed into [d][slot] pages
-  for (int h = h0; h < h0 + nh; ++h) {
-    constexpr int V16 = 16 / sizeof(T);
-    __syncthreads();
-    for (int e = threadIdx.x; e < nt * (D / V16); e += THREADS) {
-      const int j = e / (D / V16), c = (e % (D / V16)) * V16;
-      *reinterpret_cast<uint4 *>(&vt[j][c]) =
-          *reinterpret_cast<const uint4 *>(src + j * a.ld + static_cast<size_t>(a.nq + a.nkv + h) * D + c);
-    }
-    __syncthreads();
-    // 16 consecutive threads cover one d-row's tokens (consecutive slots)
-    for (int e = threadIdx.x; e < TT * D; e += THREADS) {
-      const int d = e / TT, j = e % TT;
-      const int pg = j < nt ? s_page[j] : -1;
-      if (pg >= 0)
-        static_cast<T *>(a.v)[((static_cast<size_t>(pg) * a.nkv + h) * D + d) * PAGE + s_pos[j] % PAGE] = vt[j][d];
     }
   }
 }
@@ -303,7 +353,9 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
   a.q_out = q_out;
   a.status = static_cast<int *>(workspace);
   const int tiles = (total_new + TT - 1) / TT;
-  a.hpc = 1;
+  // as many kv heads per CTA as leave two CTAs per SM
+  a.hpc = MAX_HPC;
+  while (a.hpc > 1 && static_cast<long long>(tiles) * ((nkv + a.hpc - 1) / a.hpc) < 2LL * sms) a.hpc /= 2;
   const dim3 grid(tiles, (nkv + a.hpc - 1) / a.hpc);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RopeArgs &rp = rope_of(d, a.rotate ? rope_base : 1e6f);
