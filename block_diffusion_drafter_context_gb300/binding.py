@@ -157,26 +157,18 @@ def _stream(s):
     return s if isinstance(s, int) else s.cuda_stream
 
 
-class on_device:
-    """``with on_device(dev):`` - dev the current CUDA device of the block; no
-    device call when it already is."""
-    __slots__ = ("want", "old")
+_raw_stream = None
 
-    def __init__(self, device):
-        self.want = device.index
 
-    def __enter__(self):
+def raw_stream(device: int) -> int:
+    """The current stream of a device as a handle (torch's own fast lookup where
+    it has one: the stream object takes as long to make as a small kernel runs)."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
-        old = torch.cuda.current_device()
-        self.old = None
-        if self.want is not None and old != self.want:
-            torch.cuda.set_device(self.want)
-            self.old = old
-
-    def __exit__(self, *exc):
-        if self.old is not None:
-            import torch
-            torch.cuda.set_device(self.old)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _raw_stream(device)
 
 
 # ---------------------------------------------------------------- C names

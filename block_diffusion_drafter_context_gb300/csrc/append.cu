@@ -12,8 +12,6 @@
 #include "rope.cuh"
 #include "target.h"
 
-#include <mutex>
-
 namespace dflash {
 namespace {
 
@@ -294,18 +292,15 @@ int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, i
   return DFLASH_OK;
 }
 
-int device_sms(int *sms) {
-  static std::mutex mu;
-  static int known[64] = {};
-  int dev = -1;
-  if (int e = cuda_check(cudaGetDevice(&dev), "cudaGetDevice")) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev >= 0 && dev < 64 && known[dev]) {
-    *sms = known[dev];
-    return DFLASH_OK;
-  }
-  if (int e = cuda_check(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev), "SM count")) return e;
-  if (dev >= 0 && dev < 64) known[dev] = *sms;
+int current_device(Device *d) {
+  static std::atomic<int> known[64] = {};
+  if (int e = cuda_check(cudaGetDevice(&d->index), "cudaGetDevice")) return e;
+  const bool slot = d->index >= 0 && d->index < 64;
+  d->sms = slot ? known[d->index].load(std::memory_order_relaxed) : 0;
+  if (d->sms) return DFLASH_OK;
+  if (int e = cuda_check(cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->index), "SM count"))
+    return e;
+  if (slot) known[d->index].store(d->sms, std::memory_order_relaxed);
   return DFLASH_OK;
 }
 
@@ -328,8 +323,8 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
     return set_error(DFLASH_ERR_ARG, "append_kv: eps / rope_base out of range");
   if (reinterpret_cast<uintptr_t>(q_out) & 15) return set_error(DFLASH_ERR_ALIGN, "append_kv: q_out not 16-byte aligned");
   if (batch == 0 || total_new == 0) return DFLASH_OK;
-  int sms = 0;
-  if (int e = device_sms(&sms)) return e;
+  Device dev;
+  if (int e = current_device(&dev)) return e;
   const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
   AppendArgs a = {};
   a.qkv = qkv;
@@ -355,7 +350,7 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
   const int tiles = (total_new + TT - 1) / TT;
   // as many kv heads per CTA as leave two CTAs per SM
   a.hpc = MAX_HPC;
-  while (a.hpc > 1 && static_cast<long long>(tiles) * ((nkv + a.hpc - 1) / a.hpc) < 2LL * sms) a.hpc /= 2;
+  while (a.hpc > 1 && static_cast<long long>(tiles) * ((nkv + a.hpc - 1) / a.hpc) < 2LL * dev.sms) a.hpc /= 2;
   const dim3 grid(tiles, (nkv + a.hpc - 1) / a.hpc);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RopeArgs &rp = rope_of(d, a.rotate ? rope_base : 1e6f);

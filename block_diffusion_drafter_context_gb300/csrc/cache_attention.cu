@@ -641,33 +641,31 @@ int tile_rows_bf16(const dflash_heads &h, int max_new) {
 }
 
 template <int D, int MT>
-int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sms, cudaStream_t s) {
+int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
   using S = Shape<D, MT>;
   auto *kernel = decode_kernel<D, MT>;
-  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM),
-                         "cache_attention shared memory"))
-    return e;
+  static std::atomic<uint64_t> smem_set;
+  if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
   if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
   p.min_chunks = 2;
   const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
-  launch_pdl(kernel, dim3(min(sms * S::CTAS, most)), dim3(160), S::SMEM, s, tk, tv, p);
+  launch_pdl(kernel, dim3(min(dev.sms * S::CTAS, most)), dim3(160), S::SMEM, s, tk, tv, p);
   return cuda_check(cudaGetLastError(), "cache_attention launch");
 }
 
 template <int D>
-int launch_f32(const Params &p, int sms, cudaStream_t s) {
+int launch_f32(const Params &p, const Device &dev, cudaStream_t s) {
   constexpr int SMEM = (2 * PAGE * (D + 4) + 2 * D * (PAGE + 4) + F_ROWS * D + F_ROWS * PAGE + 24) * 4;
   auto *kernel = decode_f32_kernel<D>;
-  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM),
-                         "cache_attention shared memory"))
-    return e;
+  static std::atomic<uint64_t> smem_set;
+  if (int e = allow_smem(smem_set, dev, kernel, SMEM)) return e;
   // few (request, kv head, row tile)s: their pages split over several CTAs
   const long long items = static_cast<long long>(p.B) * p.nkv * p.tiles;
   const long long cap = static_cast<long long>(PART_BYTES / (F_ROWS * (D + 2) * 4)) / items;
-  long long split = (3LL * sms + items - 1) / items;
+  long long split = (3LL * dev.sms + items - 1) / items;
   split = split > (p.max_pages + 1) / 2 ? (p.max_pages + 1) / 2 : split;
   split = split > cap ? cap : split;
   split = split < 1 ? 1 : split;
@@ -716,8 +714,8 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   if (window < 0 || !(scale > 0.f) || !(scale < 3.0e38f))
     return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0 and scale positive and finite");
   if (batch == 0 || total_new == 0) return DFLASH_OK;
-  int sms = 0;
-  if (int e = device_sms(&sms)) return e;
+  Device dev;
+  if (int e = current_device(&dev)) return e;
   const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
   Params p = {};
   p.q = q;
@@ -744,17 +742,17 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (hs->dtype == DFLASH_F32) {
     p.tiles = row_tiles(*hs, max_new, F_ROWS);
-    return d == 64 ? launch_f32<64>(p, sms, s) : launch_f32<128>(p, sms, s);
+    return d == 64 ? launch_f32<64>(p, dev, s) : launch_f32<128>(p, dev, s);
   }
   if (d == 128 && max_new * p.g > 32) {
     p.tiles = 1;
-    return launch_verify(*hs, *kv, p, sms, s);
+    return launch_verify(*hs, *kv, p, dev, s);
   }
   const int tr = tile_rows_bf16(*hs, max_new);
   p.tiles = row_tiles(*hs, max_new, tr);
   if (tr == 16)
-    return d == 64 ? launch_decode<64, 1>(*hs, *kv, p, sms, s) : launch_decode<128, 1>(*hs, *kv, p, sms, s);
-  return d == 64 ? launch_decode<64, 2>(*hs, *kv, p, sms, s) : launch_decode<128, 2>(*hs, *kv, p, sms, s);
+    return d == 64 ? launch_decode<64, 1>(*hs, *kv, p, dev, s) : launch_decode<128, 1>(*hs, *kv, p, dev, s);
+  return d == 64 ? launch_decode<64, 2>(*hs, *kv, p, dev, s) : launch_decode<128, 2>(*hs, *kv, p, dev, s);
 }
 
 }  // extern "C"

@@ -116,6 +116,6 @@ __device__ __forceinline__ void join_parts(const Params &p, const Chunk &c, int 
 }
 
 // Query rows > 32 per (request, kv head) on tcgen05 (cache_attention_tc.cu).
-int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sms, cudaStream_t s);
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s);
 
 }  // namespace dflash

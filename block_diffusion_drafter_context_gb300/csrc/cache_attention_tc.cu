@@ -513,17 +513,16 @@ __global__ void __launch_bounds__(NTHR, 1)
 
 }  // namespace
 
-int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int sms, cudaStream_t s) {
-  if (int e = cuda_check(cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM),
-                         "cache_attention shared memory"))
-    return e;
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
+  static std::atomic<uint64_t> smem_set;
+  if (int e = allow_smem(smem_set, dev, verify_kernel, SMEM)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
   if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
   p.min_chunks = 4;
   const int most = static_cast<int>(PART_TOTAL / (2 * PART));
-  launch_pdl(verify_kernel, dim3(sms < most ? sms : most), dim3(NTHR), SMEM, s, tk, tv, p);
+  launch_pdl(verify_kernel, dim3(dev.sms < most ? dev.sms : most), dim3(NTHR), SMEM, s, tk, tv, p);
   return cuda_check(cudaGetLastError(), "cache_attention launch");
 }
 

@@ -478,8 +478,8 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   if (reinterpret_cast<uintptr_t>(logits) % size)
     return set_error(DFLASH_ERR_ALIGN, "token_logprobs: logits not aligned to their elements");
   if (rows > (1 << 27)) return set_error(DFLASH_ERR_SHAPE, "token_logprobs: at most 2^27 rows per call");
-  int sms = 0;
-  if (int e = device_sms(&sms)) return e;
+  Device dev;
+  if (int e = current_device(&dev)) return e;
   Args a = {};
   a.x = logits;
   a.ld = row_stride;
@@ -497,15 +497,17 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   // fp32 rows of 151 936: 42 us on one CTA, 25 on 4, 32 on 16; 640 rows: 101
   // on one, 129 on 4).
   int cs = 1;
-  while (cs < MAX_CLUSTER && 2LL * rows * cs < CTAS * sms && static_cast<long long>(cs) * PER_STAGE < vocab) cs *= 2;
+  while (cs < MAX_CLUSTER && 2LL * rows * cs < CTAS * dev.sms && static_cast<long long>(cs) * PER_STAGE < vocab) cs *= 2;
   auto *kernel = dtype == DFLASH_F32 ? logprobs_kernel<float> : logprobs_kernel<__nv_bfloat16>;
-  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM),
-                         "token_logprobs shared memory"))
-    return e;
-  if (cs > 8)
+  static std::atomic<uint64_t> smem_set[2], wide_set[2];
+  const int which = dtype == DFLASH_F32;
+  if (int e = allow_smem(smem_set[which], dev, kernel, SMEM)) return e;
+  if (cs > 8 && !(dev.index < 64 && wide_set[which].load(std::memory_order_relaxed) >> dev.index & 1)) {
     if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
                            "token_logprobs cluster size"))
       return e;
+    if (dev.index < 64) wide_set[which].fetch_or(1ull << dev.index, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   a.cs = cs;
   cfg.gridDim = dim3(static_cast<unsigned>(cs) * rows);

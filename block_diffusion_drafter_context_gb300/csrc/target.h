@@ -2,6 +2,8 @@
 // cache, attention over it).
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace dflash {
@@ -14,8 +16,23 @@ int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, i
                  long long row_stride, int row_elems, const int32_t *cu_new, int total_new, const int32_t *ctx_len,
                  int batch, const void *workspace, size_t workspace_bytes, size_t need);
 int check_heads(const char *who, const dflash_heads *hs);
-// SM count of the current device, looked up once per device
-int device_sms(int *sms);
+// The current device and its SM count, looked up once per device.
+struct Device {
+  int index = 0, sms = 0;
+};
+int current_device(Device *d);
+// A kernel's dynamic shared memory limit, set once per device (`done`: a bit
+// per device, one mask per kernel; devices past 63 are set on every call).
+template <typename K>
+int allow_smem(std::atomic<uint64_t> &done, const Device &d, K *kernel, int bytes) {
+  const uint64_t bit = d.index < 64 ? 1ull << d.index : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return DFLASH_OK;
+  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                         "dynamic shared memory"))
+    return e;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return DFLASH_OK;
+}
 
 inline int elt_bytes(const dflash_heads &h) { return h.dtype == DFLASH_F32 ? 4 : 2; }
 // first element of a layer's K (and V) pages

@@ -7,6 +7,8 @@ drafting arithmetic happens in libdflash.
 """
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 
 from . import binding as B
@@ -185,10 +187,17 @@ class PagedKV:
         self.k = alloc(shape, dtype=dt, device=device)
         self.v = alloc(vshape, dtype=dt, device=device)
         self.page_table = to_device(np.ascontiguousarray(page_table, dtype=np.int32), device)
-        self.num_pages = int(num_pages)
-        self.max_pages = int(page_table.shape[1])
+        self._describe()
+
+    def _describe(self):
+        """The C struct, and what the operators compare their own shape with."""
+        L, pages, nkv, _, d = self.k.shape
+        self.num_pages, self.max_pages = int(pages), int(self.page_table.shape[1])
+        self.n_layers, self.batch_rows = int(L), int(self.page_table.shape[0])
+        self.layer_sig = (self.k.dtype, self.k.device, int(nkv), int(d))
         self.struct = B.dflash_kv(self.k.data_ptr(), self.v.data_ptr(), self.page_table.data_ptr(),
                                   self.num_pages, self.max_pages)
+        self.struct_ref = ctypes.byref(self.struct)
 
     @classmethod
     def from_tensors(cls, k, v, page_table):
@@ -210,8 +219,7 @@ class PagedKV:
             raise ValueError("k, v and page_table must be on one CUDA device")
         kv = cls.__new__(cls)
         kv.k, kv.v, kv.page_table = k, v, page_table
-        kv.num_pages, kv.max_pages = int(pages), int(page_table.shape[1])
-        kv.struct = B.dflash_kv(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), kv.num_pages, kv.max_pages)
+        kv._describe()
         return kv
 
     def fill_from_templates(self, tk: np.ndarray, tv: np.ndarray, page_map: np.ndarray):
