@@ -39,8 +39,9 @@ struct Shape {
 
 struct __align__(16) Ctrl {
   uint64_t full[6], empty[6], cons;
-  long long lo, total;
-  int n_mine, G, b, h, rt, k;              // the run's first chunk: page k of (b, h, rt)
+  long long lo;
+  Runs runs;
+  int n_mine, b, h, rt, k;                 // the run's first chunk: page k of (b, h, rt)
   int abort_flag, merge;
   Chunk chunk[6];
 };
@@ -84,16 +85,15 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       if (lane >= o) inc += t;
     }
     const long long total = __shfl_sync(0xffffffffu, inc, 31) * p.nkv;
-    const long long want = (total + p.min_chunks - 1) / p.min_chunks;
-    const int G = static_cast<int>(want < static_cast<long long>(gridDim.x) ? (want < 1 ? 1 : want) : gridDim.x);
+    Runs runs;
+    runs.cut(total, p.min_chunks, gridDim.x);
     const int c = blockIdx.x;
-    const long long lo = c < G ? run_lo(c, total, G) : 0, hi = c < G ? run_lo(c + 1, total, G) : 0;
+    const long long lo = c < runs.G ? runs.lo(c) : 0, hi = c < runs.G ? runs.lo(c + 1) : 0;
     const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
     if (lane == 0) {
       ct->n_mine = static_cast<int>(hi - lo);
       ct->lo = lo;
-      ct->total = total;
-      ct->G = G;
+      ct->runs = runs;
     }
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
@@ -103,9 +103,10 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         if (lo < pre + span) {
           const long long off = lo - pre;
           ct->b = b;
-          ct->h = static_cast<int>(off / head);
-          ct->rt = static_cast<int>(off % head / item);
-          ct->k = static_cast<int>(off % item);
+          const long long h = quotient(off, head), rt = quotient(off - h * head, item);
+          ct->h = static_cast<int>(h);
+          ct->rt = static_cast<int>(rt);
+          ct->k = static_cast<int>(off - h * head - rt * item);
           break;
         }
         pre += span;
@@ -119,8 +120,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     if (n == 0) return;
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
     const uint64_t pol = policy_evict_first();
-    const long long total = ct->total;
-    const int G = ct->G;
+    const Runs runs = ct->runs;
+    int cf = 0, cl = 0;
     int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
     long long x = ct->lo;
     Req r = request(p, b, false);
@@ -137,12 +138,14 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
       if (lane == 0) {
         if (bad) report(p.status, DFLASH_ERR_DEVICE);
-        const long long start = x - k, end = start + r.np;
-        const int cf = run_owner(start, total, G), cl = run_owner(end - 1, total, G);
+        if (first) {
+          cf = runs.owner(x - k);
+          cl = runs.owner(x - k + r.np - 1);
+        }
         Chunk c;
         c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (cf == cl ? WHOLE : 0);
-        c.cf = cf, c.cl = cl, c.slot0 = run_lo(cf, total, G) == start, c.slot = i - k <= 0 ? 0 : 1;
+        c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
         c.nrow0 = c.nn = c.nh = c.pad = 0;
         ct->chunk[st] = c;
         mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * 2);
@@ -382,13 +385,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
           acc.w = fmaf(f, v.w, acc.w);
         }
         if (whole) {
-          const int row_g = c.rt * ROWS + r, tok = c.row0 + row_g / p.g, hq = c.h * p.g + row_g % p.g;
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                     (static_cast<size_t>(tok) * (p.nkv * p.g) + hq) * D + c4) =
-              make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          if (p.lse && c4 == 0)
-            p.lse[static_cast<size_t>(tok) * (p.nkv * p.g) + hq] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+          write_row<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), c.rt * ROWS + r, c4, acc, M, L);
         } else {
           __stcg(reinterpret_cast<float4 *>(part + r * D + c4), acc);
           if (c4 == 0) {
@@ -410,7 +407,9 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         ct->merge = done;
       }
       if (!(ok = csync())) break;
-      if (ct->merge) join_parts<D>(p, c, S::PART, ROWS, rows, c.rt * ROWS, ctid, 128);
+      if (ct->merge)
+        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS, rows,
+                      c.rt * ROWS, ctid, 128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
     }
@@ -615,19 +614,10 @@ __global__ void __launch_bounds__(F_THREADS) decode_f32_kernel(const Params p) {
     __threadfence();
   }
   __syncthreads();
-  if (!last || !writer) return;
+  if (!last) return;
   const float *all = p.partials + static_cast<size_t>(blockIdx.x) * gridDim.y * FP;
-  for (int i = 0; i < rows; ++i) {
-    float M = -INFINITY, L = 0.f, o = 0.f;
-    for (int y = 0; y < static_cast<int>(gridDim.y); ++y) M = fmaxf(M, __ldcg(all + y * FP + F_ROWS * D + i));
-    for (int y = 0; y < static_cast<int>(gridDim.y); ++y) {
-      const float *pp = all + y * FP;
-      const float mw = __ldcg(pp + F_ROWS * D + i), f = mw == -INFINITY ? 0.f : exp2f(mw - M);
-      L = fmaf(f, __ldcg(pp + F_ROWS * D + F_ROWS + i), L);
-      o = fmaf(f, __ldcg(pp + i * D + col), o);
-    }
-    write(i, o, M, L);
-  }
+  join_tile<float, D, 1, 8>(dest_of(p, r.row0, h), [&](int i) { return all + i * FP; }, gridDim.y, F_ROWS, rows,
+                            rt * F_ROWS, tid, F_THREADS);
 }
 
 // ------------------------------------------------------------------ host

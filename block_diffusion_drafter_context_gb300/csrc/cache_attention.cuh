@@ -58,13 +58,28 @@ __device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
   return r;
 }
 
-// the runs: CTA c of G takes list positions [run_lo(c), run_lo(c + 1))
-__device__ __forceinline__ long long run_lo(int c, long long total, int G) {
-  return static_cast<long long>(c) * total / G;
+// How the list of `total` pages is shared out: G CTAs take runs of `base` pages,
+// the first `rem` of them one more.  64-bit divisions are some 150 cycles
+// each, so lists below 2^32 (all but absurd ones) divide in 32 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
-__device__ __forceinline__ int run_owner(long long x, long long total, int G) {
-  return static_cast<int>(((x + 1) * G + total - 1) / total) - 1;
-}
+struct Runs {
+  long long total, base;
+  int G, rem;
+  __device__ __forceinline__ void cut(long long n, int min_chunks, int ctas) {
+    total = n;
+    const long long want = quotient(n + min_chunks - 1, min_chunks);
+    G = static_cast<int>(want < ctas ? (want < 1 ? 1 : want) : ctas);
+    base = quotient(n, G);
+    rem = static_cast<int>(n - base * G);
+  }
+  __device__ __forceinline__ long long lo(int c) const { return c * base + min(c, rem); }
+  __device__ __forceinline__ int owner(long long x) const {   // the CTA whose run holds page x
+    const long long big = rem * (base + 1);
+    return static_cast<int>(x < big ? quotient(x, base + 1) : rem + quotient(x - big, base));
+  }
+};
 
 // What the consumers need to know of a chunk, written by the producer beside
 // the chunk's data.
@@ -77,42 +92,93 @@ struct Chunk {
 enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 
 
-// The partials of one tile: O rows [rows][D], maxima [rows], sums [rows], a
-// tile's slot at (CTA * 2 + slot) * stride.  The last contributor to arrive
-// joins contributors c.cf..c.cl in order and writes rows 0..rows-1 (of the
-// tile starting at query row row_base); `tid` of `nthr` threads.
-template <int D>
-__device__ __forceinline__ void join_parts(const Params &p, const Chunk &c, int stride, int tile_rows, int rows,
-                                           int row_base, int tid, int nthr) {
-  auto src = [&](int cc) -> const float * {
-    return p.partials + (static_cast<size_t>(cc) * 2 + (cc > c.cf || c.slot0 ? 0 : 1)) * stride;
-  };
-  for (int e = tid; e < rows * (D / 4); e += nthr) {
-    const int r = e / (D / 4), c4 = (e % (D / 4)) * 4;
+// Where a tile's rows go.  By value: a reference to the kernel's parameters
+// would move them out of the constant bank.
+struct Dest {
+  void *out;
+  float *lse;
+  int row0, h, nkv, g;     // the request's first row, the kv head
+};
+__device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h) { return {p.out, p.lse, row0, h, p.nkv, p.g}; }
+
+// One query row's output, columns c4 .. c4 + 3, and its log-sum-exp.
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
+  const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  T *dst = static_cast<T *>(p.out) + at * D + c4;
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  else
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (p.lse && c4 == 0) p.lse[at] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+}
+
+// The join of a tile cut over several CTAs, by the last of them to arrive: np
+// partials (O [tile_rows][D], maxima [tile_rows], sums [tile_rows], at
+// src(0..np-1)), in that order.  The partials sit in L2, so the time is its
+// latency: NV float4 columns and B partials per thread are in flight.
+template <typename T, int D, int NV, int B, typename Src>
+__device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int tile_rows, int rows, int row_base, int tid,
+                                          int nthr) {
+  constexpr int PER = D / 4 / NV;   // items per row
+  for (int e = tid; e < rows * PER; e += nthr) {
+    const int r = e / PER, c = (e % PER) * 4;   // columns c + 4 PER k
     float M = -INFINITY, L = 0.f;
-#pragma unroll 8
-    for (int cc = c.cf; cc <= c.cl; ++cc) M = fmaxf(M, __ldcg(src(cc) + tile_rows * D + r));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int cc = c.cf; cc <= c.cl; ++cc) {
-      const float *pp = src(cc);
-      const float mw = __ldcg(pp + tile_rows * D + r), lw = __ldcg(pp + tile_rows * D + tile_rows + r);
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(pp + r * D + c4));
-      const float f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-      L = fmaf(f, lw, L);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+    float4 acc[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < np; i += B) {
+      float m[B], l[B];
+      float4 v[B][NV];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const float *pp = src(min(i + u, np - 1));
+        m[u] = __ldcg(pp + tile_rows * D + r);
+        l[u] = __ldcg(pp + tile_rows * D + tile_rows + r);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) v[u][k] = __ldcg(reinterpret_cast<const float4 *>(pp + r * D + c + 4 * PER * k));
+      }
+      float mn = M;
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        if (i + u >= np) m[u] = -INFINITY;
+        mn = fmaxf(mn, m[u]);
+      }
+      if (mn == -INFINITY) continue;
+      const float f = fast_exp2(M - mn);
+      M = mn;
+      L *= f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) acc[k].x *= f, acc[k].y *= f, acc[k].z *= f, acc[k].w *= f;
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const float w = fast_exp2(m[u] - mn);
+        L = fmaf(w, l[u], L);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          acc[k].x = fmaf(w, v[u][k].x, acc[k].x);
+          acc[k].y = fmaf(w, v[u][k].y, acc[k].y);
+          acc[k].z = fmaf(w, v[u][k].z, acc[k].z);
+          acc[k].w = fmaf(w, v[u][k].w, acc[k].w);
+        }
+      }
     }
-    const int row = row_base + r, tok = c.row0 + row / p.g, hq = c.h * p.g + row % p.g;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                               (static_cast<size_t>(tok) * (p.nkv * p.g) + hq) * D + c4) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse && c4 == 0)
-      p.lse[static_cast<size_t>(tok) * (p.nkv * p.g) + hq] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) write_row<T, D>(p, row_base + r, c + 4 * PER * k, acc[k], M, L);
   }
+}
+// the same for the runs' partials: np contributors from CTA cf on, a tile's
+// slot at (CTA * 2 + slot) * stride.  Not inlined: the kernels' main loops have
+// no registers to spare for it.
+template <int D>
+__device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, int np, int slot0, int stride, int tile_rows,
+                                        int rows, int row_base, int tid, int nthr) {
+  auto src = [&](int i) { return partials + (static_cast<size_t>(cf + i) * 2 + (i > 0 || slot0 ? 0 : 1)) * stride; };
+  if (rows * (D / 4) <= 2 * nthr)
+    join_tile<__nv_bfloat16, D, 1, 8>(p, src, np, tile_rows, rows, row_base, tid, nthr);
+  else
+    join_tile<__nv_bfloat16, D, 4, 4>(p, src, np, tile_rows, rows, row_base, tid, nthr);
 }
 
 // Query rows > 32 per (request, kv head) on tcgen05 (cache_attention_tc.cu).

@@ -31,8 +31,9 @@ __device__ __forceinline__ uint32_t q_col(int buf) { return buf ? 448u : 192u; }
 
 struct __align__(16) Ctrl {
   uint64_t full[ST], empty[ST], sfull[NSB], sempty[NSB], pfull[2], pdone[2], qfull[2], oempty, cons, drain;
-  long long lo, total;
-  int n_mine, G, b, h, k;                                // the run's first page: k of (b, h)
+  long long lo;
+  Runs runs;
+  int n_mine, b, h, k;                                   // the run's first page: k of (b, h)
   uint32_t tmem;
   int abort_flag, merge;
   Chunk chunk[ST];
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctrl *ct = reinterpret_cast<Ctrl *>(ring + ST * STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = p.g, nact = (g * p.max_new + 31) / 32;   // softmax warps with query rows
+  const int g = p.g;
   volatile int *abort_flag = &ct->abort_flag;
 
   if (threadIdx.x == 0) {
@@ -55,15 +56,15 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&ct->sfull[i], 1);
-      mbar_init(&ct->sempty[i], nact);
+      mbar_init(&ct->sempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ct->pfull[i], nact);
+      mbar_init(&ct->pfull[i], 4);
       mbar_init(&ct->pdone[i], 1);
-      mbar_init(&ct->qfull[i], nact);
+      mbar_init(&ct->qfull[i], 4);
     }
-    mbar_init(&ct->oempty, nact);
-    mbar_init(&ct->cons, nact);
+    mbar_init(&ct->oempty, 4);
+    mbar_init(&ct->cons, 4);
     mbar_init(&ct->drain, 2);   // both MMA issuers
     ct->abort_flag = 0;
     fence_mbar_init();
@@ -103,16 +104,15 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (lane >= o) inc += t;
     }
     const long long total = __shfl_sync(0xffffffffu, inc, 31) * p.nkv;
-    const long long want = (total + p.min_chunks - 1) / p.min_chunks;
-    const int G = static_cast<int>(want < static_cast<long long>(gridDim.x) ? (want < 1 ? 1 : want) : gridDim.x);
+    Runs runs;
+    runs.cut(total, p.min_chunks, gridDim.x);
     const int c = blockIdx.x;
-    const long long lo = c < G ? run_lo(c, total, G) : 0, hi = c < G ? run_lo(c + 1, total, G) : 0;
+    const long long lo = c < runs.G ? runs.lo(c) : 0, hi = c < runs.G ? runs.lo(c + 1) : 0;
     const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
     if (lane == 0) {
       ct->n_mine = static_cast<int>(hi - lo);
       ct->lo = lo;
-      ct->total = total;
-      ct->G = G;
+      ct->runs = runs;
     }
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
@@ -120,8 +120,9 @@ __global__ void __launch_bounds__(NTHR, 1)
         const long long np = request(p, b, false).np, span = np * p.nkv;
         if (lo < pre + span) {
           ct->b = b;
-          ct->h = static_cast<int>((lo - pre) / np);
-          ct->k = static_cast<int>((lo - pre) % np);
+          const long long h = quotient(lo - pre, np);
+          ct->h = static_cast<int>(h);
+          ct->k = static_cast<int>(lo - pre - h * np);
           break;
         }
         pre += span;
@@ -135,8 +136,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     // ------------------------------------------------------------ producer
     if (n > 0) {
       const uint64_t pol = policy_evict_first();
-      const long long total = ct->total;
-      const int G = ct->G;
+      const Runs runs = ct->runs;
+      int cf = 0, cl = 0;
       int b = ct->b, h = ct->h, k = ct->k, issued = 0;
       long long x = ct->lo;
       Req r = request(p, b, false), nr = r;   // this tile's request, and the next tile's
@@ -162,12 +163,15 @@ __global__ void __launch_bounds__(NTHR, 1)
         const bool bad = page < 0 || page >= p.num_pages;
         if (lane == 0) {
           if (bad) report(p.status, DFLASH_ERR_DEVICE);
-          const long long start = x - k, end = start + r.np;
+          if (fresh || i == 0) {
+            cf = runs.owner(x - k);
+            cl = runs.owner(x - k + r.np - 1);
+          }
           Chunk c;
           c.b = b, c.h = h, c.rt = 0, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
-          c.cf = run_owner(start, total, G), c.cl = run_owner(end - 1, total, G);
+          c.cf = cf, c.cl = cl;
           c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (c.cf == c.cl ? WHOLE : 0);
-          c.slot0 = run_lo(c.cf, total, G) == start, c.slot = i - k <= 0 ? 0 : 1;
+          c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
           c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = 0;
           ct->chunk[st] = c;
           mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
@@ -267,8 +271,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       umma_commit(&ct->drain);
       mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
     }
-  } else if ((warp & 3) < nact && n > 0) {
+  } else if (n > 0) {
     // ------------------------------------------------------------ softmax
+    // (all four warps, with query rows or not: the joins want the threads)
     const int quad = warp & 3, row = quad * 32 + lane, tid = row;   // TMEM lane = query row
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int tok = row / g, head = row % g;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int held = newest - t0 + 1;
       if (held < PAGE && (held & 15) && !(c.flags & BAD)) {
         uint8_t *v = ring + st * STAGE + KB;
-        for (int dr = tid; dr < D; dr += nact * 32)
+        for (int dr = tid; dr < D; dr += 4 * 32)
           for (int e = held; e & 15; ++e)
             *reinterpret_cast<uint16_t *>(v + dr * 128 + (((e >> 3) ^ (dr & 7)) << 4) + (e & 7) * 2) = 0;
         fence_proxy_async_smem();
@@ -497,7 +502,9 @@ __global__ void __launch_bounds__(NTHR, 1)
         ct->merge = done;
       }
       if (!(ok = csync())) break;
-      if (ct->merge) join_parts<D>(p, c, PART, MROWS, rows, 0, tid, nact * 32);
+      if (ct->merge)
+        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, PART, MROWS, rows, 0, tid,
+                      4 * 32);
     }
     if (!ok) {
       report(p.status, DFLASH_ERR_TIMEOUT);
