@@ -46,7 +46,11 @@ struct __align__(16) Ctrl {
   Chunk chunk[6];
 };
 
-template <int D, int MT>
+// CL: few (request, kv head, row tile)s over short capacities.  One cluster of
+// p.cs CTAs per tile shares its pages out evenly, with no list to scan, and
+// the shares meet in distributed shared memory: on a request of 2 048 tokens
+// the partials' way through L2 and its counter took 5 of 15 us.
+template <int D, int MT, bool CL>
 __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using S = Shape<D, MT>;
@@ -69,7 +73,18 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
   volatile int *abort_flag = &ct->abort_flag;
   auto tiles_of = [&](const Req &r) { return (r.n * p.g + ROWS - 1) / ROWS; };
   pdl_start();
-  if (warp == 0) {
+  if (CL) {
+    if (threadIdx.x == 0) {
+      const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+      ct->b = list / (p.nkv * p.tiles);
+      ct->h = list / p.tiles % p.nkv;
+      ct->rt = list % p.tiles;
+      const Req r = request(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
+      const int np = ct->rt < tiles_of(r) ? r.np : 0;
+      ct->k = rank * np / p.cs;
+      ct->n_mine = (rank + 1) * np / p.cs - ct->k;
+    }
+  } else if (warp == 0) {
     // Lane i sums the chunks of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
@@ -117,7 +132,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
   const int n = ct->n_mine;
   if (warp == 0) {
     // ------------------------------------------------------------ producer (the whole warp walks)
-    if (n == 0) return;
+    if (!CL && n == 0) return;
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
     const uint64_t pol = policy_evict_first();
     const Runs runs = ct->runs;
@@ -132,19 +147,19 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / NST) & 1) ^ 1), abort_flag, WAIT_NS);
       ok = !__any_sync(0xffffffffu, !ok);
       if (!ok) break;
-      const bool first = i == 0 || k == 0, last = i == n - 1 || k == r.np - 1;
+      const bool first = i == 0 || (!CL && k == 0), last = i == n - 1 || (!CL && k == r.np - 1);
       const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
       const bool bad = page < 0 || page >= p.num_pages;
       const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
       if (lane == 0) {
         if (bad) report(p.status, DFLASH_ERR_DEVICE);
-        if (first) {
+        if (!CL && first) {
           cf = runs.owner(x - k);
           cl = runs.owner(x - k + r.np - 1);
         }
         Chunk c;
         c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
-        c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (cf == cl ? WHOLE : 0);
+        c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
         c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
         c.nrow0 = c.nn = c.nh = c.pad = 0;
         ct->chunk[st] = c;
@@ -166,7 +181,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         tma_load_2d_hint(dk + KB, &tmV, &ct->full[st], 0, rowv, pol);
       }
       issued = i + 1;
-      if (++k == r.np) {
+      if (++k == r.np && !CL) {
         k = 0;
         if (++rt == tiles_of(r)) {
           rt = 0;
@@ -185,10 +200,18 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     // every issued copy lands before the shared memory goes away
     for (int i = max(0, issued - NST); i < issued; ++i)
       mbar_wait(&ct->full[i % NST], static_cast<uint32_t>((i / NST) & 1), nullptr, WAIT_NS);
-    return;
+    if (!CL) return;
   }
   // -------------------------------------------------------------- consumers
-  const int cw = warp - 1, ctid = threadIdx.x - 32;
+  const int cw = warp - 1, ctid = static_cast<int>(threadIdx.x) - 32;
+  // CL: the CTA's share after its last page, in the stage behind that page's:
+  // O [ROWS][D], (maximum, sum) [ROWS]
+  auto share = [&](int st) { return reinterpret_cast<float *>(base + ((st + 1) % NST) * S::STAGE); };
+  auto share_stage = [&](int np, int rank) {
+    const int k = (rank + 1) * np / p.cs - rank * np / p.cs;
+    return k > 0 ? (k - 1) % NST : 0;
+  };
+  static_assert(S::STAGE >= ROWS * (D + 2) * 4, "share");
   uint32_t cphase = 0;
   auto waitw = [&](uint64_t *bar, uint32_t par) -> bool {   // warp-uniform bounded wait
     const bool ok = mbar_wait(bar, par, abort_flag, WAIT_NS);
@@ -205,7 +228,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
   float o[MT][NT][4], m[MT][2], l[MT][2];
   int top[MT][2];                             // the last position a row sees
   bool ok = true;
-  for (int i = 0; i < n && ok; ++i) {
+  const int n_use = CL && warp == 0 ? 0 : n;   // CL: the producer waits for the cluster at the end
+  for (int i = 0; i < n_use && ok; ++i) {
     const int st = i % NST;
     ok = waitw(&ct->full[st], static_cast<uint32_t>((i / NST) & 1));
     if (!ok) break;
@@ -384,7 +408,11 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
           acc.z = fmaf(f, v.z, acc.z);
           acc.w = fmaf(f, v.w, acc.w);
         }
-        if (whole) {
+        if (CL) {   // this CTA's share, in a stage that holds nothing any more
+          float *xo = share(st);
+          *reinterpret_cast<float4 *>(xo + r * D + c4) = acc;
+          if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * r) = make_float2(M, L);
+        } else if (whole) {
           write_row<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), c.rt * ROWS + r, c4, acc, M, L);
         } else {
           __stcg(reinterpret_cast<float4 *>(part + r * D + c4), acc);
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         }
       }
     }
-    if (!ok) break;
+    if (!ok || CL) break;
     if (!whole) {
       __threadfence();
       if (!(ok = csync())) break;
@@ -420,6 +448,57 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
   if (!ok) {
     report(p.status, DFLASH_ERR_TIMEOUT);
     *abort_flag = 1;
+  }
+  if constexpr (CL) {
+    // ---- the cluster's shares: every CTA finishes a part of the tile's columns
+    const Req r = request(p, ct->b, false);
+    const int rows = min(ROWS, r.n * p.g - ct->rt * ROWS), rank = static_cast<int>(cluster_ctarank());
+    const int np = rows > 0 ? r.np : 0;
+    float *xo = share(share_stage(np, rank));
+    if (n == 0 || !ok)   // nothing to add
+      for (int i = ctid; i >= 0 && i < ROWS; i += 128) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
+    __syncwarp();
+    cluster_sync();
+    for (int e = rank * 128 + ctid; ctid >= 0 && e < rows * (D / 4); e += p.cs * 128) {
+      const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
+      float M = -INFINITY, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < p.cs; k0 += 8) {
+        float2 ml[8];
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {   // the shares' places differ by how many pages a CTA had
+          const int k = min(k0 + u, p.cs - 1);
+          const float *xk = share(share_stage(np, k));
+          ml[u] = ld_dsmem_f2(dsmem_addr(xk + ROWS * D + 2 * row, k));
+          v[u] = ld_dsmem_f4(dsmem_addr(xk + row * D + c4, k));
+        }
+        float mn = M;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (k0 + u >= p.cs) ml[u] = make_float2(-INFINITY, 0.f);
+          mn = fmaxf(mn, ml[u].x);
+        }
+        if (mn == -INFINITY) continue;
+        const float f = fast_exp2(M - mn);
+        M = mn;
+        L *= f;
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (ml[u].y == 0.f) continue;   // a share of nothing was never written
+          const float w = fast_exp2(ml[u].x - mn);
+          L = fmaf(w, ml[u].y, L);
+          acc.x = fmaf(w, v[u].x, acc.x);
+          acc.y = fmaf(w, v[u].y, acc.y);
+          acc.z = fmaf(w, v[u].z, acc.z);
+          acc.w = fmaf(w, v[u].w, acc.w);
+        }
+      }
+      write_row<__nv_bfloat16, D>(dest_of(p, r.row0, ct->h), ct->rt * ROWS + row, c4, acc, M, L);
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while its share is read
   }
 }
 
@@ -630,20 +709,35 @@ int tile_rows_bf16(const dflash_heads &h, int max_new) {
   return max_new * (h.n_q_heads / h.n_kv_heads) <= 16 ? 16 : 32;
 }
 
-template <int D, int MT>
+template <int D, int MT, bool CL>
 int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
   using S = Shape<D, MT>;
-  auto *kernel = decode_kernel<D, MT>;
-  static std::atomic<uint64_t> smem_set;
+  auto *kernel = decode_kernel<D, MT, CL>;
+  static std::atomic<uint64_t> smem_set, wide_set;
   if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
+  if (CL && p.cs > 8)
+    if (int e = allow_wide_clusters(wide_set, dev, kernel)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
   if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
   p.min_chunks = 2;
   const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
-  launch_pdl(kernel, dim3(min(dev.sms * S::CTAS, most)), dim3(160), S::SMEM, s, tk, tv, p);
-  return cuda_check(cudaGetLastError(), "cache_attention launch");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.tiles * p.cs) : static_cast<unsigned>(min(dev.sms * S::CTAS, most)));
+  cfg.blockDim = dim3(160);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL ? p.cs : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, tk, tv, p), "cache_attention launch");
 }
 
 template <int D>
@@ -740,9 +834,20 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   }
   const int tr = tile_rows_bf16(*hs, max_new);
   p.tiles = row_tiles(*hs, max_new, tr);
-  if (tr == 16)
-    return d == 64 ? launch_decode<64, 1>(*hs, *kv, p, dev, s) : launch_decode<128, 1>(*hs, *kv, p, dev, s);
-  return d == 64 ? launch_decode<64, 2>(*hs, *kv, p, dev, s) : launch_decode<128, 2>(*hs, *kv, p, dev, s);
+  // Clusters of up to 16 CTAs (8 where a CTA fills its SM) per tile while one CTA per SM holds them all,
+  // and the capacity leaves a CTA 16 pages at most: beyond that the balanced
+  // runs over the whole GPU are faster.
+  const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
+  p.cs = 1;
+  while (p.cs < (tr == 16 ? 16 : 8) && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  const bool cl = p.cs > 1 && kv->max_pages <= 16 * p.cs;
+#define DECODE(D_, MT_) \
+  return cl ? launch_decode<D_, MT_, true>(*hs, *kv, p, dev, s) : launch_decode<D_, MT_, false>(*hs, *kv, p, dev, s)
+  if (d == 64 && tr == 16) DECODE(64, 1);
+  if (d == 64) DECODE(64, 2);
+  if (tr == 16) DECODE(128, 1);
+  DECODE(128, 2);
+#undef DECODE
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@ struct Params {
   int B, nkv, g, total, max_new, window;
   int tiles;                               // row tiles of a (request, kv head) at most: counter stride
   int min_chunks;
+  int cs;                                  // cluster form: CTAs per tile
   float scale_log2;
   int *counters;
   float *partials;

@@ -502,12 +502,8 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   static std::atomic<uint64_t> smem_set[2], wide_set[2];
   const int which = dtype == DFLASH_F32;
   if (int e = allow_smem(smem_set[which], dev, kernel, SMEM)) return e;
-  if (cs > 8 && !(dev.index < 64 && wide_set[which].load(std::memory_order_relaxed) >> dev.index & 1)) {
-    if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
-                           "token_logprobs cluster size"))
-      return e;
-    if (dev.index < 64) wide_set[which].fetch_or(1ull << dev.index, std::memory_order_relaxed);
-  }
+  if (cs > 8)
+    if (int e = allow_wide_clusters(wide_set[which], dev, kernel)) return e;
   cudaLaunchConfig_t cfg = {};
   a.cs = cs;
   cfg.gridDim = dim3(static_cast<unsigned>(cs) * rows);

@@ -33,6 +33,16 @@ int allow_smem(std::atomic<uint64_t> &done, const Device &d, K *kernel, int byte
   done.fetch_or(bit, std::memory_order_relaxed);
   return DFLASH_OK;
 }
+// the same for clusters of more than 8 CTAs
+template <typename K>
+int allow_wide_clusters(std::atomic<uint64_t> &done, const Device &d, K *kernel) {
+  const uint64_t bit = d.index < 64 ? 1ull << d.index : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return DFLASH_OK;
+  if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), "cluster size"))
+    return e;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return DFLASH_OK;
+}
 
 inline int elt_bytes(const dflash_heads &h) { return h.dtype == DFLASH_F32 ? 4 : 2; }
 // first element of a layer's K (and V) pages
