@@ -9,30 +9,32 @@
 // are read once for all its g query heads and all new tokens (rows r = i g +
 // query head, R = n g of them).  At 2 d bf16 values a token and 4 d R
 // operations on them the pass is bound by HBM, and the work is the flat list
-// of pages over (request, kv head, row tile), cut into equal runs, one
-// persistent CTA each, so that ragged batches and a single long request both
-// fill the GPU.  A (request, kv head, row tile) cut by a run boundary leaves
-// (max, sum, O) partials, and the last contributor to arrive joins them in
+// of pages over (request, kv head), cut into equal runs, one persistent CTA
+// each, so that ragged batches and a single long request both fill the GPU.
+// A (request, kv head) cut by a run boundary leaves (max, sum, O) partials, and the last contributor to arrive joins them in
 // contributor order: the same bits on every call.
 #include "cache_attention.cuh"
 
 namespace dflash {
 namespace {
 
-// ------------------------------------------------------------------ bf16, up to 32 rows per tile: warp MMAs
-// A tile of MT x 16 query rows per (request, kv head) on mma.sync: with so few
-// rows the tensor work is a fraction of the HBM time whichever way it is
-// issued, and register accumulators keep a page's path short.  Warp 0
+// ------------------------------------------------------------------ bf16, up to 16 query rows per (request, kv head): warp MMAs
+// One 16-row tile on mma.sync: with so few rows the tensor work is a fraction
+// of the HBM time whichever way it is issued, and register accumulators keep a
+// page's path short.  (Two tiles of 16 rows per warp, tried for 17..32 rows,
+// left one CTA per SM at 255 registers: 149 us against 103 of the tcgen05 form
+// for 5 tokens x 4 heads at 128k.)  Warp 0
 // produces: K page as 128-byte-swizzled 64-column halves, V^T page, and for a
 // new tile its query rows, into a ring of NST stages.  Warps 1-4 each take 16
 // tokens of every page with a maximum, sum and O of their own (no exchange
 // per page) and meet when the tile ends, in the last page's stage.
-template <int D, int MT>
+constexpr int ROWS = 16;
+template <int D>
 struct Shape {
   static constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;
-  static constexpr int ROWS = MT * 16, QP = D * 2 + 16, QB = ROWS * QP;    // query rows, padded pitch
-  static constexpr int NST = D == 64 ? 6 : MT == 1 ? 3 : 5;
-  static constexpr int CTAS = MT == 1 ? 2 : 1;                             // per SM
+  static constexpr int QP = D * 2 + 16, QB = ROWS * QP;                    // query rows at a padded pitch
+  static constexpr int NST = D == 64 ? 6 : 3;
+  static constexpr int CTAS = 2;                                           // per SM
   static constexpr int SMEM = 1024 + NST * (STAGE + QB) + 1024;
   static constexpr int PART = ROWS * (D + 2);                              // floats of a partial
 };
@@ -41,20 +43,20 @@ struct __align__(16) Ctrl {
   uint64_t full[6], empty[6], cons;
   long long lo;
   Runs runs;
-  int n_mine, b, h, rt, k;                 // the run's first chunk: page k of (b, h, rt)
+  int n_mine, b, h, k;                     // the run's first page: k of (b, h)
   int abort_flag, merge;
   Chunk chunk[6];
 };
 
-// CL: few (request, kv head, row tile)s over short capacities.  One cluster of
+// CL: few (request, kv head)s over short capacities.  One cluster of
 // p.cs CTAs per tile shares its pages out evenly, with no list to scan, and
 // the shares meet in distributed shared memory: on a request of 2 048 tokens
 // the partials' way through L2 and its counter took 5 of 15 us.
-template <int D, int MT, bool CL>
-__global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
+template <int D, bool CL>
+__global__ void __launch_bounds__(160, Shape<D>::CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
-  using S = Shape<D, MT>;
-  constexpr int NST = S::NST, KB = S::KB, ROWS = S::ROWS, NT = D / 8, KS = D / 16;
+  using S = Shape<D>;
+  constexpr int NST = S::NST, KB = S::KB, NT = D / 8, KS = D / 16;
   static_assert(sizeof(Ctrl) <= 1024 && S::SMEM <= 232448 / S::CTAS, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -71,28 +73,22 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     fence_mbar_init();
   }
   volatile int *abort_flag = &ct->abort_flag;
-  auto tiles_of = [&](const Req &r) { return (r.n * p.g + ROWS - 1) / ROWS; };
   pdl_start();
   if (CL) {
     if (threadIdx.x == 0) {
       const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
-      ct->b = list / (p.nkv * p.tiles);
-      ct->h = list / p.tiles % p.nkv;
-      ct->rt = list % p.tiles;
-      const Req r = request(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
-      const int np = ct->rt < tiles_of(r) ? r.np : 0;
+      ct->b = list / p.nkv;
+      ct->h = list % p.nkv;
+      const int np = request(p, ct->b, rank == 0 && ct->h == 0).np;
       ct->k = rank * np / p.cs;
       ct->n_mine = (rank + 1) * np / p.cs - ct->k;
     }
   } else if (warp == 0) {
-    // Lane i sums the chunks of a contiguous slice of the requests; a warp
+    // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Req r = request(p, b, blockIdx.x == 0);
-      sum += static_cast<long long>(r.np) * tiles_of(r);
-    }
+    for (int b = b0; b < b1; ++b) sum += request(p, b, blockIdx.x == 0).np;
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -113,15 +109,12 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
       for (int b = b0; b < b1; ++b) {
-        const Req r = request(p, b, false);
-        const long long item = r.np, head = item * tiles_of(r), span = head * p.nkv;
+        const long long np = request(p, b, false).np, span = np * p.nkv;
         if (lo < pre + span) {
-          const long long off = lo - pre;
+          const long long h = quotient(lo - pre, np);
           ct->b = b;
-          const long long h = quotient(off, head), rt = quotient(off - h * head, item);
           ct->h = static_cast<int>(h);
-          ct->rt = static_cast<int>(rt);
-          ct->k = static_cast<int>(off - h * head - rt * item);
+          ct->k = static_cast<int>(lo - pre - h * np);
           break;
         }
         pre += span;
@@ -137,7 +130,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     const uint64_t pol = policy_evict_first();
     const Runs runs = ct->runs;
     int cf = 0, cl = 0;
-    int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
+    int b = ct->b, h = ct->h, k = ct->k;
     long long x = ct->lo;
     Req r = request(p, b, false);
     int issued = 0;
@@ -150,7 +143,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       const bool first = i == 0 || (!CL && k == 0), last = i == n - 1 || (!CL && k == r.np - 1);
       const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
       const bool bad = page < 0 || page >= p.num_pages;
-      const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
+      const int live = first ? r.n * p.g : 0;   // query rows to load
       if (lane == 0) {
         if (bad) report(p.status, DFLASH_ERR_DEVICE);
         if (!CL && first) {
@@ -158,18 +151,17 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
           cl = runs.owner(x - k + r.np - 1);
         }
         Chunk c;
-        c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+        c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
         c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-        c.nrow0 = c.nn = c.nh = c.pad = 0;
+        c.nrow0 = c.nn = c.nh = c.pad = c.pad2 = 0;
         ct->chunk[st] = c;
         mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * 2);
       }
       __syncwarp();
       if (lane < live) {
-        const int row = rt * ROWS + lane, i_new = row / p.g;
         bulk_load(sQ + st * S::QB + lane * S::QP,
-                  q + static_cast<size_t>(r.row0 + i_new) * p.ldq + static_cast<size_t>(h * p.g + row % p.g) * D, D * 2,
+                  q + static_cast<size_t>(r.row0 + lane / p.g) * p.ldq + static_cast<size_t>(h * p.g + lane % p.g) * D, D * 2,
                   &ct->full[st]);
       }
       if (lane == 0 && !bad) {
@@ -183,13 +175,10 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       issued = i + 1;
       if (++k == r.np && !CL) {
         k = 0;
-        if (++rt == tiles_of(r)) {
-          rt = 0;
-          if (++h == p.nkv && i + 1 < n) {
-            h = 0;
-            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
-            while (r.np == 0 && b + 1 < p.B);
-          }
+        if (++h == p.nkv && i + 1 < n) {
+          h = 0;
+          do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+          while (r.np == 0 && b + 1 < p.B);
         }
       }
     }
@@ -224,51 +213,42 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
     ++cphase;
     return ok;
   };
-  uint32_t qf[MT][KS][4];
-  float o[MT][NT][4], m[MT][2], l[MT][2];
-  int top[MT][2];                             // the last position a row sees
+  uint32_t qf[KS][4];
+  float o[NT][4], m[2], l[2];                 // rows lane / 4 and lane / 4 + 8
+  int top[2];                                 // the last position a row sees
   bool ok = true;
   const int n_use = CL && warp == 0 ? 0 : n;   // CL: the producer waits for the cluster at the end
   for (int i = 0; i < n_use && ok; ++i) {
     const int st = i % NST;
     ok = waitw(&ct->full[st], static_cast<uint32_t>((i / NST) & 1));
     if (!ok) break;
-    const Chunk c = ct->chunk[st];
+    const Chunk &c = ct->chunk[st];   // stays until the stage is released: no registers for it
     uint8_t *stage = base + st * S::STAGE;
     if (c.flags & FIRST) {
       const uint32_t qa = smem_u32(sQ + st * S::QB) + ((lane & 7) + (lane & 8)) * S::QP + (lane >> 4) * 16;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int kk = 0; kk < KS; ++kk) ldmatrix_x4(qa + kk * 32, qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3]);
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-          ldmatrix_x4(qa + mt * 16 * S::QP + kk * 32, qf[mt][kk][0], qf[mt][kk][1], qf[mt][kk][2], qf[mt][kk][3]);
+      for (int e = 0; e < 2; ++e) {
+        // rows past the tile's are zeros, whatever the slot held: they have
+        // a say in when the warp moves its maxima
+        const int row = e * 8 + (lane >> 2);
+        if (row >= c.n * p.g)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // rows past the tile's are zeros, whatever the slot held: they have
-          // a say in when the warp moves its maxima
-          if (c.rt * ROWS + mt * 16 + e * 8 + (lane >> 2) >= c.n * p.g)
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) qf[mt][kk][e] = qf[mt][kk][2 + e] = 0u;
-          m[mt][e] = -INFINITY;
-          l[mt][e] = 0.f;
-          top[mt][e] = c.ctx + min(c.n - 1, (c.rt * ROWS + mt * 16 + e * 8 + (lane >> 2)) / p.g);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][t][e] = 0.f;
+          for (int kk = 0; kk < KS; ++kk) qf[kk][e] = qf[kk][2 + e] = 0u;
+        m[e] = -INFINITY;
+        l[e] = 0.f;
+        top[e] = c.ctx + min(c.n - 1, row / p.g);
       }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
     }
     const int t0 = c.page * PAGE + cw * 16;   // this warp's 16 positions
     const int newest = c.ctx + c.n - 1, oldest = p.window > 0 ? c.ctx - p.window + 1 : 0;
     if (!(c.flags & BAD) && t0 <= newest && t0 + 15 >= oldest) {
-      float s[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][t][e] = 0.f;
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       const int ktok = cw * 16 + (lane >> 4) * 8 + (lane & 7);
       const uint32_t ka = smem_u32(stage) + ktok * 128;
 #pragma unroll
@@ -276,62 +256,54 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         uint32_t b0, b1, b2, b3;
         const int ch = (kk & 3) * 2 + ((lane >> 3) & 1);
         ldmatrix_x4(ka + (kk >> 2) * (PAGE * 128) + ((ch ^ (ktok & 7)) << 4), b0, b1, b2, b3);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816(s[mt][0], qf[mt][kk], b0, b1);
-          mma_bf16_16816(s[mt][1], qf[mt][kk], b2, b3);
-        }
+        mma_bf16_16816(s[0], qf[kk], b0, b1);
+        mma_bf16_16816(s[1], qf[kk], b2, b3);
       }
       // positions a row does not see (whatever their slots hold)
       const bool edge = t0 + 15 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
       if (edge) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int pos = t0 + t * 8 + (lane & 3) * 2 + (e & 1), hi = top[mt][e >> 1];
-              if (pos > hi || (p.window > 0 && pos <= hi - p.window)) s[mt][t][e] = -INFINITY;
-            }
-      }
-      uint32_t pa[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float mx[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = fmaxf(fmaxf(s[mt][0][2 * e] * p.scale_log2, s[mt][0][2 * e + 1] * p.scale_log2),
-                          fmaxf(s[mt][1][2 * e] * p.scale_log2, s[mt][1][2 * e + 1] * p.scale_log2));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-          mx[e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        }
-        const bool need = mx[0] > m[mt][0] + RESCALE_LOG2 || mx[1] > m[mt][1] + RESCALE_LOG2;
-        if (__any_sync(0xffffffffu, need)) {
-          float f[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mn = fmaxf(m[mt][e], mx[e]);
-            f[e] = mn == -INFINITY ? 1.f : fast_exp2(m[mt][e] - mn);
-            m[mt][e] = mn;
-            l[mt][e] *= f[e];
+          for (int e = 0; e < 4; ++e) {
+            const int pos = t0 + t * 8 + (lane & 3) * 2 + (e & 1), hi = top[e >> 1];
+            if (pos > hi || (p.window > 0 && pos <= hi - p.window)) s[t][e] = -INFINITY;
           }
+      }
+      float mx[2];
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][t][e] *= f[e >> 1];
-        }
+      for (int e = 0; e < 2; ++e) {
+        float v = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])) * p.scale_log2;
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+        mx[e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+      }
+      const bool need = mx[0] > m[0] + RESCALE_LOG2 || mx[1] > m[1] + RESCALE_LOG2;
+      if (__any_sync(0xffffffffu, need)) {
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float nm = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
-          const float p0 = fast_exp2(fmaf(s[mt][0][2 * e], p.scale_log2, nm));
-          const float p1 = fast_exp2(fmaf(s[mt][0][2 * e + 1], p.scale_log2, nm));
-          const float p2 = fast_exp2(fmaf(s[mt][1][2 * e], p.scale_log2, nm));
-          const float p3 = fast_exp2(fmaf(s[mt][1][2 * e + 1], p.scale_log2, nm));
-          l[mt][e] += (p0 + p1) + (p2 + p3);
-          pa[mt][e] = pack_bf16(p0, p1);
-          pa[mt][2 + e] = pack_bf16(p2, p3);
+          const float mn = fmaxf(m[e], mx[e]);
+          f[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
+          m[e] = mn;
+          l[e] *= f[e];
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] *= f[e >> 1];
+      }
+      // P rounded to bf16, the type its product with V takes; the sum keeps fp32
+      uint32_t pa[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float nm = m[e] == -INFINITY ? 0.f : -m[e];
+        const float p0 = fast_exp2(fmaf(s[0][2 * e], p.scale_log2, nm));
+        const float p1 = fast_exp2(fmaf(s[0][2 * e + 1], p.scale_log2, nm));
+        const float p2 = fast_exp2(fmaf(s[1][2 * e], p.scale_log2, nm));
+        const float p3 = fast_exp2(fmaf(s[1][2 * e + 1], p.scale_log2, nm));
+        l[e] += (p0 + p1) + (p2 + p3);
+        pa[e] = pack_bf16(p0, p1);
+        pa[2 + e] = pack_bf16(p2, p3);
       }
       // slots past the newest token may hold anything: their V becomes 0
       const bool stale = t0 + 15 > newest;
@@ -348,11 +320,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
         uint32_t b0, b1, b2, b3;
         ldmatrix_x4(va + (t * 8 + dr) * 128 + ((vch ^ (dr & 7)) << 4), b0, b1, b2, b3);
         if (stale) b0 &= keep0, b1 &= keep1, b2 &= keep0, b3 &= keep1;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma_bf16_16816(o[mt][t], pa[mt], b0, b1);
-          mma_bf16_16816(o[mt][t + 1], pa[mt], b2, b3);
-        }
+        mma_bf16_16816(o[t], pa, b0, b1);
+        mma_bf16_16816(o[t + 1], pa, b2, b3);
       }
     }
     if (!(c.flags & LAST)) {
@@ -361,65 +330,59 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       continue;
     }
     // ---- the end of this CTA's part of the tile: the four warps' shares are
-    // joined in the stage this chunk occupied, 16 rows at a time.  O is laid
-    // out [warp][row][D] with the columns XORed by the row (no bank conflicts).
+    // joined in the stage this page occupied, O as [warp][row][D] with the
+    // columns XORed by the row (no bank conflicts)
     const bool whole = c.flags & WHOLE;
     float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * S::PART;
-    const int rows = min(ROWS, c.n * p.g - c.rt * ROWS);
+    const int rows = c.n * p.g;
     float *so = reinterpret_cast<float *>(stage);
     float *sm = reinterpret_cast<float *>(sQ + st * S::QB);   // [4][16] maxima, then sums (the Q slot is consumed)
     static_assert(S::QB >= 4 * 16 * 2 * 4 && S::STAGE == 4 * 16 * D * 4, "join scratch");
+    if (!(ok = csync())) break;   // every warp has read the stage
 #pragma unroll
-    for (int mt = 0; mt < MT && ok; ++mt) {
-      ok = csync();   // every warp has read the stage (and the previous 16 rows' sums)
-      if (!ok) break;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float s = l[mt][e];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        const int row = (lane >> 2) + e * 8;
-        if ((lane & 3) == 0) {
-          sm[cw * 16 + row] = m[mt][e];
-          sm[64 + cw * 16 + row] = s;
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int col = (t * 8 + (lane & 3) * 2) ^ ((row & 7) << 3);
-          *reinterpret_cast<float2 *>(so + (cw * 16 + row) * D + col) = make_float2(o[mt][t][2 * e], o[mt][t][2 * e + 1]);
-        }
+    for (int e = 0; e < 2; ++e) {
+      float s = l[e];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      const int row = (lane >> 2) + e * 8;
+      if ((lane & 3) == 0) {
+        sm[cw * 16 + row] = m[e];
+        sm[64 + cw * 16 + row] = s;
       }
-      ok = csync();
-      if (!ok) break;
-      for (int e = ctid; e < 16 * (D / 4); e += 128) {
-        const int row = e / (D / 4), c4 = (e % (D / 4)) * 4, r = mt * 16 + row;
-        if (r >= rows) break;
-        float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w * 16 + row]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int t = 0; t < NT; ++t) {
+        const int col = (t * 8 + (lane & 3) * 2) ^ ((row & 7) << 3);
+        *reinterpret_cast<float2 *>(so + (cw * 16 + row) * D + col) = make_float2(o[t][2 * e], o[t][2 * e + 1]);
+      }
+    }
+    if (!(ok = csync())) break;
+    for (int e = ctid; e < rows * (D / 4); e += 128) {
+      const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float mw = sm[w * 16 + row], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
-          const float4 v = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * D + (c4 ^ ((row & 7) << 3)));
-          L = fmaf(f, sm[64 + w * 16 + row], L);
-          acc.x = fmaf(f, v.x, acc.x);
-          acc.y = fmaf(f, v.y, acc.y);
-          acc.z = fmaf(f, v.z, acc.z);
-          acc.w = fmaf(f, v.w, acc.w);
-        }
-        if (CL) {   // this CTA's share, in a stage that holds nothing any more
-          float *xo = share(st);
-          *reinterpret_cast<float4 *>(xo + r * D + c4) = acc;
-          if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * r) = make_float2(M, L);
-        } else if (whole) {
-          write_row<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), c.rt * ROWS + r, c4, acc, M, L);
-        } else {
-          __stcg(reinterpret_cast<float4 *>(part + r * D + c4), acc);
-          if (c4 == 0) {
-            __stcg(part + ROWS * D + r, M);
-            __stcg(part + ROWS * D + ROWS + r, L);
-          }
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w * 16 + row]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float mw = sm[w * 16 + row], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+        const float4 v = *reinterpret_cast<const float4 *>(so + (w * 16 + row) * D + (c4 ^ ((row & 7) << 3)));
+        L = fmaf(f, sm[64 + w * 16 + row], L);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (CL) {   // this CTA's share, in a stage that holds nothing any more
+        float *xo = share(st);
+        *reinterpret_cast<float4 *>(xo + row * D + c4) = acc;
+        if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * row) = make_float2(M, L);
+      } else if (whole) {
+        write_row<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), row, c4, acc, M, L);
+      } else {
+        __stcg(reinterpret_cast<float4 *>(part + row * D + c4), acc);
+        if (c4 == 0) {
+          __stcg(part + ROWS * D + row, M);
+          __stcg(part + ROWS * D + ROWS + row, L);
         }
       }
     }
@@ -428,7 +391,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       __threadfence();
       if (!(ok = csync())) break;
       if (ctid == 0) {
-        int *ctr = p.counters + (static_cast<size_t>(c.b) * p.nkv + c.h) * p.tiles + c.rt;
+        int *ctr = p.counters + static_cast<size_t>(c.b) * p.nkv + c.h;
         const int old = atomicAdd(ctr, 1), done = old == c.cl - c.cf;
         if (done) atomicExch(ctr, 0);
         __threadfence();
@@ -436,8 +399,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS, rows,
-                      c.rt * ROWS, ctid, 128);
+        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS, rows, ctid,
+                      128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
     }
@@ -452,9 +415,8 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
     const Req r = request(p, ct->b, false);
-    const int rows = min(ROWS, r.n * p.g - ct->rt * ROWS), rank = static_cast<int>(cluster_ctarank());
-    const int np = rows > 0 ? r.np : 0;
-    float *xo = share(share_stage(np, rank));
+    const int rows = r.n * p.g, rank = static_cast<int>(cluster_ctarank());
+    float *xo = share(share_stage(r.np, rank));
     if (n == 0 || !ok)   // nothing to add
       for (int i = ctid; i >= 0 && i < ROWS; i += 128) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
     __syncwarp();
@@ -469,7 +431,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {   // the shares' places differ by how many pages a CTA had
           const int k = min(k0 + u, p.cs - 1);
-          const float *xk = share(share_stage(np, k));
+          const float *xk = share(share_stage(r.np, k));
           ml[u] = ld_dsmem_f2(dsmem_addr(xk + ROWS * D + 2 * row, k));
           v[u] = ld_dsmem_f4(dsmem_addr(xk + row * D + c4, k));
         }
@@ -495,7 +457,7 @@ __global__ void __launch_bounds__(160, Shape<D, MT>::CTAS)
           acc.w = fmaf(w, v[u].w, acc.w);
         }
       }
-      write_row<__nv_bfloat16, D>(dest_of(p, r.row0, ct->h), ct->rt * ROWS + row, c4, acc, M, L);
+      write_row<__nv_bfloat16, D>(dest_of(p, r.row0, ct->h), row, c4, acc, M, L);
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while its share is read
@@ -695,8 +657,7 @@ __global__ void __launch_bounds__(F_THREADS) decode_f32_kernel(const Params p) {
   __syncthreads();
   if (!last) return;
   const float *all = p.partials + static_cast<size_t>(blockIdx.x) * gridDim.y * FP;
-  join_tile<float, D, 1, 8>(dest_of(p, r.row0, h), [&](int i) { return all + i * FP; }, gridDim.y, F_ROWS, rows,
-                            rt * F_ROWS, tid, F_THREADS);
+  join_tile<float, D, 1, 8>(dest_of(p, r.row0, h, rt * F_ROWS), [&](int i) { return all + i * FP; }, gridDim.y, F_ROWS, rows, tid, F_THREADS);
 }
 
 // ------------------------------------------------------------------ host
@@ -704,15 +665,10 @@ int row_tiles(const dflash_heads &h, int max_new, int tile_rows) {
   return (max_new * (h.n_q_heads / h.n_kv_heads) + tile_rows - 1) / tile_rows;
 }
 
-// rows of a tile: 16 where the call's rows fit, else 32
-int tile_rows_bf16(const dflash_heads &h, int max_new) {
-  return max_new * (h.n_q_heads / h.n_kv_heads) <= 16 ? 16 : 32;
-}
-
-template <int D, int MT, bool CL>
+template <int D, bool CL>
 int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
-  using S = Shape<D, MT>;
-  auto *kernel = decode_kernel<D, MT, CL>;
+  using S = Shape<D>;
+  auto *kernel = decode_kernel<D, CL>;
   static std::atomic<uint64_t> smem_set, wide_set;
   if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   if (CL && p.cs > 8)
@@ -724,7 +680,7 @@ int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   p.min_chunks = 2;
   const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.tiles * p.cs) : static_cast<unsigned>(min(dev.sms * S::CTAS, most)));
+  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.cs) : static_cast<unsigned>(min(dev.sms * S::CTAS, most)));
   cfg.blockDim = dim3(160);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
@@ -828,26 +784,16 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
     p.tiles = row_tiles(*hs, max_new, F_ROWS);
     return d == 64 ? launch_f32<64>(p, dev, s) : launch_f32<128>(p, dev, s);
   }
-  if (d == 128 && max_new * p.g > 32) {
-    p.tiles = 1;
-    return launch_verify(*hs, *kv, p, dev, s);
-  }
-  const int tr = tile_rows_bf16(*hs, max_new);
-  p.tiles = row_tiles(*hs, max_new, tr);
-  // Clusters of up to 16 CTAs (8 where a CTA fills its SM) per tile while one CTA per SM holds them all,
-  // and the capacity leaves a CTA 16 pages at most: beyond that the balanced
-  // runs over the whole GPU are faster.
-  const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
+  if (max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
+  // Clusters of up to 16 CTAs per (request, kv head) while one CTA per SM holds
+  // them all, and the capacity leaves a CTA 16 pages at most: beyond that the
+  // balanced runs over the whole GPU are faster.
+  const long long lists = static_cast<long long>(batch) * nkv;
   p.cs = 1;
-  while (p.cs < (tr == 16 ? 16 : 8) && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  while (p.cs < 16 && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
   const bool cl = p.cs > 1 && kv->max_pages <= 16 * p.cs;
-#define DECODE(D_, MT_) \
-  return cl ? launch_decode<D_, MT_, true>(*hs, *kv, p, dev, s) : launch_decode<D_, MT_, false>(*hs, *kv, p, dev, s)
-  if (d == 64 && tr == 16) DECODE(64, 1);
-  if (d == 64) DECODE(64, 2);
-  if (tr == 16) DECODE(128, 1);
-  DECODE(128, 2);
-#undef DECODE
+  if (d == 64) return cl ? launch_decode<64, true>(*hs, *kv, p, dev, s) : launch_decode<64, false>(*hs, *kv, p, dev, s);
+  return cl ? launch_decode<128, true>(*hs, *kv, p, dev, s) : launch_decode<128, false>(*hs, *kv, p, dev, s);
 }
 
 }  // extern "C"

@@ -25,7 +25,7 @@ struct Params {
   const int32_t *page_table, *cu_new, *ctx_len;
   int max_pages, num_pages;
   int B, nkv, g, total, max_new, window;
-  int tiles;                               // row tiles of a (request, kv head) at most: counter stride
+  int tiles;                               // fp32 form: row tiles of a (request, kv head)
   int min_chunks;
   int cs;                                  // cluster form: CTAs per tile
   float scale_log2;
@@ -85,10 +85,10 @@ struct Runs {
 // What the consumers need to know of a chunk, written by the producer beside
 // the chunk's data.
 struct Chunk {
-  int b, h, rt, page;        // request, kv head, row tile, page of the request
+  int b, h, page, pad;       // request, kv head, page of the request
   int row0, n, ctx, flags;   // FIRST / LAST of this CTA's part, BAD page, WHOLE: no other CTA has a part
   int cf, cl, slot0, slot;   // contributors cf..cl; whether cf's part is its first; this part's slot
-  int nrow0, nn, nh, pad;    // the tile after this one, where this CTA has a part of it: its rows and kv head (nn 0: none)
+  int nrow0, nn, nh, pad2;   // the tile after this one, where this CTA has a part of it: its rows and kv head (nn 0: none)
 };
 enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 
@@ -99,12 +99,16 @@ struct Dest {
   void *out;
   float *lse;
   int row0, h, nkv, g;     // the request's first row, the kv head
+  int base;                // the tile's first query row
 };
-__device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h) { return {p.out, p.lse, row0, h, p.nkv, p.g}; }
+__device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h, int base = 0) {
+  return {p.out, p.lse, row0, h, p.nkv, p.g, base};
+}
 
-// One query row's output, columns c4 .. c4 + 3, and its log-sum-exp.
+// Row `row` of the tile: output columns c4 .. c4 + 3, and its log-sum-exp.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
+  row += p.base;
   const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   T *dst = static_cast<T *>(p.out) + at * D + c4;
@@ -120,8 +124,7 @@ __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4
 // src(0..np-1)), in that order.  The partials sit in L2, so the time is its
 // latency: NV float4 columns and B partials per thread are in flight.
 template <typename T, int D, int NV, int B, typename Src>
-__device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int tile_rows, int rows, int row_base, int tid,
-                                          int nthr) {
+__device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int tile_rows, int rows, int tid, int nthr) {
   constexpr int PER = D / 4 / NV;   // items per row
   for (int e = tid; e < rows * PER; e += nthr) {
     const int r = e / PER, c = (e % PER) * 4;   // columns c + 4 PER k
@@ -166,7 +169,7 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
       }
     }
 #pragma unroll
-    for (int k = 0; k < NV; ++k) write_row<T, D>(p, row_base + r, c + 4 * PER * k, acc[k], M, L);
+    for (int k = 0; k < NV; ++k) write_row<T, D>(p, r, c + 4 * PER * k, acc[k], M, L);
   }
 }
 // the same for the runs' partials: np contributors from CTA cf on, a tile's
@@ -174,15 +177,15 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
 // no registers to spare for it.
 template <int D>
 __device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, int np, int slot0, int stride, int tile_rows,
-                                        int rows, int row_base, int tid, int nthr) {
+                                        int rows, int tid, int nthr) {
   auto src = [&](int i) { return partials + (static_cast<size_t>(cf + i) * 2 + (i > 0 || slot0 ? 0 : 1)) * stride; };
   if (rows * (D / 4) <= 2 * nthr)
-    join_tile<__nv_bfloat16, D, 1, 8>(p, src, np, tile_rows, rows, row_base, tid, nthr);
+    join_tile<__nv_bfloat16, D, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else
-    join_tile<__nv_bfloat16, D, 4, 4>(p, src, np, tile_rows, rows, row_base, tid, nthr);
+    join_tile<__nv_bfloat16, D, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
 }
 
-// Query rows > 32 per (request, kv head) on tcgen05 (cache_attention_tc.cu).
+// 17..128 query rows per (request, kv head) on tcgen05 (cache_attention_tc.cu).
 int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s);
 
 }  // namespace dflash

@@ -1,5 +1,5 @@
-// The verification form of dflash_cache_attention: 33..128 query rows per
-// (request, kv head), head_dim 128, bf16, on the 5th-generation tensor cores.
+// The verification form of dflash_cache_attention: 17..128 query rows per
+// (request, kv head), bf16, on the 5th-generation tensor cores.
 //
 // At 80 rows (5 heads x 16 tokens) a 64-token page is 2.6 MFLOP of products on
 // 32 KB: 0.55 PFLOP/s at HBM speed, past what warp-level MMAs reach, so S = Q
@@ -20,28 +20,39 @@
 namespace dflash {
 namespace {
 
-constexpr int D = 128, MROWS = 128;
-constexpr int ST = 6, NSB = 3;                           // ring depth, S buffers
-constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;         // K page as two halves of [64][64], then V^T [128][64]
-constexpr int SMEM = 1024 + ST * STAGE + 1024;
+constexpr int MROWS = 128;
+constexpr int NSB = 3;                                   // S buffers
 constexpr int NTHR = 224;
-constexpr int PART = MROWS * (D + 2);
 constexpr uint32_t TMEM_COLS = 512, O_COL = 256, P_COL = 384;   // S at 0, 64, 128; P: two buffers of 32 columns
-__device__ __forceinline__ uint32_t q_col(int buf) { return buf ? 448u : 192u; }   // Q: 64 columns each
+template <int D>
+struct Shape {
+  static constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;       // K page as halves of [64][64], then V^T [D][64]
+  static constexpr int ST = D == 128 ? 6 : 12;                  // ring depth
+  static constexpr int SMEM = 1024 + ST * STAGE + 2048;
+  static constexpr int PART = MROWS * (D + 2);
+};
+constexpr int MAX_ST = 12;
+__device__ __forceinline__ uint32_t q_col(int buf) { return buf ? 448u : 192u; }   // Q: D / 2 columns each
 
 struct __align__(16) Ctrl {
-  uint64_t full[ST], empty[ST], sfull[NSB], sempty[NSB], pfull[2], pdone[2], qfull[2], oempty, cons, drain;
+  uint64_t full[MAX_ST], empty[MAX_ST], sfull[NSB], sempty[NSB], pfull[2], pdone[2], qfull[2], oempty, cons, drain;
   long long lo;
   Runs runs;
   int n_mine, b, h, k;                                   // the run's first page: k of (b, h)
   uint32_t tmem;
   int abort_flag, merge;
-  Chunk chunk[ST];
+  Chunk chunk[MAX_ST];
 };
-static_assert(sizeof(Ctrl) <= 1024 && SMEM <= 232448, "shared memory");
+static_assert(sizeof(Ctrl) <= 2048, "shared memory");
 
+// CL: few (request, kv head)s over short capacities: one cluster of p.cs CTAs
+// per tile, joined in distributed shared memory.
+template <int D, bool CL>
 __global__ void __launch_bounds__(NTHR, 1)
     verify_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using S = Shape<D>;
+  constexpr int ST = S::ST, KB = S::KB, STAGE = S::STAGE;
+  static_assert(S::SMEM <= 232448, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctrl *ct = reinterpret_cast<Ctrl *>(ring + ST * STAGE);
@@ -91,7 +102,16 @@ __global__ void __launch_bounds__(NTHR, 1)
     tc_fence_before();
   }
   pdl_start();
-  if (warp == 0) {
+  if (CL) {
+    if (threadIdx.x == 0) {
+      const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
+      ct->b = list / p.nkv;
+      ct->h = list % p.nkv;
+      const int np = request(p, ct->b, rank == 0 && ct->h == 0).np;
+      ct->k = rank * np / p.cs;
+      ct->n_mine = (rank + 1) * np / p.cs - ct->k;
+    }
+  } else if (warp == 0) {
     // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
@@ -147,7 +167,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         const int st = i % ST;
         if (fresh) {   // the tile after this one, if the run reaches it
           nb = b, nh = h + 1, nr = r;
-          if (n - i <= r.np - k) {
+          if (CL || n - i <= r.np - k) {
             nr.n = 0;
           } else if (nh == p.nkv) {
             nh = 0;
@@ -163,23 +183,24 @@ __global__ void __launch_bounds__(NTHR, 1)
         const bool bad = page < 0 || page >= p.num_pages;
         if (lane == 0) {
           if (bad) report(p.status, DFLASH_ERR_DEVICE);
-          if (fresh || i == 0) {
+          if (!CL && fresh) {
             cf = runs.owner(x - k);
             cl = runs.owner(x - k + r.np - 1);
           }
           Chunk c;
-          c.b = b, c.h = h, c.rt = 0, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+          c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
           c.cf = cf, c.cl = cl;
-          c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (c.cf == c.cl ? WHOLE : 0);
+          c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && c.cf == c.cl ? WHOLE : 0);
           c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = 0;
+          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = c.pad2 = 0;
           ct->chunk[st] = c;
           mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
           if (!bad) {
             uint8_t *dk = ring + st * STAGE;
             const int rowk = (page * p.nkv + h) * PAGE, rowv = (page * p.nkv + h) * D;
-            tma_load_2d_hint(dk, &tmK, &ct->full[st], 0, rowk, pol);
-            tma_load_2d_hint(dk + KB / 2, &tmK, &ct->full[st], 64, rowk, pol);
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_2d_hint(dk + half * (PAGE * 128), &tmK, &ct->full[st], half * 64, rowk, pol);
             tma_load_2d_hint(dk + KB, &tmV, &ct->full[st], 0, rowv, pol);
           }
         }
@@ -223,7 +244,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)   // 16 dims = 8 columns of Q per k-step
             umma_bf16_ts(tmem + sb * PAGE, qa + static_cast<uint32_t>(kk * 8),
-                         sdesc_k_sw128(k0 + (kk >> 2) * (KB / 2) + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+                         sdesc_k_sw128(k0 + (kk >> 2) * (PAGE * 128) + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
         }
         umma_commit(&ct->sfull[sb]);
       }
@@ -298,11 +319,11 @@ __global__ void __launch_bounds__(NTHR, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
                                                          static_cast<size_t>(row0 + (live ? tok : 0)) * p.ldq +
                                                          static_cast<size_t>(h * g + head) * D);
-      uint4 u[16];
+      uint4 u[D / 8];
 #pragma unroll
-      for (int t = 0; t < 16; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
+      for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {
+      for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t w[16];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -450,9 +471,10 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (!(ok = waitw(&ct->pdone[i & 1], static_cast<uint32_t>((i >> 1) & 1)))) break;
       tc_fence_after();
       const bool whole = c.flags & WHOLE, live = tok < c.n;
+      float *xo = reinterpret_cast<float *>(ring);   // CL: this CTA's share, in the ring, idle now
       const int rows = c.n * g;
       const size_t at = static_cast<size_t>(c.row0 + (live ? tok : 0)) * (p.nkv * g) + c.h * g + head;
-      float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * PART;
+      float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * S::PART;
       const float inv = 1.f / l;
 #pragma unroll
       for (int c0 = 0; c0 < D / 16; c0 += 4) {
@@ -467,7 +489,12 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(ov[u][e]) : 0.f;   // l 0: O was never written
           if (!live) continue;
-          if (whole) {
+          if (CL) {   // float4s XORed by the row: no bank conflicts
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              *reinterpret_cast<float4 *>(xo + row * D + ((((c0 + u) * 4 + t) ^ (row & (D / 4 - 1))) << 2)) =
+                  make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+          } else if (whole) {
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = l > 0.f ? pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
@@ -482,6 +509,10 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
       }
       tc_fence_before();
+      if (CL) {
+        if (live) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * row) = make_float2(m, l);
+        break;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct->oempty);   // the next tile may overwrite O
       if (whole) {
@@ -503,8 +534,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, PART, MROWS, rows, 0, tid,
-                      4 * 32);
+        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, MROWS, rows, tid, 4 * 32);
     }
     if (!ok) {
       report(p.status, DFLASH_ERR_TIMEOUT);
@@ -516,21 +546,88 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+  if constexpr (CL) {
+    // ---- the cluster's shares: every CTA finishes a part of the tile's columns
+    const Req r = request(p, ct->b, false);
+    const int rows = r.n * g, rank = static_cast<int>(cluster_ctarank());
+    float *xo = reinterpret_cast<float *>(ring);
+    if (n == 0 || ct->abort_flag)   // nothing to add
+      for (int i = threadIdx.x; i < MROWS; i += NTHR) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
+    __syncwarp();
+    cluster_sync();
+    const Dest dest = dest_of(p, r.row0, ct->h);
+    for (int e = rank * NTHR + threadIdx.x; e < rows * (D / 4); e += p.cs * NTHR) {
+      const int row = e / (D / 4), c = e % (D / 4);
+      const float *at = xo + row * D + ((c ^ (row & (D / 4 - 1))) << 2), *ml_at = xo + MROWS * D + 2 * row;
+      float2 ml[8];
+      float4 v[8];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = min(u, p.cs - 1);
+        ml[u] = ld_dsmem_f2(dsmem_addr(ml_at, k));
+        v[u] = ld_dsmem_f4(dsmem_addr(at, k));
+        if (u >= p.cs) ml[u] = make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, ml[u].x);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (ml[u].y == 0.f) continue;   // a share of nothing was never written
+        const float w = fast_exp2(ml[u].x - M);
+        L = fmaf(w, ml[u].y, L);
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      write_row<__nv_bfloat16, D>(dest, row, c * 4, acc, M, L);
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while its share is read
+  }
 }
 
 }  // namespace
 
-int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
+template <int D, bool CL>
+static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
+  using S = Shape<D>;
+  auto *kernel = verify_kernel<D, CL>;
   static std::atomic<uint64_t> smem_set;
-  if (int e = allow_smem(smem_set, dev, verify_kernel, SMEM)) return e;
+  if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
   if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
   p.min_chunks = 4;
-  const int most = static_cast<int>(PART_TOTAL / (2 * PART));
-  launch_pdl(verify_kernel, dim3(dev.sms < most ? dev.sms : most), dim3(NTHR), SMEM, s, tk, tv, p);
-  return cuda_check(cudaGetLastError(), "cache_attention launch");
+  const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.cs) : static_cast<unsigned>(dev.sms < most ? dev.sms : most));
+  cfg.blockDim = dim3(NTHR);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL ? p.cs : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, tk, tv, p), "cache_attention launch");
+}
+
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
+  // the same rule as for narrower tiles: clusters while one CTA per SM holds
+  // them all and a CTA gets 16 pages at most
+  const long long lists = static_cast<long long>(p.B) * p.nkv;
+  p.cs = 1;
+  while (p.cs < 8 && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  const bool cl = p.cs > 1 && kv.max_pages <= 16 * p.cs;
+  if (hs.head_dim == 64) return cl ? launch<64, true>(hs, kv, p, dev, s) : launch<64, false>(hs, kv, p, dev, s);
+  return cl ? launch<128, true>(hs, kv, p, dev, s) : launch<128, false>(hs, kv, p, dev, s);
 }
 
 }  // namespace dflash
