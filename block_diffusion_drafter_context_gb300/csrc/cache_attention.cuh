@@ -181,6 +181,8 @@ __device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, i
   auto src = [&](int i) { return partials + (static_cast<size_t>(cf + i) * 2 + (i > 0 || slot0 ? 0 : 1)) * stride; };
   if (rows * (D / 4) <= 2 * nthr)
     join_tile<__nv_bfloat16, D, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
+  else if (np > 4)
+    join_tile<__nv_bfloat16, D, 4, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else
     join_tile<__nv_bfloat16, D, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
 }

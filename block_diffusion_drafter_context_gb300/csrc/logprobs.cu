@@ -18,8 +18,8 @@
 namespace dflash {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32, CTAS = 3;   // CTAS: resident per SM
-constexpr int MAX_CLUSTER = 16;
+constexpr int THREADS = 256, WARPS = THREADS / 32, CTAS = 4;   // CTAS: resident per SM
+constexpr int MAX_CLUSTER = 8;
 constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
 // y - m in log2 units below which e^(y-m) is 0 in fp32: masked logits are kept
 // here, so that 0 * (y - m) stays 0
@@ -94,22 +94,28 @@ template <> struct Vec<__nv_bfloat16> {
   }
 };
 
-// ---- shared memory of a CTA: a ring of 64 KB of logits in stages of 32 logits
-// per thread (fewer made the meetings dominate: 101 against 88 us at 640 fp32
-// rows of 151 936), then
-constexpr int PER_STAGE = 32 * THREADS, RING = 65536, MAX_STAGES = 4;
+// ---- shared memory of a CTA: for each warp a ring of STAGES x 2 KB of logits
+// (4 vectors per lane), then.  Two stages: 4 CTAs an SM have 64 KB in flight,
+// all that HBM's latency asks for; four stages made it slower (96 against 84
+// us at 640 fp32 rows of 151 936).
+constexpr int STAGES = 2, U = 4, SV = 32 * U;
+constexpr int SEGS = 8;                              // parts of the stream whose maxima each thread keeps
+constexpr int RING = WARPS * STAGES * SV * 16;
+constexpr int MIN_SHARE = 8192;                      // logits of a CTA at least, where a row is cut
+constexpr int MAX_SHARE = 400 << 10;                 // bytes of a CTA at most, while there are CTAs for a row left
 constexpr int LIST = 512;                            // candidates a CTA can list
-constexpr int FOLD_FIRST = 24, FOLD = 96;            // the length above which the list is folded: first, then
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 struct Shared {
   alignas(16) uint64_t list[LIST];                   // candidates for the 16 largest (value, id) keys, unordered
   uint64_t best[TOP_K];      // the 16 largest in order, 0 where there are fewer
-  uint64_t full[MAX_STAGES], mail;
+  uint64_t full[WARPS][STAGES], mail;
   alignas(16) uint64_t peer_keys[MAX_CLUSTER * TOP_K];   // rank 0: every CTA's best
   float4 peer_stat[MAX_CLUSTER];                         // rank 0: (m, z, w, count) of every CTA
   float4 warp_stat[WARPS];
-  float warp_two[WARPS], warp_tau[WARPS];
-  int listed;                // candidates offered
+  float warp_two[WARPS];
+  float seg[SEGS][THREADS];  // the threads' maxima, by part
+  uint16_t owners[SEGS * THREADS];   // the (part, thread) pairs whose maximum reaches the floor
+  int listed, owned, failed;
 };
 constexpr int SMEM = RING + static_cast<int>(sizeof(Shared)) + 16;
 
@@ -174,37 +180,38 @@ __device__ __forceinline__ void pick16(const uint64_t *keys, int n, uint64_t *be
 }
 
 // One cluster per row.  The row's 16-byte-aligned vectors are cut evenly over
-// its cs CTAs; the elements before and after them (a row may start at any
-// element) go to rank 0's first warp.  A CTA streams its share through a ring
-// of bulk copies, so the bytes in flight do not depend on how far the
-// arithmetic is, and meets once per stage.
+// its cs CTAs and their warps; the elements before and after them (a row may
+// start at any element) go to rank 0's first warp.  Every warp streams its
+// share through a ring of bulk copies of its own and meets nobody until the
+// share is done.
 //   Sums: d = (x - m) c and e = 2^d per logit, two logits per instruction
 //   where the instruction set has it (subtract, scale, both sums).
 //   Rank: counted only in vectors whose maximum reaches the token's logit.
-//   Alternatives: logits at or above a floor that at least 16 logits reach
-//   (at first the smallest of the 8 warps' second largest lane maxima, which
-//   some 40 of 8192 logits reach) go to a list: a lane collects the bits of
-//   its hits, takes room for them at once and reads them back from the ring
-//   (a vote or an atomic per logit took four times as long).  The list is
-//   folded to its 16 largest once, which makes the floor the 16th of what was
-//   seen, and again only if it grows long.  A stage that overflows the list
-//   raises the floor to the 16th of what the list holds and is offered again.
+//   Alternatives: the stream keeps no list.  A thread's running maximum m is
+//   also the maximum of what it saw; 16 threads reach the 16th largest of
+//   these maxima, so the 16 largest logits reach it too, and they all lie
+//   where a thread's maximum does.  The threads keep one maximum for each
+//   eighth of the stream, so that only some 16 of the 2048 pieces are read
+//   again.  (A list kept during the stream, with
+//   votes, atomics and a meeting per stage, took 89 us where this takes 79 at
+//   640 fp32 rows of 151 936.)
 // Each CTA sends its 16 keys and sums to rank 0.
 template <typename T>
 __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
-  constexpr int N = Vec<T>::N, U = 32 / N, SV = PER_STAGE / N;   // vectors per thread, and of a stage
-  constexpr int STAGES = RING / 16 / SV;
-  static_assert(STAGES >= 2 && STAGES <= MAX_STAGES, "ring");
-  extern __shared__ uint4 ring[];
-  Shared &sh = *reinterpret_cast<Shared *>(ring + RING / 16);
+  constexpr int N = Vec<T>::N;
+  extern __shared__ uint4 ring_all[];
+  Shared &sh = *reinterpret_cast<Shared *>(ring_all + RING / 16);
   const int cs = a.cs, row = blockIdx.x / cs, rank = blockIdx.x % cs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint4 *ring = ring_all + warp * STAGES * SV;
+  uint64_t *full = sh.full[warp];
+  if (lane == 0)
+    for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(&sh.full[i], 1);
     mbar_init(&sh.mail, cs);
-    fence_mbar_init();
-    sh.listed = 0;
+    sh.listed = sh.owned = sh.failed = 0;
   }
+  if (lane == 0) fence_mbar_init();
   pdl_start();
   const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(row) * a.ld;
   const int id = a.ids[row], V = a.V;
@@ -222,83 +229,66 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
     }
     return;
   }
-  __syncthreads();                // the barriers are set up
-  if (cs > 1) cluster_arrive();   // waited for before a peer's mailbox is written
   const int head = min(V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / static_cast<int>(sizeof(T)));
   const int nv = (V - head) / N;
   const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
-  const int v0 = static_cast<int>(static_cast<long long>(rank) * nv / cs);
-  const int mine = static_cast<int>(static_cast<long long>(rank + 1) * nv / cs) - v0;   // this CTA's vectors
-  const int ns = (mine + SV - 1) / SV;
+  // This CTA's vectors, and this warp's pieces of SV of them: every WARPS-th,
+  // so that the CTA as a whole reads on (8 streams a row cost a third of the
+  // DRAM rate).
+  constexpr int STEP = WARPS * SV;
+  const int cta0 = static_cast<int>(static_cast<long long>(rank) * nv / cs);
+  const int end = static_cast<int>(static_cast<long long>(rank + 1) * nv / cs), v0 = cta0 + warp * SV;
+  const int ns = v0 < end ? (end - v0 + STEP - 1) / STEP : 0;
   auto fetch = [&](int s) {
-    const int n = min(SV, mine - s * SV);
-    mbar_arrive_expect_tx(&sh.full[s % STAGES], n * 16);
-    bulk_load(ring + (s % STAGES) * SV, xv + v0 + static_cast<size_t>(s) * SV, n * 16, &sh.full[s % STAGES]);
+    const int n = min(SV, end - v0 - s * STEP);
+    mbar_arrive_expect_tx(&full[s % STAGES], n * 16);
+    bulk_load(ring + (s % STAGES) * SV, xv + v0 + static_cast<size_t>(s) * STEP, n * 16, &full[s % STAGES]);
   };
-  if (tid == 0)
+  if (lane == 0)
     for (int s = 0; s < min(STAGES, ns); ++s) fetch(s);
   const bool known = id < V, want = a.n_top > 0;
   const float xt = known ? Elt<T>::ld(x + id) : INFINITY, xt_up = next_up(xt);
   const float c = a.inv_t * LOG2E_F;
   const uint64_t c2 = pack2(c, c);
+  __syncthreads();                // barriers and counters are set up
+  if (cs > 1) cluster_arrive();   // waited for before a peer's mailbox is written
   float m = -INFINITY;
   uint64_t z2 = pack2(0.f, 0.f), w2 = z2;
   int cnt = 0;
-  const int ends = rank == 0 ? head + (V - head - nv * N) : 0;   // < 2 N <= 16 elements outside of the vectors
-  int listed = ends;              // keys in the list before the current stage
-  if (rank == 0 && warp == 0) {
-    const int i = lane < head ? lane : head + nv * N + (lane - head);
-    if (lane < ends) {
-      const float v = Elt<T>::ld(x + i);
-      m = v;
-      z2 = pack2(v == -INFINITY ? 0.f : 1.f, 0.f);
-      cnt = v > xt || (v == xt && i < id);
-      sh.list[lane] = make_key(v, i);
-    }
-    if (lane == 0) sh.listed = ends;
-  }
-  if (want && ends) __syncthreads();
-  float floor_v = -INFINITY;   // at least 16 of the row's logits are at or above (floor_v, floor_k)
-  uint64_t floor_k = 0;
-  bool folded = false, ok = true;
-  for (int s = 0; s < ns; ++s) {
-    ok = ok && mbar_wait(&sh.full[s % STAGES], static_cast<uint32_t>((s / STAGES) & 1), nullptr, WAIT_NS);
-    const int n = ok ? min(SV, mine - s * SV) : 0;
-    const uint4 *st = ring + (s % STAGES) * SV;
+  // the stages of the CTA's longest warp, in SEGS parts
+  const int seg_len = ((end - cta0 + STEP - 1) / STEP + SEGS - 1) / SEGS;
+  float seg = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < SEGS; ++i) sh.seg[i][tid] = -INFINITY;
+  bool ok = true;
+  for (int s = 0, part = 0, left = seg_len; s < ns; ++s) {
+    ok = mbar_wait(&full[s % STAGES], static_cast<uint32_t>((s / STAGES) & 1), nullptr, WAIT_NS);
+    ok = !__any_sync(0xffffffffu, !ok);
+    if (!ok) break;
+    const int n = min(SV, end - v0 - s * STEP);
     uint4 raw[U];
-    float vmax[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       raw[u] = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
-      if (u * THREADS + tid < n) raw[u] = st[u * THREADS + tid];
+      if (u * 32 + lane < n) raw[u] = ring[(s % STAGES) * SV + u * 32 + lane];
     }
-    float mx = -INFINITY;
+    __syncwarp();
+    if (lane == 0 && s + STAGES < ns) fetch(s + STAGES);   // the stage is in registers
+    float vmax[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float v[N];
       Vec<T>::unpack(raw[u], v);
       vmax[u] = max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3]));
       if (N == 8) vmax[u] = max_nan(vmax[u], max_nan(max_nan(v[N - 4], v[N - 3]), max_nan(v[N - 2], v[N - 1])));
-      mx = max_nan(mx, vmax[u]);
+      seg = max_nan(seg, vmax[u]);
     }
-    if (want && s == 0) {
-      const float one = warp_max_nan(mx);
-      const int who = __ffs(__ballot_sync(0xffffffffu, mx == one)) - 1;   // -1: NaN
-      const float two = warp_max_nan(lane == who ? -INFINITY : mx);
-      if (lane == 0) sh.warp_two[warp] = two;
-      __syncthreads();
-      floor_v = sh.warp_two[0];
-#pragma unroll
-      for (int i = 1; i < WARPS; ++i) floor_v = fminf(floor_v, sh.warp_two[i]);
-      if (floor_v == -INFINITY) {   // a warp without two: 16 of one warp's lanes instead
-        const float tau = warp_16th_largest(mx, lane);
-        if (lane == 0) sh.warp_tau[warp] = tau;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < WARPS; ++i) floor_v = fmaxf(floor_v, sh.warp_tau[i]);
-      }
+    const float mn = max_nan(m, seg);
+    if (--left == 0 || s + 1 == ns) {
+      sh.seg[part++][tid] = seg;
+      seg = -INFINITY;
+      left = seg_len;
     }
-    const float mn = max_nan(m, mx);
     if (mn != m) {
       const float d = fmaxf((m - mn) * c, FAR), f = fast_exp2(d);
       const uint64_t f2 = pack2(f, f);
@@ -322,13 +312,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
         w2 = fma2(e2, pack2(d0, d1), w2);
       }
     }
-    const int i0 = head + (v0 + s * SV + tid) * N;
+    const int i0 = head + (v0 + s * STEP + lane) * N;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * THREADS * N;
+      const int i = i0 + u * 32 * N;
       const float reach = i + N <= id ? xt : xt_up;   // before the token equal logits count too
       const bool own = static_cast<unsigned>(id - i) < static_cast<unsigned>(N);   // the token's own vector
-      if ((vmax[u] >= reach || own) && u * THREADS + tid < n) {
+      if ((vmax[u] >= reach || own) && u * 32 + lane < n) {
         float v[N];
         Vec<T>::unpack(raw[u], v);
 #pragma unroll
@@ -338,60 +328,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
           for (int k = 0; k < N; ++k) cnt += i + k < id && v[k] == xt;
       }
     }
-    if (!want) {
-      ok = __syncthreads_and(ok);
-    } else {
-      for (;;) {
-        if (mx >= floor_v) {   // few lanes, once the floor is tight
-          uint32_t hits = 0;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float v[N];
-            Vec<T>::unpack(raw[u], v);
-#pragma unroll
-            for (int k = 0; k < N; ++k) hits |= v[k] >= floor_v ? 1u << (u * N + k) : 0u;
-            if (u * THREADS + tid >= n) hits &= (1u << (u * N)) - 1;
-          }
-          auto key_of = [&](int e) {
-            const int u = e / N, k = e % N;
-            return make_key(Elt<T>::ld(reinterpret_cast<const T *>(st + u * THREADS + tid) + k), i0 + u * THREADS * N + k);
-          };
-          for (uint32_t left = floor_k ? hits : 0u; left; left &= left - 1) {   // equal values of higher ids: out
-            const int e = __ffs(left) - 1;
-            if (key_of(e) < floor_k) hits &= ~(1u << e);
-          }
-          for (int to = hits ? atomicAdd(&sh.listed, __popc(hits)) : 0; hits; hits &= hits - 1, ++to)
-            if (to < LIST) sh.list[to] = key_of(__ffs(hits) - 1);
-        }
-        ok = __syncthreads_and(ok);
-        const int total = sh.listed;
-        __syncthreads();   // read by all before it changes
-        if (total <= LIST && (s + 1 == ns || total <= (folded ? FOLD : FOLD_FIRST))) {
-          listed = total;
-          break;
-        }
-        pick16(sh.list, min(total, LIST), sh.best);
-        __syncthreads();
-        folded = true;
-        floor_k = max(floor_k, sh.best[TOP_K - 1]);
-        floor_v = floor_k ? key_value(floor_k) : -INFINITY;
-        if (total <= LIST) {
-          if (tid < TOP_K) sh.list[tid] = sh.best[tid];
-          listed = min(total, TOP_K);
-        }                      // else this stage again, above the new floor
-        if (tid == 0) sh.listed = listed;
-        __syncthreads();
-        if (total <= LIST) break;
-      }
-    }
-    if (tid == 0 && ok && s + STAGES < ns) fetch(s + STAGES);
   }
-  if (!ok) {   // a copy did not arrive: no answer
-    m = NAN;
-    if (tid == 0)   // let every issued copy land before the shared memory goes away
-      for (int s = 0; s < ns; ++s) mbar_wait(&sh.full[s % STAGES], static_cast<uint32_t>((s / STAGES) & 1), nullptr, WAIT_NS / 64);
+  if (!ok) {   // a copy did not arrive: no answer; the others land before the shared memory goes away
+    sh.failed = 1;
+    for (int s = 0; s < min(STAGES, ns); ++s)
+      mbar_wait(&full[s], static_cast<uint32_t>(((ns - 1 - s) / STAGES) & 1), nullptr, WAIT_NS / 8);
   }
-  // ---- the CTA's sums and its 16 keys
+  const float seen = m;   // the maximum of this thread's vectors
   Stat st;
   {
     float z0, z1, w0, w1;
@@ -399,20 +342,114 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
     unpack2(w2, w0, w1);
     st = {m, z0 + z1, w0 + w1};
   }
-  warp_join(st, cnt, c);
-  if (lane == 0) {
-    sh.warp_stat[warp] = make_float4(st.m, st.z, st.w, __int_as_float(cnt));
+  if (rank == 0 && warp == 0) {   // the elements outside of the vectors: < 2 N <= 16
+    const int ends = head + (V - head - nv * N), i = lane < head ? lane : nv * N + lane;
+    if (lane < ends) {
+      const float v = Elt<T>::ld(x + i);
+      if (v != -INFINITY) {
+        rebase(st, max_nan(st.m, v), c);
+        const float d = fmaxf((v - st.m) * c, FAR), e = fast_exp2(d);
+        st.z += e;
+        st.w = fmaf(e, d, st.w);
+      }
+      cnt += v > xt || (v == xt && i < id);
+      sh.list[lane] = make_key(v, i);
+    }
+    if (lane == 0) sh.listed = ends;
   }
-  __syncthreads();
-  if (want) pick16(sh.list, listed, sh.best);
+  // ---- the CTA's sums
+  warp_join(st, cnt, c);
+  if (lane == 0) sh.warp_stat[warp] = make_float4(st.m, st.z, st.w, __int_as_float(cnt));
+  if (want) {
+    // ---- a floor under the 16th largest of the threads' maxima: some 40
+    // threads reach the smallest of the 8 warps' second largest
+    const float one = warp_max_nan(seen);
+    const int who = __ffs(__ballot_sync(0xffffffffu, seen == one)) - 1;   // -1: NaN
+    const float two = warp_max_nan(lane == who ? -INFINITY : seen);
+    if (lane == 0) sh.warp_two[warp] = two;
+    __syncthreads();
+    const int listed = sh.listed;
+    float floor_v = sh.warp_two[0];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) floor_v = fminf(floor_v, sh.warp_two[i]);
+    // (their (maximum, thread) keys pass through the list behind the ends' keys)
+    uint64_t *maxima = sh.list + TOP_K;
+    if (seen >= floor_v) maxima[atomicAdd(&sh.owned, 1)] = make_key(seen, tid);
+    __syncthreads();
+    pick16(maxima, sh.owned, sh.best);
+    __syncthreads();
+    uint64_t floor_k = sh.best[TOP_K - 1];
+    floor_v = floor_k ? key_value(floor_k) : -INFINITY;   // fewer than 16 threads hold anything comparable
+    floor_k = 0;
+    if (tid == 0) sh.owned = 0;
+    __syncthreads();
+    if (seen >= floor_v)
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i)
+        if (sh.seg[i][tid] >= floor_v) sh.owners[atomicAdd(&sh.owned, 1)] = static_cast<uint16_t>(i * THREADS + tid);
+    __syncthreads();
+    const int owned = sh.owned;
+    // ---- their vectors again: keys at or above the floor into the list; an
+    // overflow raises the floor to the 16th of what the list holds
+    for (;;) {
+      // item = (a piece's vector number, piece)
+      const int items = owned * seg_len * U;
+      constexpr int B = 4;   // loads in flight per thread
+      for (int e0 = tid; e0 < items; e0 += THREADS * B) {
+        uint4 raw[B];
+        int at[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          const int e = e0 + u * THREADS;
+          at[u] = -1;
+          if (e < items) {
+            const int k = e / owned, o = sh.owners[e - k * owned], t = o % THREADS;
+            const int i = cta0 + ((o / THREADS) * seg_len + k / U) * STEP + (t >> 5) * SV + (k % U) * 32 + (t & 31);
+            if (i < end) {
+              at[u] = i;
+              raw[u] = __ldg(xv + i);
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+          if (at[u] < 0) continue;
+          float v[N];
+          Vec<T>::unpack(raw[u], v);
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+            if (v[k] >= floor_v) {
+              const uint64_t key = make_key(v[k], head + at[u] * N + k);
+              if (key >= floor_k) {
+                const int to = atomicAdd(&sh.listed, 1);
+                if (to < LIST) sh.list[to] = key;
+              }
+            }
+        }
+      }
+      __syncthreads();
+      const int total = sh.listed;
+      pick16(sh.list, min(total, LIST), sh.best);
+      __syncthreads();
+      if (total <= LIST) break;
+      floor_k = sh.best[TOP_K - 1];
+      floor_v = key_value(floor_k);
+      if (tid == 0) sh.listed = listed;
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
   auto gather = [&](const float4 *of, int k) {   // a warp: the first k shares joined
     const float4 q = lane < k ? of[lane] : make_float4(-INFINITY, 0.f, 0.f, __int_as_float(0));
     st = {q.x, q.y, q.z};
     cnt = __float_as_int(q.w);
     warp_join(st, cnt, c);
   };
-  if (warp == 0) gather(sh.warp_stat, WARPS);
-  __syncthreads();   // best is complete
+  if (warp == 0) {
+    gather(sh.warp_stat, WARPS);
+    if (sh.failed) st.m = NAN;
+  }
   // ---- the cluster: every CTA's share into rank 0's mailbox
   if (cs > 1) {
     cluster_wait();
@@ -492,18 +529,17 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   a.rank = rank;
   a.top_ids = top_ids;
   a.top_lp = top_logprobs;
-  // Rows enough for half of the resident CTAs take one CTA each; fewer are cut
-  // over clusters until that many CTAs work, each with a stage at least (64
-  // fp32 rows of 151 936: 42 us on one CTA, 25 on 4, 32 on 16; 640 rows: 101
-  // on one, 129 on 4).
+  // One CTA per row where the rows fill a quarter of the resident CTAs, more
+  // where they do not (64 fp32 rows of 151 936: 27 us on one CTA each, 21 on 4,
+  // 30 on 16) and where a CTA's share is long against the tail of a wave of
+  // them (640 such rows: 82 us on one, 79 on 2, 88 on 4).
   int cs = 1;
-  while (cs < MAX_CLUSTER && 2LL * rows * cs < CTAS * dev.sms && static_cast<long long>(cs) * PER_STAGE < vocab) cs *= 2;
+  while (cs < MAX_CLUSTER && ((4LL * rows * cs < CTAS * dev.sms && static_cast<long long>(cs) * MIN_SHARE < vocab) ||
+                              static_cast<long long>(vocab) * size > static_cast<long long>(cs) * MAX_SHARE))
+    cs *= 2;
   auto *kernel = dtype == DFLASH_F32 ? logprobs_kernel<float> : logprobs_kernel<__nv_bfloat16>;
-  static std::atomic<uint64_t> smem_set[2], wide_set[2];
-  const int which = dtype == DFLASH_F32;
-  if (int e = allow_smem(smem_set[which], dev, kernel, SMEM)) return e;
-  if (cs > 8)
-    if (int e = allow_wide_clusters(wide_set[which], dev, kernel)) return e;
+  static std::atomic<uint64_t> smem_set[2];
+  if (int e = allow_smem(smem_set[dtype == DFLASH_F32], dev, kernel, SMEM)) return e;
   cudaLaunchConfig_t cfg = {};
   a.cs = cs;
   cfg.gridDim = dim3(static_cast<unsigned>(cs) * rows);
