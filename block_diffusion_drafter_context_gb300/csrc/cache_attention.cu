@@ -18,45 +18,78 @@
 namespace dflash {
 namespace {
 
-// ------------------------------------------------------------------ bf16, up to 16 query rows per (request, kv head): warp MMAs
-// One 16-row tile on mma.sync: with so few rows the tensor work is a fraction
-// of the HBM time whichever way it is issued, and register accumulators keep a
-// page's path short.  (Two tiles of 16 rows per warp, tried for 17..32 rows,
-// left one CTA per SM at 255 registers: 149 us against 103 of the tcgen05 form
-// for 5 tokens x 4 heads at 128k.)  Warp 0
-// produces: K page as 128-byte-swizzled 64-column halves, V^T page, and for a
-// new tile its query rows, into a ring of NST stages.  Warps 1-4 each take 16
-// tokens of every page with a maximum, sum and O of their own (no exchange
-// per page) and meet when the tile ends, in the last page's stage.
+// ------------------------------------------------------------------ tiles of 16 query rows: warp MMAs
+// bf16 calls with up to 16 rows per (request, kv head), and every fp32 call in
+// tiles of 16.  One tile on mma.sync: with so few rows the tensor work is a
+// fraction of the HBM time whichever way it is issued, and register
+// accumulators keep a page's path short.  (Two tiles of 16 rows per warp,
+// tried for 17..32 bf16 rows, left one CTA per SM at 255 registers: 149 us
+// against 103 of the tcgen05 form for 5 tokens x 4 heads at 128k.)
+//
+// Warp 0 produces: the K page as 128-byte-wide swizzled column blocks, the V^T
+// page (fp32: as two blocks of 32 slots), and for a new tile its query rows,
+// into a ring of NST stages.  Warps 1-4 each take 16 tokens of every page with
+// a maximum, sum and O of their own (no exchange per page) and meet when the
+// tile ends, in the last page's stage.
+//
+// fp32 operands go through the tensor cores as sums of two tf32 parts, x = hi
+// + lo with hi rounded to 11 bits and lo the exact rest: hi hi + hi lo + lo hi
+// leaves out lo lo (2^-24 of a product) and the bits of lo past 11 (2^-23), so
+// a product is good to about fp32's own rounding.  On CUDA cores the same
+// products took three times as long: a value from shared memory served 4 rows.
 constexpr int ROWS = 16;
-template <int D>
+template <typename T, int D>
 struct Shape {
-  static constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;
-  static constexpr int QP = D * 2 + 16, QB = ROWS * QP;                    // query rows at a padded pitch
-  static constexpr int NST = D == 64 ? 6 : 3;
-  static constexpr int CTAS = 2;                                           // per SM
+  static constexpr int SIZE = sizeof(T);
+  static constexpr int KB = PAGE * D * SIZE, STAGE = 2 * KB;
+  static constexpr int QP = D * SIZE + 16, QB = ROWS * QP;                 // query rows at a padded pitch
+  static constexpr int NST = D * SIZE == 128 ? 6 : 3;
+  static constexpr int CTAS = D * SIZE == 512 ? 1 : 2;                     // per SM
   static constexpr int SMEM = 1024 + NST * (STAGE + QB) + 1024;
   static constexpr int PART = ROWS * (D + 2);                              // floats of a partial
 };
+
+// x = hi + lo, hi of 11 significant bits (to nearest); the product reads 11 of lo
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += A B from split operands, small terms first
+__device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t b0,
+                                          uint32_t b1) {
+  uint32_t h0, l0, h1, l1;
+  split_tf32(b0, h0, l0);
+  split_tf32(b1, h1, l1);
+  mma_tf32(d, al, h0, h1);
+  mma_tf32(d, ah, l0, l1);
+  mma_tf32(d, ah, h0, h1);
+}
 
 struct __align__(16) Ctrl {
   uint64_t full[6], empty[6], cons;
   long long lo;
   Runs runs;
-  int n_mine, b, h, k;                     // the run's first page: k of (b, h)
+  int n_mine, b, h, rt, k;                 // the run's first page: k of tile (b, h, rt)
   int abort_flag, merge;
   Chunk chunk[6];
 };
 
-// CL: few (request, kv head)s over short capacities.  One cluster of
+// CL: few tiles over short capacities.  One cluster of
 // p.cs CTAs per tile shares its pages out evenly, with no list to scan, and
 // the shares meet in distributed shared memory: on a request of 2 048 tokens
 // the partials' way through L2 and its counter took 5 of 15 us.
-template <int D, bool CL>
-__global__ void __launch_bounds__(160, Shape<D>::CTAS)
+template <typename T, int D, bool CL>
+__global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
-  using S = Shape<D>;
-  constexpr int NST = S::NST, KB = S::KB, NT = D / 8, KS = D / 16;
+  using S = Shape<T, D>;
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int NST = S::NST, KB = S::KB, NT = D / 8, KS = D * S::SIZE / 32;   // k-steps of 32 bytes
   static_assert(sizeof(Ctrl) <= 1024 && S::SMEM <= 232448 / S::CTAS, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -73,13 +106,16 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
     fence_mbar_init();
   }
   volatile int *abort_flag = &ct->abort_flag;
+  auto tiles_of = [&](const Req &r) { return F32 ? (r.n * p.g + ROWS - 1) / ROWS : r.n > 0; };
   pdl_start();
   if (CL) {
     if (threadIdx.x == 0) {
-      const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
-      ct->b = list / p.nkv;
-      ct->h = list % p.nkv;
-      const int np = request(p, ct->b, rank == 0 && ct->h == 0).np;
+      const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs, head = list / p.tiles;
+      ct->b = head / p.nkv;
+      ct->h = head % p.nkv;
+      ct->rt = list % p.tiles;
+      const Req r = request(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
+      const int np = ct->rt < tiles_of(r) ? r.np : 0;
       ct->k = rank * np / p.cs;
       ct->n_mine = (rank + 1) * np / p.cs - ct->k;
     }
@@ -88,7 +124,10 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += request(p, b, blockIdx.x == 0).np;
+    for (int b = b0; b < b1; ++b) {
+      const Req r = request(p, b, blockIdx.x == 0);
+      sum += static_cast<long long>(r.np) * tiles_of(r);
+    }
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -109,12 +148,14 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
       for (int b = b0; b < b1; ++b) {
-        const long long np = request(p, b, false).np, span = np * p.nkv;
+        const Req r = request(p, b, false);
+        const long long np = r.np, head = np * tiles_of(r), span = head * p.nkv;
         if (lo < pre + span) {
-          const long long h = quotient(lo - pre, np);
+          const long long h = quotient(lo - pre, head), rt = quotient(lo - pre - h * head, np);
           ct->b = b;
           ct->h = static_cast<int>(h);
-          ct->k = static_cast<int>(lo - pre - h * np);
+          ct->rt = static_cast<int>(rt);
+          ct->k = static_cast<int>(lo - pre - h * head - rt * np);
           break;
         }
         pre += span;
@@ -126,11 +167,11 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
   if (warp == 0) {
     // ------------------------------------------------------------ producer (the whole warp walks)
     if (!CL && n == 0) return;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q);
+    const T *q = static_cast<const T *>(p.q);
     const uint64_t pol = policy_evict_first();
     const Runs runs = ct->runs;
     int cf = 0, cl = 0;
-    int b = ct->b, h = ct->h, k = ct->k;
+    int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
     long long x = ct->lo;
     Req r = request(p, b, false);
     int issued = 0;
@@ -143,7 +184,7 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
       const bool first = i == 0 || (!CL && k == 0), last = i == n - 1 || (!CL && k == r.np - 1);
       const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
       const bool bad = page < 0 || page >= p.num_pages;
-      const int live = first ? r.n * p.g : 0;   // query rows to load
+      const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
       if (lane == 0) {
         if (bad) report(p.status, DFLASH_ERR_DEVICE);
         if (!CL && first) {
@@ -151,34 +192,41 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
           cl = runs.owner(x - k + r.np - 1);
         }
         Chunk c;
-        c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+        c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
         c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-        c.nrow0 = c.nn = c.nh = c.pad = c.pad2 = 0;
+        c.nrow0 = c.nn = c.nh = c.pad = 0;
         ct->chunk[st] = c;
-        mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * 2);
+        mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * S::SIZE);
       }
       __syncwarp();
       if (lane < live) {
+        const int row = rt * ROWS + lane;
         bulk_load(sQ + st * S::QB + lane * S::QP,
-                  q + static_cast<size_t>(r.row0 + lane / p.g) * p.ldq + static_cast<size_t>(h * p.g + lane % p.g) * D, D * 2,
-                  &ct->full[st]);
+                  q + static_cast<size_t>(r.row0 + row / p.g) * p.ldq + static_cast<size_t>(h * p.g + row % p.g) * D,
+                  D * S::SIZE, &ct->full[st]);
       }
       if (lane == 0 && !bad) {
         uint8_t *dk = base + st * S::STAGE;
         const int rowk = (page * p.nkv + h) * PAGE, rowv = (page * p.nkv + h) * D;
+        constexpr int W = 128 / S::SIZE;   // elements of a block's width
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half)
-          tma_load_2d_hint(dk + half * (PAGE * 128), &tmK, &ct->full[st], half * 64, rowk, pol);
-        tma_load_2d_hint(dk + KB, &tmV, &ct->full[st], 0, rowv, pol);
+        for (int i = 0; i < D / W; ++i)
+          tma_load_2d_hint(dk + i * (PAGE * 128), &tmK, &ct->full[st], i * W, rowk, pol);
+#pragma unroll
+        for (int i = 0; i < PAGE / W; ++i)
+          tma_load_2d_hint(dk + KB + i * (D * 128), &tmV, &ct->full[st], i * W, rowv, pol);
       }
       issued = i + 1;
       if (++k == r.np && !CL) {
         k = 0;
-        if (++h == p.nkv && i + 1 < n) {
-          h = 0;
-          do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
-          while (r.np == 0 && b + 1 < p.B);
+        if (++rt == tiles_of(r)) {
+          rt = 0;
+          if (++h == p.nkv && i + 1 < n) {
+            h = 0;
+            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+            while (r.np == 0 && b + 1 < p.B);
+          }
         }
       }
     }
@@ -216,6 +264,22 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
   uint32_t qf[KS][4];
   float o[NT][4], m[2], l[2];                 // rows lane / 4 and lane / 4 + 8
   int top[2];                                 // the last position a row sees
+  // Also at the end of a tile, where nothing of it is live any more: the join
+  // is a call, and would otherwise save all of this around it.
+  auto clear = [&]() {
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qf[kk][e] = 0u;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    top[0] = top[1] = 0;
+  };
+  clear();
   bool ok = true;
   const int n_use = CL && warp == 0 ? 0 : n;   // CL: the producer waits for the cluster at the end
   for (int i = 0; i < n_use && ok; ++i) {
@@ -232,18 +296,12 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
       for (int e = 0; e < 2; ++e) {
         // rows past the tile's are zeros, whatever the slot held: they have
         // a say in when the warp moves its maxima
-        const int row = e * 8 + (lane >> 2);
+        const int row = c.rt * ROWS + e * 8 + (lane >> 2);
         if (row >= c.n * p.g)
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) qf[kk][e] = qf[kk][2 + e] = 0u;
-        m[e] = -INFINITY;
-        l[e] = 0.f;
         top[e] = c.ctx + min(c.n - 1, row / p.g);
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] = 0.f;
     }
     const int t0 = c.page * PAGE + cw * 16;   // this warp's 16 positions
     const int newest = c.ctx + c.n - 1, oldest = p.window > 0 ? c.ctx - p.window + 1 : 0;
@@ -253,11 +311,19 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
       const uint32_t ka = smem_u32(stage) + ktok * 128;
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
-        uint32_t b0, b1, b2, b3;
+        uint32_t b0, b1, b2, b3;   // 8 tokens x 16 bytes each: tokens 0-7, then 8-15
         const int ch = (kk & 3) * 2 + ((lane >> 3) & 1);
         ldmatrix_x4(ka + (kk >> 2) * (PAGE * 128) + ((ch ^ (ktok & 7)) << 4), b0, b1, b2, b3);
-        mma_bf16_16816(s[0], qf[kk], b0, b1);
-        mma_bf16_16816(s[1], qf[kk], b2, b3);
+        if constexpr (F32) {
+          uint32_t qh[4], ql[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_tf32(qf[kk][e], qh[e], ql[e]);
+          mma_split(s[0], qh, ql, b0, b1);
+          mma_split(s[1], qh, ql, b2, b3);
+        } else {
+          mma_bf16_16816(s[0], qf[kk], b0, b1);
+          mma_bf16_16816(s[1], qf[kk], b2, b3);
+        }
       }
       // positions a row does not see (whatever their slots hold)
       const bool edge = t0 + 15 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
@@ -292,36 +358,64 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[t][e] *= f[e >> 1];
       }
-      // P rounded to bf16, the type its product with V takes; the sum keeps fp32
-      uint32_t pa[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float nm = m[e] == -INFINITY ? 0.f : -m[e];
-        const float p0 = fast_exp2(fmaf(s[0][2 * e], p.scale_log2, nm));
-        const float p1 = fast_exp2(fmaf(s[0][2 * e + 1], p.scale_log2, nm));
-        const float p2 = fast_exp2(fmaf(s[1][2 * e], p.scale_log2, nm));
-        const float p3 = fast_exp2(fmaf(s[1][2 * e + 1], p.scale_log2, nm));
-        l[e] += (p0 + p1) + (p2 + p3);
-        pa[e] = pack_bf16(p0, p1);
-        pa[2 + e] = pack_bf16(p2, p3);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) s[t][2 * e + u] = fast_exp2(fmaf(s[t][2 * e + u], p.scale_log2, nm));
+        l[e] += (s[0][2 * e] + s[0][2 * e + 1]) + (s[1][2 * e] + s[1][2 * e + 1]);
       }
       // slots past the newest token may hold anything: their V becomes 0
       const bool stale = t0 + 15 > newest;
-      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-      if (stale) {
-        const int pos = t0 + (lane & 3) * 2;
-        keep0 = pos + 1 <= newest ? 0xffffffffu : pos <= newest ? 0xffffu : 0u;
-        keep1 = pos + 9 <= newest ? 0xffffffffu : pos + 8 <= newest ? 0xffffu : 0u;
-      }
+      const int mine = t0 + (lane & 3) * 2;   // this lane's tokens: mine, mine + 1, mine + 8, mine + 9
       const uint32_t va = smem_u32(stage + KB);
-      const int dr = (lane >> 4) * 8 + (lane & 7), vch = cw * 2 + ((lane >> 3) & 1);
+      if constexpr (F32) {
+        // the accumulators of 8 tokens are an A operand whose k index t stands
+        // for token 2t and t + 4 for 2t + 1; V's lanes read the same pairs
+        uint32_t ph[2][4], pl[2][4];
 #pragma unroll
-      for (int t = 0; t < NT; t += 2) {
-        uint32_t b0, b1, b2, b3;
-        ldmatrix_x4(va + (t * 8 + dr) * 128 + ((vch ^ (dr & 7)) << 4), b0, b1, b2, b3);
-        if (stale) b0 &= keep0, b1 &= keep1, b2 &= keep0, b3 &= keep1;
-        mma_bf16_16816(o[t], pa, b0, b1);
-        mma_bf16_16816(o[t + 1], pa, b2, b3);
+        for (int t = 0; t < 2; ++t) {
+          split_tf32(__float_as_uint(s[t][0]), ph[t][0], pl[t][0]);
+          split_tf32(__float_as_uint(s[t][2]), ph[t][1], pl[t][1]);
+          split_tf32(__float_as_uint(s[t][1]), ph[t][2], pl[t][2]);
+          split_tf32(__float_as_uint(s[t][3]), ph[t][3], pl[t][3]);
+        }
+        const uint32_t vb = va + (cw >> 1) * (D * 128) + (lane >> 2) * 128 + (lane & 1) * 8;
+        const int ch = (cw & 1) * 4 + ((lane & 3) >> 1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // 8 tokens per step
+            uint32_t b0, b1;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(b0), "=r"(b1)
+                         : "r"(vb + t * 1024 + (((ch + 2 * u) ^ (lane >> 2)) << 4)));
+            if (stale) {
+              if (mine + 8 * u > newest) b0 = 0u;
+              if (mine + 8 * u + 1 > newest) b1 = 0u;
+            }
+            mma_split(o[t], ph[u], pl[u], b0, b1);
+          }
+      } else {
+        // P rounded to bf16, the type its product with V takes; the sum keeps fp32
+        const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                                pack_bf16(s[1][2], s[1][3])};
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        if (stale) {
+          keep0 = mine + 1 <= newest ? 0xffffffffu : mine <= newest ? 0xffffu : 0u;
+          keep1 = mine + 9 <= newest ? 0xffffffffu : mine + 8 <= newest ? 0xffffu : 0u;
+        }
+        const int dr = (lane >> 4) * 8 + (lane & 7), vch = cw * 2 + ((lane >> 3) & 1);
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+          uint32_t b0, b1, b2, b3;
+          ldmatrix_x4(va + (t * 8 + dr) * 128 + ((vch ^ (dr & 7)) << 4), b0, b1, b2, b3);
+          if (stale) b0 &= keep0, b1 &= keep1, b2 &= keep0, b3 &= keep1;
+          mma_bf16_16816(o[t], pa, b0, b1);
+          mma_bf16_16816(o[t + 1], pa, b2, b3);
+        }
       }
     }
     if (!(c.flags & LAST)) {
@@ -334,10 +428,10 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
     // columns XORed by the row (no bank conflicts)
     const bool whole = c.flags & WHOLE;
     float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * S::PART;
-    const int rows = c.n * p.g;
+    const int rows = min(ROWS, c.n * p.g - c.rt * ROWS);
     float *so = reinterpret_cast<float *>(stage);
     float *sm = reinterpret_cast<float *>(sQ + st * S::QB);   // [4][16] maxima, then sums (the Q slot is consumed)
-    static_assert(S::QB >= 4 * 16 * 2 * 4 && S::STAGE == 4 * 16 * D * 4, "join scratch");
+    static_assert(S::QB >= 4 * 16 * 2 * 4 && S::STAGE >= 4 * 16 * D * 4, "join scratch");
     if (!(ok = csync())) break;   // every warp has read the stage
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -377,7 +471,7 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
         *reinterpret_cast<float4 *>(xo + row * D + c4) = acc;
         if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * row) = make_float2(M, L);
       } else if (whole) {
-        write_row<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), row, c4, acc, M, L);
+        write_row<T, D>(dest_of(p, c.row0, c.h, c.rt * ROWS), row, c4, acc, M, L);
       } else {
         __stcg(reinterpret_cast<float4 *>(part + row * D + c4), acc);
         if (c4 == 0) {
@@ -391,7 +485,7 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
       __threadfence();
       if (!(ok = csync())) break;
       if (ctid == 0) {
-        int *ctr = p.counters + static_cast<size_t>(c.b) * p.nkv + c.h;
+        int *ctr = p.counters + (static_cast<size_t>(c.b) * p.nkv + c.h) * p.tiles + c.rt;
         const int old = atomicAdd(ctr, 1), done = old == c.cl - c.cf;
         if (done) atomicExch(ctr, 0);
         __threadfence();
@@ -399,14 +493,15 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS, rows, ctid,
-                      128);
+        join_parts<T, D>(dest_of(p, c.row0, c.h, c.rt * ROWS), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS,
+                         rows, ctid, 128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
     }
     fence_proxy_async_smem();   // the stage was written by plain stores: before the next bulk copy into it
     __syncwarp();
     if (lane == 0) mbar_arrive(&ct->empty[st]);
+    clear();
   }
   if (!ok) {
     report(p.status, DFLASH_ERR_TIMEOUT);
@@ -415,8 +510,8 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
     const Req r = request(p, ct->b, false);
-    const int rows = r.n * p.g, rank = static_cast<int>(cluster_ctarank());
-    float *xo = share(share_stage(r.np, rank));
+    const int rows = min(ROWS, r.n * p.g - ct->rt * ROWS), rank = static_cast<int>(cluster_ctarank());
+    float *xo = share(share_stage(rows > 0 ? r.np : 0, rank));
     if (n == 0 || !ok)   // nothing to add
       for (int i = ctid; i >= 0 && i < ROWS; i += 128) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
     __syncwarp();
@@ -457,230 +552,37 @@ __global__ void __launch_bounds__(160, Shape<D>::CTAS)
           acc.w = fmaf(w, v[u].w, acc.w);
         }
       }
-      write_row<__nv_bfloat16, D>(dest_of(p, r.row0, ct->h), row, c4, acc, M, L);
+      write_row<T, D>(dest_of(p, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while its share is read
   }
 }
 
-// ------------------------------------------------------------------ fp32
-// CUDA cores (tensor-core formats would round the inputs).  One CTA takes a
-// share of the pages of a tile of 8 query rows of one (request, kv head):
-// thread t scores token t % 64 for rows 4 (t / 64) .., then sums column t
-// (of D) of P V for all 8 rows, so a K or V value read from shared memory
-// serves 4 or 8 rows.  Shares are joined by the last CTA to arrive.
-constexpr int F_ROWS = 8, F_THREADS = 128;
-
-template <int D>
-__global__ void __launch_bounds__(F_THREADS) decode_f32_kernel(const Params p) {
-  constexpr int KP = D + 4, VP = PAGE + 4, NC = D == 128 ? 1 : 2;   // NC threads share a column at D = 64
-  extern __shared__ float4 smem4[];
-  float *sk = reinterpret_cast<float *>(smem4);      // [2][64][KP]
-  float *sv = sk + 2 * PAGE * KP;                    // [2][D][VP]
-  float *sq = sv + 2 * D * VP;                       // [8][D]
-  float *sp = sq + F_ROWS * D;                       // [8][64] scores, then probabilities
-  float *st = sp + F_ROWS * PAGE;                    // [3][8] maximum, sum, factor
-  __shared__ int last;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_start();
-  const int rt = blockIdx.x % p.tiles, h = blockIdx.x / p.tiles % p.nkv, b = blockIdx.x / (p.tiles * p.nkv);
-  const Req r = request(p, b, blockIdx.y == 0 && rt == 0 && h == 0 && tid == 0);
-  const int rows = min(F_ROWS, r.n * p.g - rt * F_ROWS);
-  if (rows <= 0) return;
-  const int k0 = static_cast<int>(static_cast<long long>(blockIdx.y) * r.np / gridDim.y);
-  const int k1 = static_cast<int>(static_cast<long long>(blockIdx.y + 1) * r.np / gridDim.y);
-  const float *kc = static_cast<const float *>(p.k), *vc = static_cast<const float *>(p.v);
-  const float *q = static_cast<const float *>(p.q);
-  auto page_of = [&](int k) {
-    const int pg = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
-    return pg >= 0 && pg < p.num_pages ? pg : -1;
-  };
-  auto load = [&](int k, int buf) {   // 16-byte asynchronous copies, rows at a padded pitch
-    const int pg = page_of(k);
-    if (pg >= 0) {
-      const float *gk = kc + (static_cast<size_t>(pg) * p.nkv + h) * PAGE * D;
-      const float *gv = vc + (static_cast<size_t>(pg) * p.nkv + h) * PAGE * D;
-      for (int e = tid; e < PAGE * D / 4; e += F_THREADS) {
-        const uint32_t dk = smem_u32(sk + buf * PAGE * KP + (e / (D / 4)) * KP + (e % (D / 4)) * 4);
-        const uint32_t dv = smem_u32(sv + buf * D * VP + (e / (PAGE / 4)) * VP + (e % (PAGE / 4)) * 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dk), "l"(gk + 4 * e) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dv), "l"(gv + 4 * e) : "memory");
-      }
-    } else if (tid == 0) {
-      report(p.status, DFLASH_ERR_DEVICE);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  if (k0 < k1) load(k0, 0);
-  for (int e = tid; e < F_ROWS * D; e += F_THREADS) {
-    const int row = rt * F_ROWS + e / D;
-    sq[e] = e / D < rows ? q[static_cast<size_t>(r.row0 + row / p.g) * p.ldq +
-                             static_cast<size_t>(h * p.g + row % p.g) * D + e % D]
-                         : 0.f;
-  }
-  if (tid < F_ROWS) {
-    st[tid] = -INFINITY;
-    st[8 + tid] = 0.f;
-  }
-  float acc[F_ROWS];
-#pragma unroll
-  for (int i = 0; i < F_ROWS; ++i) acc[i] = 0.f;
-  const int tok = tid % PAGE, rg = (tid / PAGE) * 4;       // scores: token, rows rg .. rg + 3
-  const int col = tid % D, part_t = NC == 2 ? (tid / D) * (PAGE / 2) : 0;
-  const int newest = r.ctx + r.n - 1;
-  for (int k = k0; k < k1; ++k) {
-    const int buf = (k - k0) & 1;
-    if (k + 1 < k1) {
-      load(k + 1, buf ^ 1);
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-    } else {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-    }
-    __syncthreads();
-    const bool have = page_of(k) >= 0;
-    const float *kr = sk + buf * PAGE * KP + tok * KP;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (have) {
-#pragma unroll 8
-      for (int c = 0; c < D; c += 4) {
-        const float4 kv = *reinterpret_cast<const float4 *>(kr + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 qv = *reinterpret_cast<const float4 *>(sq + (rg + i) * D + c);
-          s[i] = fmaf(kv.x, qv.x, s[i]);
-          s[i] = fmaf(kv.y, qv.y, s[i]);
-          s[i] = fmaf(kv.z, qv.z, s[i]);
-          s[i] = fmaf(kv.w, qv.w, s[i]);
-        }
-      }
-    }
-    const int pos = (r.p0 + k) * PAGE + tok;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int hi = r.ctx + min(r.n - 1, (rt * F_ROWS + rg + i) / p.g);
-      const bool see = have && pos <= hi && (p.window <= 0 || pos > hi - p.window);
-      sp[(rg + i) * PAGE + tok] = see ? s[i] * p.scale_log2 : -INFINITY;
-    }
-    __syncthreads();
-    // running maximum and sum: warp w serves rows 2 w, 2 w + 1
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = warp * 2 + i;
-      const float a = sp[row * PAGE + lane], c = sp[row * PAGE + 32 + lane];
-      const float mo = st[row], mn = fmaxf(mo, warp_max(fmaxf(a, c)));
-      const float nm = mn == -INFINITY ? 0.f : -mn;
-      const float pa = exp2f(a + nm), pc = exp2f(c + nm), f = mn == -INFINITY ? 1.f : exp2f(mo - mn);
-      const float sum = warp_sum(pa + pc);
-      sp[row * PAGE + lane] = pa;
-      sp[row * PAGE + 32 + lane] = pc;
-      __syncwarp();
-      if (lane == 0) {
-        st[row] = mn;
-        st[8 + row] = st[8 + row] * f + sum;
-        st[16 + row] = f;
-      }
-    }
-    __syncthreads();
-    if (have) {
-      const float *vr = sv + buf * D * VP + col * VP + part_t;
-      const int left = newest - (r.p0 + k) * PAGE - part_t;   // slots past the newest token may hold anything
-#pragma unroll
-      for (int i = 0; i < F_ROWS; ++i) acc[i] *= st[16 + i];
-#pragma unroll 4
-      for (int c = 0; c < PAGE / NC; c += 4) {
-        float4 vv = *reinterpret_cast<const float4 *>(vr + c);
-        if (left < PAGE) {
-          if (c > left) vv.x = 0.f;
-          if (c + 1 > left) vv.y = 0.f;
-          if (c + 2 > left) vv.z = 0.f;
-          if (c + 3 > left) vv.w = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < F_ROWS; ++i) {
-          const float4 pv = *reinterpret_cast<const float4 *>(sp + i * PAGE + part_t + c);
-          acc[i] = fmaf(pv.x, vv.x, acc[i]);
-          acc[i] = fmaf(pv.y, vv.y, acc[i]);
-          acc[i] = fmaf(pv.z, vv.z, acc[i]);
-          acc[i] = fmaf(pv.w, vv.w, acc[i]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < F_ROWS; ++i) acc[i] *= st[16 + i];
-    }
-    __syncthreads();
-  }
-  if (NC == 2) {   // the two halves of a column's tokens
-    __syncthreads();
-    if (tid >= D)
-#pragma unroll
-      for (int i = 0; i < F_ROWS; ++i) sk[i * D + col] = acc[i];
-    __syncthreads();
-    if (tid < D)
-#pragma unroll
-      for (int i = 0; i < F_ROWS; ++i) acc[i] += sk[i * D + col];
-  }
-  __syncthreads();
-  const bool writer = tid < D;
-  auto write = [&](int i, float o, float M, float L) {
-    const int row = rt * F_ROWS + i, t = r.row0 + row / p.g, hq = h * p.g + row % p.g;
-    const size_t at = static_cast<size_t>(t) * (p.nkv * p.g) + hq;
-    static_cast<float *>(p.out)[at * D + col] = L > 0.f ? o / L : 0.f;
-    if (p.lse && col == 0) p.lse[at] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
-  };
-  if (gridDim.y == 1) {
-    if (writer)
-#pragma unroll
-      for (int i = 0; i < F_ROWS; ++i)
-        if (i < rows) write(i, acc[i], st[i], st[8 + i]);
-    return;
-  }
-  constexpr int FP = F_ROWS * (D + 2);
-  float *part = p.partials + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * FP;
-  if (writer)
-#pragma unroll
-    for (int i = 0; i < F_ROWS; ++i) __stcg(part + i * D + col, acc[i]);
-  if (tid < F_ROWS) {
-    __stcg(part + F_ROWS * D + tid, st[tid]);
-    __stcg(part + F_ROWS * D + F_ROWS + tid, st[8 + tid]);
-  }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    int *ctr = p.counters + blockIdx.x;
-    const int old = atomicAdd(ctr, 1);
-    last = old == static_cast<int>(gridDim.y) - 1;
-    if (last) atomicExch(ctr, 0);
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  const float *all = p.partials + static_cast<size_t>(blockIdx.x) * gridDim.y * FP;
-  join_tile<float, D, 1, 8>(dest_of(p, r.row0, h, rt * F_ROWS), [&](int i) { return all + i * FP; }, gridDim.y, F_ROWS, rows, tid, F_THREADS);
-}
-
 // ------------------------------------------------------------------ host
-int row_tiles(const dflash_heads &h, int max_new, int tile_rows) {
-  return (max_new * (h.n_q_heads / h.n_kv_heads) + tile_rows - 1) / tile_rows;
+// row tiles of a (request, kv head) at most
+int row_tiles(const dflash_heads &h, int max_new) {
+  return h.dtype == DFLASH_F32 ? (max_new * (h.n_q_heads / h.n_kv_heads) + ROWS - 1) / ROWS : 1;
 }
 
-template <int D, bool CL>
+template <typename T, int D, bool CL>
 int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
-  using S = Shape<D>;
-  auto *kernel = decode_kernel<D, CL>;
+  using S = Shape<T, D>;
+  auto *kernel = decode_kernel<T, D, CL>;
   static std::atomic<uint64_t> smem_set, wide_set;
   if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   if (CL && p.cs > 8)
     if (int e = allow_wide_clusters(wide_set, dev, kernel)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
-  if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
-  if (int e = make_tmap_2d(&tv, p.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, PAGE, pages * D, PAGE * 2, 64, D)) return e;
+  constexpr auto type = S::SIZE == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr int W = 128 / S::SIZE;
+  if (int e = make_tmap_2d(&tk, p.k, type, S::SIZE, D, pages * PAGE, D * S::SIZE, W, PAGE)) return e;
+  if (int e = make_tmap_2d(&tv, p.v, type, S::SIZE, PAGE, pages * D, PAGE * S::SIZE, W, D)) return e;
   p.min_chunks = 2;
   const int most = static_cast<int>(PART_TOTAL / (2 * S::PART));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.cs) : static_cast<unsigned>(min(dev.sms * S::CTAS, most)));
+  cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.tiles * p.cs) : static_cast<unsigned>(min(dev.sms * S::CTAS, most)));
   cfg.blockDim = dim3(160);
   cfg.dynamicSmemBytes = S::SMEM;
   cfg.stream = s;
@@ -696,26 +598,9 @@ int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   return cuda_check(cudaLaunchKernelEx(&cfg, kernel, tk, tv, p), "cache_attention launch");
 }
 
-template <int D>
-int launch_f32(const Params &p, const Device &dev, cudaStream_t s) {
-  constexpr int SMEM = (2 * PAGE * (D + 4) + 2 * D * (PAGE + 4) + F_ROWS * D + F_ROWS * PAGE + 24) * 4;
-  auto *kernel = decode_f32_kernel<D>;
-  static std::atomic<uint64_t> smem_set;
-  if (int e = allow_smem(smem_set, dev, kernel, SMEM)) return e;
-  // few (request, kv head, row tile)s: their pages split over several CTAs
-  const long long items = static_cast<long long>(p.B) * p.nkv * p.tiles;
-  const long long cap = static_cast<long long>(PART_BYTES / (F_ROWS * (D + 2) * 4)) / items;
-  long long split = (3LL * dev.sms + items - 1) / items;
-  split = split > (p.max_pages + 1) / 2 ? (p.max_pages + 1) / 2 : split;
-  split = split > cap ? cap : split;
-  split = split < 1 ? 1 : split;
-  launch_pdl(kernel, dim3(static_cast<unsigned>(items), static_cast<unsigned>(split)), dim3(F_THREADS), SMEM, s, p);
-  return cuda_check(cudaGetLastError(), "cache_attention launch");
-}
-
-// counters: one per (request, kv head, row tile), of the narrowest tile any path uses
+// one per (request, kv head, row tile)
 size_t counter_count(const dflash_heads &h, int batch, int max_new) {
-  return static_cast<size_t>(batch) * h.n_kv_heads * row_tiles(h, max_new, F_ROWS);
+  return static_cast<size_t>(batch) * h.n_kv_heads * row_tiles(h, max_new);
 }
 
 }  // namespace
@@ -780,20 +665,23 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   p.counters = reinterpret_cast<int *>(static_cast<char *>(workspace) + HEADER_BYTES + PART_BYTES);
   p.status = static_cast<int *>(workspace);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (hs->dtype == DFLASH_F32) {
-    p.tiles = row_tiles(*hs, max_new, F_ROWS);
-    return d == 64 ? launch_f32<64>(p, dev, s) : launch_f32<128>(p, dev, s);
-  }
-  if (max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
-  // Clusters of up to 16 CTAs per (request, kv head) while one CTA per SM holds
-  // them all, and the capacity leaves a CTA 16 pages at most: beyond that the
-  // balanced runs over the whole GPU are faster.
-  const long long lists = static_cast<long long>(batch) * nkv;
+  const bool f32 = hs->dtype == DFLASH_F32;
+  p.tiles = row_tiles(*hs, max_new);
+  if (!f32 && max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
+  // Clusters of up to 16 CTAs (8 where a CTA fills its SM) per tile while one
+  // CTA per SM holds them all, and the capacity leaves a CTA 16 pages at most:
+  // beyond that the balanced runs over the whole GPU are faster.
+  const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
   p.cs = 1;
-  while (p.cs < 16 && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  while (p.cs < (f32 && d == 128 ? 8 : 16) && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
   const bool cl = p.cs > 1 && kv->max_pages <= 16 * p.cs;
-  if (d == 64) return cl ? launch_decode<64, true>(*hs, *kv, p, dev, s) : launch_decode<64, false>(*hs, *kv, p, dev, s);
-  return cl ? launch_decode<128, true>(*hs, *kv, p, dev, s) : launch_decode<128, false>(*hs, *kv, p, dev, s);
+#define DECODE(T_, D_) \
+  return cl ? launch_decode<T_, D_, true>(*hs, *kv, p, dev, s) : launch_decode<T_, D_, false>(*hs, *kv, p, dev, s)
+  if (f32 && d == 64) DECODE(float, 64);
+  if (f32) DECODE(float, 128);
+  if (d == 64) DECODE(__nv_bfloat16, 64);
+  DECODE(__nv_bfloat16, 128);
+#undef DECODE
 }
 
 }  // extern "C"

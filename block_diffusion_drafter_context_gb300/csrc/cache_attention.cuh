@@ -25,7 +25,7 @@ struct Params {
   const int32_t *page_table, *cu_new, *ctx_len;
   int max_pages, num_pages;
   int B, nkv, g, total, max_new, window;
-  int tiles;                               // fp32 form: row tiles of a (request, kv head)
+  int tiles;                               // row tiles of a (request, kv head) at most (bf16: 1)
   int min_chunks;
   int cs;                                  // cluster form: CTAs per tile
   float scale_log2;
@@ -85,10 +85,10 @@ struct Runs {
 // What the consumers need to know of a chunk, written by the producer beside
 // the chunk's data.
 struct Chunk {
-  int b, h, page, pad;       // request, kv head, page of the request
+  int b, h, rt, page;        // request, kv head, row tile, page of the request
   int row0, n, ctx, flags;   // FIRST / LAST of this CTA's part, BAD page, WHOLE: no other CTA has a part
   int cf, cl, slot0, slot;   // contributors cf..cl; whether cf's part is its first; this part's slot
-  int nrow0, nn, nh, pad2;   // the tile after this one, where this CTA has a part of it: its rows and kv head (nn 0: none)
+  int nrow0, nn, nh, pad;    // the tile after this one, where this CTA has a part of it: its rows and kv head (nn 0: none)
 };
 enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 
@@ -175,16 +175,16 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
 // the same for the runs' partials: np contributors from CTA cf on, a tile's
 // slot at (CTA * 2 + slot) * stride.  Not inlined: the kernels' main loops have
 // no registers to spare for it.
-template <int D>
+template <typename T, int D>
 __device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, int np, int slot0, int stride, int tile_rows,
                                         int rows, int tid, int nthr) {
   auto src = [&](int i) { return partials + (static_cast<size_t>(cf + i) * 2 + (i > 0 || slot0 ? 0 : 1)) * stride; };
   if (rows * (D / 4) <= 2 * nthr)
-    join_tile<__nv_bfloat16, D, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else if (np > 4)
-    join_tile<__nv_bfloat16, D, 4, 8>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, 4, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else
-    join_tile<__nv_bfloat16, D, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
 }
 
 // 17..128 query rows per (request, kv head) on tcgen05 (cache_attention_tc.cu).

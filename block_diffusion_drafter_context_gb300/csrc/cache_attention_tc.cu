@@ -188,11 +188,11 @@ __global__ void __launch_bounds__(NTHR, 1)
             cl = runs.owner(x - k + r.np - 1);
           }
           Chunk c;
-          c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+          c.b = b, c.h = h, c.rt = 0, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
           c.cf = cf, c.cl = cl;
           c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && c.cf == c.cl ? WHOLE : 0);
           c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = c.pad2 = 0;
+          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = 0;
           ct->chunk[st] = c;
           mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
           if (!bad) {
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, MROWS, rows, tid, 4 * 32);
+        join_parts<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, MROWS, rows, tid, 4 * 32);
     }
     if (!ok) {
       report(p.status, DFLASH_ERR_TIMEOUT);
