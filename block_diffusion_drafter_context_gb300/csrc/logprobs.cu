@@ -272,8 +272,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
       raw[u] = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
       if (u * 32 + lane < n) raw[u] = ring[(s % STAGES) * SV + u * 32 + lane];
     }
-    __syncwarp();
-    if (lane == 0 && s + STAGES < ns) fetch(s + STAGES);   // the stage is in registers
     float vmax[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -289,13 +287,17 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
       seg = -INFINITY;
       left = seg_len;
     }
-    if (mn != m) {
-      const float d = fmaxf((m - mn) * c, FAR), f = fast_exp2(d);
+    // The vote needs every lane's maximum, so behind it the stage is in
+    // registers and may be refilled.  (Behind a mere __syncwarp loads were
+    // still on their way when the next copy's first bytes came.)
+    if (__any_sync(0xffffffffu, mn != m)) {
+      const float d = m == mn ? 0.f : fmaxf((m - mn) * c, FAR), f = fast_exp2(d);
       const uint64_t f2 = pack2(f, f);
       w2 = mul2(f2, fma2(z2, pack2(d, d), w2));
       z2 = mul2(f2, z2);
       m = mn;
     }
+    if (lane == 0 && s + STAGES < ns) fetch(s + STAGES);
     const uint64_t neg2 = pack2(-mn, -mn);
 #pragma unroll
     for (int u = 0; u < U; ++u) {

@@ -333,6 +333,43 @@ def test_logprobs_match_oracle(dtype, rows, V, pad, kind):
         assert abs(got["entropy"][r] - ent) <= 3 * e * (np.log(V) + 2), (r, got["entropy"][r], ent)
 
 
+@pytest.mark.parametrize("dtype,rows,V", [("f32", 700, 151936), ("bf16", 700, 151936), ("f32", 64, 151936),
+                                          ("bf16", 500, 40001), ("f32", 3, 1500000)])
+def test_logprobs_of_a_full_gpu(dtype, rows, V):
+    """Rows enough to keep every SM's memory pipes busy, and few long ones: all
+    rows against fp64 sums, exact counts and a stable sort on the GPU."""
+    import torch
+    from block_diffusion_drafter_context_gb300.target import token_logprobs
+    g = torch.Generator("cuda").manual_seed(rows + V)
+    x = (torch.randn(rows, V, generator=g, device="cuda") * 2.5).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ids = torch.where(torch.rand(rows, generator=g, device="cuda") < 0.5, x.argmax(1),
+                      torch.randint(0, V, (rows,), generator=g, device="cuda"))
+    ids[::7] = -1
+    live = (ids >= 0).nonzero()[:, 0]
+    first = None
+    for _ in range(3):
+        got = token_logprobs(x, ids.int(), temperature=0.8)
+        if first is None:
+            first = got
+            at = torch.arange(V, device="cuda")
+            for part in live.split(64):
+                y, t = x[part].double() / 0.8, ids[part][:, None]
+                lse = y.logsumexp(1, keepdim=True)
+                mine, lp = x[part].gather(1, t), y - lse
+                # fp32: as in the test above, logits up to 6 * 2.5 / 0.8
+                e = (6 * 20 + V / 256 + 32) * 2.0 ** -24
+                for key, ref, tol in (("logprob", lp.gather(1, t)[:, 0], 2 * e),
+                                      ("entropy", -(lp.exp() * lp).sum(1), 3 * e * (np.log(V) + 2)),
+                                      ("top_logprobs", lp.topk(16, dim=1).values, 2 * e)):
+                    assert (got[key][part].double() - ref).abs().max() <= tol, key
+                before = (x[part] > mine) | ((x[part] == mine) & (at < t))
+                assert torch.equal(got["rank"][part].long(), before.sum(1))
+                order = torch.sort(x[part], dim=1, descending=True, stable=True).indices[:, :16]
+                assert torch.equal(got["top_ids"][part].long(), order)
+        for key in got:      # the same bits on every call
+            assert torch.equal(got[key], first[key]), key
+
+
 def test_logprobs_of_rows_without_a_distribution():
     """Nothing but -inf: probability 0 everywhere; a NaN or +inf logit: NaN;
     an id past the vocabulary: NaN and rank -1."""
