@@ -230,6 +230,46 @@ def test_long_request_is_split_and_joined(nq, nkv, d, dtype, n):
     c.check_attention(out, lse)
 
 
+@pytest.mark.parametrize("nq,nkv,d,dtype,B,top,new,window", [
+    (32, 8, 128, "bf16", 40, 6000, 1, 0), (40, 8, 128, "bf16", 24, 5000, 16, 0), (32, 8, 64, "bf16", 40, 4000, 8, 0),
+    (16, 8, 64, "bf16", 64, 3000, 2, 700), (16, 4, 128, "f32", 24, 3000, 3, 0), (32, 8, 64, "f32", 16, 3000, 8, 900),
+    (8, 1, 128, "bf16", 1, 120000, 1, 0), (8, 1, 128, "bf16", 1, 120000, 7, 0), (4, 4, 128, "bf16", 300, 90, 1, 0)])
+def test_attention_of_a_full_gpu(nq, nkv, d, dtype, B, top, new, window):
+    """Ragged batches that keep every SM's pipes busy, and one request over all
+    of them: all rows against fp64 on the GPU (the same bounds), three calls
+    with the same bits."""
+    import torch
+    rng = np.random.default_rng(B + d + new)
+    ctx = sorted(int(v) for v in rng.integers(top // 8, top + 1, B))
+    c = Batch(nq, nkv, d, dtype, ctx, [1 + (b * 7) % new for b in range(B)], seed=B, window=window, max_new=new)
+    out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, window=window, want_lse=True)
+    assert c.ops.status() == 0
+    g, scale, unit = nq // nkv, d ** -0.5, U["bf16"] if dtype == "bf16" else 0.0
+    for b in range(B):
+        n, L = c.new[b], c.ctx[b] + c.new[b]
+        pages = torch.from_numpy(c.table[b, :-(-L // PAGE)].astype(np.int64)).cuda()
+        k = c.k[1, pages].permute(1, 0, 2, 3).reshape(nkv, -1, d)[:, :L].double()
+        v = c.v[1, pages].permute(1, 0, 3, 2).reshape(nkv, -1, d)[:, :L].double()
+        rows = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        q = c.q[rows].double().view(n, nkv, g, d).permute(1, 0, 2, 3)        # [nkv, n, g, d]
+        s = torch.einsum("hngd,htd->hngt", q, k) * scale
+        size = torch.einsum("hngd,htd->hngt", q.abs(), k.abs()).max() * scale   # what a score's sum is made of
+        pos, key = c.ctx[b] + torch.arange(n, device="cuda")[:, None], torch.arange(L, device="cuda")
+        see = (key <= pos) & ((key > pos - window) if window else True)
+        s = s.masked_fill(~see[None, :, None], -float("inf"))
+        ref_lse = s.logsumexp(-1)
+        w = (s - ref_lse[..., None]).exp()
+        ref, spread = (torch.einsum("hngt,htd->hngd", w, x) for x in (v, v.abs()))
+        e = float(2 * d * 2.0 ** -24 * size + L * 2.0 ** -24 + 2.0 ** -20)
+        got = out[rows].double().view(n, nkv, g, d).permute(1, 0, 2, 3)
+        assert ((got - ref).abs() <= (unit + e) * spread + U[dtype] * ref.abs() + 1e-30).all(), b
+        got = lse[rows].double().view(n, nkv, g).permute(1, 0, 2)
+        assert ((got - ref_lse).abs() <= e + 2.0 ** -22 * (1 + ref_lse.abs())).all(), b
+    for _ in range(3):
+        again = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, window=window, want_lse=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_scores_and_large_values(dtype):
     """Scores far apart (the maximum moves by hundreds along the request)."""
