@@ -34,8 +34,8 @@ namespace {
 //
 // fp32 operands go through the tensor cores as sums of two tf32 parts, x = hi
 // + lo with hi rounded to 11 bits and lo the exact rest: hi hi + hi lo + lo hi
-// leaves out lo lo (2^-24 of a product) and the bits of lo past 11 (2^-23), so
-// a product is good to about fp32's own rounding.  On CUDA cores the same
+// leaves out lo lo and the bits of lo past 11, each about 2^-24 of a product,
+// so it is good to about fp32's own rounding.  On CUDA cores the same
 // products took three times as long: a value from shared memory served 4 rows.
 constexpr int ROWS = 16;
 template <typename T, int D>
@@ -49,9 +49,11 @@ struct Shape {
   static constexpr int PART = ROWS * (D + 2);                              // floats of a partial
 };
 
-// x = hi + lo, hi of 11 significant bits (to nearest); the product reads 11 of lo
+// x = hi + lo, hi of 11 significant bits (to nearest, in integer arithmetic:
+// the conversion instruction runs at a quarter of its rate); the product reads
+// 11 bits of lo
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(x)));
+  hi = (x + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -60,14 +62,17 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// d += A B from split operands, small terms first
-__device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], uint32_t b0,
-                                          uint32_t b1) {
+// d += A B from split operands, the small terms in dl (may be d itself).  The
+// tensor cores cut their sums off instead of rounding them, so sums that go on
+// for long are kept short here and added up outside: with O accumulated over
+// all pages the outputs came out 5e-6 too small at 32k positions.
+__device__ __forceinline__ void mma_split(float (&d)[4], float (&dl)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          uint32_t b0, uint32_t b1) {
   uint32_t h0, l0, h1, l1;
   split_tf32(b0, h0, l0);
   split_tf32(b1, h1, l1);
-  mma_tf32(d, al, h0, h1);
-  mma_tf32(d, ah, l0, l1);
+  mma_tf32(dl, al, h0, h1);
+  mma_tf32(dl, ah, l0, l1);
   mma_tf32(d, ah, h0, h1);
 }
 
@@ -307,6 +312,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     const int newest = c.ctx + c.n - 1, oldest = p.window > 0 ? c.ctx - p.window + 1 : 0;
     if (!(c.flags & BAD) && t0 <= newest && t0 + 15 >= oldest) {
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float sl[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // fp32: the small terms
       const int ktok = cw * 16 + (lane >> 4) * 8 + (lane & 7);
       const uint32_t ka = smem_u32(stage) + ktok * 128;
 #pragma unroll
@@ -318,12 +324,16 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
           uint32_t qh[4], ql[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) split_tf32(qf[kk][e], qh[e], ql[e]);
-          mma_split(s[0], qh, ql, b0, b1);
-          mma_split(s[1], qh, ql, b2, b3);
+          mma_split(s[0], sl[0], qh, ql, b0, b1);
+          mma_split(s[1], sl[1], qh, ql, b2, b3);
         } else {
           mma_bf16_16816(s[0], qf[kk], b0, b1);
           mma_bf16_16816(s[1], qf[kk], b2, b3);
         }
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] += sl[e >> 2][e & 3];
       }
       // positions a row does not see (whatever their slots hold)
       const bool edge = t0 + 15 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
@@ -385,7 +395,8 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
         const uint32_t vb = va + (cw >> 1) * (D * 128) + (lane >> 2) * 128 + (lane & 1) * 8;
         const int ch = (cw & 1) * 4 + ((lane & 3) >> 1);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int u = 0; u < 2; ++u) {   // 8 tokens per step
             uint32_t b0, b1;
@@ -396,8 +407,11 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
               if (mine + 8 * u > newest) b0 = 0u;
               if (mine + 8 * u + 1 > newest) b1 = 0u;
             }
-            mma_split(o[t], ph[u], pl[u], b0, b1);
+            mma_split(d, d, ph[u], pl[u], b0, b1);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][e] += d[e];
+        }
       } else {
         // P rounded to bf16, the type its product with V takes; the sum keeps fp32
         const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
