@@ -272,8 +272,8 @@ int check_heads(const char *who, const dflash_heads *hs) {
 int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, int layer, const void *rows,
                  long long row_stride, int row_elems, const int32_t *cu_new, int total_new, const int32_t *ctx_len,
                  int batch, const void *workspace, size_t workspace_bytes, size_t need) {
-  if (!kv || !kv->k_cache || !kv->v_cache || !kv->page_table || !cu_new || !ctx_len || !workspace ||
-      (total_new > 0 && !rows))
+  if (!kv || !kv->k_cache || !kv->v_cache || !workspace ||
+      (batch > 0 && (!kv->page_table || !cu_new || !ctx_len)) || (total_new > 0 && batch > 0 && !rows))
     return set_error(DFLASH_ERR_ARG, "%s: null argument", who);
   if (batch < 0 || batch > DFLASH_MAX_BATCH || total_new < 0 || layer < 0)
     return set_error(DFLASH_ERR_ARG, "%s: batch, total_new or layer out of range", who);

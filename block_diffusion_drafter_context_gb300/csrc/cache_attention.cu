@@ -128,11 +128,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Req r = request(p, b, blockIdx.x == 0);
-      sum += static_cast<long long>(r.np) * tiles_of(r);
-    }
+    const long long sum = sum_pages(p, b0, b1, blockIdx.x == 0, tiles_of);
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -682,12 +678,14 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   const bool f32 = hs->dtype == DFLASH_F32;
   p.tiles = row_tiles(*hs, max_new);
   if (!f32 && max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
-  // Clusters of up to 16 CTAs (8 where a CTA fills its SM) per tile while one
-  // CTA per SM holds them all, and the capacity leaves a CTA 16 pages at most:
-  // beyond that the balanced runs over the whole GPU are faster.
+  // Clusters of up to 16 CTAs per tile while one CTA per SM holds them all (8,
+  // and three quarters of the SMs, where a CTA fills its SM), and the capacity
+  // leaves a CTA 16 pages at most: beyond that the balanced runs over the whole
+  // GPU are faster.
   const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
   p.cs = 1;
-  while (p.cs < (f32 && d == 128 ? 8 : 16) && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  const bool big = f32 && d == 128;
+  while (p.cs < (big ? 8 : 16) && lists * p.cs * 2 <= (big ? dev.sms * 3 / 4 : dev.sms)) p.cs *= 2;
   const bool cl = p.cs > 1 && kv->max_pages <= 16 * p.cs;
 #define DECODE(T_, D_) \
   return cl ? launch_decode<T_, D_, true>(*hs, *kv, p, dev, s) : launch_decode<T_, D_, false>(*hs, *kv, p, dev, s)

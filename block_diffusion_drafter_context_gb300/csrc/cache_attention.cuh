@@ -40,11 +40,11 @@ struct Req {
   int row0, n, ctx, p0, np;
 };
 
-__device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
+__device__ __forceinline__ Req make_request(const Params &p, int row0, int next, int ctx, bool tell) {
   Req r;
-  r.row0 = p.cu_new[b];
-  const long long n = static_cast<long long>(p.cu_new[b + 1]) - r.row0;
-  r.ctx = p.ctx_len[b];
+  r.row0 = row0;
+  const long long n = static_cast<long long>(next) - row0;
+  r.ctx = ctx;
   const bool ok = r.row0 >= 0 && n >= 0 && n <= p.max_new && r.row0 + n <= p.total && r.ctx >= 0 &&
                   r.ctx + n <= static_cast<long long>(p.max_pages) * PAGE;
   if (!ok && tell) report(p.status, DFLASH_ERR_DEVICE);
@@ -57,6 +57,30 @@ __device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
     r.np = (r.ctx + r.n - 1) / PAGE - r.p0 + 1;
   }
   return r;
+}
+
+__device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
+  return make_request(p, p.cu_new[b], p.cu_new[b + 1], p.ctx_len[b], tell);
+}
+// Pages of requests b0 .. b1-1, each as often as it has row tiles; four
+// requests' loads at a time (one by one, 4096 requests took 45 us).
+template <typename Tiles>
+__device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, bool tell, Tiles tiles_of) {
+  long long sum = 0;
+  for (int b = b0; b < b1; b += 4) {
+    int row0[5], ctx[4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) row0[i] = p.cu_new[min(b + i, p.B)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ctx[i] = p.ctx_len[min(b + i, p.B - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (b + i < b1) {
+        const Req r = make_request(p, row0[i], row0[i + 1], ctx[i], tell);
+        sum += static_cast<long long>(r.np) * tiles_of(r);
+      }
+  }
+  return sum;
 }
 
 // How the list of `total` pages is shared out: G CTAs take runs of `base` pages,

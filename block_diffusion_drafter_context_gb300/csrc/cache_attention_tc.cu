@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += request(p, b, blockIdx.x == 0).np;
+    const long long sum = sum_pages(p, b0, b1, blockIdx.x == 0, [](const Req &) { return 1; });
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -620,11 +619,12 @@ static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
 }
 
 int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
-  // the same rule as for narrower tiles: clusters while one CTA per SM holds
-  // them all and a CTA gets 16 pages at most
+  // the rule of the narrower tiles: clusters while the SMs hold them all (three
+  // quarters of them: a cluster stays within a GPC, and 16 of 8 CTAs that fill
+  // an SM each took two waves, 14 us against 8) and a CTA gets 16 pages at most
   const long long lists = static_cast<long long>(p.B) * p.nkv;
   p.cs = 1;
-  while (p.cs < 8 && lists * p.cs * 2 <= dev.sms) p.cs *= 2;
+  while (p.cs < 8 && lists * p.cs * 2 <= dev.sms * 3 / 4) p.cs *= 2;
   const bool cl = p.cs > 1 && kv.max_pages <= 16 * p.cs;
   if (hs.head_dim == 64) return cl ? launch<64, true>(hs, kv, p, dev, s) : launch<64, false>(hs, kv, p, dev, s);
   return cl ? launch<128, true>(hs, kv, p, dev, s) : launch<128, false>(hs, kv, p, dev, s);

@@ -504,7 +504,9 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
  *   scale:    positive and finite, e.g. 1/sqrt(d).
  *   out:      device [total_new][nq*d] (dtype) out.
  *   lse:      device fp32 [total_new][nq] out, or NULL.
- * Cache slots past a request's newest token may hold anything (NaN too).
+ * Cache slots past a request's newest token may hold anything (NaN too); the
+ * K and V of its own tokens are finite (0 times an infinite V of a position
+ * that another of the request's tokens sees is NaN).
  * A page index outside [0, num_pages) drops that page's positions and is
  * reported as DFLASH_ERR_DEVICE; a token left without any gets out = 0 and
  * lse = -inf.  A request whose cu_new or ctx_len is out of range (or that has

@@ -270,6 +270,38 @@ def test_attention_of_a_full_gpu(nq, nkv, d, dtype, B, top, new, window):
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+@pytest.mark.parametrize("B", [257, 1100, 4096])
+def test_large_batches(B):
+    """Batches past one and two steps of the lookups, many requests without new
+    tokens, every request inside one page: append, then attention."""
+    import torch
+    rng = np.random.default_rng(B)
+    new = rng.integers(0, 3, B)
+    new[0], new[-1] = 1, 2
+    c = Batch(2, 1, 64, "f32", rng.integers(0, 62, B).tolist(), new.tolist(), seed=B, stale=0.0, max_new=2)
+    q = c.ops.append_kv(c.kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    out, lse = c.ops.attend(c.kv, 1, q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    owner = torch.repeat_interleave(torch.arange(B), torch.tensor(c.new)).cuda()
+    pos = c.ctx_d[owner].long() + torch.arange(c.T, device="cuda") - c.cu_d[owner]
+    page = c.kv.page_table[owner, 0].long()
+    x = c.qkv.double().view(c.T, 4, 64)
+    assert torch.equal(c.v[1, page, 0, :, pos].double(), x[:, 3])
+    y = x[:, :3] / (x[:, :3].pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+    y = y * torch.stack([c.g_q, c.g_q, c.g_k]).double()
+    ang = pos.double()[:, None] * 1e6 ** (-2 * torch.arange(32, device="cuda").double() / 64)
+    z = torch.complex(y[..., :32].contiguous(), y[..., 32:].contiguous()) * torch.polar(torch.ones_like(ang), ang)[:, None]
+    y = torch.cat([z.real, z.imag], -1)
+    assert (q.double().view(c.T, 2, 64) - y[:, :2]).abs().max() <= 1.5e-6 * 10
+    assert (c.k[1, page, 0, pos].double() - y[:, 2]).abs().max() <= 1.5e-6 * 10
+    s = torch.einsum("thd,tkd->thk", q.double().view(c.T, 2, 64), c.k[1, page, 0].double()) / 8
+    s = s.masked_fill((torch.arange(64, device="cuda") > pos[:, None])[:, None], -float("inf"))
+    ref = torch.einsum("thk,tdk->thd", s.softmax(-1), c.v[1, page, 0].double())
+    # scores up to about 30 of 64 products: 2 * 64 * 2^-24 * 8 * 30 / 8 on a probability
+    assert (out.double().view(c.T, 2, 64) - ref).abs().max() <= 3e-4
+    assert (lse.double() - s.logsumexp(-1)).abs().max() <= 3e-4
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_peaked_scores_and_large_values(dtype):
     """Scores far apart (the maximum moves by hundreds along the request)."""

@@ -111,8 +111,11 @@ def test_logprobs(lib, kw, code):
 
 
 def test_empty_calls_do_nothing(lib):
-    assert append(lib, batch=0) == 0 and append(lib, total=0, qkv=None) == 0
-    assert attend(lib, batch=0) == 0 and attend(lib, total=0, q=None, out=None) == 0
+    none = dict(batch=0, cu=None, ctx=None)
+    assert append(lib, **none) == 0 and append(lib, total=0, qkv=None) == 0
+    assert append(lib, kv=cache(page_table=None), qkv=None, **none) == 0
+    assert attend(lib, **none) == 0 and attend(lib, total=0, q=None, out=None) == 0
+    assert attend(lib, kv=cache(page_table=None), q=None, **none) == 0
     assert logprobs(lib, rows=0, x=None) == 0
 
 
