@@ -679,14 +679,16 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   p.tiles = row_tiles(*hs, max_new);
   if (!f32 && max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
   // Clusters of up to 16 CTAs per tile while one CTA per SM holds them all (8,
-  // and three quarters of the SMs, where a CTA fills its SM), and the capacity
-  // leaves a CTA 16 pages at most: beyond that the balanced runs over the whole
-  // GPU are faster.
+  // and three quarters of the SMs, where a CTA fills its SM), down to a CTA per
+  // tile while all are resident, and while the capacity leaves a CTA 16 pages
+  // at most: beyond that the balanced runs over the whole GPU are faster
+  // (32 x 8 tiles of 1..4 pages: 9 us on a CTA each, 14 in runs; 64 x 8 the
+  // same either way, 256 x 8 51 and 39).
   const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
   p.cs = 1;
   const bool big = f32 && d == 128;
   while (p.cs < (big ? 8 : 16) && lists * p.cs * 2 <= (big ? dev.sms * 3 / 4 : dev.sms)) p.cs *= 2;
-  const bool cl = p.cs > 1 && kv->max_pages <= 16 * p.cs;
+  const bool cl = kv->max_pages <= 16 * p.cs && lists <= (big ? dev.sms : 2 * dev.sms);
 #define DECODE(T_, D_) \
   return cl ? launch_decode<T_, D_, true>(*hs, *kv, p, dev, s) : launch_decode<T_, D_, false>(*hs, *kv, p, dev, s)
   if (f32 && d == 64) DECODE(float, 64);

@@ -621,11 +621,12 @@ static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
 int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
   // the rule of the narrower tiles: clusters while the SMs hold them all (three
   // quarters of them: a cluster stays within a GPC, and 16 of 8 CTAs that fill
-  // an SM each took two waves, 14 us against 8) and a CTA gets 16 pages at most
+  // an SM each took two waves, 14 us against 9), a CTA per tile while all are
+  // resident, 16 pages per CTA at most
   const long long lists = static_cast<long long>(p.B) * p.nkv;
   p.cs = 1;
   while (p.cs < 8 && lists * p.cs * 2 <= dev.sms * 3 / 4) p.cs *= 2;
-  const bool cl = p.cs > 1 && kv.max_pages <= 16 * p.cs;
+  const bool cl = kv.max_pages <= 16 * p.cs && lists <= dev.sms;
   if (hs.head_dim == 64) return cl ? launch<64, true>(hs, kv, p, dev, s) : launch<64, false>(hs, kv, p, dev, s);
   return cl ? launch<128, true>(hs, kv, p, dev, s) : launch<128, false>(hs, kv, p, dev, s);
 }
