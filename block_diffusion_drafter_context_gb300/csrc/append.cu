@@ -275,7 +275,7 @@ int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, i
   if (!kv || !kv->k_cache || !kv->v_cache || !workspace ||
       (batch > 0 && (!kv->page_table || !cu_new || !ctx_len)) || (total_new > 0 && batch > 0 && !rows))
     return set_error(DFLASH_ERR_ARG, "%s: null argument", who);
-  if (batch < 0 || batch > DFLASH_MAX_BATCH || total_new < 0 || layer < 0)
+  if (batch < 0 || batch > DFLASH_MAX_BATCH || total_new < 0 || total_new > (1 << 30) || layer < 0)
     return set_error(DFLASH_ERR_ARG, "%s: batch, total_new or layer out of range", who);
   if (kv->num_pages <= 0 || kv->max_pages <= 0 || kv->max_pages > (1 << 18))
     return set_error(DFLASH_ERR_SHAPE, "%s: num_pages must be positive and max_pages in 1..2^18", who);
@@ -287,6 +287,8 @@ int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, i
       (reinterpret_cast<uintptr_t>(kv->k_cache) & 15) || (reinterpret_cast<uintptr_t>(kv->v_cache) & 15) ||
       (reinterpret_cast<uintptr_t>(workspace) & 15))
     return set_error(DFLASH_ERR_ALIGN, "%s: rows, their stride, the cache and the workspace must be 16-byte aligned", who);
+  if (off_words(cu_new, ctx_len, kv->page_table))
+    return set_error(DFLASH_ERR_ALIGN, "%s: index arrays must be aligned to their elements", who);
   if (workspace_bytes < need)
     return set_error(DFLASH_ERR_SHAPE, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
   return DFLASH_OK;
@@ -322,6 +324,7 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
   if (!(eps >= 0.f) || !(rope_base == 0.f || (rope_base > 1.f && rope_base < 3.0e38f)))
     return set_error(DFLASH_ERR_ARG, "append_kv: eps / rope_base out of range");
   if (reinterpret_cast<uintptr_t>(q_out) & 15) return set_error(DFLASH_ERR_ALIGN, "append_kv: q_out not 16-byte aligned");
+  if (off_words(g_q, g_k)) return set_error(DFLASH_ERR_ALIGN, "append_kv: g_q and g_k must be aligned to their elements");
   if (batch == 0 || total_new == 0) return DFLASH_OK;
   Device dev;
   if (int e = current_device(&dev)) return e;

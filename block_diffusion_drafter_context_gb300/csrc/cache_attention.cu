@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       const int row = (lane >> 2) + e * 8;
       if ((lane & 3) == 0) {
-        sm[cw * 16 + row] = m[e];
+        sm[cw * 16 + row] = join_max(m[e], s);
         sm[64 + cw * 16 + row] = s;
       }
 #pragma unroll
@@ -646,8 +646,9 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
     return e;
   if (total_new > 0 && !out) return set_error(DFLASH_ERR_ARG, "cache_attention: null out");
   if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(DFLASH_ERR_ALIGN, "cache_attention: out not 16-byte aligned");
-  if (window < 0 || !(scale > 0.f) || !(scale < 3.0e38f))
-    return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0 and scale positive and finite");
+  if (off_words(lse)) return set_error(DFLASH_ERR_ALIGN, "cache_attention: lse not aligned to its elements");
+  if (window < 0 || !(scale > 0.f) || !(scale < 2.0e38f))   // its product with log2(e) is finite
+    return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0 and scale positive and below 2e38");
   if (batch == 0 || total_new == 0) return DFLASH_OK;
   Device dev;
   if (int e = current_device(&dev)) return e;

@@ -129,18 +129,22 @@ __device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h, int ba
   return {p.out, p.lse, row0, h, p.nkv, p.g, base};
 }
 
+// A share's maximum as it goes into a join: +inf where its sum is NaN (a NaN
+// score; maxima pass over NaN), which makes the joined row NaN too.
+__device__ __forceinline__ float join_max(float m, float l) { return l == l ? m : INFINITY; }
+
 // Row `row` of the tile: output columns c4 .. c4 + 3, and its log-sum-exp.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
   row += p.base;
   const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;   // L NaN: so is the row
   T *dst = static_cast<T *>(p.out) + at * D + c4;
   if constexpr (sizeof(T) == 4)
     *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   else
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (p.lse && c4 == 0) p.lse[at] = L > 0.f ? (M + log2f(L)) * LN2_F : -INFINITY;
+  if (p.lse && c4 == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2_F;
 }
 
 // The join of a tile cut over several CTAs, by the last of them to arrive: np

@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           tmem_regs_ready(ov[u]);
           float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = l > 0.f ? __uint_as_float(ov[u][e]) : 0.f;   // l 0: O was never written
+          for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(ov[u][e]);   // l 0: O was never written
           if (!live) continue;
           if (CL) {   // float4s XORed by the row: no bank conflicts
 #pragma unroll
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           } else if (whole) {
             uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = l > 0.f ? pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv) : 0u;
+            for (int e = 0; e < 8; ++e) w[e] = l == 0.f ? 0u : pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + (c0 + u) * 16);
             dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -509,17 +509,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       tc_fence_before();
       if (CL) {
-        if (live) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * row) = make_float2(m, l);
+        if (live) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * row) = make_float2(join_max(m, l), l);
         break;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct->oempty);   // the next tile may overwrite O
       if (whole) {
-        if (live && p.lse) p.lse[at] = l > 0.f ? (m + log2f(l)) * LN2_F : -INFINITY;
+        if (live && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2_F;
         continue;
       }
       if (live) {
-        __stcg(part + MROWS * D + row, m);
+        __stcg(part + MROWS * D + row, join_max(m, l));
         __stcg(part + MROWS * D + MROWS + row, l);
       }
       __threadfence();

@@ -514,8 +514,8 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   if (!logits || !token_ids || !logprob || !entropy || !rank || (n_top > 0 && (!top_ids || !top_logprobs)))
     return set_error(DFLASH_ERR_ARG, "token_logprobs: null pointer");
   const int size = dtype == DFLASH_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(logits) % size)
-    return set_error(DFLASH_ERR_ALIGN, "token_logprobs: logits not aligned to their elements");
+  if (reinterpret_cast<uintptr_t>(logits) % size || off_words(token_ids, logprob, entropy, rank, top_ids, top_logprobs))
+    return set_error(DFLASH_ERR_ALIGN, "token_logprobs: arrays must be aligned to their elements");
   if (rows > (1 << 27)) return set_error(DFLASH_ERR_SHAPE, "token_logprobs: at most 2^27 rows per call");
   Device dev;
   if (int e = current_device(&dev)) return e;

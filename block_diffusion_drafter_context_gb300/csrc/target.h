@@ -44,6 +44,11 @@ int allow_wide_clusters(std::atomic<uint64_t> &done, const Device &d, K *kernel)
   return DFLASH_OK;
 }
 
+// whether any of these pointers to 4-byte elements is misaligned
+template <typename... P>
+inline bool off_words(const P *...p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) != 0;
+}
 inline int elt_bytes(const dflash_heads &h) { return h.dtype == DFLASH_F32 ? 4 : 2; }
 // first element of a layer's K (and V) pages
 inline size_t layer_offset(const dflash_heads &h, const dflash_kv &kv, int layer) {

@@ -448,7 +448,9 @@ DFLASH_API int dflash_topk16_noalloc(const float *logits, int rows, int vocab, i
  * Ragged batches: request b owns rows cu_new[b] .. cu_new[b+1]-1 of the
  * token-major buffers, at positions ctx_len[b] ...  A request may have no
  * new tokens.  Rows from cu_new[batch] to total_new (the padding of a
- * captured batch) are neither read nor written. */
+ * captured batch; total_new <= 2^30) may hold anything and are not written.
+ * No two tokens of a call go to the same slot of a page; pages may be shared
+ * between requests where they are only read (a common prefix). */
 
 /* Heads of one attention layer. */
 typedef struct dflash_heads {
@@ -483,9 +485,10 @@ DFLASH_API size_t dflash_target_workspace_bytes(const dflash_heads *hs, int max_
  *              the q heads are not read.
  *   kv->max_pages <= 2^18 (positions below 2^24).
  * A token whose position has no valid page (or whose request's cu_new or
- * ctx_len is out of range) is not appended and is reported as
- * DFLASH_ERR_DEVICE in the status word of `workspace` (at least 256 bytes;
- * usually the one dflash_cache_attention uses). */
+ * ctx_len is out of range) is not appended, and that, like a cu_new[batch]
+ * above total_new, is reported as DFLASH_ERR_DEVICE in the status word of
+ * `workspace` (at least 256 bytes; usually the one dflash_cache_attention
+ * uses). */
 DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
                      long long row_stride, const float *g_q, const float *g_k, float eps, float rope_base,
                      const int32_t *cu_new, int total_new, const int32_t *ctx_len, int batch, void *q_out,
@@ -501,12 +504,13 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
  *             a row; q_stride in elements, a multiple of 16 bytes.
  *   cu_new:   device int32 [batch+1]; at most max_new (1..16) per request.
  *   window:   0: every position up to p; > 0: the last `window` of them.
- *   scale:    positive and finite, e.g. 1/sqrt(d).
- *   out:      device [total_new][nq*d] (dtype) out.
+ *   scale:    positive, below 2e38, e.g. 1/sqrt(d).
+ *   out:      device [total_new][nq*d] (dtype) out, not overlapping q.
  *   lse:      device fp32 [total_new][nq] out, or NULL.
  * Cache slots past a request's newest token may hold anything (NaN too); the
- * K and V of its own tokens are finite (0 times an infinite V of a position
- * that another of the request's tokens sees is NaN).
+ * K and V of its own tokens are finite, in fp32 below 2^127 (0 times an
+ * infinite V of a position that another of the request's tokens sees is NaN).
+ * A query that is not finite makes its own row's out and lse NaN.
  * A page index outside [0, num_pages) drops that page's positions and is
  * reported as DFLASH_ERR_DEVICE; a token left without any gets out = 0 and
  * lse = -inf.  A request whose cu_new or ctx_len is out of range (or that has

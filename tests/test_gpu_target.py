@@ -326,6 +326,41 @@ def test_missing_pages_are_dropped_and_reported(nq, nkv, d, dtype, new):
     assert c.ops.status() == 0
 
 
+@pytest.mark.parametrize("nq,nkv,d,dtype", [(8, 2, 128, "bf16"), (16, 2, 64, "bf16"), (4, 2, 64, "f32"),
+                                            (4, 1, 128, "f32")])
+@pytest.mark.parametrize("ctx,new", [([70, 200, 3], [1, 1, 1]), ([70, 200, 3], [9, 16, 2]), ([20000, 70], [1, 1]),
+                                     ([20000, 70], [9, 3]), ([64] * 90, [3] * 90)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_spoils_its_own_row_alone(nq, nkv, d, dtype, ctx, new, value):
+    """Few short requests, a long one cut over many CTAs, many short ones: a
+    NaN or an infinity in one head of one token's query makes that row NaN,
+    never a plausible 0, and leaves the other rows within their bounds."""
+    import torch
+    c = Batch(nq, nkv, d, dtype, ctx, new, seed=nq + len(ctx), max_new=max(new))
+    good, good_lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    q = c.q.clone()
+    for row, head in ((0, nq - 1), (c.T - 1, 0)):
+        q[row, head * d + 5] = value
+    out, lse = c.ops.attend(c.kv, 1, q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    spoiled = torch.zeros_like(good, dtype=torch.bool)
+    for row, head in ((0, nq - 1), (c.T - 1, 0)):
+        spoiled[row, head * d:(head + 1) * d] = True
+    assert torch.equal(out.isnan(), spoiled) and torch.equal(lse.isnan(), spoiled[:, ::d])
+    c.check_attention(torch.where(spoiled, good, out), torch.where(spoiled[:, ::d], good_lse, lse))
+
+
+@pytest.mark.parametrize("new", [1, 6])
+def test_requests_share_the_pages_of_a_common_prefix(new):
+    import torch
+    c = Batch(8, 2, 128, "bf16", [300, 300, 300], [new] * 3, seed=new, max_new=new)
+    c.table[1:, :4] = c.table[0, :4]          # 256 tokens in common
+    c.kv.page_table.copy_(torch.from_numpy(c.table))
+    out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    c.check_attention(out, lse)
+
+
 def test_requests_out_of_range_are_left_unwritten():
     import torch
     c = Batch(4, 2, 128, "bf16", [10, 20, 30], [1, 3, 2], max_new=4)

@@ -65,7 +65,7 @@ def test_heads(lib, call, hs, code):
 @pytest.mark.parametrize("kv,code", [
     (dict(k_cache=None), -1), (dict(v_cache=None), -1), (dict(page_table=None), -1), (dict(num_pages=0), -2),
     (dict(max_pages=0), -2), (dict(max_pages=(1 << 18) + 1), -2), (dict(num_pages=1 << 23), -2),
-    (dict(k_cache=FAKE + 8), -3), (dict(v_cache=FAKE + 2), -3),
+    (dict(k_cache=FAKE + 8), -3), (dict(v_cache=FAKE + 2), -3), (dict(page_table=FAKE + 2), -3),
 ])
 def test_cache(lib, call, kv, code):
     assert call(lib, kv=cache(**kv)) == code
@@ -76,6 +76,7 @@ def test_cache(lib, call, kv, code):
     (dict(cu=None), -1), (dict(ctx=None), -1), (dict(ws=None), -1), (dict(batch=-1), -1), (dict(batch=4097), -1),
     (dict(total=-1), -1), (dict(layer=-1), -1), (dict(ld=1000), -2), (dict(ld=-1536), -2), (dict(ld=1537), -3),
     (dict(ws=FAKE + 4), -3), (dict(ws_bytes=255), -2),
+    (dict(total=(1 << 30) + 1), -1), (dict(cu=FAKE + 2), -3), (dict(ctx=FAKE + 1), -3),
 ])
 def test_shared_arguments(lib, call, kw, code):
     assert call(lib, **kw) == code
@@ -84,7 +85,7 @@ def test_shared_arguments(lib, call, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(qkv=None), -1), (dict(qkv=FAKE + 8), -3), (dict(g_q=None), -1), (dict(g_k=None), -1), (dict(eps=-1.0), -1),
     (dict(eps=float("nan")), -1), (dict(base=1.0), -1), (dict(base=-5.0), -1), (dict(base=float("inf")), -1),
-    (dict(base=float("nan")), -1), (dict(q_out=FAKE + 4), -3),
+    (dict(base=float("nan")), -1), (dict(q_out=FAKE + 4), -3), (dict(g_q=FAKE + 2), -3), (dict(g_k=FAKE + 2), -3),
 ])
 def test_append(lib, kw, code):
     assert append(lib, **kw) == code
@@ -93,7 +94,7 @@ def test_append(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), -1), (dict(q=FAKE + 8), -3), (dict(out=None), -1), (dict(out=FAKE + 8), -3), (dict(max_new=0), -1),
     (dict(max_new=17), -1), (dict(window=-1), -1), (dict(scale=0.0), -1), (dict(scale=-0.1), -1),
-    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(scale=2.5e38), -1), (dict(lse=FAKE + 2), -3),
 ])
 def test_attention(lib, kw, code):
     assert attend(lib, **kw) == code
@@ -105,6 +106,7 @@ def test_attention(lib, kw, code):
     (dict(temp=float("nan")), -1), (dict(temp=1e5), -1), (dict(x=None), -1), (dict(ids=None), -1), (dict(lp=None), -1),
     (dict(ent=None), -1), (dict(rank=None), -1), (dict(top=None), -1), (dict(top_lp=None), -1), (dict(x=FAKE + 2), -3),
     (dict(dtype=0, x=FAKE + 1), -3), (dict(rows=(1 << 27) + 1), -2),
+    (dict(ids=FAKE + 1), -3), (dict(lp=FAKE + 2), -3), (dict(rank=FAKE + 2), -3), (dict(top=FAKE + 2), -3),
 ])
 def test_logprobs(lib, kw, code):
     assert logprobs(lib, **kw) == code
