@@ -80,6 +80,16 @@ template <> struct Vec<float> {
   static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[4]) {
     x[0] = __uint_as_float(u.x), x[1] = __uint_as_float(u.y), x[2] = __uint_as_float(u.z), x[3] = __uint_as_float(u.w);
   }
+  template <int U>
+  static __device__ __forceinline__ float maximum(const uint4 (&u)[U]) {
+    float m[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      m[i] = max_nan(max_nan(__uint_as_float(u[i].x), __uint_as_float(u[i].y)), max_nan(__uint_as_float(u[i].z), __uint_as_float(u[i].w)));
+#pragma unroll
+    for (int i = 1; i < U; ++i) m[0] = max_nan(m[0], m[i]);
+    return m[0];
+  }
 };
 template <> struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
@@ -92,15 +102,32 @@ template <> struct Vec<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  template <int U>
+  static __device__ __forceinline__ float maximum(const uint4 (&u)[U]) {
+    uint32_t m[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) m[i] = max2(max2(u[i].x, u[i].y), max2(u[i].z, u[i].w));
+#pragma unroll
+    for (int i = 1; i < U; ++i) m[0] = max2(m[0], m[i]);
+    return max_nan(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xffff0000u));
+  }
 };
 
 // ---- shared memory of a CTA: for each warp a ring of STAGES x 2 KB of logits
 // (4 vectors per lane), then.  Two stages: 4 CTAs an SM have 64 KB in flight,
-// all that HBM's latency asks for; four stages made it slower (96 against 84
-// us at 640 fp32 rows of 151 936).
-constexpr int STAGES = 2, U = 4, SV = 32 * U;
+// all that HBM's latency asks for; four stages made it slower (123 against 114
+// us at 1024 fp32 rows of 151 936).  Where the grid leaves an SM two CTAs at
+// most, four: a CTA's own round trips are the time there (64 such rows on 4
+// CTAs each: 20 us with two stages, 15 with four).
+constexpr int WIDE = 2, DEEP = 4;                    // stages
+constexpr int U = 4, SV = 32 * U;
 constexpr int SEGS = 8;                              // parts of the stream whose maxima each thread keeps
-constexpr int RING = WARPS * STAGES * SV * 16;
+constexpr int ring_bytes(int stages) { return WARPS * stages * SV * 16; }
 constexpr int MIN_SHARE = 8192;                      // logits of a CTA at least, where a row is cut
 constexpr int MAX_SHARE = 400 << 10;                 // bytes of a CTA at most, while there are CTAs for a row left
 constexpr int LIST = 512;                            // candidates a CTA can list
@@ -108,7 +135,7 @@ constexpr unsigned long long WAIT_NS = 2000000000ull;
 struct Shared {
   alignas(16) uint64_t list[LIST];                   // candidates for the 16 largest (value, id) keys, unordered
   uint64_t best[TOP_K];      // the 16 largest in order, 0 where there are fewer
-  uint64_t full[WARPS][STAGES], mail;
+  uint64_t full[WARPS][DEEP], mail;
   alignas(16) uint64_t peer_keys[MAX_CLUSTER * TOP_K];   // rank 0: every CTA's best
   float4 peer_stat[MAX_CLUSTER];                         // rank 0: (m, z, w, count) of every CTA
   float4 warp_stat[WARPS];
@@ -117,7 +144,8 @@ struct Shared {
   uint16_t owners[SEGS * THREADS];   // the (part, thread) pairs whose maximum reaches the floor
   int listed, owned, failed;
 };
-constexpr int SMEM = RING + static_cast<int>(sizeof(Shared)) + 16;
+constexpr int smem_bytes(int stages) { return ring_bytes(stages) + static_cast<int>(sizeof(Shared)) + 16; }
+static_assert(smem_bytes(WIDE) + 1024 <= 233472 / CTAS && smem_bytes(DEEP) + 1024 <= 233472 / 2, "shared memory");
 
 __device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
@@ -185,8 +213,9 @@ __device__ __forceinline__ void pick16(const uint64_t *keys, int n, uint64_t *be
 // share through a ring of bulk copies of its own and meets nobody until the
 // share is done.
 //   Sums: d = (x - m) c and e = 2^d per logit, two logits per instruction
-//   where the instruction set has it (subtract, scale, both sums).
-//   Rank: counted only in vectors whose maximum reaches the token's logit.
+//   where the instruction set has it (subtract, scale, both sums; the maxima
+//   of bf16 logits too: 86 us without, 80 with it at 1024 rows of 151 936).
+//   Rank: counted only where a stage's maximum reaches the token's logit.
 //   Alternatives: the stream keeps no list.  A thread's running maximum m is
 //   also the maximum of what it saw; 16 threads reach the 16th largest of
 //   these maxima, so the 16 largest logits reach it too, and they all lie
@@ -196,11 +225,11 @@ __device__ __forceinline__ void pick16(const uint64_t *keys, int n, uint64_t *be
 //   votes, atomics and a meeting per stage, took 89 us where this takes 79 at
 //   640 fp32 rows of 151 936.)
 // Each CTA sends its 16 keys and sums to rank 0.
-template <typename T>
+template <typename T, int STAGES>
 __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
   constexpr int N = Vec<T>::N;
   extern __shared__ uint4 ring_all[];
-  Shared &sh = *reinterpret_cast<Shared *>(ring_all + RING / 16);
+  Shared &sh = *reinterpret_cast<Shared *>(ring_all + ring_bytes(STAGES) / 16);
   const int cs = a.cs, row = blockIdx.x / cs, rank = blockIdx.x % cs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint4 *ring = ring_all + warp * STAGES * SV;
@@ -267,20 +296,19 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
     if (!ok) break;
     const int n = min(SV, end - v0 - s * STEP);
     uint4 raw[U];
+    const uint4 *stage = ring + (s % STAGES) * SV + lane;
+    if (n == SV) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      raw[u] = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
-      if (u * 32 + lane < n) raw[u] = ring[(s % STAGES) * SV + u * 32 + lane];
-    }
-    float vmax[U];
+      for (int u = 0; u < U; ++u) raw[u] = stage[u * 32];
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[N];
-      Vec<T>::unpack(raw[u], v);
-      vmax[u] = max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3]));
-      if (N == 8) vmax[u] = max_nan(vmax[u], max_nan(max_nan(v[N - 4], v[N - 3]), max_nan(v[N - 2], v[N - 1])));
-      seg = max_nan(seg, vmax[u]);
+      for (int u = 0; u < U; ++u) {
+        raw[u] = make_uint4(Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE, Vec<T>::NONE);
+        if (u * 32 + lane < n) raw[u] = stage[u * 32];
+      }
     }
+    const float top = Vec<T>::maximum(raw);
+    seg = max_nan(seg, top);
     const float mn = max_nan(m, seg);
     if (--left == 0 || s + 1 == ns) {
       sh.seg[part++][tid] = seg;
@@ -314,18 +342,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
         w2 = fma2(e2, pack2(d0, d1), w2);
       }
     }
-    const int i0 = head + (v0 + s * STEP + lane) * N;
+    if (top >= xt) {   // otherwise nothing to count: the token's own vector reaches its logit
+      const int i0 = head + (v0 + s * STEP + lane) * N;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 32 * N;
-      const float reach = i + N <= id ? xt : xt_up;   // before the token equal logits count too
-      const bool own = static_cast<unsigned>(id - i) < static_cast<unsigned>(N);   // the token's own vector
-      if ((vmax[u] >= reach || own) && u * 32 + lane < n) {
+      for (int u = 0; u < U; ++u) {
+        if (u * 32 + lane >= n) continue;
+        const int i = i0 + u * 32 * N;
+        const float reach = i + N <= id ? xt : xt_up;   // before the token equal logits count too
         float v[N];
         Vec<T>::unpack(raw[u], v);
 #pragma unroll
         for (int k = 0; k < N; ++k) cnt += v[k] >= reach;
-        if (own)
+        if (static_cast<unsigned>(id - i) < static_cast<unsigned>(N))   // the token's own vector
 #pragma unroll
           for (int k = 0; k < N; ++k) cnt += i + k < id && v[k] == xt;
       }
@@ -532,21 +560,24 @@ extern "C" DFLASH_API int dflash_token_logprobs(const void *logits, int dtype, i
   a.top_ids = top_ids;
   a.top_lp = top_logprobs;
   // One CTA per row where the rows fill a quarter of the resident CTAs, more
-  // where they do not (64 fp32 rows of 151 936: 27 us on one CTA each, 21 on 4,
-  // 30 on 16) and where a CTA's share is long against the tail of a wave of
+  // where they do not (64 fp32 rows of 151 936: 28 us on one CTA each, 15 on 4,
+  // 23 on 8) and where a CTA's share is long against the tail of a wave of
   // them (640 such rows: 82 us on one, 79 on 2, 88 on 4).
   int cs = 1;
   while (cs < MAX_CLUSTER && ((4LL * rows * cs < CTAS * dev.sms && static_cast<long long>(cs) * MIN_SHARE < vocab) ||
                               static_cast<long long>(vocab) * size > static_cast<long long>(cs) * MAX_SHARE))
     cs *= 2;
-  auto *kernel = dtype == DFLASH_F32 ? logprobs_kernel<float> : logprobs_kernel<__nv_bfloat16>;
-  static std::atomic<uint64_t> smem_set[2];
-  if (int e = allow_smem(smem_set[dtype == DFLASH_F32], dev, kernel, SMEM)) return e;
+  const bool f32 = dtype == DFLASH_F32, deep = static_cast<long long>(rows) * cs <= 2 * dev.sms;
+  auto *kernel = deep ? (f32 ? logprobs_kernel<float, DEEP> : logprobs_kernel<__nv_bfloat16, DEEP>)
+                      : (f32 ? logprobs_kernel<float, WIDE> : logprobs_kernel<__nv_bfloat16, WIDE>);
+  const int smem = smem_bytes(deep ? DEEP : WIDE);
+  static std::atomic<uint64_t> smem_set[4];
+  if (int e = allow_smem(smem_set[f32 + 2 * deep], dev, kernel, smem)) return e;
   cudaLaunchConfig_t cfg = {};
   a.cs = cs;
   cfg.gridDim = dim3(static_cast<unsigned>(cs) * rows);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
