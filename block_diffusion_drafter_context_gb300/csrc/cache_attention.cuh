@@ -21,7 +21,7 @@ struct Params {
   long long ldq;
   void *out;
   float *lse;
-  const void *k, *v;                       // this layer (fp32 path; the bf16 path goes through tensor maps)
+  const void *k, *v;                       // this layer (read through tensor maps)
   const int32_t *page_table, *cu_new, *ctx_len;
   int max_pages, num_pages;
   int B, nkv, g, total, max_new, window;
