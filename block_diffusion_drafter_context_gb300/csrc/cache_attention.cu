@@ -36,7 +36,8 @@ namespace {
 // + lo with hi rounded to 11 bits and lo the exact rest: hi hi + hi lo + lo hi
 // leaves out lo lo and the bits of lo past 11, each about 2^-24 of a product,
 // so it is good to about fp32's own rounding.  On CUDA cores the same
-// products took three times as long: a value from shared memory served 4 rows.
+// products took two to five times as long (a value from shared memory served 4
+// rows).
 constexpr int ROWS = 16;
 template <typename T, int D>
 struct Shape {
