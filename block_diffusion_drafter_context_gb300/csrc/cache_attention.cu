@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
         c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
         c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-        c.nrow0 = c.nn = c.nh = c.pad = 0;
         ct->chunk[st] = c;
         mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * S::SIZE);
       }

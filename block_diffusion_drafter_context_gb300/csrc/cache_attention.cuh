@@ -112,7 +112,6 @@ struct Chunk {
   int b, h, rt, page;        // request, kv head, row tile, page of the request
   int row0, n, ctx, flags;   // FIRST / LAST of this CTA's part, BAD page, WHOLE: no other CTA has a part
   int cf, cl, slot0, slot;   // contributors cf..cl; whether cf's part is its first; this part's slot
-  int nrow0, nn, nh, pad;    // the tile after this one, where this CTA has a part of it: its rows and kv head (nn 0: none)
 };
 enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 

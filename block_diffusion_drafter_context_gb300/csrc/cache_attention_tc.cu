@@ -5,15 +5,19 @@
 // 32 KB: 0.55 PFLOP/s at HBM speed, past what warp-level MMAs reach, so S = Q
 // K^T and O += P V are tcgen05.mma with M = 128 rows (the tile's, padded), S
 // and O in tensor memory, and Q and P as A operands from tensor memory too:
-// the shared memory then holds nothing but a 6-page K / V^T ring.  One
+// the shared memory then holds nothing but a ring of K / V^T pages.  One
 // persistent CTA per SM with a warp per duty:
-//   warp 0     walks the CTA's run of pages and feeds the ring by TMA;
-//   warp 1     issues S = Q K^T (N = 64, K = 128) into one of three buffers;
-//   warps 2-5  one tensor-memory lane (= query row) per thread: mask, online
-//              softmax in the exp2 domain, P back to tensor memory in bf16;
-//              O is rescaled only when a row's maximum grows by 2^8; the next
-//              tile's query rows are written a tile ahead;
-//   warp 6     issues O += P V (N = 128, K = the page's tokens rounded to 16).
+//   warp 0      walks the CTA's run of pages and feeds the ring by TMA;
+//   warp 1      issues S = Q K^T (N = 64, K = D) into one of the S buffers;
+//   warp 2      issues O += P V (N = D, K = the page's tokens rounded to 16);
+//   warps 4-7   softmax of the run's even pages, warps 8-11 of the odd ones: one
+//               tensor-memory lane (= query row) per thread: mask, online
+//               softmax in the exp2 domain, P in bf16 over the page's S.
+// A page's softmax is longer than its share of HBM's time (0.8 us against 0.4
+// at D = 64), hence two groups.  Each has its own O, maximum and sum; O is
+// rescaled only when a row's maximum grows by 2^8.  The group with a tile's
+// last page joins the two and writes, while the other begins the next tile:
+// it writes that tile's query rows as soon as the last S of this one is there.
 // Row r of a tile is token r / g, query head r % g of the group.
 #include "cache_attention.cuh"
 
@@ -21,29 +25,43 @@ namespace dflash {
 namespace {
 
 constexpr int MROWS = 128;
-constexpr int NSB = 3;                                   // S buffers
-constexpr int NTHR = 224;
-constexpr uint32_t TMEM_COLS = 512, O_COL = 256, P_COL = 384;   // S at 0, 64, 128; P: two buffers of 32 columns
+constexpr int NTHR = 384;
+constexpr uint32_t TMEM_COLS = 512;
+// Tensor memory: S buffers of 64 columns (P takes the first half of each), Q,
+// two O of D columns: 512 columns at D = 128.
 template <int D>
 struct Shape {
   static constexpr int KB = PAGE * D * 2, STAGE = 2 * KB;       // K page as halves of [64][64], then V^T [D][64]
   static constexpr int ST = D == 128 ? 6 : 12;                  // ring depth
-  static constexpr int SMEM = 1024 + ST * STAGE + 2048;
+  static constexpr int NSB = D == 128 ? 3 : 4;                  // S buffers
+  static constexpr uint32_t Q_COL = NSB * PAGE, O_COL = D == 128 ? 256 : 384;   // O of group w at O_COL + w D
+  static constexpr int SMEM = 1024 + ST * STAGE + 4096;
   static constexpr int PART = MROWS * (D + 2);
+  static_assert(Q_COL + D / 2 <= O_COL && O_COL + 2 * D <= TMEM_COLS, "tensor memory");
 };
-constexpr int MAX_ST = 12;
-__device__ __forceinline__ uint32_t q_col(int buf) { return buf ? 448u : 192u; }   // Q: D / 2 columns each
+constexpr int MAX_ST = 12, MAX_SB = 4;
 
+// What the other warps need to know of a page, written by the producer beside
+// the page's data.  The tile's part in this CTA's run is pages i0 .. i1 of it.
+struct Page {
+  int b, h, page, row0, n, ctx;
+  int flags;                 // BAD page, WHOLE: no other CTA has a part of the tile
+  int cf, cl, slot0, slot;   // as in Chunk
+  int i0, i1, pad;
+};
 struct __align__(16) Ctrl {
-  uint64_t full[MAX_ST], empty[MAX_ST], sfull[NSB], sempty[NSB], pfull[2], pdone[2], qfull[2], oempty, cons, drain;
+  uint64_t full[MAX_ST], empty[MAX_ST];    // a page's data; its last reader (the PV) is done
+  uint64_t sfull[MAX_SB], pfull[MAX_SB], pdone[MAX_SB];   // S written; P written; PV done, the buffer is free
+  uint64_t qfull, oempty[2], ml[2], cons[2], drain;       // [2]: of a softmax group
   long long lo;
   Runs runs;
   int n_mine, b, h, k;                                   // the run's first page: k of (b, h)
   uint32_t tmem;
-  int abort_flag, merge;
-  Chunk chunk[MAX_ST];
+  int abort_flag, merge[2];
+  float2 helper[2][MROWS];                 // (maximum, sum) of the group without the tile's last page
+  Page page[MAX_ST];
 };
-static_assert(sizeof(Ctrl) <= 2048, "shared memory");
+static_assert(sizeof(Ctrl) <= 4096, "shared memory");
 
 // CL: few (request, kv head)s over short capacities: one cluster of p.cs CTAs
 // per tile, joined in distributed shared memory.
@@ -51,7 +69,7 @@ template <int D, bool CL>
 __global__ void __launch_bounds__(NTHR, 1)
     verify_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using S = Shape<D>;
-  constexpr int ST = S::ST, KB = S::KB, STAGE = S::STAGE;
+  constexpr int ST = S::ST, KB = S::KB, STAGE = S::STAGE, NSB = S::NSB;
   static_assert(S::SMEM <= 232448, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -67,15 +85,15 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&ct->sfull[i], 1);
-      mbar_init(&ct->sempty[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&ct->pfull[i], 4);
       mbar_init(&ct->pdone[i], 1);
-      mbar_init(&ct->qfull[i], 4);
     }
-    mbar_init(&ct->oempty, 4);
-    mbar_init(&ct->cons, 4);
+    mbar_init(&ct->qfull, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ct->oempty[i], 4);
+      mbar_init(&ct->ml[i], 4);
+      mbar_init(&ct->cons[i], 4);
+    }
     mbar_init(&ct->drain, 2);   // both MMA issuers
     ct->abort_flag = 0;
     fence_mbar_init();
@@ -88,19 +106,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ct->tmem;
-  if (warp >= 2 && warp <= 5) {
-    // P and Q rows that no lane writes enter the products too: zeros
-    const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    const uint32_t lz = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-#pragma unroll
-    for (int c = 0; c < 64; c += 16) {
-      tmem_st16_nw(lz + P_COL + c, z);
-      tmem_st16_nw(lz + q_col(0) + c, z);
-      tmem_st16_nw(lz + q_col(1) + c, z);
-    }
-    tmem_wait_st();
-    tc_fence_before();
-  }
   pdl_start();
   if (CL) {
     if (threadIdx.x == 0) {
@@ -156,28 +161,20 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (n > 0) {
       const uint64_t pol = policy_evict_first();
       const Runs runs = ct->runs;
-      int cf = 0, cl = 0;
+      int cf = 0, cl = 0, i0 = 0, i1 = 0;
       int b = ct->b, h = ct->h, k = ct->k, issued = 0;
       long long x = ct->lo;
-      Req r = request(p, b, false), nr = r;   // this tile's request, and the next tile's
-      int nb = b, nh = h;
+      Req r = request(p, b, false);
       bool ok = true, fresh = true;
       for (int i = 0; i < n; ++i, ++x) {
         const int st = i % ST;
-        if (fresh) {   // the tile after this one, if the run reaches it
-          nb = b, nh = h + 1, nr = r;
-          if (CL || n - i <= r.np - k) {
-            nr.n = 0;
-          } else if (nh == p.nkv) {
-            nh = 0;
-            do nr = request(p, ++nb, false);
-            while (nr.np == 0 && nb + 1 < p.B);
-          }
+        if (fresh) {
+          i0 = i;
+          i1 = CL ? n - 1 : min(n - 1, i + r.np - 1 - k);
         }
         ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
         ok = !__any_sync(0xffffffffu, !ok);
         if (!ok) break;
-        const bool last = i == n - 1 || k == r.np - 1;
         const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
         const bool bad = page < 0 || page >= p.num_pages;
         if (lane == 0) {
@@ -186,13 +183,12 @@ __global__ void __launch_bounds__(NTHR, 1)
             cf = runs.owner(x - k);
             cl = runs.owner(x - k + r.np - 1);
           }
-          Chunk c;
-          c.b = b, c.h = h, c.rt = 0, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
-          c.cf = cf, c.cl = cl;
-          c.flags = (fresh ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && c.cf == c.cl ? WHOLE : 0);
-          c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
-          c.nrow0 = nr.row0, c.nn = nr.n, c.nh = nh, c.pad = 0;
-          ct->chunk[st] = c;
+          Page c;
+          c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
+          c.flags = (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
+          c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
+          c.i0 = i0, c.i1 = i1, c.pad = 0;
+          ct->page[st] = c;
           mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
           if (!bad) {
             uint8_t *dk = ring + st * STAGE;
@@ -206,10 +202,14 @@ __global__ void __launch_bounds__(NTHR, 1)
         __syncwarp();
         issued = i + 1;
         fresh = false;
-        if (++k == r.np) {
+        if (++k == r.np && !CL) {
           k = 0;
-          b = nb, h = nh, r = nr;
           fresh = true;
+          if (++h == p.nkv && i + 1 < n) {
+            h = 0;
+            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+            while (r.np == 0 && b + 1 < p.B);
+          }
         }
       }
       if (!ok && lane == 0) {
@@ -224,22 +224,20 @@ __global__ void __launch_bounds__(NTHR, 1)
     // ------------------------------------------------------------ QK issuer
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(MROWS, PAGE);
-      int seg = -1;
+      int seg = 0;
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         const int st = i % ST, sb = i % NSB;
         ok = mbar_wait(&ct->full[st], static_cast<uint32_t>((i / ST) & 1), abort_flag, WAIT_NS);
         if (!ok) break;
-        const int flags = ct->chunk[st].flags;
-        if (flags & FIRST) {
-          ++seg;
-          ok = mbar_wait(&ct->qfull[seg & 1], static_cast<uint32_t>((seg >> 1) & 1), abort_flag, WAIT_NS);
-        }
-        ok = ok && mbar_wait(&ct->sempty[sb], static_cast<uint32_t>(((i / NSB) & 1) ^ 1), abort_flag, WAIT_NS);
+        const Page &c = ct->page[st];
+        const bool bad = c.flags & BAD;
+        if (i == c.i0) ok = mbar_wait(&ct->qfull, static_cast<uint32_t>(seg++ & 1), abort_flag, WAIT_NS);
+        ok = ok && mbar_wait(&ct->pdone[sb], static_cast<uint32_t>(((i / NSB) & 1) ^ 1), abort_flag, WAIT_NS);
         if (!ok) break;
         tc_fence_after();
-        if (!(flags & BAD)) {
-          const uint32_t k0 = smem_u32(ring + st * STAGE), qa = tmem + q_col(seg & 1);
+        if (!bad) {
+          const uint32_t k0 = smem_u32(ring + st * STAGE), qa = tmem + S::Q_COL;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)   // 16 dims = 8 columns of Q per k-step
             umma_bf16_ts(tmem + sb * PAGE, qa + static_cast<uint32_t>(kk * 8),
@@ -254,34 +252,34 @@ __global__ void __launch_bounds__(NTHR, 1)
       umma_commit(&ct->drain);   // every issued MMA retires before TMEM is released
       mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
     }
-  } else if (warp == 6) {
+  } else if (warp == 2) {
     // ------------------------------------------------------------ PV issuer
     if (lane == 0 && n > 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(MROWS, D);
-      int seg = -1;
-      bool ok = true, started = false;   // started: O holds something of this tile
+      int uses[2] = {0, 0};              // tiles in which an O had a part
+      bool ok = true, started[2] = {false, false};   // O holds something of this tile
       for (int i = 0; i < n && ok; ++i) {
-        const int st = i % ST, pb = i & 1;
+        const int st = i % ST, sb = i % NSB, w = i & 1;
         ok = mbar_wait(&ct->full[st], static_cast<uint32_t>((i / ST) & 1), abort_flag, WAIT_NS) &&
-             mbar_wait(&ct->pfull[pb], static_cast<uint32_t>((i >> 1) & 1), abort_flag, WAIT_NS);
+             mbar_wait(&ct->pfull[sb], static_cast<uint32_t>((i / NSB) & 1), abort_flag, WAIT_NS);
         if (!ok) break;
-        const Chunk &c = ct->chunk[st];
-        if (c.flags & FIRST) {
-          started = false;
-          if (++seg > 0) ok = mbar_wait(&ct->oempty, static_cast<uint32_t>((seg - 1) & 1), abort_flag, WAIT_NS);
+        const Page &c = ct->page[st];
+        if (i <= c.i0 + 1) {   // the O's first page of this tile
+          started[w] = false;
+          if (uses[w]++ > 0) ok = mbar_wait(&ct->oempty[w], static_cast<uint32_t>(uses[w] & 1), abort_flag, WAIT_NS);
           if (!ok) break;
         }
         tc_fence_after();
         // only the 16-token steps that hold tokens of the request
         const int left = c.ctx + c.n - c.page * PAGE, steps = (c.flags & BAD) ? 0 : (min(left, PAGE) + 15) / 16;
-        const uint32_t pt = tmem + P_COL + static_cast<uint32_t>(pb * 32), v0 = smem_u32(ring + st * STAGE + KB);
+        const uint32_t pt = tmem + static_cast<uint32_t>(sb * PAGE), v0 = smem_u32(ring + st * STAGE + KB);
 #pragma unroll
         for (int kk = 0; kk < PAGE / 16; ++kk)
           if (kk < steps)
-            umma_bf16_ts(tmem + O_COL, pt + static_cast<uint32_t>(kk * 8), sdesc_k_sw128(v0 + kk * 32), idesc,
-                         (kk > 0 || started) ? 1u : 0u);
-        started = started || steps > 0;
-        umma_commit(&ct->pdone[pb]);
+            umma_bf16_ts(tmem + S::O_COL + w * D, pt + static_cast<uint32_t>(kk * 8), sdesc_k_sw128(v0 + kk * 32), idesc,
+                         (kk > 0 || started[w]) ? 1u : 0u);
+        started[w] = started[w] || steps > 0;
+        umma_commit(&ct->pdone[sb]);
         umma_commit(&ct->empty[st]);   // PV is the last reader of the stage
       }
       if (!ok) {
@@ -291,63 +289,62 @@ __global__ void __launch_bounds__(NTHR, 1)
       umma_commit(&ct->drain);
       mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
     }
-  } else if (n > 0) {
+  } else if (warp >= 4 && n > 0) {
     // ------------------------------------------------------------ softmax
-    // (all four warps, with query rows or not: the joins want the threads)
-    const int quad = warp & 3, row = quad * 32 + lane, tid = row;   // TMEM lane = query row
+    // (all four warps of a group, with query rows or not: the joins want the threads)
+    const int wg = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane, tid = row;   // TMEM lane = query row
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t my_o = lane_base + S::O_COL + wg * D, its_o = lane_base + S::O_COL + (wg ^ 1) * D;
     const int tok = row / g, head = row % g;
     uint32_t cphase = 0;
-    int seg = -1;
+    int uses = 0, helped = 0;       // tiles this group had a part in; those of them it closed with the other's help
     bool ok = true;
-    float m = -INFINITY, l = 0.f;   // maximum (scaled, log2) and sum of this row
+    float m = -INFINITY, l = 0.f;   // maximum (scaled, log2) and sum of this row over the group's pages of the tile
     auto waitw = [&](uint64_t *bar, uint32_t par) -> bool {   // warp-uniform bounded wait
       const bool done = mbar_wait(bar, par, abort_flag, WAIT_NS);
       return !__any_sync(0xffffffffu, !done);
     };
-    auto csync = [&]() -> bool {   // the softmax warps meet
+    auto csync = [&]() -> bool {   // the group's warps meet
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ct->cons);
-      const bool done = waitw(&ct->cons, cphase & 1);
+      if (lane == 0) mbar_arrive(&ct->cons[wg]);
+      const bool done = waitw(&ct->cons[wg], cphase & 1);
       ++cphase;
       return done;
     };
-    // this lane's query row of a tile into Q buffer qb: column c holds dims 2c and 2c + 1
-    auto write_q = [&](int row0, int nn, int h, int qb) {
-      const bool live = tok < nn;
-      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                         static_cast<size_t>(row0 + (live ? tok : 0)) * p.ldq +
-                                                         static_cast<size_t>(h * g + head) * D);
-      uint4 u[D / 8];
-#pragma unroll
-      for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int c4 = 0; c4 < D / 32; ++c4) {
-        uint32_t w[16];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          w[4 * t] = u[4 * c4 + t].x;
-          w[4 * t + 1] = u[4 * c4 + t].y;
-          w[4 * t + 2] = u[4 * c4 + t].z;
-          w[4 * t + 3] = u[4 * c4 + t].w;
-        }
-        tmem_st16_nw(lane_base + q_col(qb) + static_cast<uint32_t>(16 * c4), w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ct->qfull[qb]);
-    };
-    for (int i = 0; i < n && ok; ++i) {
+    for (int i = wg; i < n && ok; i += 2) {
       const int st = i % ST, sb = i % NSB;
       if (!(ok = waitw(&ct->full[st], static_cast<uint32_t>((i / ST) & 1)))) break;
-      const Chunk c = ct->chunk[st];
-      const bool first = c.flags & FIRST, last = c.flags & LAST;
-      if (first) {
-        ++seg;
-        if (i == 0) write_q(c.row0, c.n, c.h, 0);   // the others were written a tile ahead
-        m = -INFINITY;
-        l = 0.f;
+      const Page &c = ct->page[st];   // stays until this page's PV, which waits for this group
+      const bool first = i <= c.i0 + 1;
+      if (first) ++uses;
+      if (i == c.i0) {
+        // the tile's query rows, this lane's: column c holds dims 2c and 2c +
+        // 1.  Q is free once the last S of the tile before is complete.
+        const bool live = tok < c.n;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                           static_cast<size_t>(c.row0 + (live ? tok : 0)) * p.ldq +
+                                                           static_cast<size_t>(c.h * g + head) * D);
+        uint4 u[D / 8];
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
+        if (i > 0 && !(ok = waitw(&ct->sfull[(i - 1) % NSB], static_cast<uint32_t>(((i - 1) / NSB) & 1)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+          uint32_t w[16];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            w[4 * t] = u[4 * c4 + t].x;
+            w[4 * t + 1] = u[4 * c4 + t].y;
+            w[4 * t + 2] = u[4 * c4 + t].z;
+            w[4 * t + 3] = u[4 * c4 + t].w;
+          }
+          tmem_st16_nw(lane_base + S::Q_COL + static_cast<uint32_t>(16 * c4), w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct->qfull);
       }
       if (!(ok = waitw(&ct->sfull[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;
       tc_fence_after();
@@ -364,15 +361,13 @@ __global__ void __launch_bounds__(NTHR, 1)
           for (int e = 0; e < 16; ++e) x[16 * t + e] = __uint_as_float(r[t][e]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ct->sempty[sb]);
       // positions this row does not see (whatever their slots hold)
       const int t0 = c.page * PAGE, newest = c.ctx + c.n - 1;
-      const bool edge = (c.flags & BAD) || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+      const bool bad = c.flags & BAD;
+      const bool edge = bad || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
       if (edge) {
         const int top = c.ctx + min(c.n - 1, tok);
-        const int hi = (c.flags & BAD) ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
+        const int hi = bad ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
 #pragma unroll
         for (int e = 0; e < PAGE; ++e)
           if (e > hi || e < lo) x[e] = -INFINITY;
@@ -391,28 +386,28 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (first) {
         m = mx;
+        l = 0.f;
       } else {
         const bool need = mx > m + RESCALE_LOG2;
-        if (__any_sync(0xffffffffu, need)) {   // O holds pages up to i - 1: wait for that PV, rescale in TMEM
-          if (!(ok = waitw(&ct->pdone[(i - 1) & 1], static_cast<uint32_t>(((i - 1) >> 1) & 1)))) break;
+        if (__any_sync(0xffffffffu, need)) {   // O holds the group's pages up to i - 2: wait for that PV, rescale in TMEM
+          if (!(ok = waitw(&ct->pdone[(i - 2) % NSB], static_cast<uint32_t>(((i - 2) / NSB) & 1)))) break;
           tc_fence_after();
           const float f = need ? fast_exp2(m - mx) : 1.f;
 #pragma unroll
-          for (int c0 = 0; c0 < D / 16; c0 += 4) {
-            uint32_t ov[4][16];
+          for (int c0 = 0; c0 < D / 16; c0 += 2) {
+            uint32_t ov[2][16];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) tmem_ld16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+            for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, ov[u]);
             tmem_wait_ld();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 2; ++u) {
               tmem_regs_ready(ov[u]);
 #pragma unroll
               for (int e = 0; e < 16; ++e) ov[u][e] = __float_as_uint(__uint_as_float(ov[u][e]) * f);
-              tmem_st16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+              tmem_st16_nw(my_o + (c0 + u) * 16, ov[u]);
             }
           }
           tmem_wait_st();
-          tc_fence_before();
           if (need) {
             l *= f;
             m = mx;
@@ -433,60 +428,82 @@ __global__ void __launch_bounds__(NTHR, 1)
         s3 += x[e + 3];
       }
       l += (s0 + s1) + (s2 + s3);
-      // P buffer i & 1 was last read by the PV of page i - 2
-      if (i >= 2 && !(ok = waitw(&ct->pdone[i & 1], static_cast<uint32_t>(((i - 2) >> 1) & 1)))) break;
-      tc_fence_after();
-      {
+      {   // P over this page's S
         uint32_t w0[16], w1[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           w0[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
           w1[j] = pack_bf16(x[32 + 2 * j], x[32 + 2 * j + 1]);
         }
-        const uint32_t pcol = lane_base + P_COL + static_cast<uint32_t>((i & 1) * 32);
-        tmem_st16_nw(pcol, w0);
-        tmem_st16_nw(pcol + 16, w1);
+        tmem_st16_nw(lane_base + sb * PAGE, w0);
+        tmem_st16_nw(lane_base + sb * PAGE + 16, w1);
         tmem_wait_st();
       }
       // slots past the newest token may hold anything: in the 16-token step
       // that the PV reads with them, V becomes 0
       const int held = newest - t0 + 1;
-      if (held < PAGE && (held & 15) && !(c.flags & BAD)) {
+      if (held < PAGE && (held & 15) && !bad) {
         uint8_t *v = ring + st * STAGE + KB;
         for (int dr = tid; dr < D; dr += 4 * 32)
           for (int e = held; e & 15; ++e)
             *reinterpret_cast<uint16_t *>(v + dr * 128 + (((e >> 3) ^ (dr & 7)) << 4) + (e & 7) * 2) = 0;
         fence_proxy_async_smem();
       }
+      const Page last = c;   // the stage may go once P is handed over
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ct->pfull[i & 1]);
-      // the next tile's query rows into the other buffer: it held the previous
-      // tile's, whose products all completed before this warp read their scores
-      if (first && c.nn > 0) write_q(c.nrow0, c.nn, c.nh, (seg + 1) & 1);
-      if (!last) continue;
+      if (lane == 0) mbar_arrive(&ct->pfull[sb]);
+      if (i + 1 < last.i1) continue;
+      if (i + 1 == last.i1) {
+        // the other group closes the tile: this one's maxima and sums for it,
+        // once it has read those of the tile before
+        if (uses > 1 && !(ok = waitw(&ct->oempty[wg], static_cast<uint32_t>(uses & 1)))) break;
+        ct->helper[wg][row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct->ml[wg]);
+        continue;
+      }
 
-      // ---- the end of this CTA's part of the tile
-      if (!(ok = waitw(&ct->pdone[i & 1], static_cast<uint32_t>((i >> 1) & 1)))) break;
+      // ---- the end of this CTA's part of the tile, i == i1
+      const bool two = last.i1 > last.i0;   // the other group has a part
+      float2 its = make_float2(-INFINITY, 0.f);
+      if (two) {
+        if (!(ok = waitw(&ct->ml[wg ^ 1], static_cast<uint32_t>(helped++ & 1)))) break;
+        its = ct->helper[wg ^ 1][row];
+      }
+      if (!(ok = waitw(&ct->pdone[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;   // and with it every PV before
       tc_fence_after();
-      const bool whole = c.flags & WHOLE, live = tok < c.n;
+      m = join_max(m, l);
+      its.x = join_max(its.x, its.y);
+      const float M = fmaxf(m, its.x);
+      const float f0 = l == 0.f ? 0.f : fast_exp2(m - M), f1 = its.y == 0.f ? 0.f : fast_exp2(its.x - M);
+      const float L = f0 * l + f1 * its.y;
+      const bool whole = last.flags & WHOLE, live = tok < last.n;
       float *xo = reinterpret_cast<float *>(ring);   // CL: this CTA's share, in the ring, idle now
-      const int rows = c.n * g;
-      const size_t at = static_cast<size_t>(c.row0 + (live ? tok : 0)) * (p.nkv * g) + c.h * g + head;
-      float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + c.slot) * S::PART;
-      const float inv = 1.f / l;
+      const int rows = last.n * g;
+      const size_t at = static_cast<size_t>(last.row0 + (live ? tok : 0)) * (p.nkv * g) + last.h * g + head;
+      float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-      for (int c0 = 0; c0 < D / 16; c0 += 4) {
-        uint32_t ov[4][16];
+      for (int c0 = 0; c0 < D / 16; c0 += 2) {
+        uint32_t a[2][16], b[2][16];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) tmem_ld16_nw(lane_base + O_COL + (c0 + u) * 16, ov[u]);
+        for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
+        if (two)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) tmem_ld16_nw(its_o + (c0 + u) * 16, b[u]);
         tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          tmem_regs_ready(ov[u]);
+        for (int u = 0; u < 2; ++u) {
+          tmem_regs_ready(a[u]);
           float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(ov[u][e]);   // l 0: O was never written
+          for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : f0 * __uint_as_float(a[u][e]);   // sum 0: O was never written
+          if (two) {
+            tmem_regs_ready(b[u]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = its.y == 0.f ? v[e] : fmaf(f1, __uint_as_float(b[u][e]), v[e]);
+          }
           if (!live) continue;
           if (CL) {   // float4s XORed by the row: no bank conflicts
 #pragma unroll
@@ -496,7 +513,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           } else if (whole) {
             uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = l == 0.f ? 0u : pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + (c0 + u) * 16);
             dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -509,31 +526,35 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       tc_fence_before();
       if (CL) {
-        if (live) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * row) = make_float2(join_max(m, l), l);
+        if (live) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * row) = make_float2(M, L);
         break;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ct->oempty);   // the next tile may overwrite O
+      if (lane == 0) {   // the next tiles may overwrite the O
+        mbar_arrive(&ct->oempty[wg]);
+        if (two) mbar_arrive(&ct->oempty[wg ^ 1]);
+      }
       if (whole) {
-        if (live && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2_F;
+        if (live && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2_F;
         continue;
       }
       if (live) {
-        __stcg(part + MROWS * D + row, join_max(m, l));
-        __stcg(part + MROWS * D + MROWS + row, l);
+        __stcg(part + MROWS * D + row, M);
+        __stcg(part + MROWS * D + MROWS + row, L);
       }
       __threadfence();
       if (!(ok = csync())) break;
       if (tid == 0) {
-        int *ctr = p.counters + static_cast<size_t>(c.b) * p.nkv + c.h;
-        const int old = atomicAdd(ctr, 1), done = old == c.cl - c.cf;
+        int *ctr = p.counters + static_cast<size_t>(last.b) * p.nkv + last.h;
+        const int old = atomicAdd(ctr, 1), done = old == last.cl - last.cf;
         if (done) atomicExch(ctr, 0);
         __threadfence();
-        ct->merge = done;
+        ct->merge[wg] = done;
       }
       if (!(ok = csync())) break;
-      if (ct->merge)
-        join_parts<__nv_bfloat16, D>(dest_of(p, c.row0, c.h), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, MROWS, rows, tid, 4 * 32);
+      if (ct->merge[wg])
+        join_parts<__nv_bfloat16, D>(dest_of(p, last.row0, last.h), p.partials, last.cf, last.cl - last.cf + 1, last.slot0,
+                                     S::PART, MROWS, rows, tid, 4 * 32);
     }
     if (!ok) {
       report(p.status, DFLASH_ERR_TIMEOUT);
