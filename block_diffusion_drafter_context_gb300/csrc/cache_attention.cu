@@ -24,7 +24,7 @@ namespace {
 // fraction of the HBM time whichever way it is issued, and register
 // accumulators keep a page's path short.  (Two tiles of 16 rows per warp,
 // tried for 17..32 bf16 rows, left one CTA per SM at 255 registers: 149 us
-// against 103 of the tcgen05 form for 5 tokens x 4 heads at 128k.)
+// against 96 of the tcgen05 form for 5 tokens x 4 heads at 128k.)
 //
 // Warp 0 produces: the K page as 128-byte-wide swizzled column blocks, the V^T
 // page (fp32: as two blocks of 32 slots), and for a new tile its query rows,

@@ -13,8 +13,9 @@
 //   warps 4-7   softmax of the run's even pages, warps 8-11 of the odd ones: one
 //               tensor-memory lane (= query row) per thread: mask, online
 //               softmax in the exp2 domain, P in bf16 over the page's S.
-// A page's softmax is longer than its share of HBM's time (0.8 us against 0.4
-// at D = 64), hence two groups.  Each has its own O, maximum and sum; O is
+// A page's softmax alone is as long as its share of HBM's time at D = 128 and
+// twice as long at D = 64, hence two groups (64 requests x 16 tokens x 5 heads
+// at 16k..32k: 1021 us with one, 940 with two, the copy rate).  Each has its own O, maximum and sum; O is
 // rescaled only when a row's maximum grows by 2^8.  The group with a tile's
 // last page joins the two and writes, while the other begins the next tile:
 // it writes that tile's query rows as soon as the last S of this one is there.
@@ -348,105 +349,117 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (!(ok = waitw(&ct->sfull[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;
       tc_fence_after();
-      float x[PAGE];
-      {
-        uint32_t r[4][16];   // the four loads in flight together
-#pragma unroll
-        for (int t = 0; t < 4; ++t) tmem_ld16_nw(lane_base + sb * PAGE + 16 * t, r[t]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          tmem_regs_ready(r[t]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[16 * t + e] = __uint_as_float(r[t][e]);
-        }
-      }
-      // positions this row does not see (whatever their slots hold)
       const int t0 = c.page * PAGE, newest = c.ctx + c.n - 1;
       const bool bad = c.flags & BAD;
-      const bool edge = bad || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
-      if (edge) {
-        const int top = c.ctx + min(c.n - 1, tok);
-        const int hi = bad ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
+      // In a cluster a warp without query rows leaves its lanes of P as they
+      // are: they only reach their own rows of O (8 requests of 900..1000
+      // positions, 32 rows: 17 us, 18 without; in runs of many short tiles it
+      // was 4 % slower).
+      if (!CL || quad * 32 < c.n * g) {
+        float x[PAGE];
+        {
+          uint32_t r[4][16];   // the four loads in flight together
 #pragma unroll
-        for (int e = 0; e < PAGE; ++e)
-          if (e > hi || e < lo) x[e] = -INFINITY;
-      }
-      float mx;
-      {
-        float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
+          for (int t = 0; t < 4; ++t) tmem_ld16_nw(lane_base + sb * PAGE + 16 * t, r[t]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int e = 4; e < PAGE; e += 4) {
-          a0 = fmaxf(a0, x[e]);
-          a1 = fmaxf(a1, x[e + 1]);
-          a2 = fmaxf(a2, x[e + 2]);
-          a3 = fmaxf(a3, x[e + 3]);
+          for (int t = 0; t < 4; ++t) {
+            tmem_regs_ready(r[t]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[16 * t + e] = __uint_as_float(r[t][e]);
+          }
         }
-        mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.scale_log2;
-      }
-      if (first) {
-        m = mx;
-        l = 0.f;
-      } else {
-        const bool need = mx > m + RESCALE_LOG2;
-        if (__any_sync(0xffffffffu, need)) {   // O holds the group's pages up to i - 2: wait for that PV, rescale in TMEM
-          if (!(ok = waitw(&ct->pdone[(i - 2) % NSB], static_cast<uint32_t>(((i - 2) / NSB) & 1)))) break;
-          tc_fence_after();
-          const float f = need ? fast_exp2(m - mx) : 1.f;
+        // positions this row does not see (whatever their slots hold)
+        const bool edge = bad || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+        if (edge) {
+          const int top = c.ctx + min(c.n - 1, tok);
+          const int hi = bad ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
 #pragma unroll
-          for (int c0 = 0; c0 < D / 16; c0 += 2) {
-            uint32_t ov[2][16];
+          for (int e = 0; e < PAGE; ++e)
+            if (e > hi || e < lo) x[e] = -INFINITY;
+        }
+        float mx;
+        {
+          float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, ov[u]);
-            tmem_wait_ld();
+          for (int e = 4; e < PAGE; e += 4) {
+            a0 = fmaxf(a0, x[e]);
+            a1 = fmaxf(a1, x[e + 1]);
+            a2 = fmaxf(a2, x[e + 2]);
+            a3 = fmaxf(a3, x[e + 3]);
+          }
+          mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.scale_log2;
+        }
+        if (first) {
+          m = mx;
+          l = 0.f;
+        } else {
+          const bool need = mx > m + RESCALE_LOG2;
+          if (__any_sync(0xffffffffu, need)) {   // O holds the group's pages up to i - 2: wait for that PV, rescale in TMEM
+            if (!(ok = waitw(&ct->pdone[(i - 2) % NSB], static_cast<uint32_t>(((i - 2) / NSB) & 1)))) break;
+            tc_fence_after();
+            const float f = need ? fast_exp2(m - mx) : 1.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              tmem_regs_ready(ov[u]);
+            for (int c0 = 0; c0 < D / 16; c0 += 2) {
+              uint32_t ov[2][16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) ov[u][e] = __float_as_uint(__uint_as_float(ov[u][e]) * f);
-              tmem_st16_nw(my_o + (c0 + u) * 16, ov[u]);
+              for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, ov[u]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                tmem_regs_ready(ov[u]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[u][e] = __float_as_uint(__uint_as_float(ov[u][e]) * f);
+                tmem_st16_nw(my_o + (c0 + u) * 16, ov[u]);
+              }
+            }
+            tmem_wait_st();
+            if (need) {
+              l *= f;
+              m = mx;
             }
           }
-          tmem_wait_st();
-          if (need) {
-            l *= f;
-            m = mx;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m;
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int e = 0; e < PAGE; e += 4) {
+          x[e] = fast_exp2(fmaf(x[e], p.scale_log2, nm));
+          x[e + 1] = fast_exp2(fmaf(x[e + 1], p.scale_log2, nm));
+          x[e + 2] = fast_exp2(fmaf(x[e + 2], p.scale_log2, nm));
+          x[e + 3] = fast_exp2(fmaf(x[e + 3], p.scale_log2, nm));
+          s0 += x[e];
+          s1 += x[e + 1];
+          s2 += x[e + 2];
+          s3 += x[e + 3];
+        }
+        l += (s0 + s1) + (s2 + s3);
+        {   // P over this page's S
+          uint32_t w0[16], w1[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            w0[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+            w1[j] = pack_bf16(x[32 + 2 * j], x[32 + 2 * j + 1]);
           }
+          tmem_st16_nw(lane_base + sb * PAGE, w0);
+          tmem_st16_nw(lane_base + sb * PAGE + 16, w1);
+          tmem_wait_st();
         }
-      }
-      const float nm = m == -INFINITY ? 0.f : -m;
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-      for (int e = 0; e < PAGE; e += 4) {
-        x[e] = fast_exp2(fmaf(x[e], p.scale_log2, nm));
-        x[e + 1] = fast_exp2(fmaf(x[e + 1], p.scale_log2, nm));
-        x[e + 2] = fast_exp2(fmaf(x[e + 2], p.scale_log2, nm));
-        x[e + 3] = fast_exp2(fmaf(x[e + 3], p.scale_log2, nm));
-        s0 += x[e];
-        s1 += x[e + 1];
-        s2 += x[e + 2];
-        s3 += x[e + 3];
-      }
-      l += (s0 + s1) + (s2 + s3);
-      {   // P over this page's S
-        uint32_t w0[16], w1[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          w0[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-          w1[j] = pack_bf16(x[32 + 2 * j], x[32 + 2 * j + 1]);
-        }
-        tmem_st16_nw(lane_base + sb * PAGE, w0);
-        tmem_st16_nw(lane_base + sb * PAGE + 16, w1);
-        tmem_wait_st();
       }
       // slots past the newest token may hold anything: in the 16-token step
       // that the PV reads with them, V becomes 0
       const int held = newest - t0 + 1;
       if (held < PAGE && (held & 15) && !bad) {
-        uint8_t *v = ring + st * STAGE + KB;
-        for (int dr = tid; dr < D; dr += 4 * 32)
-          for (int e = held; e & 15; ++e)
-            *reinterpret_cast<uint16_t *>(v + dr * 128 + (((e >> 3) ^ (dr & 7)) << 4) + (e & 7) * 2) = 0;
+        const int ch = held >> 3, kept = held & 7;   // the 8-slot chunk with the first such slot
+        for (int dr = tid; dr < D; dr += 4 * 32) {
+          uint4 *v = reinterpret_cast<uint4 *>(ring + st * STAGE + KB + dr * 128);
+          uint4 w = v[ch ^ (dr & 7)];
+          uint32_t *e = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] &= 2 * j + 1 < kept ? 0xffffffffu : 2 * j < kept ? 0xffffu : 0u;
+          v[ch ^ (dr & 7)] = w;
+          if (!(ch & 1)) v[(ch + 1) ^ (dr & 7)] = make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();
       }
       const Page last = c;   // the stage may go once P is handed over
