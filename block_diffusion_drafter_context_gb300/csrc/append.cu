@@ -15,7 +15,7 @@
 namespace dflash {
 namespace {
 
-constexpr int TT = 16;        // tokens per CTA
+constexpr int TT = 16;        // tokens per CTA at most
 constexpr int THREADS = 256;
 constexpr int MAX_HPC = 4;    // kv heads per CTA
 
@@ -27,7 +27,7 @@ struct AppendArgs {
   int rotate;
   const int32_t *cu_new, *ctx_len, *page_table;
   int B, total, max_pages, num_pages;
-  int nq, nkv, g, hpc;        // hpc: kv heads (with their q heads) per CTA
+  int nq, nkv, g, hpc, tt;    // kv heads (with their q heads) and tokens per CTA
   void *k, *v, *q_out;
   int *status;
 };
@@ -54,6 +54,15 @@ template <> struct Four<__nv_bfloat16> {
   }
 };
 
+// A kernel parameter's element by its generic address: lanes that read
+// neighbours share one access, where the constant bank takes one per address
+// (walking the table uniformly took 2 us of a CTA).
+__device__ __forceinline__ float param_at(const float *p) {
+  float v;
+  asm volatile("ld.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // The last b < B with cu[b] <= t, for both of a warp's tokens at once.  Up to
 // 256 requests every entry is loaded side by side (one dependent load, where a
 // binary search takes eight); more are searched 32 ways first.
@@ -79,31 +88,42 @@ __device__ __forceinline__ void requests_of(const int32_t *cu, int B, int t0, in
   b1 = base + max(__reduce_add_sync(0xffffffffu, c1) - 1, 0);
 }
 
-// CTA (16 tokens, up to 4 kv heads with their q heads).  A row (one head of
+// CTA (4 to 16 tokens, up to 4 kv heads with their q heads).  A row (one head of
 // one token) is D / 8 lanes; lane l holds values 4l..4l+3 of both halves, so
 // that the rotation's pairs are its own (with 8 consecutive values per lane
 // the exchange and the rotation table made shared memory the bound: 159 us
-// for 23 040 prompt tokens of 32 + 16 heads).  The first rows' loads and the V rows' copies into shared
-// memory do not depend on where the tokens belong, so they are under way
-// while each token's request, page and rotation are looked up (three
-// dependent loads).  The rotation of the tile's tokens is tabulated once and
+// for 23 040 prompt tokens of 32 + 16 heads, where this takes 94).  The first
+// rows' loads and the V rows' copies into shared memory do not depend on where
+// the tokens belong, so they are under way while each token's request, page
+// and rotation are looked up (three dependent loads).  The rotation of the tile's tokens is tabulated once and
 // shared by the heads.  V leaves transposed.
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, const RopeArgs rp) {
+__global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, const __grid_constant__ RopeArgs rp) {
   constexpr int LPR = D / 8, HALF = D / 2, ROWS = THREADS / LPR, V16 = 16 / sizeof(T);
   using F = Four<T>;
   __shared__ __align__(16) float2 cs[TT][HALF];      // pairs 4l + 2q, 4l + 2q + 1 as float4 number q LPR + l
   __shared__ __align__(16) T vt[MAX_HPC][TT][D + V16];
+  __shared__ __align__(16) float gains[2][D];
   __shared__ int s_page[TT], s_pos[TT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * TT, h0 = blockIdx.y * a.hpc, nh = min(a.hpc, a.nkv - h0);
-  const int rows = min(TT, a.total - t0);              // rows of the buffer; the batch may end before
+  const int t0 = blockIdx.x * a.tt, h0 = blockIdx.y * a.hpc, nh = min(a.hpc, a.nkv - h0);
+  const int rows = min(a.tt, a.total - t0);            // rows of the buffer; the batch may end before
   const int sh = rows > 8 ? 4 : rows > 4 ? 3 : rows > 2 ? 2 : rows > 1 ? 1 : 0;   // a power of two of tokens
   const int nqh = a.q_out ? nh * a.g : 0, items = (nqh + nh) << sh;               // rows (head, token): q heads, then k
   const int slot = threadIdx.x / LPR, l = threadIdx.x % LPR;                      // this thread's row of a pass, its lane in it
   float th_hi[HALF / 32], th_lo[HALF / 32];
-  if (a.rotate) lane_thetas(rp, lane, th_hi, th_lo);
+  if (a.rotate) {
+#pragma unroll
+    for (int i = 0; i < HALF / 32; ++i) {
+      th_hi[i] = param_at(rp.th_hi + lane + 32 * i);
+      th_lo[i] = param_at(rp.th_lo + lane + 32 * i);
+    }
+  }
   pdl_start();
+  if (a.g_q && threadIdx.x < D) {
+    gains[0][threadIdx.x] = a.g_q[threadIdx.x];
+    gains[1][threadIdx.x] = a.g_k[threadIdx.x];
+  }
   const T *src = static_cast<const T *>(a.qkv) + static_cast<size_t>(t0) * a.ld;
   for (int e = threadIdx.x; e < nh * rows * (D / V16); e += THREADS) {
     const int c = (e % (D / V16)) * V16, hj = e / (D / V16), h = hj / rows, j = hj - h * rows;
@@ -127,7 +147,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
   };
   load(slot);
   // ---- where the tokens go: warp w looks up tokens w and w + 8
-  const int end = a.cu_new[a.B], total = min(a.total, end), nt = min(TT, total - t0);
+  const int end = a.cu_new[a.B], total = min(a.total, end), nt = min(a.tt, total - t0);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (end > a.total || end < 0))
     report(a.status, DFLASH_ERR_DEVICE);
   {
@@ -166,24 +186,18 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   if (nt <= 0) return;
-  float gq[8], gk[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = (i >> 2) * HALF + 4 * l + (i & 3);
-    gq[i] = a.g_q ? a.g_q[c] : 1.f;
-    gk[i] = a.g_k ? a.g_k[c] : 1.f;
-  }
   // ---- v heads, transposed into [d][slot] pages.  Consecutive lanes take a
   // d-row's consecutive slots: what costs here is the number of sectors each
   // store instruction touches (lanes along d took 7 times as long)
   {
     const int pg = s_page[0], sl = s_pos[0] % PAGE;
-    const bool packed = nt == TT && pg >= 0 && s_page[TT - 1] == pg && sl % V16 == 0 && s_pos[TT - 1] % PAGE == sl + TT - 1;
+    const bool packed = nt == a.tt && nt >= V16 && pg >= 0 && s_page[nt - 1] == pg && sl % V16 == 0 &&
+                        s_pos[nt - 1] % PAGE == sl + nt - 1;
     T *vc = static_cast<T *>(a.v);
-    if (packed) {   // the tile is 16 slots of one page, on 16-byte boundaries
-      constexpr int GR = TT / V16;
-      for (int e = threadIdx.x; e < nh * D * GR; e += THREADS) {
-        const int grp = e % GR, d = e / GR % D, h = e / (GR * D);
+    if (packed) {   // the tile is consecutive slots of one page, on 16-byte boundaries
+      const int gs = sh - (V16 == 8 ? 3 : 2);   // log2 of a d-row's 16-byte groups
+      for (int e = threadIdx.x; e < nh * D << gs; e += THREADS) {
+        const int grp = e & ((1 << gs) - 1), d = (e >> gs) % D, h = (e >> gs) / D;
         __align__(16) T w[V16];
 #pragma unroll
         for (int i = 0; i < V16; ++i) w[i] = vt[h][grp * V16 + i][d];
@@ -217,7 +231,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float r = rsqrtf(ss / D + a.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= r * (isq ? gq[i] : gk[i]);
+        for (int i = 0; i < 8; i += 4) {
+          const float4 w = *reinterpret_cast<const float4 *>(&gains[isq ? 0 : 1][(i >> 2) * HALF + 4 * l]);
+          x[i] *= r * w.x, x[i + 1] *= r * w.y, x[i + 2] *= r * w.z, x[i + 3] *= r * w.w;
+        }
       }
       const float4 *c4 = reinterpret_cast<const float4 *>(cs[live ? j : 0]);
       const float4 ca = c4[l], cb = c4[LPR + l];
@@ -350,11 +367,15 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
   a.v = static_cast<char *>(kv->v_cache) + off;
   a.q_out = q_out;
   a.status = static_cast<int *>(workspace);
-  const int tiles = (total_new + TT - 1) / TT;
-  // as many kv heads per CTA as leave two CTAs per SM
+  // as many kv heads per CTA as leave two CTAs per SM, then as many tokens as
+  // leave four (64 requests x 16 tokens, 8 kv heads: 10.9 us in 1024 CTAs of 8
+  // tokens, 12.8 in 512 of 16; 64 x 1: 4.1 in tiles of 4 tokens, 6.6 of 16)
+  a.tt = TT;
   a.hpc = MAX_HPC;
-  while (a.hpc > 1 && static_cast<long long>(tiles) * ((nkv + a.hpc - 1) / a.hpc) < 2LL * dev.sms) a.hpc /= 2;
-  const dim3 grid(tiles, (nkv + a.hpc - 1) / a.hpc);
+  auto ctas = [&] { return static_cast<long long>((total_new + a.tt - 1) / a.tt) * ((nkv + a.hpc - 1) / a.hpc); };
+  while (a.hpc > 1 && ctas() < 2LL * dev.sms) a.hpc /= 2;
+  while (a.tt > 4 && ctas() < 4LL * dev.sms) a.tt /= 2;
+  const dim3 grid((total_new + a.tt - 1) / a.tt, (nkv + a.hpc - 1) / a.hpc);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RopeArgs &rp = rope_of(d, a.rotate ? rope_base : 1e6f);
   if (hs->dtype == DFLASH_F32)

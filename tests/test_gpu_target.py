@@ -138,6 +138,36 @@ def test_append_matches_oracle(nq, nkv, d, dtype, norm):
     assert np.array_equal(v1[1], vr, equal_nan=True)          # V is copied
 
 
+@pytest.mark.parametrize("nq,nkv,d,dtype,ctx,new", [
+    (8, 4, 128, "bf16", [0, 64, 8, 5], [1500, 700, 1000, 600]), (16, 8, 64, "bf16", [0, 128, 3], [5000, 4096, 2000]),
+    (4, 4, 64, "f32", [0, 12, 66], [3000, 2500, 900]), (8, 8, 128, "f32", [0, 4], [2048, 8000])])
+def test_append_of_prompts(nq, nkv, d, dtype, ctx, new):
+    """Prompts long enough for every tile of tokens, at slots that are and are
+    not on 16-byte boundaries: all rows against the formula in 64 bits."""
+    import torch
+    c = Batch(nq, nkv, d, dtype, ctx, new, seed=nq + d, stale=0.0, pad_rows=3)
+    before = c.k.clone(), c.v.clone()
+    q = c.ops.append_kv(c.kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    assert c.ops.status() == 0
+    owner = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new)).cuda()
+    pos = c.ctx_d[owner].long() + torch.arange(c.T, device="cuda") - c.cu_d[owner]
+    page, slot = c.kv.page_table[owner, pos // PAGE].long(), pos % PAGE
+    x = c.qkv[:c.T].view(c.T, nq + 2 * nkv, d)
+    assert torch.equal(c.v[1, page, :, :, slot], x[:, nq + nkv:])          # V is copied
+    y = x[:, :nq + nkv].double()
+    y = y / (y.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+    y = y * torch.cat([c.g_q.expand(nq, d), c.g_k.expand(nkv, d)]).double()
+    ang = pos.double()[:, None] * 1e6 ** (-2 * torch.arange(d // 2, device="cuda").double() / d)
+    z = torch.complex(y[..., :d // 2].contiguous(), y[..., d // 2:].contiguous()) * torch.polar(torch.ones_like(ang), ang)[:, None]
+    ref, size = torch.cat([z.real, z.imag], -1), torch.cat([z.abs(), z.abs()], -1)
+    tol = U[dtype] * ref.abs() + (16 * 2.0 ** -24 + 5e-7) * size           # as in test_append_matches_oracle
+    assert ((q[:c.T].double().view(c.T, nq, d) - ref[:, :nq]).abs() <= tol[:, :nq]).all()
+    assert ((c.k[1, page, :, slot].double() - ref[:, nq:]).abs() <= tol[:, nq:]).all()
+    # every other slot, and the other layer, as they were
+    c.k[1, page, :, slot], c.v[1, page, :, :, slot] = before[0][1, page, :, slot], before[1][1, page, :, :, slot]
+    assert torch.equal(c.k, before[0]) and torch.equal(c.v, before[1])
+
+
 def test_append_at_the_far_end_of_the_positions():
     """Positions up to 2^24 - 1 (2^18 pages): the angle keeps its accuracy."""
     import torch
