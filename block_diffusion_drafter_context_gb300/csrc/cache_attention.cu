@@ -526,44 +526,48 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       for (int i = ctid; i >= 0 && i < ROWS; i += 128) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
     __syncwarp();
     cluster_sync();
-    for (int e = rank * 128 + ctid; ctid >= 0 && e < rows * (D / 4); e += p.cs * 128) {
-      const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
-      float M = -INFINITY, L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k0 = 0; k0 < p.cs; k0 += 8) {
-        float2 ml[8];
-        float4 v[8];
+    // Each CTA an equal part, all of a column's shares in flight: left to
+    // the first CTAs, in two rounds, it took 5200 cycles for 4 rows of 16 shares.
+    const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
+    auto join = [&](auto in_flight) {
+      constexpr int N = decltype(in_flight)::value;
+      for (int e = rank * per + ctid; ctid >= 0 && e < end; e += 128) {
+        const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
+        float2 ml[N];
+        float4 v[N];
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {   // the shares' places differ by how many pages a CTA had
-          const int k = min(k0 + u, p.cs - 1);
+        for (int u = 0; u < N; ++u) {   // the shares' places differ by how many pages a CTA had
+          const int k = min(u, p.cs - 1);
           const float *xk = share(share_stage(r.np, k));
           ml[u] = ld_dsmem_f2(dsmem_addr(xk + ROWS * D + 2 * row, k));
           v[u] = ld_dsmem_f4(dsmem_addr(xk + row * D + c4, k));
         }
-        float mn = M;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (k0 + u >= p.cs) ml[u] = make_float2(-INFINITY, 0.f);
-          mn = fmaxf(mn, ml[u].x);
+        for (int u = 0; u < N; ++u) {
+          if (u >= p.cs) ml[u] = make_float2(-INFINITY, 0.f);
+          M = fmaxf(M, ml[u].x);
         }
-        if (mn == -INFINITY) continue;
-        const float f = fast_exp2(M - mn);
-        M = mn;
-        L *= f;
-        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < N; ++u) {
           if (ml[u].y == 0.f) continue;   // a share of nothing was never written
-          const float w = fast_exp2(ml[u].x - mn);
+          const float w = fast_exp2(ml[u].x - M);
           L = fmaf(w, ml[u].y, L);
           acc.x = fmaf(w, v[u].x, acc.x);
           acc.y = fmaf(w, v[u].y, acc.y);
           acc.z = fmaf(w, v[u].z, acc.z);
           acc.w = fmaf(w, v[u].w, acc.w);
         }
+        write_row<T, D>(dest_of(p, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
       }
-      write_row<T, D>(dest_of(p, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
-    }
+    };
+    if (p.cs > 8)
+      join(Count<16>());
+    else if (p.cs > 2)
+      join(Count<8>());
+    else
+      join(Count<2>());
     __syncwarp();
     cluster_sync();   // no CTA leaves while its share is read
   }
@@ -683,7 +687,7 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
   // and three quarters of the SMs, where a CTA fills its SM), down to a CTA per
   // tile while all are resident, and while the capacity leaves a CTA 16 pages
   // at most: beyond that the balanced runs over the whole GPU are faster
-  // (32 x 8 tiles of 1..4 pages: 9 us on a CTA each, 14 in runs; 64 x 8 the
+  // (32 x 8 tiles of 1..4 pages: 8.5 us on a CTA each, 14 in runs; 64 x 8 the
   // same either way, 256 x 8 51 and 39).
   const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
   p.cs = 1;

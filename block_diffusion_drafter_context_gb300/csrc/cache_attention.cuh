@@ -115,6 +115,11 @@ struct Chunk {
 };
 enum { FIRST = 1, LAST = 2, BAD = 4, WHOLE = 8 };
 
+// a number as a type, for lambdas
+template <int N>
+struct Count {
+  static constexpr int value = N;
+};
 
 // Where a tile's rows go.  By value: a reference to the kernel's parameters
 // would move them out of the constant bank.

@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     __syncwarp();
     cluster_sync();
     const Dest dest = dest_of(p, r.row0, ct->h);
-    for (int e = rank * NTHR + threadIdx.x; e < rows * (D / 4); e += p.cs * NTHR) {
+    const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
+    for (int e = rank * per + threadIdx.x; e < end; e += NTHR) {
       const int row = e / (D / 4), c = e % (D / 4);
       const float *at = xo + row * D + ((c ^ (row & (D / 4 - 1))) << 2), *ml_at = xo + MROWS * D + 2 * row;
       float2 ml[8];
