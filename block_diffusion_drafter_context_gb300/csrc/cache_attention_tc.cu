@@ -434,7 +434,8 @@ __global__ void __launch_bounds__(NTHR, 1)
           s3 += x[e + 3];
         }
         l += (s0 + s1) + (s2 + s3);
-        {   // P over this page's S
+        {   // P over this page's S, rounded to bf16 (with a second part for the rest of each value and a second product
+            // the S buffers come round too late: 64 x 16 at 16k..32k took 1065 us instead of 949)
           uint32_t w0[16], w1[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {

@@ -141,7 +141,8 @@ class TargetOps:
         that already holds their K and V: out [tokens][nq d], with want_lse
         also the log-sum-exp [tokens][nq].  max_new: the most new tokens of a
         request in this call (default: the object's); the narrower it is, the
-        better the kernel fits."""
+        better the kernel fits.  In bf16 the probabilities are rounded to bf16
+        for their product with V; sums, maxima and lse are fp32."""
         torch = self._torch
         if stream is not None or torch.cuda.current_device() != self.device.index:
             with _on(stream, self.device):

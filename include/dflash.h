@@ -507,6 +507,9 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
  *   scale:    positive, below 2e38, e.g. 1/sqrt(d).
  *   out:      device [total_new][nq*d] (dtype) out, not overlapping q.
  *   lse:      device fp32 [total_new][nq] out, or NULL.
+ * bf16 calls round the probabilities exp(s_t - m) to bf16 for their product
+ * with V (the sum below them and lse keep fp32): beside its own rounding out
+ * is off by up to 2^-8 of sum_t p_t |v_t|.  fp32 calls keep them to 2^-22.
  * Cache slots past a request's newest token may hold anything (NaN too); the
  * K and V of its own tokens are finite, in fp32 below 2^127 (0 times an
  * infinite V of a position that another of the request's tokens sees is NaN).
