@@ -333,7 +333,11 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       }
       // positions a row does not see (whatever their slots hold)
       const bool edge = t0 + 15 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+      float low[2] = {LOWEST, LOWEST};   // -inf where a row sees none of the 16
       if (edge) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (t0 > top[e] || (p.window > 0 && t0 + 15 <= top[e] - p.window)) low[e] = -INFINITY;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       for (int e = 0; e < 2; ++e) {
         float v = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])) * p.scale_log2;
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        mx[e] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        mx[e] = fmaxf(v, low[e]);
       }
       const bool need = mx[0] > m[0] + RESCALE_LOG2 || mx[1] > m[1] + RESCALE_LOG2;
       if (__any_sync(0xffffffffu, need)) {

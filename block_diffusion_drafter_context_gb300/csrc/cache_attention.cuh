@@ -5,6 +5,7 @@
 #include "common.cuh"
 #include "target.h"
 
+#include <float.h>
 #include <math.h>
 
 namespace dflash {
@@ -137,18 +138,29 @@ __device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h, int ba
 // score; maxima pass over NaN), which makes the joined row NaN too.
 __device__ __forceinline__ float join_max(float m, float l) { return l == l ? m : INFINITY; }
 
+// A row's maximum is -inf only where it sees no position; a row that sees some,
+// all with scores of -inf (an infinite query, an overflow), has LOWEST.  With a
+// sum of 0 the first is out = 0, lse = -inf, the second 0 / 0 = NaN.
+constexpr float LOWEST = -FLT_MAX;
+__device__ __forceinline__ float inverse_sum(float M, float L) {   // L NaN: so is the row
+  return L != 0.f ? 1.f / L : M == -INFINITY ? 0.f : NAN;
+}
+__device__ __forceinline__ float log_sum(float M, float L) {
+  return L != 0.f ? (M + log2f(L)) * LN2_F : M == -INFINITY ? -INFINITY : NAN;
+}
+
 // Row `row` of the tile: output columns c4 .. c4 + 3, and its log-sum-exp.
 template <typename T, int D>
 __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
   row += p.base;
   const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
-  const float inv = L == 0.f ? 0.f : 1.f / L;   // L NaN: so is the row
+  const float inv = inverse_sum(M, L);
   T *dst = static_cast<T *>(p.out) + at * D + c4;
   if constexpr (sizeof(T) == 4)
     *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
   else
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (p.lse && c4 == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2_F;
+  if (p.lse && c4 == 0) p.lse[at] = log_sum(M, L);
 }
 
 // The join of a tile cut over several CTAs, by the last of them to arrive: np

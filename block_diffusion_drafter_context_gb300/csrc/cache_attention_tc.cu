@@ -371,9 +371,11 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         // positions this row does not see (whatever their slots hold)
         const bool edge = bad || t0 + PAGE - 1 > c.ctx || (p.window > 0 && t0 < newest - p.window + 1);
+        float low = LOWEST;   // -inf where the row sees nothing of the page
         if (edge) {
           const int top = c.ctx + min(c.n - 1, tok);
           const int hi = bad ? -1 : top - t0, lo = p.window > 0 ? top - p.window + 1 - t0 : 0;
+          if (hi < 0 || lo >= PAGE) low = -INFINITY;
 #pragma unroll
           for (int e = 0; e < PAGE; ++e)
             if (e > hi || e < lo) x[e] = -INFINITY;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             a2 = fmaxf(a2, x[e + 2]);
             a3 = fmaxf(a3, x[e + 3]);
           }
-          mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.scale_log2;
+          mx = fmaxf(fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * p.scale_log2, low);
         }
         if (first) {
           m = mx;
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int rows = last.n * g;
       const size_t at = static_cast<size_t>(last.row0 + (live ? tok : 0)) * (p.nkv * g) + last.h * g + head;
       float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = inverse_sum(M, L);
 #pragma unroll
       for (int c0 = 0; c0 < D / 16; c0 += 2) {
         uint32_t a[2][16], b[2][16];
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (two) mbar_arrive(&ct->oempty[wg ^ 1]);
       }
       if (whole) {
-        if (live && p.lse) p.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * LN2_F;
+        if (live && p.lse) p.lse[at] = log_sum(M, L);
         continue;
       }
       if (live) {

@@ -513,7 +513,8 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
  * Cache slots past a request's newest token may hold anything (NaN too); the
  * K and V of its own tokens are finite, in fp32 below 2^127 (0 times an
  * infinite V of a position that another of the request's tokens sees is NaN).
- * A query that is not finite makes its own row's out and lse NaN.
+ * A query that is not finite makes its own row's out and lse NaN, and so do
+ * scores that overflow to +inf anywhere or to -inf everywhere.
  * A page index outside [0, num_pages) drops that page's positions and is
  * reported as DFLASH_ERR_DEVICE; a token left without any gets out = 0 and
  * lse = -inf.  A request whose cu_new or ctx_len is out of range (or that has
