@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < SEGS; ++i) sh.seg[i][tid] = -INFINITY;
   bool ok = true;
-  for (int s = 0, part = 0, left = seg_len; s < ns; ++s) {
+  int s = 0;
+  for (int part = 0, left = seg_len; s < ns; ++s) {
     ok = mbar_wait(&full[s % STAGES], static_cast<uint32_t>((s / STAGES) & 1), nullptr, WAIT_NS);
     ok = !__any_sync(0xffffffffu, !ok);
     if (!ok) break;
@@ -359,10 +360,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
       }
     }
   }
-  if (!ok) {   // a copy did not arrive: no answer; the others land before the shared memory goes away
+  if (!ok) {   // a copy did not arrive: no answer; those under way land before the shared memory goes away
     sh.failed = 1;
-    for (int s = 0; s < min(STAGES, ns); ++s)
-      mbar_wait(&full[s], static_cast<uint32_t>(((ns - 1 - s) / STAGES) & 1), nullptr, WAIT_NS / 8);
+    for (int t = s; t < min(ns, s + STAGES); ++t)
+      mbar_wait(&full[t % STAGES], static_cast<uint32_t>((t / STAGES) & 1), nullptr, WAIT_NS / 8);
   }
   const float seen = m;   // the maximum of this thread's vectors
   Stat st;
