@@ -135,7 +135,7 @@ constexpr unsigned long long WAIT_NS = 2000000000ull;
 struct Shared {
   alignas(16) uint64_t list[LIST];                   // candidates for the 16 largest (value, id) keys, unordered
   uint64_t best[TOP_K];      // the 16 largest in order, 0 where there are fewer
-  uint64_t full[WARPS][DEEP], mail;
+  uint64_t full[WARPS][DEEP];
   alignas(16) uint64_t peer_keys[MAX_CLUSTER * TOP_K];   // rank 0: every CTA's best
   float4 peer_stat[MAX_CLUSTER];                         // rank 0: (m, z, w, count) of every CTA
   float4 warp_stat[WARPS];
@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
   if (lane == 0)
     for (int i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
   if (tid == 0) {
-    mbar_init(&sh.mail, cs);
     sh.listed = sh.owned = sh.failed = 0;
   }
   if (lane == 0) fence_mbar_init();
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
   const float c = a.inv_t * LOG2E_F;
   const uint64_t c2 = pack2(c, c);
   __syncthreads();                // barriers and counters are set up
-  if (cs > 1) cluster_arrive();   // waited for before a peer's mailbox is written
+  if (cs > 1) cluster_arrive();   // waited for before rank 0's shared memory is written
   float m = -INFINITY;
   uint64_t z2 = pack2(0.f, 0.f), w2 = z2;
   int cnt = 0;
@@ -290,11 +289,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
 #pragma unroll
   for (int i = 0; i < SEGS; ++i) sh.seg[i][tid] = -INFINITY;
   bool ok = true;
-  int s = 0;
-  for (int part = 0, left = seg_len; s < ns; ++s) {
+  for (int s = 0, part = 0, left = seg_len; s < ns; ++s) {
     ok = mbar_wait(&full[s % STAGES], static_cast<uint32_t>((s / STAGES) & 1), nullptr, WAIT_NS);
     ok = !__any_sync(0xffffffffu, !ok);
-    if (!ok) break;
+    if (!ok) {   // a copy did not arrive: no answer; those under way land before the shared memory goes away
+      sh.failed = 1;
+      for (int t = s; t < min(ns, s + STAGES); ++t)
+        mbar_wait(&full[t % STAGES], static_cast<uint32_t>((t / STAGES) & 1), nullptr, WAIT_NS / 8);
+      break;
+    }
     const int n = min(SV, end - v0 - s * STEP);
     uint4 raw[U];
     const uint4 *stage = ring + (s % STAGES) * SV + lane;
@@ -359,11 +362,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
           for (int k = 0; k < N; ++k) cnt += i + k < id && v[k] == xt;
       }
     }
-  }
-  if (!ok) {   // a copy did not arrive: no answer; those under way land before the shared memory goes away
-    sh.failed = 1;
-    for (int t = s; t < min(ns, s + STAGES); ++t)
-      mbar_wait(&full[t % STAGES], static_cast<uint32_t>((t / STAGES) & 1), nullptr, WAIT_NS / 8);
   }
   const float seen = m;   // the maximum of this thread's vectors
   Stat st;
@@ -483,18 +481,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
     gather(sh.warp_stat, WARPS);
     if (sh.failed) st.m = NAN;
   }
-  // ---- the cluster: every CTA's share into rank 0's mailbox
+  // ---- the cluster: every CTA's share into rank 0's shared memory
   if (cs > 1) {
     cluster_wait();
     if (warp == 0) {
       if (lane < TOP_K) st_dsmem_u64(dsmem_addr(&sh.peer_keys[rank * TOP_K + lane], 0), want ? sh.best[lane] : 0);
       if (lane == 31) st_dsmem_f4(dsmem_addr(&sh.peer_stat[rank], 0), make_float4(st.m, st.z, st.w, __int_as_float(cnt)));
-      fence_acq_rel_cluster();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(dsmem_addr(&sh.mail, 0));
     }
+    // Every CTA gets here (its waits are bounded), and rank 0 stays until all
+    // have: no share goes to shared memory that is not its own any more.
+    cluster_arrive();
+    cluster_wait();
     if (rank != 0) return;
-    const bool all = mbar_wait_cluster(&sh.mail, 0, nullptr, WAIT_NS);
     if (want) {   // a key's place is the number of keys above it (0: a CTA with fewer than 16)
       const int n = cs * TOP_K, i = tid >> 1;
       const uint64_t mine = i < n ? sh.peer_keys[i] : 0;
@@ -511,7 +509,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {
     }
     if (warp == 0) {
       gather(sh.peer_stat, cs);
-      if (!all) st.m = NAN;
     }
   }
   if (warp != 0) return;
