@@ -106,3 +106,75 @@ def test_overflow_to_minus_infinity_at_some_keys_alone(nq, nkv, d, dtype, new, w
     tol = ((U["bf16"] if dtype == "bf16" else 0) + e) * spread + U[dtype] * np.abs(ref) + 1e-30
     assert (np.abs(np64(out) - ref) <= tol).all()
     assert (np.abs(np64(lse) - rlse) <= e + 2.0 ** -22 * (1 + np.abs(rlse))).all()
+
+
+# ------------------------------------------------------------------ the form that cuts the pages into runs
+def bad_pages(which, n):
+    """Page numbers of a request of n pages.  A run is 2 pages at least (4 in
+    the wider tiles), so 11 in a row are some CTA's whole part."""
+    return {"first": [0], "last": [n - 1], "a whole part": list(range(20, 31)), "both ends": [0, 1, n - 2, n - 1],
+            "every": list(range(n)), "alternate": list(range(0, n, 2))}[which]
+
+
+@pytest.mark.parametrize("nq,nkv,d,dtype", FORMS)
+@pytest.mark.parametrize("new", [1, 9])
+@pytest.mark.parametrize("which", ["first", "last", "a whole part", "both ends", "every", "alternate"])
+def test_missing_pages_in_runs(nq, nkv, d, dtype, new, which):
+    """A request of 94 pages that lost some, between two whole ones: the lost
+    positions drop out, a token left without any gets out 0 and lse -inf, the
+    others keep their bits."""
+    import torch
+    c = widen(Batch(nq, nkv, d, dtype, [700, 6000, 90], [1, new, 2], seed=new + d, max_new=max(2, new)))
+    whole, whole_lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    lost = bad_pages(which, -(-(6000 + new) // PAGE))
+    c.table[1, lost] = [(-7, 1 << 20, c.k.shape[1])[i % 3] for i in range(len(lost))]
+    widen(c)
+    out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == -7 and c.ops.status() == 0
+    c.check_attention(out, lse)
+    rows = torch.ones(c.T, dtype=torch.bool, device="cuda")
+    rows[1:1 + new] = False
+    assert torch.equal(out[rows], whole[rows]) and torch.equal(lse[rows], whole_lse[rows])
+    again, lse2 = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == -7 and torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("nq,nkv,d,dtype", FORMS)
+@pytest.mark.parametrize("what", ["context", "too many", "capacity"])
+def test_requests_out_of_range_in_runs(nq, nkv, d, dtype, what):
+    """Invalid requests first, in the middle (two in a row) and last in a batch
+    of long ones: reported, their rows unwritten, the others right."""
+    import torch
+    ctx, new = [400, 2500, 64, 1000, 3000, 200], [3, 2, 3, 3, 1, 3]
+    c = widen(Batch(nq, nkv, d, dtype, ctx, new, seed=d, pad_rows=2))
+    good, good_lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    c.check_attention(good, good_lse)
+    bad, max_new, at = [0, 2, 3, 5], 16, c.ctx_d.clone()
+    if what == "too many":
+        max_new = 2
+    else:   # 300 pages hold 19 200 positions
+        at[bad] = torch.tensor([-1, 2 ** 31 - 1, -2 ** 31, 300 * PAGE - 2] if what == "context" else [300 * PAGE - 2] * 4,
+                               dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(good, 7.0), torch.full_like(good_lse, 7.0)
+    c.ops.attend(c.kv, 1, c.q, c.cu_d, at, max_new=max_new, out=out, lse=lse)
+    assert c.ops.status() == -7 and c.ops.status() == 0
+    left = torch.ones(c.T + 2, dtype=torch.bool, device="cuda")
+    for b in (1, 4):
+        left[int(c.cu[b]):int(c.cu[b + 1])] = False
+    assert (out[left] == 7).all() and (lse[left] == 7).all()
+    out[left], lse[left] = good[left], good_lse[left]
+    c.check_attention(out, lse)
+
+
+@pytest.mark.parametrize("nq,nkv,d,dtype", FORMS)
+@pytest.mark.parametrize("new", [1, 6])
+def test_a_common_prefix_in_runs(nq, nkv, d, dtype, new):
+    """Three requests that share their first 40 pages."""
+    c = Batch(nq, nkv, d, dtype, [3000, 2600, 4000], [new] * 3, seed=new, max_new=new)
+    c.table[1:, :40] = c.table[0, :40]
+    widen(c)
+    out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    c.check_attention(out, lse)
