@@ -178,3 +178,36 @@ def test_a_common_prefix_in_runs(nq, nkv, d, dtype, new):
     out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
     assert c.ops.status() == 0
     c.check_attention(out, lse)
+
+
+# ------------------------------------------------------------------ far positions
+@pytest.mark.parametrize("base", [1.0001, 2.0, 10.0, 1e4, 5e5, 1e6])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first,bound", [(0, 4e-7), (2 ** 17 - 4096, 4e-7), (2 ** 20 - 4096, 4e-7), (2 ** 22 - 8192, 4e-7),
+                                         (2 ** 23 - 4096, 8.5e-7), (15339979 - 4096, 8.5e-7), (2 ** 24 - 8192, 8.5e-7)])
+def test_rotation_angles(base, d, first, bound):
+    """Heads of (1, 0) pairs come out as the cosines and sines themselves, so
+    each is off by the angle's error and sincosf's 2 ulp (2^-23) at most: 8192
+    positions from `first` on, every pair, against the angle in 64 bits."""
+    import torch
+    from block_diffusion_drafter_context_gb300.drafter import PagedKV
+    from block_diffusion_drafter_context_gb300.target import TargetOps
+    n, page0 = 8192, first // PAGE
+    table = torch.full((1, 2 ** 18), -1, dtype=torch.int32, device="cuda")
+    count = (first + n - 1) // PAGE - page0 + 1
+    table[0, page0:page0 + count] = torch.arange(count, device="cuda", dtype=torch.int32)
+    k, v = (torch.zeros(1, count, 1, *s, device="cuda") for s in ((PAGE, d), (d, PAGE)))
+    x = torch.zeros(n, 3 * d, device="cuda")
+    x[:, :d // 2] = 1
+    x[:, d:d + d // 2] = 1
+    ops = TargetOps(1, 1, d, dtype="f32", max_batch=1, rope_base=base)
+    q = ops.append_kv(PagedKV.from_tensors(k, v, table), 0, x, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                      torch.tensor([first], dtype=torch.int32, device="cuda"))
+    assert ops.status() == 0
+    # the base is an fp32 argument; fp64 angles are off by 2^24 * 2^-52 = 4e-9
+    theta = float(np.float32(base)) ** (-2.0 * torch.arange(d // 2, dtype=torch.float64, device="cuda") / d)
+    pos = torch.arange(first, first + n, device="cuda")
+    angle = pos.double()[:, None] * theta
+    ref = torch.cat([angle.cos(), angle.sin()], 1)
+    assert (q.double() - ref).abs().max() <= bound + 2.0 ** -23 + 1e-8
+    assert torch.equal(k[0, (pos // PAGE) - page0, 0, pos % PAGE], q)     # the key's head is the same pairs
