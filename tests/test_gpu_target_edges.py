@@ -211,3 +211,38 @@ def test_rotation_angles(base, d, first, bound):
     ref = torch.cat([angle.cos(), angle.sin()], 1)
     assert (q.double() - ref).abs().max() <= bound + 2.0 ** -23 + 1e-8
     assert torch.equal(k[0, (pos // PAGE) - page0, 0, pos % PAGE], q)     # the key's head is the same pairs
+
+
+# ------------------------------------------------------------------ log probabilities with few tokens left
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(1, 151936), (5, 40001), (40, 20000), (650, 9000)])
+@pytest.mark.parametrize("alive", [1, 2, 5, 15, 16, 17])
+def test_logprobs_of_rows_with_few_finite_logits(dtype, rows, V, alive):
+    """A grammar's mask: 1 to 17 finite logits in rows cut over clusters and in
+    rows of one CTA; the places behind them are -inf logits, lowest ids first."""
+    import torch
+    from block_diffusion_drafter_context_gb300.target import token_logprobs
+    rng = np.random.default_rng(rows + V + alive)
+    x = np.full((rows, V), -np.inf, dtype=np.float32)
+    for r in range(rows):
+        # the ends of the row and the first ids among them in every third row
+        at = rng.choice(V, alive, replace=False)
+        if r % 3 == 0:
+            at = np.unique(np.concatenate([[0, V - 1, 3, V - 2], rng.choice(V, alive, replace=False)])[:alive])
+        x[r, at] = rng.standard_normal(len(at)) * 3
+    x = torch.from_numpy(x).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    ids = rng.integers(0, V, rows)
+    ids[::2] = np64(x).argmax(1)[::2]
+    got = token_logprobs(x, torch.from_numpy(ids.astype(np.int32)).cuda(), temperature=0.7)
+    got = {k: v.cpu().numpy() for k, v in got.items()}
+    x64 = np64(x)
+    for r in list(range(min(rows, 6))) + ([rows - 1] if rows > 6 else []):
+        lp, ent, rank, top, top_lp = O.token_logprobs(x64[r], ids[r], 0.7, 16)
+        assert got["rank"][r] == rank and list(got["top_ids"][r]) == top, r
+        # fp32: logits up to 15 / 0.7 scaled (2 roundings each), 17 summands, exp2 and log2 to 2^-21
+        e = (6 * 22 + 17 + 32) * 2.0 ** -24
+        assert got["logprob"][r] == lp if np.isinf(lp) else abs(got["logprob"][r] - lp) <= 2 * e
+        assert abs(got["entropy"][r] - ent) <= 3 * e * 5
+        inf = np.isinf(top_lp)
+        assert np.array_equal(np.isneginf(got["top_logprobs"][r]), inf)
+        assert (np.abs(got["top_logprobs"][r][~inf] - top_lp[~inf]) <= 2 * e).all()
