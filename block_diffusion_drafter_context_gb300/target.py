@@ -51,7 +51,8 @@ class TargetOps:
 
     max_batch, max_new: the largest batch and the most new tokens per request
     (1..16) of an ``attend`` call; ``append_kv`` takes any number of tokens.
-    rope_base: 0 for layers without rotation."""
+    rope_base: 0 for layers without rotation.  The object outlives its calls:
+    one that is let go frees the workspace for the stream it was made on."""
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, dtype="bf16", max_batch=64, max_new=16, rope_base=1e6,
                  eps=1e-6, device="cuda"):
@@ -64,6 +65,9 @@ class TargetOps:
         self.ws_bytes = B.dflash_target_workspace_bytes(self.heads, self.max_batch, self.max_new)
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        with torch.cuda.device(self.device):     # the first call may be on another stream
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
         self.layer_sig = (self.dtype, self.device, self.nkv, self.d)
         self._torch, self._lib, self._i32 = torch, B.load(), torch.int32
         self._heads, self._ws, self._scale = ctypes.byref(self.heads), self.workspace.data_ptr(), self.d ** -0.5

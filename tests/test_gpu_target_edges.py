@@ -246,3 +246,30 @@ def test_logprobs_of_rows_with_few_finite_logits(dtype, rows, V, alive):
         inf = np.isinf(top_lp)
         assert np.array_equal(np.isneginf(got["top_logprobs"][r]), inf)
         assert (np.abs(got["top_logprobs"][r][~inf] - top_lp[~inf]) <= 2 * e).all()
+
+
+# ------------------------------------------------------------------ streams
+@pytest.mark.parametrize("nq,nkv,d,dtype", [(8, 2, 128, "bf16"), (16, 2, 128, "bf16"), (4, 2, 64, "f32")])
+def test_a_new_object_is_used_on_another_stream_at_once(nq, nkv, d, dtype):
+    """The workspace's memory held something else, and the stream it is made on
+    is busy for a while: the first call on another stream finds it cleared."""
+    import torch
+    from block_diffusion_drafter_context_gb300.target import TargetOps
+    new = 16 if dtype == "bf16" else 2
+    c = widen(Batch(nq, nkv, d, dtype, [9000, 300], [new, 1], seed=3))
+    want, want_lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    side = torch.cuda.Stream()
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    size = c.ops.ws_bytes
+    del c.ops
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = torch.full((size,), 0x55, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del old
+    torch.cuda._sleep(200_000_000)      # about 0.1 s
+    ops = TargetOps(nq, nkv, d, dtype=dtype, max_batch=2)
+    ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, out=out, lse=lse, stream=side)
+    torch.cuda.synchronize()
+    assert ops.status() == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
