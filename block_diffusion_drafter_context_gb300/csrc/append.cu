@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
   load(slot);
   // ---- where the tokens go: warp w looks up tokens w and w + 8
   const int end = a.cu_new[a.B], total = min(a.total, end), nt = min(a.tt, total - t0);
+  const int begin = a.cu_new[0], j0 = begin > t0 ? begin - t0 : 0;   // the tile's rows before the first request's are left alone
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (end > a.total || end < 0))
     report(a.status, DFLASH_ERR_DEVICE);
   {
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
       if (j >= nt) continue;
       const bool ok = pg[k] >= 0 && pg[k] < a.num_pages;
       if (lane == 0) {
-        if (!ok) report(a.status, DFLASH_ERR_DEVICE);
+        if (!ok && j >= j0) report(a.status, DFLASH_ERR_DEVICE);
         s_page[j] = ok ? pg[k] : -1;
         s_pos[j] = max(pos[k], 0);
       }
@@ -213,13 +214,14 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
     }
   }
   // ---- q and k heads
+  const unsigned mine = max(nt - j0, 0);
   for (int it0 = slot; it0 - slot < items; it0 += ROWS * U) {   // uniform trip count
     if (it0 != slot) load(it0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (it0 - slot + u * ROWS >= items) break;   // uniform
       const int it = it0 + u * ROWS, j = it & ((1 << sh) - 1), hh = it >> sh;
-      const bool live = it < items && j < nt, isq = hh < nqh;
+      const bool live = it < items && static_cast<unsigned>(j - j0) < mine, isq = hh < nqh;
       float x[8], y[8];
       F::unpack(raw[u][0], x);
       F::unpack(raw[u][1], x + 4);

@@ -114,7 +114,8 @@ class TargetOps:
         """K and V of the rows of qkv ([tokens][(nq + 2 nkv) d], the fused
         projection) into the pages of their requests, K normed (g_k) and
         rotated; returns the normed (g_q) and rotated queries [tokens][nq d].
-        Rows from cu_new[batch] on are left alone, in q_out too."""
+        Rows before cu_new[0] and from cu_new[batch] on are left alone, in
+        q_out too."""
         torch = self._torch
         if stream is not None or torch.cuda.current_device() != self.device.index:
             with _on(stream, self.device):

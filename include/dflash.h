@@ -447,8 +447,9 @@ DFLASH_API int dflash_topk16_noalloc(const float *logits, int rows, int vocab, i
  *
  * Ragged batches: request b owns rows cu_new[b] .. cu_new[b+1]-1 of the
  * token-major buffers, at positions ctx_len[b] ...  A request may have no
- * new tokens.  Rows from cu_new[batch] to total_new (the padding of a
- * captured batch; total_new <= 2^30) may hold anything and are not written.
+ * new tokens.  Rows before cu_new[0] (a part of a batch, given by a slice of
+ * its cu_new) and from cu_new[batch] to total_new (the padding of a captured
+ * batch; total_new <= 2^30) may hold anything and are not written.
  * No two tokens of a call go to the same slot of a page; pages may be shared
  * between requests where they are only read (a common prefix). */
 

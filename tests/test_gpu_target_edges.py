@@ -273,3 +273,51 @@ def test_a_new_object_is_used_on_another_stream_at_once(nq, nkv, d, dtype):
     torch.cuda.synchronize()
     assert ops.status() == 0
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# ------------------------------------------------------------------ a part of a batch
+@pytest.mark.parametrize("nq,nkv,d,dtype", FORMS)
+@pytest.mark.parametrize("new", [[3, 2, 1, 4, 2], [16, 16, 5, 7, 16], [30, 70, 9, 1, 50]])
+@pytest.mark.parametrize("wide", [False, True])
+def test_the_requests_of_a_slice(nq, nkv, d, dtype, new, wide):
+    """Requests 2 and 3 alone, by slices of cu_new, ctx_len and the page table
+    and the whole batch's rows: what the whole batch gives in their rows and
+    slots, nothing reported, every other row and slot as it was."""
+    import torch
+    from block_diffusion_drafter_context_gb300.drafter import PagedKV
+    c = Batch(nq, nkv, d, dtype, [100, 7, 250, 60, 0], new, seed=d + new[0], stale=0.0, pad_rows=2)
+    if wide:
+        widen(c)
+    k0, v0 = c.k.clone(), c.v.clone()
+    few = max(new) <= 16
+    q = c.ops.append_kv(c.kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    out = c.ops.attend(c.kv, 1, q, c.cu_d, c.ctx_d) if few else None
+    k1, v1 = c.k.clone(), c.v.clone()
+    c.k.copy_(k0), c.v.copy_(v0)
+    kv = PagedKV.from_tensors(c.k, c.v, c.kv.page_table[2:4])
+    cu, ctx = c.cu_d[2:5], c.ctx_d[2:4]
+    q2 = torch.full_like(q, 7.0)
+    c.ops.append_kv(kv, 1, c.qkv, cu, ctx, c.g_q, c.g_k, q_out=q2)
+    assert c.ops.status() == 0
+    mine = torch.zeros(c.T + 2, dtype=torch.bool, device="cuda")
+    mine[int(c.cu[2]):int(c.cu[4])] = True
+    assert torch.equal(q2[mine], q[mine]) and (q2[~mine] == 7).all()
+    pages = [int(p) for b in (2, 3) for p in c.table[b] if p >= 0]
+    rest = [p for p in range(c.k.shape[1]) if p not in pages]
+    assert torch.equal(c.k[1, pages], k1[1, pages]) and torch.equal(c.v[1, pages], v1[1, pages])
+    assert torch.equal(c.k[1, rest], k0[1, rest]) and torch.equal(c.v[1, rest], v0[1, rest])
+    assert torch.equal(c.k[0], k0[0]) and torch.equal(c.v[0], v0[0])
+    if few:
+        out2, lse2 = torch.full_like(out, 7.0), torch.full((c.T + 2, nq), 7.0, device="cuda")
+        c.ops.attend(kv, 1, q2, cu, ctx, out=out2, lse=lse2)
+        assert c.ops.status() == 0
+        assert (out2[~mine] == 7).all() and (lse2[~mine] == 7).all()
+        out2[~mine], lse2[~mine] = 0, 0
+        want, want_lse, spread = c.attend_ref(q)
+        # the roundings of Batch.check_attention, kept apart because only two requests are there
+        q64 = np64(q)[:c.T].reshape(c.T, nq, d)
+        e = 2 * d * 2.0 ** -24 * np.abs(q64).sum(-1).max() * np.abs(np64(c.k[1])).max() * d ** -0.5 + 300 * 2.0 ** -24 + 2.0 ** -20
+        at = mine.cpu().numpy()
+        tol = ((U["bf16"] if dtype == "bf16" else 0) + e) * spread[at] + U[dtype] * np.abs(want[at]) + 1e-30
+        assert (np.abs(np64(out2)[at] - want[at]) <= tol).all()
+        assert (np.abs(np64(lse2)[at] - want_lse[at]) <= e + 2.0 ** -22 * (1 + np.abs(want_lse[at]))).all()
