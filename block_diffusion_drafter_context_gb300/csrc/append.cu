@@ -92,11 +92,11 @@ __device__ __forceinline__ void requests_of(const int32_t *cu, int B, int t0, in
 // one token) is D / 8 lanes; lane l holds values 4l..4l+3 of both halves, so
 // that the rotation's pairs are its own (with 8 consecutive values per lane
 // the exchange and the rotation table made shared memory the bound: 159 us
-// for 23 040 prompt tokens of 32 + 16 heads, where this takes 94).  The first
+// for 23 040 prompt tokens of 32 + 16 heads, where this takes 95).  The first
 // rows' loads and the V rows' copies into shared memory do not depend on where
 // the tokens belong, so they are under way while each token's request, page
-// and rotation are looked up (three dependent loads).  The rotation of the tile's tokens is tabulated once and
-// shared by the heads.  V leaves transposed.
+// and rotation are looked up (three dependent loads).  The rotation of the
+// tile's tokens is tabulated once and shared by the heads.  V leaves transposed.
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, const __grid_constant__ RopeArgs rp) {
   constexpr int LPR = D / 8, HALF = D / 2, ROWS = THREADS / LPR, V16 = 16 / sizeof(T);
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
   load(slot);
   // ---- where the tokens go: warp w looks up tokens w and w + 8
   const int end = a.cu_new[a.B], total = min(a.total, end), nt = min(a.tt, total - t0);
-  const int begin = a.cu_new[0], j0 = begin > t0 ? begin - t0 : 0;   // the tile's rows before the first request's are left alone
+  const int begin = a.cu_new[0], j0 = begin > t0 ? begin - t0 : 0;   // rows before the first request's: left alone
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (end > a.total || end < 0))
     report(a.status, DFLASH_ERR_DEVICE);
   {

@@ -11,8 +11,9 @@
 // operations on them the pass is bound by HBM, and the work is the flat list
 // of pages over (request, kv head), cut into equal runs, one persistent CTA
 // each, so that ragged batches and a single long request both fill the GPU.
-// A (request, kv head) cut by a run boundary leaves (max, sum, O) partials, and the last contributor to arrive joins them in
-// contributor order: the same bits on every call.
+// A (request, kv head) cut by a run boundary leaves (max, sum, O) partials, and
+// the last contributor to arrive joins them in contributor order: the same bits
+// on every call.
 #include "cache_attention.cuh"
 
 namespace dflash {
@@ -24,7 +25,7 @@ namespace {
 // fraction of the HBM time whichever way it is issued, and register
 // accumulators keep a page's path short.  (Two tiles of 16 rows per warp,
 // tried for 17..32 bf16 rows, left one CTA per SM at 255 registers: 149 us
-// against 96 of the tcgen05 form for 5 tokens x 4 heads at 128k.)
+// against 103 of the tcgen05 form, 95 by now, for 5 tokens x 4 heads at 128k.)
 //
 // Warp 0 produces: the K page as 128-byte-wide swizzled column blocks, the V^T
 // page (fp32: as two blocks of 32 slots), and for a new tile its query rows,

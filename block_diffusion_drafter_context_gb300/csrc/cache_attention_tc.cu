@@ -15,10 +15,11 @@
 //               softmax in the exp2 domain, P in bf16 over the page's S.
 // A page's softmax alone is as long as its share of HBM's time at D = 128 and
 // twice as long at D = 64, hence two groups (64 requests x 16 tokens x 5 heads
-// at 16k..32k: 1021 us with one, 940 with two, the copy rate).  Each has its own O, maximum and sum; O is
-// rescaled only when a row's maximum grows by 2^8.  The group with a tile's
-// last page joins the two and writes, while the other begins the next tile:
-// it writes that tile's query rows as soon as the last S of this one is there.
+// at 16k..32k: 1021 us with one, 940 with two, the copy rate).  Each has its
+// own O, maximum and sum; O is rescaled only when a row's maximum grows by 2^8.
+// The group with a tile's last page joins the two and writes, while the other
+// begins the next tile: it writes that tile's query rows as soon as the last S
+// of this one is there.
 // Row r of a tile is token r / g, query head r % g of the group.
 #include "cache_attention.cuh"
 
@@ -436,8 +437,8 @@ __global__ void __launch_bounds__(NTHR, 1)
           s3 += x[e + 3];
         }
         l += (s0 + s1) + (s2 + s3);
-        {   // P over this page's S, rounded to bf16 (with a second part for the rest of each value and a second product
-            // the S buffers come round too late: 64 x 16 at 16k..32k took 1065 us instead of 949)
+        {   // P over this page's S, rounded to bf16 (with a second product for the rest of each
+            // value the S buffers come round too late: 64 x 16 at 16k..32k 1065 us, 949 without)
           uint32_t w0[16], w1[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {

@@ -7,9 +7,11 @@
 // Everything comes from one pass over the logits: a running (m, z, w = sum
 // e^(y-m) (y-m)) per thread, joined as m' = max, z' = z e^(m-m'),
 // w' = e^(m-m') (w + z (m - m')); the rank is a count against the token's own
-// logit, read first; the alternatives are a filtered top-16 scan.  Bound by
-// the logits' HBM bytes; a row is cut over a cluster of CTAs, which join
-// through distributed shared memory, so that no workspace is needed.
+// logit, read first; the alternatives lie where a thread's maximum reaches the
+// 16th largest of the threads' maxima, and only those pieces of the row are
+// read again.  Bound by the logits' HBM bytes; a row is cut over a cluster of
+// CTAs, which join through distributed shared memory, so that no workspace is
+// needed.
 #include "top16.cuh"
 #include "target.h"
 
@@ -119,11 +121,11 @@ template <> struct Vec<__nv_bfloat16> {
 };
 
 // ---- shared memory of a CTA: for each warp a ring of STAGES x 2 KB of logits
-// (4 vectors per lane), then.  Two stages: 4 CTAs an SM have 64 KB in flight,
-// all that HBM's latency asks for; four stages made it slower (123 against 114
-// us at 1024 fp32 rows of 151 936).  Where the grid leaves an SM two CTAs at
-// most, four: a CTA's own round trips are the time there (64 such rows on 4
-// CTAs each: 20 us with two stages, 15 with four).
+// (4 vectors per lane), then the struct below.  Two stages: 128 KB of rings for
+// an SM's 4 CTAs; four stages were slower (123 against 114 us at 1024 fp32 rows
+// of 151 936).  Where the grid leaves an SM two CTAs at most,
+// four: a CTA's own round trips are the time there (64 such rows on 4 CTAs
+// each: 20 us with two stages, 15 with four).
 constexpr int WIDE = 2, DEEP = 4;                    // stages
 constexpr int U = 4, SV = 32 * U;
 constexpr int SEGS = 8;                              // parts of the stream whose maxima each thread keeps
@@ -222,8 +224,10 @@ __device__ __forceinline__ void pick16(const uint64_t *keys, int n, uint64_t *be
 //   where a thread's maximum does.  The threads keep one maximum for each
 //   eighth of the stream, so that only some 16 of the 2048 pieces are read
 //   again.  (A list kept during the stream, with
-//   votes, atomics and a meeting per stage, took 89 us where this takes 79 at
-//   640 fp32 rows of 151 936.)
+//   votes, atomics and a meeting per stage, took 89 us where this takes 78 at
+//   640 fp32 rows of 151 936.)  With fewer than 16 finite logits in a CTA's
+//   share the floor is -inf, and all of the share is read again, some three
+//   times: 520 us at 640 such rows.
 // Each CTA sends its 16 keys and sums to rank 0.
 template <typename T, int STAGES>
 __global__ void __launch_bounds__(THREADS, CTAS) logprobs_kernel(const Args a) {

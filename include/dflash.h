@@ -512,8 +512,9 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
  * with V (the sum below them and lse keep fp32): beside its own rounding out
  * is off by up to 2^-8 of sum_t p_t |v_t|.  fp32 calls keep them to 2^-22.
  * Cache slots past a request's newest token may hold anything (NaN too); the
- * K and V of its own tokens are finite, in fp32 below 2^127 (0 times an
- * infinite V of a position that another of the request's tokens sees is NaN).
+ * K and V of its own tokens are finite, in fp32 they and the queries below
+ * 2^127 (0 times an infinite V of a position that another of the request's
+ * tokens sees, or that lies before its window, is NaN).
  * A query that is not finite makes its own row's out and lse NaN, and so do
  * scores that overflow to +inf anywhere or to -inf everywhere.
  * A page index outside [0, num_pages) drops that page's positions and is
