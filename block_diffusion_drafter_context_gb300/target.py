@@ -38,8 +38,8 @@ def _on(stream, device):
     torch = _torch()
     if stream is None:
         return torch.cuda.device(device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device)
+    if isinstance(stream, int):   # handle 0 is the default stream; ExternalStream(0) would be one of torch's own
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"a stream of {stream.device}, tensors on {device}")
     return torch.cuda.stream(stream)

@@ -321,3 +321,39 @@ def test_the_requests_of_a_slice(nq, nkv, d, dtype, new, wide):
         tol = ((U["bf16"] if dtype == "bf16" else 0) + e) * spread[at] + U[dtype] * np.abs(want[at]) + 1e-30
         assert (np.abs(np64(out2)[at] - want[at]) <= tol).all()
         assert (np.abs(np64(lse2)[at] - want_lse[at]) <= e + 2.0 ** -22 * (1 + np.abs(want_lse[at]))).all()
+
+
+@pytest.mark.parametrize("which", ["default", "default's handle", "stream", "stream's handle", "current"])
+def test_calls_follow_the_stream_they_are_given(which):
+    """Inputs that a busy stream has still to write: every call on that stream
+    (named as an object or a handle, 0 for the default one) sees them."""
+    import torch
+    from block_diffusion_drafter_context_gb300.target import token_logprobs
+    c = Batch(8, 2, 128, "bf16", [200, 70], [2, 3], seed=2, stale=0.0)
+    x, ids = torch.randn(5, 5000, device="cuda"), torch.arange(5, dtype=torch.int32, device="cuda")
+    k0, v0 = c.k.clone(), c.v.clone()
+    q = c.ops.append_kv(c.kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    out = c.ops.attend(c.kv, 1, q, c.cu_d, c.ctx_d)
+    lp = token_logprobs(x, ids)
+    k1, v1 = c.k.clone(), c.v.clone()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    on = torch.cuda.default_stream() if which.startswith("default") else other if which == "current" else side
+    given = {"default": on, "default's handle": on.cuda_stream, "stream": on, "stream's handle": on.cuda_stream,
+             "current": None}[which]
+    assert which != "default's handle" or given == 0
+    qkv, logits = torch.zeros_like(c.qkv), torch.zeros_like(x)
+    c.k.copy_(k0), c.v.copy_(v0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(on):
+        torch.cuda._sleep(200_000_000)      # about 0.1 s
+        qkv.copy_(c.qkv), logits.copy_(x)
+    with torch.cuda.stream(other):          # the current stream, where the calls are not meant to go unless told nothing
+        q2 = c.ops.append_kv(c.kv, 1, qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k, stream=given)
+        out2 = c.ops.attend(c.kv, 1, q2, c.cu_d, c.ctx_d, stream=given)
+        lp2 = token_logprobs(logits, ids, stream=given)
+        status = c.ops.status(given)
+    torch.cuda.synchronize()
+    assert status == 0
+    assert torch.equal(q2, q) and torch.equal(out2, out) and torch.equal(c.k, k1) and torch.equal(c.v, v1)
+    for key in lp:
+        assert torch.equal(lp2[key], lp[key]), key
