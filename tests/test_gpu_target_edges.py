@@ -357,3 +357,29 @@ def test_calls_follow_the_stream_they_are_given(which):
     assert torch.equal(q2, q) and torch.equal(out2, out) and torch.equal(c.k, k1) and torch.equal(c.v, v1)
     for key in lp:
         assert torch.equal(lp2[key], lp[key]), key
+
+
+# ------------------------------------------------------------------ large pools
+@pytest.mark.parametrize("nq,nkv,d,dtype,pages", [(16, 8, 128, "bf16", 33500), (40, 8, 128, "bf16", 33500),
+                                                  (64, 16, 64, "bf16", 33500), (8, 4, 128, "f32", 66000)])
+def test_pages_past_32_bits_of_elements(nq, nkv, d, dtype, pages):
+    """The last pages of the second layer of a pool of more than 2^32 elements:
+    the same bits as in a small pool."""
+    import torch
+    from block_diffusion_drafter_context_gb300.drafter import PagedKV
+    c = Batch(nq, nkv, d, dtype, [300, 65, 0], [5, 1, 16], seed=d, stale=0.0)
+    k0, v0 = c.k.clone(), c.v.clone()
+    q = c.ops.append_kv(c.kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    out, lse = c.ops.attend(c.kv, 1, q, c.cu_d, c.ctx_d, want_lse=True)
+    used = c.k.shape[1]
+    assert 2 * pages * nkv * PAGE * d > 2 ** 32
+    k = torch.empty(2, pages, nkv, PAGE, d, dtype=c.dt, device="cuda")
+    v = torch.empty(2, pages, nkv, d, PAGE, dtype=c.dt, device="cuda")
+    k[1, -used:], v[1, -used:] = k0[1], v0[1]
+    table = torch.from_numpy(np.where(c.table >= 0, c.table + pages - used, -1).astype(np.int32)).cuda()
+    kv = PagedKV.from_tensors(k, v, table)
+    q2 = c.ops.append_kv(kv, 1, c.qkv, c.cu_d, c.ctx_d, c.g_q, c.g_k)
+    out2, lse2 = c.ops.attend(kv, 1, q2, c.cu_d, c.ctx_d, want_lse=True)
+    assert c.ops.status() == 0
+    assert torch.equal(q2, q) and torch.equal(out2, out) and torch.equal(lse2, lse)
+    assert torch.equal(k[1, -used:], c.k[1]) and torch.equal(v[1, -used:], c.v[1])
