@@ -383,3 +383,22 @@ def test_pages_past_32_bits_of_elements(nq, nkv, d, dtype, pages):
     assert c.ops.status() == 0
     assert torch.equal(q2, q) and torch.equal(out2, out) and torch.equal(lse2, lse)
     assert torch.equal(k[1, -used:], c.k[1]) and torch.equal(v[1, -used:], c.v[1])
+
+
+@pytest.mark.parametrize("nq,nkv,d,dtype", FORMS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_queries_with_a_row_stride(nq, nkv, d, dtype, wide):
+    """Queries as columns of a wider buffer (a fused projection's, NaN around
+    them): the bits of contiguous ones."""
+    import torch
+    c = Batch(nq, nkv, d, dtype, [300, 65, 0, 1000], [5, 0, 16, 1], seed=d, pad_rows=1)
+    if wide:
+        widen(c)
+    out, lse = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
+    step = 16 // c.q.element_size()
+    for before, behind in ((0, 2 * nkv * d), (step, 0), (3 * step, 5 * step)):
+        buf = torch.full((c.T + 1, before + nq * d + behind), float("nan"), dtype=c.dt, device="cuda")
+        buf[:, before:before + nq * d] = c.q
+        out2, lse2 = c.ops.attend(c.kv, 1, buf[:, before:before + nq * d], c.cu_d, c.ctx_d, want_lse=True)
+        assert c.ops.status() == 0
+        assert torch.equal(out2[:c.T], out[:c.T]) and torch.equal(lse2[:c.T], lse[:c.T])
