@@ -29,6 +29,7 @@ EXPORTS = (
     "dflash_debug_gemm_plan", "dflash_set_gemm_pairs", "dflash_fp8_weights_to_bf16",
     "dflash_debug_gemm_pair_clusters", "dflash_set_fused_topk",
     "dflash_target_workspace_bytes", "dflash_append_kv", "dflash_cache_attention", "dflash_token_logprobs",
+    "dflash_shared_attention", "dflash_shared_rows_bytes",
 )
 
 
@@ -123,6 +124,9 @@ def load(path: str = LIB_PATH):
                                  vp, i, vp, i, vp, vp, c_size_t, vp]),
         "dflash_cache_attention": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, i, vp, i, i, i,
                                        c_float, vp, vp, vp, c_size_t, vp]),
+        "dflash_shared_attention": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, i, vp, i, i, i,
+                                        c_float, vp, vp, vp, c_size_t, vp, c_size_t, vp]),
+        "dflash_shared_rows_bytes": (c_size_t, [POINTER(dflash_heads), i, i]),
         "dflash_token_logprobs": (i, [vp, i, i, i, c_longlong, vp, c_float, i, vp, vp, vp, vp, vp, vp]),
         "dflash_last_error": (ctypes.c_char_p, []),
         "dflash_topk16_noalloc": (i, [vp, i, i, vp, vp, vp]),
@@ -336,6 +340,22 @@ def dflash_cache_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_strid
     return _check(load().dflash_cache_attention(ctypes.byref(heads), ctypes.byref(kv), layer, _p(q), q_stride,
                                                 _p(cu_new), total_new, _p(ctx_len), batch, max_new, window, scale,
                                                 _p(out), _p(lse), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_shared_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_stride, cu_new, total_new, ctx_len, batch,
+                            max_new, shared_len, scale, out, lse, rows, rows_bytes, workspace, workspace_bytes,
+                            stream=None):
+    return _check(load().dflash_shared_attention(ctypes.byref(heads), ctypes.byref(kv), layer, _p(q), q_stride,
+                                                 _p(cu_new), total_new, _p(ctx_len), batch, max_new, shared_len, scale,
+                                                 _p(out), _p(lse), _p(rows), rows_bytes, _p(workspace),
+                                                 workspace_bytes, _stream(stream)))
+
+
+def dflash_shared_rows_bytes(heads: dflash_heads, max_batch: int, max_new: int) -> int:
+    n = load().dflash_shared_rows_bytes(ctypes.byref(heads), max_batch, max_new)
+    if n == 0:
+        raise DflashError(-1, dflash_last_error())
+    return n
 
 
 def dflash_token_logprobs(logits, dtype, rows, vocab, row_stride, token_ids, temperature, n_top, logprob, entropy,

@@ -1,6 +1,7 @@
 // Causal attention of the newest 1..16 tokens of each request over its paged
 // cache, which already holds their own keys and values
-// (dflash_cache_attention): decode steps and verification passes.
+// (dflash_cache_attention): decode steps and verification passes; and the same
+// behind a prefix that the requests share (dflash_shared_attention).
 //
 // For query head q of token i (position p = ctx + i) and its kv head's keys:
 //   s_t = scale q.k_t over p - window < t <= p,
@@ -91,7 +92,7 @@ struct __align__(16) Ctrl {
 // p.cs CTAs per tile shares its pages out evenly, with no list to scan, and
 // the shares meet in distributed shared memory: on a request of 2 048 tokens
 // the partials' way through L2 and its counter took 5 of 15 us.
-template <typename T, int D, bool CL>
+template <typename T, int D, bool CL, bool PRE>
 __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using S = Shape<T, D>;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       ct->b = head / p.nkv;
       ct->h = head % p.nkv;
       ct->rt = list % p.tiles;
-      const Req r = request(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
+      const Req r = request<PRE>(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
       const int np = ct->rt < tiles_of(r) ? r.np : 0;
       ct->k = rank * np / p.cs;
       ct->n_mine = (rank + 1) * np / p.cs - ct->k;
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    const long long sum = sum_pages(p, b0, b1, blockIdx.x == 0, tiles_of);
+    const long long sum = sum_pages<PRE>(p, b0, b1, blockIdx.x == 0, tiles_of);
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
       for (int b = b0; b < b1; ++b) {
-        const Req r = request(p, b, false);
+        const Req r = request<PRE>(p, b, false);
         const long long np = r.np, head = np * tiles_of(r), span = head * p.nkv;
         if (lo < pre + span) {
           const long long h = quotient(lo - pre, head), rt = quotient(lo - pre - h * head, np);
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     int cf = 0, cl = 0;
     int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
     long long x = ct->lo;
-    Req r = request(p, b, false);
+    Req r = request<PRE>(p, b, false);
     int issued = 0;
     bool ok = true;
     for (int i = 0; i < n; ++i, ++x) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       ok = !__any_sync(0xffffffffu, !ok);
       if (!ok) break;
       const bool first = i == 0 || (!CL && k == 0), last = i == n - 1 || (!CL && k == r.np - 1);
-      const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
+      const int page = pages_of<PRE>(p, b)[r.p0 + k];
       const bool bad = page < 0 || page >= p.num_pages;
       const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
       if (lane == 0) {
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
           rt = 0;
           if (++h == p.nkv && i + 1 < n) {
             h = 0;
-            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+            do r = request<PRE>(p, ++b, false);   // i + 1 < n: another request with work follows
             while (r.np == 0 && b + 1 < p.B);
           }
         }
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
         *reinterpret_cast<float4 *>(xo + row * D + c4) = acc;
         if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * row) = make_float2(M, L);
       } else if (whole) {
-        write_row<T, D>(dest_of(p, c.row0, c.h, c.rt * ROWS), row, c4, acc, M, L);
+        write_row<T, D, PRE>(dest_of<PRE>(p, D, c.row0, c.h, c.rt * ROWS), row, c4, acc, M, L);
       } else {
         __stcg(reinterpret_cast<float4 *>(part + row * D + c4), acc);
         if (c4 == 0) {
@@ -513,8 +514,8 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<T, D>(dest_of(p, c.row0, c.h, c.rt * ROWS), p.partials, c.cf, c.cl - c.cf + 1, c.slot0, S::PART, ROWS,
-                         rows, ctid, 128);
+        join_parts<T, D, PRE>(dest_of<PRE>(p, D, c.row0, c.h, c.rt * ROWS), p.partials, c.cf, c.cl - c.cf + 1, c.slot0,
+                              S::PART, ROWS, rows, ctid, 128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
     }
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
   }
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
-    const Req r = request(p, ct->b, false);
+    const Req r = request<PRE>(p, ct->b, false);
     const int rows = min(ROWS, r.n * p.g - ct->rt * ROWS), rank = static_cast<int>(cluster_ctarank());
     float *xo = share(share_stage(rows > 0 ? r.np : 0, rank));
     if (n == 0 || !ok)   // nothing to add
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
           acc.z = fmaf(w, v[u].z, acc.z);
           acc.w = fmaf(w, v[u].w, acc.w);
         }
-        write_row<T, D>(dest_of(p, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
+        write_row<T, D, PRE>(dest_of<PRE>(p, D, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
       }
     };
     if (p.cs > 8)
@@ -589,10 +590,10 @@ int row_tiles(const dflash_heads &h, int max_new) {
   return h.dtype == DFLASH_F32 ? (max_new * (h.n_q_heads / h.n_kv_heads) + ROWS - 1) / ROWS : 1;
 }
 
-template <typename T, int D, bool CL>
+template <typename T, int D, bool CL, bool PRE>
 int launch_decode(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
   using S = Shape<T, D>;
-  auto *kernel = decode_kernel<T, D, CL>;
+  auto *kernel = decode_kernel<T, D, CL, PRE>;
   static std::atomic<uint64_t> smem_set, wide_set;
   if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   if (CL && p.cs > 8)
@@ -627,6 +628,90 @@ size_t counter_count(const dflash_heads &h, int batch, int max_new) {
   return static_cast<size_t>(batch) * h.n_kv_heads * row_tiles(h, max_new);
 }
 
+template <typename T, int D>
+int launch_tiles(const dflash_heads &hs, const dflash_kv &kv, Params &p, bool cl, const Device &dev, cudaStream_t s) {
+  if (p.pre.pages > 0)
+    return cl ? launch_decode<T, D, true, true>(hs, kv, p, dev, s) : launch_decode<T, D, false, true>(hs, kv, p, dev, s);
+  return cl ? launch_decode<T, D, true, false>(hs, kv, p, dev, s) : launch_decode<T, D, false, false>(hs, kv, p, dev, s);
+}
+
+// One launch over p.B requests of at most `rows` query rows per kv head and
+// `pages` pages.
+int launch_attention(const dflash_heads &hs, const dflash_kv &kv, Params &p, long long rows, int pages, const Device &dev,
+                     cudaStream_t s) {
+  const bool f32 = hs.dtype == DFLASH_F32;
+  const int d = hs.head_dim;
+  if (!f32 && rows > ROWS) return launch_verify(hs, kv, p, pages, dev, s);
+  // Clusters of up to 16 CTAs per tile while one CTA per SM holds them all (8,
+  // and three quarters of the SMs, where a CTA fills its SM), down to a CTA per
+  // tile while all are resident, and while the capacity leaves a CTA 16 pages
+  // at most: beyond that the balanced runs over the whole GPU are faster
+  // (32 x 8 tiles of 1..4 pages: 8.5 us on a CTA each, 14 in runs; 64 x 8 the
+  // same either way, 256 x 8 51 and 39).
+  const long long lists = static_cast<long long>(p.B) * p.nkv * p.tiles;
+  p.cs = 1;
+  const bool big = f32 && d == 128;
+  while (p.cs < (big ? 8 : 16) && lists * p.cs * 2 <= (big ? dev.sms * 3 / 4 : dev.sms)) p.cs *= 2;
+  const bool cl = pages <= 16 * p.cs && lists <= (big ? dev.sms : 2 * dev.sms);
+  if (f32) return d == 64 ? launch_tiles<float, 64>(hs, kv, p, cl, dev, s) : launch_tiles<float, 128>(hs, kv, p, cl, dev, s);
+  return d == 64 ? launch_tiles<__nv_bfloat16, 64>(hs, kv, p, cl, dev, s)
+                 : launch_tiles<__nv_bfloat16, 128>(hs, kv, p, cl, dev, s);
+}
+
+// The arguments that both entry points share, checked and taken over; p.B == 0:
+// nothing to do.
+int take(const char *who, const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q, long long q_stride,
+         const int32_t *cu_new, int total_new, const int32_t *ctx_len, int batch, int max_new, float scale, void *out,
+         float *lse, void *workspace, size_t workspace_bytes, Params &p) {
+  if (int e = check_heads(who, hs)) return e;
+  if (max_new < 1 || max_new > TARGET_MAX_NEW)
+    return set_error(DFLASH_ERR_ARG, "%s: max_new must be 1..%d", who, TARGET_MAX_NEW);
+  const int nq = hs->n_q_heads, nkv = hs->n_kv_heads, d = hs->head_dim;
+  const size_t need = HEADER_BYTES + PART_BYTES + counter_count(*hs, batch > 0 ? batch : 0, max_new) * sizeof(int);
+  if (int e = check_target(who, hs, kv, layer, q, q_stride, nq * d, cu_new, total_new, ctx_len, batch, workspace,
+                           workspace_bytes, need))
+    return e;
+  if (total_new > 0 && !out) return set_error(DFLASH_ERR_ARG, "%s: null out", who);
+  if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(DFLASH_ERR_ALIGN, "%s: out not 16-byte aligned", who);
+  if (off_words(lse)) return set_error(DFLASH_ERR_ALIGN, "%s: lse not aligned to its elements", who);
+  if (!(scale > 0.f) || !(scale < 2.0e38f))   // its product with log2(e) is finite
+    return set_error(DFLASH_ERR_ARG, "%s: scale must be positive and below 2e38", who);
+  p = Params();
+  if (batch == 0 || total_new == 0) return DFLASH_OK;
+  const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
+  p.q = q;
+  p.ldq = q_stride;
+  p.out = out;
+  p.lse = lse;
+  p.k = static_cast<const char *>(kv->k_cache) + off;
+  p.v = static_cast<const char *>(kv->v_cache) + off;
+  p.page_table = kv->page_table;
+  p.cu_new = cu_new;
+  p.ctx_len = ctx_len;
+  p.max_pages = kv->max_pages;
+  p.num_pages = kv->num_pages;
+  p.B = batch;
+  p.nkv = nkv;
+  p.g = nq / nkv;
+  p.total = total_new;
+  p.max_new = max_new;
+  p.scale_log2 = scale * LOG2E_F;
+  p.tiles = row_tiles(*hs, max_new);
+  p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + HEADER_BYTES);
+  p.counters = reinterpret_cast<int *>(static_cast<char *>(workspace) + HEADER_BYTES + PART_BYTES);
+  p.status = static_cast<int *>(workspace);
+  return DFLASH_OK;
+}
+
+// rows of a valid batch: each of its requests has at most max_new
+int row_cap(int total_new, int batch, int max_new) {
+  const long long most = static_cast<long long>(batch) * max_new;
+  return static_cast<int>(most < total_new ? most : total_new);
+}
+size_t share_bytes(const dflash_heads &h, int rows) {
+  return static_cast<size_t>(rows) * h.n_q_heads * (h.head_dim + 2) * sizeof(float);
+}
+
 }  // namespace
 }  // namespace dflash
 
@@ -649,68 +734,75 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
                                       const int32_t *ctx_len, int batch, int max_new, int window, float scale,
                                       void *out, float *lse, void *workspace, size_t workspace_bytes,
                                       dflash_stream_t stream) {
-  const char *who = "cache_attention";
-  if (int e = check_heads(who, hs)) return e;
-  if (max_new < 1 || max_new > TARGET_MAX_NEW)
-    return set_error(DFLASH_ERR_ARG, "cache_attention: max_new must be 1..%d", TARGET_MAX_NEW);
-  const int nq = hs->n_q_heads, nkv = hs->n_kv_heads, d = hs->head_dim;
-  const size_t need = HEADER_BYTES + PART_BYTES + counter_count(*hs, batch > 0 ? batch : 0, max_new) * sizeof(int);
-  if (int e = check_target(who, hs, kv, layer, q, q_stride, nq * d, cu_new, total_new, ctx_len, batch, workspace,
-                           workspace_bytes, need))
+  if (window < 0) return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0");
+  Params p;
+  if (int e = take("cache_attention", hs, kv, layer, q, q_stride, cu_new, total_new, ctx_len, batch, max_new, scale, out,
+                   lse, workspace, workspace_bytes, p))
     return e;
-  if (total_new > 0 && !out) return set_error(DFLASH_ERR_ARG, "cache_attention: null out");
-  if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(DFLASH_ERR_ALIGN, "cache_attention: out not 16-byte aligned");
-  if (off_words(lse)) return set_error(DFLASH_ERR_ALIGN, "cache_attention: lse not aligned to its elements");
-  if (window < 0 || !(scale > 0.f) || !(scale < 2.0e38f))   // its product with log2(e) is finite
-    return set_error(DFLASH_ERR_ARG, "cache_attention: window must be >= 0 and scale positive and below 2e38");
-  if (batch == 0 || total_new == 0) return DFLASH_OK;
+  if (p.B == 0) return DFLASH_OK;
   Device dev;
   if (int e = current_device(&dev)) return e;
-  const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
-  Params p = {};
-  p.q = q;
-  p.ldq = q_stride;
-  p.out = out;
-  p.lse = lse;
-  p.k = static_cast<const char *>(kv->k_cache) + off;
-  p.v = static_cast<const char *>(kv->v_cache) + off;
-  p.page_table = kv->page_table;
-  p.cu_new = cu_new;
-  p.ctx_len = ctx_len;
-  p.max_pages = kv->max_pages;
-  p.num_pages = kv->num_pages;
-  p.B = batch;
-  p.nkv = nkv;
-  p.g = nq / nkv;
-  p.total = total_new;
-  p.max_new = max_new;
   p.window = window;
-  p.scale_log2 = scale * LOG2E_F;
-  p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + HEADER_BYTES);
-  p.counters = reinterpret_cast<int *>(static_cast<char *>(workspace) + HEADER_BYTES + PART_BYTES);
-  p.status = static_cast<int *>(workspace);
+  return launch_attention(*hs, *kv, p, static_cast<long long>(max_new) * p.g, kv->max_pages, dev,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+DFLASH_API size_t dflash_shared_rows_bytes(const dflash_heads *hs, int max_batch, int max_new) {
+  if (check_heads("shared_rows_bytes", hs)) return 0;
+  if (max_batch < 1 || max_batch > DFLASH_MAX_BATCH || max_new < 1 || max_new > TARGET_MAX_NEW) {
+    set_error(DFLASH_ERR_ARG, "shared_rows_bytes: max_batch must be 1..%d and max_new 1..%d", DFLASH_MAX_BATCH,
+              TARGET_MAX_NEW);
+    return 0;
+  }
+  return share_bytes(*hs, max_batch * max_new);
+}
+
+DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q,
+                                       long long q_stride, const int32_t *cu_new, int total_new,
+                                       const int32_t *ctx_len, int batch, int max_new, int shared_len, float scale,
+                                       void *out, float *lse, void *rows, size_t rows_bytes, void *workspace,
+                                       size_t workspace_bytes, dflash_stream_t stream) {
+  const char *who = "shared_attention";
+  Params p;
+  if (int e = take(who, hs, kv, layer, q, q_stride, cu_new, total_new, ctx_len, batch, max_new, scale, out, lse, workspace,
+                   workspace_bytes, p))
+    return e;
+  if (shared_len < 0 || shared_len % PAGE || shared_len / PAGE >= kv->max_pages)
+    return set_error(DFLASH_ERR_SHAPE, "shared_attention: shared_len must be whole pages of %d, fewer than max_pages", PAGE);
+  if (p.B == 0) return DFLASH_OK;
+  const int most = row_cap(total_new, batch, max_new);
+  if (shared_len > 0) {
+    if (!rows) return set_error(DFLASH_ERR_ARG, "shared_attention: null rows");
+    if (reinterpret_cast<uintptr_t>(rows) & 15) return set_error(DFLASH_ERR_ALIGN, "shared_attention: rows not 16-byte aligned");
+    if (rows_bytes < share_bytes(*hs, most))
+      return set_error(DFLASH_ERR_SHAPE, "shared_attention: rows of %zu bytes, %zu needed", rows_bytes, share_bytes(*hs, most));
+  }
+  Device dev;
+  if (int e = current_device(&dev)) return e;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f32 = hs->dtype == DFLASH_F32;
-  p.tiles = row_tiles(*hs, max_new);
-  if (!f32 && max_new * p.g > ROWS) return launch_verify(*hs, *kv, p, dev, s);
-  // Clusters of up to 16 CTAs per tile while one CTA per SM holds them all (8,
-  // and three quarters of the SMs, where a CTA fills its SM), down to a CTA per
-  // tile while all are resident, and while the capacity leaves a CTA 16 pages
-  // at most: beyond that the balanced runs over the whole GPU are faster
-  // (32 x 8 tiles of 1..4 pages: 8.5 us on a CTA each, 14 in runs; 64 x 8 the
-  // same either way, 256 x 8 51 and 39).
-  const long long lists = static_cast<long long>(batch) * nkv * p.tiles;
-  p.cs = 1;
-  const bool big = f32 && d == 128;
-  while (p.cs < (big ? 8 : 16) && lists * p.cs * 2 <= (big ? dev.sms * 3 / 4 : dev.sms)) p.cs *= 2;
-  const bool cl = kv->max_pages <= 16 * p.cs && lists <= (big ? dev.sms : 2 * dev.sms);
-#define DECODE(T_, D_) \
-  return cl ? launch_decode<T_, D_, true>(*hs, *kv, p, dev, s) : launch_decode<T_, D_, false>(*hs, *kv, p, dev, s)
-  if (f32 && d == 64) DECODE(float, 64);
-  if (f32) DECODE(float, 128);
-  if (d == 64) DECODE(__nv_bfloat16, 64);
-  DECODE(__nv_bfloat16, 128);
-#undef DECODE
+  const int pages = shared_len / PAGE;
+  if (pages > 0) {
+    p.pre.rows = static_cast<float *>(rows);
+    p.pre.row_cap = most;
+    p.pre.pages = pages;
+    p.pre.batch = batch;
+    // The prefix.  Tiles of 16 rows (fp32, or all there are): one request with
+    // every row in tiles; of 128 rows: runs of as many whole tokens.
+    Params x = p;
+    const bool f32 = hs->dtype == DFLASH_F32;
+    const long long all = static_cast<long long>(most) * p.g;
+    if (f32 || all <= ROWS) {
+      x.B = 1;
+      x.pre.tile_tokens = most;
+      x.tiles = static_cast<int>((all + ROWS - 1) / ROWS);
+    } else {
+      x.pre.tile_tokens = 128 / p.g;
+      x.B = (most + x.pre.tile_tokens - 1) / x.pre.tile_tokens;
+    }
+    // its tiles' counters: at most batch * row_tiles(max_new) for each kv head, as many as the second launch has
+    if (int e = launch_attention(*hs, *kv, x, all, pages, dev, s)) return e;
+  }
+  return launch_attention(*hs, *kv, p, static_cast<long long>(max_new) * p.g, kv->max_pages - pages, dev, s);
 }
 
 }  // extern "C"

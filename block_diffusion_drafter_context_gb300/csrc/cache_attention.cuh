@@ -1,5 +1,6 @@
-// What the kernels of dflash_cache_attention share: the call's parameters, the
-// list of pages they cut into runs, and the join of partial results.
+// What the kernels of dflash_cache_attention and dflash_shared_attention share:
+// the call's parameters, the list of pages they cut into runs, and the join of
+// partial results.
 #pragma once
 
 #include "common.cuh"
@@ -17,6 +18,19 @@ constexpr size_t HEADER_BYTES = 256;
 constexpr size_t PART_BYTES = 22u << 20;   // workspace for partials: (max, sum, O) of up to two tiles per CTA
 constexpr size_t PART_TOTAL = PART_BYTES / sizeof(float);
 
+// dflash_shared_attention is two launches.  The first takes the prefix that the
+// batch shares for one request: its "requests" are runs of `tile_tokens` tokens,
+// whosever they are, that see every position of the prefix, and a row's
+// (O, maximum, sum) go to `rows`.  The second takes each request's own pages,
+// and joins them where it writes a row.
+struct Prefix {
+  float *rows;         // [row_cap][nq][D] O, then [row_cap][nq] (maximum, sum); row 0 is the batch's first
+  int row_cap;         // rows a valid batch has at most
+  int pages;           // of the prefix
+  int tile_tokens;     // first launch: tokens per run; second: 0
+  int batch;           // requests (Params.B counts runs in the first launch)
+};
+
 struct Params {
   const void *q;
   long long ldq;
@@ -33,6 +47,7 @@ struct Params {
   int *counters;
   float *partials;
   int *status;
+  Prefix pre;                              // dflash_shared_attention
 };
 
 // One request's place: rows row0 .. row0+n-1, ctx tokens before them, pages
@@ -41,33 +56,65 @@ struct Req {
   int row0, n, ctx, p0, np;
 };
 
+// PRE in all of the following: a launch of dflash_shared_attention.
+template <bool PRE>
 __device__ __forceinline__ Req make_request(const Params &p, int row0, int next, int ctx, bool tell) {
   Req r;
   r.row0 = row0;
   const long long n = static_cast<long long>(next) - row0;
   r.ctx = ctx;
-  const bool ok = r.row0 >= 0 && n >= 0 && n <= p.max_new && r.row0 + n <= p.total && r.ctx >= 0 &&
-                  r.ctx + n <= static_cast<long long>(p.max_pages) * PAGE;
+  bool ok = r.row0 >= 0 && n >= 0 && n <= p.max_new && r.row0 + n <= p.total && r.ctx >= 0 &&
+            r.ctx + n <= static_cast<long long>(p.max_pages) * PAGE;
+  if (PRE) {   // behind the prefix, and among the rows that have a share of it
+    const int begin = p.cu_new[0];
+    ok = ok && begin >= 0 && row0 >= begin && next - begin <= p.pre.row_cap && (n == 0 || ctx >= p.pre.pages * PAGE);
+  }
   if (!ok && tell) report(p.status, DFLASH_ERR_DEVICE);
   r.n = ok ? static_cast<int>(n) : 0;
   r.p0 = 0;
   r.np = 0;
   if (r.n > 0) {
     const int lo = p.window > 0 ? max(0, r.ctx - p.window + 1) : 0;
-    r.p0 = lo / PAGE;
+    r.p0 = PRE ? p.pre.pages : lo / PAGE;
     r.np = (r.ctx + r.n - 1) / PAGE - r.p0 + 1;
   }
   return r;
 }
 
+// Run j of the first launch: the prefix lies before all of its tokens.
+__device__ __forceinline__ Req prefix_run(const Params &p, int j) {
+  const int begin = min(max(0, p.cu_new[0]), p.total);
+  const int end = min(p.cu_new[p.pre.batch], begin + min(p.total - begin, p.pre.row_cap));   // `rows` holds no more
+  Req r;
+  r.row0 = begin + j * p.pre.tile_tokens;
+  r.n = max(0, min(p.pre.tile_tokens, end - r.row0));
+  r.ctx = p.pre.pages * PAGE;
+  r.p0 = 0;
+  r.np = r.n > 0 ? p.pre.pages : 0;
+  return r;
+}
+template <bool PRE>
 __device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
-  return make_request(p, p.cu_new[b], p.cu_new[b + 1], p.ctx_len[b], tell);
+  if (PRE && p.pre.tile_tokens) return prefix_run(p, b);
+  return make_request<PRE>(p, p.cu_new[b], p.cu_new[b + 1], p.ctx_len[b], tell);
+}
+// its row of the page table: the first request's holds the prefix
+template <bool PRE>
+__device__ __forceinline__ const int32_t *pages_of(const Params &p, int b) {
+  return p.page_table + (PRE && p.pre.tile_tokens ? 0 : static_cast<size_t>(b) * p.max_pages);
 }
 // Pages of requests b0 .. b1-1, each as often as it has row tiles; four
 // requests' loads at a time (one by one, 4096 requests took 45 us).
-template <typename Tiles>
+template <bool PRE, typename Tiles>
 __device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, bool tell, Tiles tiles_of) {
   long long sum = 0;
+  if (PRE && p.pre.tile_tokens) {
+    for (int b = b0; b < b1; ++b) {
+      const Req r = prefix_run(p, b);
+      sum += static_cast<long long>(r.np) * tiles_of(r);
+    }
+    return sum;
+  }
   for (int b = b0; b < b1; b += 4) {
     int row0[5], ctx[4];
 #pragma unroll
@@ -77,7 +124,7 @@ __device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (b + i < b1) {
-        const Req r = make_request(p, row0[i], row0[i + 1], ctx[i], tell);
+        const Req r = make_request<PRE>(p, row0[i], row0[i + 1], ctx[i], tell);
         sum += static_cast<long long>(r.np) * tiles_of(r);
       }
   }
@@ -129,9 +176,20 @@ struct Dest {
   float *lse;
   int row0, h, nkv, g;     // the request's first row, the kv head
   int base;                // the tile's first query row
+  float *share;            // PRE: the prefix's share of the request's first row, its maximum and sum
+  float2 *share_ml;
+  bool first;              // PRE: the first launch
 };
-__device__ __forceinline__ Dest dest_of(const Params &p, int row0, int h, int base = 0) {
-  return {p.out, p.lse, row0, h, p.nkv, p.g, base};
+template <bool PRE>
+__device__ __forceinline__ Dest dest_of(const Params &p, int D, int row0, int h, int base = 0) {
+  Dest d = {p.out, p.lse, row0, h, p.nkv, p.g, base, nullptr, nullptr, false};
+  if (PRE) {
+    const size_t nq = static_cast<size_t>(p.nkv) * p.g, at = (row0 - max(0, p.cu_new[0])) * nq;
+    d.share = p.pre.rows + at * D;
+    d.share_ml = reinterpret_cast<float2 *>(p.pre.rows + static_cast<size_t>(p.pre.row_cap) * nq * D) + at;
+    d.first = p.pre.tile_tokens > 0;
+  }
+  return d;
 }
 
 // A share's maximum as it goes into a join: +inf where its sum is NaN (a NaN
@@ -149,10 +207,42 @@ __device__ __forceinline__ float log_sum(float M, float L) {
   return L != 0.f ? (M + log2f(L)) * LN2_F : M == -INFINITY ? -INFINITY : NAN;
 }
 
+// (M, L) joined with the prefix's share: the factors of both O.  A row of
+// nothing (M = -inf) has 0 in both.
+struct Join2 {
+  float own, pre;
+};
+__device__ __forceinline__ Join2 join_prefix(float &M, float &L, float2 pre) {
+  const float m = fmaxf(M, pre.x);
+  Join2 f = {0.f, 0.f};
+  if (m != -INFINITY) {
+    f.own = fast_exp2(M - m);
+    f.pre = fast_exp2(pre.x - m);
+  }
+  M = m;
+  L = f.own * L + f.pre * pre.y;
+  return f;
+}
+
 // Row `row` of the tile: output columns c4 .. c4 + 3, and its log-sum-exp.
-template <typename T, int D>
+template <typename T, int D, bool PRE>
 __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
   row += p.base;
+  if (PRE) {
+    const size_t i = static_cast<size_t>(row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
+    float4 *share = reinterpret_cast<float4 *>(p.share + i * D + c4);
+    if (p.first) {
+      __stcg(share, o);
+      if (c4 == 0) __stcg(p.share_ml + i, make_float2(M, L));
+      return;
+    }
+    const float4 v = __ldcg(share);
+    const Join2 f = join_prefix(M, L, __ldcg(p.share_ml + i));
+    o.x = f.own * o.x + f.pre * v.x;
+    o.y = f.own * o.y + f.pre * v.y;
+    o.z = f.own * o.z + f.pre * v.z;
+    o.w = f.own * o.w + f.pre * v.w;
+  }
   const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
   const float inv = inverse_sum(M, L);
   T *dst = static_cast<T *>(p.out) + at * D + c4;
@@ -167,7 +257,7 @@ __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4
 // partials (O [tile_rows][D], maxima [tile_rows], sums [tile_rows], at
 // src(0..np-1)), in that order.  The partials sit in L2, so the time is its
 // latency: NV float4 columns and B partials per thread are in flight.
-template <typename T, int D, int NV, int B, typename Src>
+template <typename T, int D, bool PRE, int NV, int B, typename Src>
 __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int tile_rows, int rows, int tid, int nthr) {
   constexpr int PER = D / 4 / NV;   // items per row
   for (int e = tid; e < rows * PER; e += nthr) {
@@ -213,25 +303,26 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
       }
     }
 #pragma unroll
-    for (int k = 0; k < NV; ++k) write_row<T, D>(p, r, c + 4 * PER * k, acc[k], M, L);
+    for (int k = 0; k < NV; ++k) write_row<T, D, PRE>(p, r, c + 4 * PER * k, acc[k], M, L);
   }
 }
 // the same for the runs' partials: np contributors from CTA cf on, a tile's
 // slot at (CTA * 2 + slot) * stride.  Not inlined: the kernels' main loops have
 // no registers to spare for it.
-template <typename T, int D>
+template <typename T, int D, bool PRE>
 __device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, int np, int slot0, int stride, int tile_rows,
                                         int rows, int tid, int nthr) {
   auto src = [&](int i) { return partials + (static_cast<size_t>(cf + i) * 2 + (i > 0 || slot0 ? 0 : 1)) * stride; };
   if (rows * (D / 4) <= 2 * nthr)
-    join_tile<T, D, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, PRE, 1, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else if (np > 4)
-    join_tile<T, D, 4, 8>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, PRE, 4, 8>(p, src, np, tile_rows, rows, tid, nthr);
   else
-    join_tile<T, D, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
+    join_tile<T, D, PRE, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
 }
 
 // 17..128 query rows per (request, kv head) on tcgen05 (cache_attention_tc.cu).
-int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s);
+// `pages`: the longest list of a (request, kv head) that the call may have.
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int pages, const Device &dev, cudaStream_t s);
 
 }  // namespace dflash

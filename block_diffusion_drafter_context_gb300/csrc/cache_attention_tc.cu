@@ -67,7 +67,7 @@ static_assert(sizeof(Ctrl) <= 4096, "shared memory");
 
 // CL: few (request, kv head)s over short capacities: one cluster of p.cs CTAs
 // per tile, joined in distributed shared memory.
-template <int D, bool CL>
+template <int D, bool CL, bool PRE>
 __global__ void __launch_bounds__(NTHR, 1)
     verify_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using S = Shape<D>;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
       ct->b = list / p.nkv;
       ct->h = list % p.nkv;
-      const int np = request(p, ct->b, rank == 0 && ct->h == 0).np;
+      const int np = request<PRE>(p, ct->b, rank == 0 && ct->h == 0).np;
       ct->k = rank * np / p.cs;
       ct->n_mine = (rank + 1) * np / p.cs - ct->k;
     }
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     // Lane i sums the pages of a contiguous slice of the requests; a warp
     // scan gives the list length and the slice holding this CTA's start.
     const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    const long long sum = sum_pages(p, b0, b1, blockIdx.x == 0, [](const Req &) { return 1; });
+    const long long sum = sum_pages<PRE>(p, b0, b1, blockIdx.x == 0, [](const Req &) { return 1; });
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
       long long pre = ex;
       for (int b = b0; b < b1; ++b) {
-        const long long np = request(p, b, false).np, span = np * p.nkv;
+        const long long np = request<PRE>(p, b, false).np, span = np * p.nkv;
         if (lo < pre + span) {
           ct->b = b;
           const long long h = quotient(lo - pre, np);
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       int cf = 0, cl = 0, i0 = 0, i1 = 0;
       int b = ct->b, h = ct->h, k = ct->k, issued = 0;
       long long x = ct->lo;
-      Req r = request(p, b, false);
+      Req r = request<PRE>(p, b, false);
       bool ok = true, fresh = true;
       for (int i = 0; i < n; ++i, ++x) {
         const int st = i % ST;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
         ok = !__any_sync(0xffffffffu, !ok);
         if (!ok) break;
-        const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + r.p0 + k];
+        const int page = pages_of<PRE>(p, b)[r.p0 + k];
         const bool bad = page < 0 || page >= p.num_pages;
         if (lane == 0) {
           if (bad) report(p.status, DFLASH_ERR_DEVICE);
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           fresh = true;
           if (++h == p.nkv && i + 1 < n) {
             h = 0;
-            do r = request(p, ++b, false);   // i + 1 < n: another request with work follows
+            do r = request<PRE>(p, ++b, false);   // i + 1 < n: another request with work follows
             while (r.np == 0 && b + 1 < p.B);
           }
         }
@@ -500,7 +500,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       const int rows = last.n * g;
       const size_t at = static_cast<size_t>(last.row0 + (live ? tok : 0)) * (p.nkv * g) + last.h * g + head;
       float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
-      const float inv = inverse_sum(M, L);
+      float Mr = M, Lr = L;   // with PRE: of the row, the prefix in it
+      Join2 fr = {1.f, 0.f};
+      const bool keep = PRE && p.pre.tile_tokens;   // the first launch: rows stay shares
+      Dest dest;
+      size_t share_at = 0;
+      if (PRE && whole) {
+        dest = dest_of<true>(p, D, last.row0, last.h);
+        share_at = static_cast<size_t>(live ? tok : 0) * (p.nkv * g) + last.h * g + head;
+        if (!keep) fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + share_at));
+      }
+      const float inv = inverse_sum(Mr, Lr);
 #pragma unroll
       for (int c0 = 0; c0 < D / 16; c0 += 2) {
         uint32_t a[2][16], b[2][16];
@@ -528,6 +538,22 @@ __global__ void __launch_bounds__(NTHR, 1)
               *reinterpret_cast<float4 *>(xo + row * D + ((((c0 + u) * 4 + t) ^ (row & (D / 4 - 1))) << 2)) =
                   make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
           } else if (whole) {
+            if (PRE) {
+              float4 *share = reinterpret_cast<float4 *>(dest.share + share_at * D + (c0 + u) * 16);
+              if (keep) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) __stcg(share + t, make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]));
+                continue;
+              }
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const float4 x = __ldcg(share + t);
+                v[4 * t] = fr.own * v[4 * t] + fr.pre * x.x;
+                v[4 * t + 1] = fr.own * v[4 * t + 1] + fr.pre * x.y;
+                v[4 * t + 2] = fr.own * v[4 * t + 2] + fr.pre * x.z;
+                v[4 * t + 3] = fr.own * v[4 * t + 3] + fr.pre * x.w;
+              }
+            }
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
@@ -552,7 +578,11 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (two) mbar_arrive(&ct->oempty[wg ^ 1]);
       }
       if (whole) {
-        if (live && p.lse) p.lse[at] = log_sum(M, L);
+        if (keep) {
+          if (live) __stcg(dest.share_ml + share_at, make_float2(M, L));
+        } else if (live && p.lse) {
+          p.lse[at] = log_sum(Mr, Lr);
+        }
         continue;
       }
       if (live) {
@@ -570,8 +600,8 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (!(ok = csync())) break;
       if (ct->merge[wg])
-        join_parts<__nv_bfloat16, D>(dest_of(p, last.row0, last.h), p.partials, last.cf, last.cl - last.cf + 1, last.slot0,
-                                     S::PART, MROWS, rows, tid, 4 * 32);
+        join_parts<__nv_bfloat16, D, PRE>(dest_of<PRE>(p, D, last.row0, last.h), p.partials, last.cf, last.cl - last.cf + 1,
+                                          last.slot0, S::PART, MROWS, rows, tid, 4 * 32);
     }
     if (!ok) {
       report(p.status, DFLASH_ERR_TIMEOUT);
@@ -585,14 +615,14 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
-    const Req r = request(p, ct->b, false);
+    const Req r = request<PRE>(p, ct->b, false);
     const int rows = r.n * g, rank = static_cast<int>(cluster_ctarank());
     float *xo = reinterpret_cast<float *>(ring);
     if (n == 0 || ct->abort_flag)   // nothing to add
       for (int i = threadIdx.x; i < MROWS; i += NTHR) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
     __syncwarp();
     cluster_sync();
-    const Dest dest = dest_of(p, r.row0, ct->h);
+    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->h);
     const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
     for (int e = rank * per + threadIdx.x; e < end; e += NTHR) {
       const int row = e / (D / 4), c = e % (D / 4);
@@ -619,7 +649,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         acc.z = fmaf(w, v[u].z, acc.z);
         acc.w = fmaf(w, v[u].w, acc.w);
       }
-      write_row<__nv_bfloat16, D>(dest, row, c * 4, acc, M, L);
+      write_row<__nv_bfloat16, D, PRE>(dest, row, c * 4, acc, M, L);
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while its share is read
@@ -628,10 +658,10 @@ __global__ void __launch_bounds__(NTHR, 1)
 
 }  // namespace
 
-template <int D, bool CL>
+template <int D, bool CL, bool PRE>
 static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
   using S = Shape<D>;
-  auto *kernel = verify_kernel<D, CL>;
+  auto *kernel = verify_kernel<D, CL, PRE>;
   static std::atomic<uint64_t> smem_set;
   if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
@@ -657,7 +687,7 @@ static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   return cuda_check(cudaLaunchKernelEx(&cfg, kernel, tk, tv, p), "cache_attention launch");
 }
 
-int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const Device &dev, cudaStream_t s) {
+int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int pages, const Device &dev, cudaStream_t s) {
   // the rule of the narrower tiles: clusters while the SMs hold them all (three
   // quarters of them: a cluster stays within a GPC, and 16 of 8 CTAs that fill
   // an SM each took two waves, 14 us against 9), a CTA per tile while all are
@@ -665,9 +695,15 @@ int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   const long long lists = static_cast<long long>(p.B) * p.nkv;
   p.cs = 1;
   while (p.cs < 8 && lists * p.cs * 2 <= dev.sms * 3 / 4) p.cs *= 2;
-  const bool cl = kv.max_pages <= 16 * p.cs && lists <= dev.sms;
-  if (hs.head_dim == 64) return cl ? launch<64, true>(hs, kv, p, dev, s) : launch<64, false>(hs, kv, p, dev, s);
-  return cl ? launch<128, true>(hs, kv, p, dev, s) : launch<128, false>(hs, kv, p, dev, s);
+  const bool cl = pages <= 16 * p.cs && lists <= dev.sms;
+  auto go = [&](auto d, auto pre) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool PRE = decltype(pre)::value;
+    return cl ? launch<D, true, PRE>(hs, kv, p, dev, s) : launch<D, false, PRE>(hs, kv, p, dev, s);
+  };
+  const bool pre = p.pre.pages > 0;
+  if (hs.head_dim == 64) return pre ? go(Count<64>(), Count<1>()) : go(Count<64>(), Count<0>());
+  return pre ? go(Count<128>(), Count<1>()) : go(Count<128>(), Count<0>());
 }
 
 }  // namespace dflash

@@ -51,11 +51,12 @@ class TargetOps:
 
     max_batch, max_new: the largest batch and the most new tokens per request
     (1..16) of an ``attend`` call; ``append_kv`` takes any number of tokens.
-    rope_base: 0 for layers without rotation.  The object outlives its calls:
+    rope_base: 0 for layers without rotation.  shared_prefix: with the scratch
+    that ``attend_shared`` wants, a row of fp32 outputs per token.  The object outlives its calls:
     one that is let go frees the workspace for the stream it was made on."""
 
     def __init__(self, n_q_heads, n_kv_heads, head_dim, dtype="bf16", max_batch=64, max_new=16, rope_base=1e6,
-                 eps=1e-6, device="cuda"):
+                 eps=1e-6, device="cuda", shared_prefix=False):
         torch = _torch()
         self.dtype = _dtype(dtype)
         self.nq, self.nkv, self.d = int(n_q_heads), int(n_kv_heads), int(head_dim)
@@ -65,6 +66,8 @@ class TargetOps:
         self.ws_bytes = B.dflash_target_workspace_bytes(self.heads, self.max_batch, self.max_new)
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        self.rows_bytes = B.dflash_shared_rows_bytes(self.heads, self.max_batch, self.max_new) if shared_prefix else 0
+        self.rows = torch.empty(self.rows_bytes, dtype=torch.uint8, device=self.device) if shared_prefix else None
         with torch.cuda.device(self.device):     # the first call may be on another stream
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream().synchronize()
@@ -109,6 +112,24 @@ class TargetOps:
         if out.dtype is not self.dtype or out.device != self.device or out.shape != (rows, width) \
                 or not out.is_contiguous():
             raise ValueError(f"{what} must be a contiguous {self.dtype} [{rows}][{width}] on {self.device}")
+
+    def _results(self, rows, out, want_lse, lse):
+        torch = self._torch
+        if out is None:
+            out = torch.empty((rows, self.nq * self.d), dtype=self.dtype, device=self.device)
+        else:
+            self._out(out, rows, "out")
+        if lse is None:
+            if want_lse:
+                lse = torch.empty((rows, self.nq), dtype=torch.float32, device=self.device)
+        else:
+            self._lse(lse, rows)
+        return out, lse
+
+    def _lse(self, lse, rows):
+        if lse.dtype is not self._torch.float32 or lse.shape != (rows, self.nq) or lse.device != self.device \
+                or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous fp32 [{rows}][{self.nq}] on {self.device}")
 
     def append_kv(self, kv, layer, qkv, cu_new, ctx_len, g_q=None, g_k=None, q_out=None, stream=None):
         """K and V of the rows of qkv ([tokens][(nq + 2 nkv) d], the fused
@@ -155,21 +176,38 @@ class TargetOps:
         ld = self._rows("q", q, self.nq * self.d)
         batch = self._cache(kv, layer, cu_new, ctx_len)
         rows = q.shape[0]
-        if out is None:
-            out = torch.empty((rows, self.nq * self.d), dtype=self.dtype, device=self.device)
-        else:
-            self._out(out, rows, "out")
-        if lse is None:
-            if want_lse:
-                lse = torch.empty((rows, self.nq), dtype=torch.float32, device=self.device)
-        elif lse.dtype is not torch.float32 or lse.shape != (rows, self.nq) or lse.device != self.device \
-                or not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous fp32 [{rows}][{self.nq}] on {self.device}")
+        out, lse = self._results(rows, out, want_lse, lse)
         rc = self._lib.dflash_cache_attention(
             self._heads, kv.struct_ref, layer, q.data_ptr(), ld, cu_new.data_ptr(), rows, ctx_len.data_ptr(), batch,
             self.max_new if max_new is None else max_new, window, self._scale if scale is None else scale,
             out.data_ptr(), None if lse is None else lse.data_ptr(), self._ws, self.ws_bytes,
             B.raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+        return out if lse is None else (out, lse)
+
+    def attend_shared(self, kv, layer, q, cu_new, ctx_len, shared_len, max_new=None, scale=None, out=None,
+                      want_lse=False, lse=None, stream=None):
+        """``attend`` (without a window) for requests that share their first
+        shared_len tokens, whole pages: those are read and multiplied once for
+        all of the batch's rows, from the pages of the first request's row of
+        the page table.  ctx_len counts them in.  Needs an object made with
+        shared_prefix=True."""
+        torch = self._torch
+        if stream is not None or torch.cuda.current_device() != self.device.index:
+            with _on(stream, self.device):
+                return self.attend_shared(kv, layer, q, cu_new, ctx_len, shared_len, max_new, scale, out, want_lse, lse)
+        if self.rows is None:
+            raise ValueError("these operators were made without shared_prefix=True")
+        ld = self._rows("q", q, self.nq * self.d)
+        batch = self._cache(kv, layer, cu_new, ctx_len)
+        rows = q.shape[0]
+        out, lse = self._results(rows, out, want_lse, lse)
+        rc = self._lib.dflash_shared_attention(
+            self._heads, kv.struct_ref, layer, q.data_ptr(), ld, cu_new.data_ptr(), rows, ctx_len.data_ptr(), batch,
+            self.max_new if max_new is None else max_new, shared_len, self._scale if scale is None else scale,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), self.rows.data_ptr(), self.rows_bytes, self._ws,
+            self.ws_bytes, B.raw_stream(self.device.index))
         if rc:
             B._check(rc)
         return out if lse is None else (out, lse)

@@ -527,6 +527,36 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
                            int batch, int max_new, int window, float scale, void *out, float *lse,
                            void *workspace, size_t workspace_bytes, dflash_stream_t stream);
 
+/* The same attention for a batch whose requests share a long prefix: the
+ * positions 0 .. shared_len-1 are read and multiplied once for the rows of all
+ * requests, and joined with each request's own positions
+ * shared_len .. ctx_len[b]+i.  Results as dflash_cache_attention's without a
+ * window, up to the order of the sums.
+ *   shared_len: tokens of the prefix, whole pages (a multiple of 64; 0: the
+ *              call is dflash_cache_attention).  Its pages are those of the
+ *              first request's row of the page table; the other rows' first
+ *              shared_len/64 entries are not read.  shared_len/64 < max_pages.
+ *   ctx_len:   the prefix counted in, >= shared_len.
+ *   rows:      scratch of dflash_shared_rows_bytes, 16-byte aligned, for the
+ *              prefix's share of every row (needs no clearing; not read or
+ *              written when shared_len is 0).  Ordered like the workspace.
+ * The arguments that dflash_cache_attention has too are as there, and so are
+ * the errors: a request whose ctx_len is below shared_len is reported as
+ * DFLASH_ERR_DEVICE and left unwritten.  So is one with a row behind the first
+ * batch * max_new of the batch, which only a batch with a request of more than
+ * max_new tokens can have.
+ * A batch of several groups with a prefix each is a call per group, with a
+ * slice of cu_new, ctx_len and the page table. */
+DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q,
+                            long long q_stride, const int32_t *cu_new, int total_new, const int32_t *ctx_len,
+                            int batch, int max_new, int shared_len, float scale, void *out, float *lse,
+                            void *rows, size_t rows_bytes, void *workspace, size_t workspace_bytes,
+                            dflash_stream_t stream);
+
+/* Bytes of `rows` for at most max_batch requests of at most max_new (1..16)
+ * new tokens; 0 for bad arguments.  Host-only. */
+DFLASH_API size_t dflash_shared_rows_bytes(const dflash_heads *hs, int max_batch, int max_new);
+
 /* Log probabilities of given tokens, with entropy, rank and the most probable
  * alternatives; e.g. of a step's committed tokens under the target logits
  * they were verified with.  Per row, y = logits / temperature:
