@@ -29,7 +29,8 @@ EXPORTS = (
     "dflash_debug_gemm_plan", "dflash_set_gemm_pairs", "dflash_fp8_weights_to_bf16",
     "dflash_debug_gemm_pair_clusters", "dflash_set_fused_topk",
     "dflash_target_workspace_bytes", "dflash_append_kv", "dflash_cache_attention", "dflash_token_logprobs",
-    "dflash_shared_attention", "dflash_shared_rows_bytes",
+    "dflash_shared_attention", "dflash_shared_rows_bytes", "dflash_append_kv_at", "dflash_add_weights",
+    "dflash_plan_eviction", "dflash_move_slots",
 )
 
 
@@ -66,6 +67,10 @@ class dflash_kv(ctypes.Structure):
 
 class dflash_heads(ctypes.Structure):
     _fields_ = [(n, c_int) for n in ("dtype", "n_q_heads", "n_kv_heads", "head_dim")]
+
+
+class dflash_slots(ctypes.Structure):
+    _fields_ = [("weights", c_void_p), ("positions", c_void_p), ("batch_rows", c_int), ("capacity", c_int)]
 
 
 class dflash_kernel_stat(ctypes.Structure):
@@ -127,6 +132,14 @@ def load(path: str = LIB_PATH):
         "dflash_shared_attention": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, i, vp, i, i, i,
                                         c_float, vp, vp, vp, c_size_t, vp, c_size_t, vp]),
         "dflash_shared_rows_bytes": (c_size_t, [POINTER(dflash_heads), i, i]),
+        "dflash_append_kv_at": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, vp, c_float, c_float,
+                                    vp, i, vp, vp, i, vp, vp, c_size_t, vp]),
+        "dflash_add_weights": (i, [POINTER(dflash_heads), POINTER(dflash_kv), POINTER(dflash_slots), i, vp, c_longlong, vp,
+                                   vp, i, vp, vp, vp, i, i, i, c_float, vp, c_size_t, vp]),
+        "dflash_plan_eviction": (i, [POINTER(dflash_heads), POINTER(dflash_slots), i, i, vp, vp, i, i, i, i, vp, i, vp, vp,
+                                     vp, c_size_t, vp]),
+        "dflash_move_slots": (i, [POINTER(dflash_heads), POINTER(dflash_kv), POINTER(dflash_slots), i, i, vp, i, vp, i, vp,
+                                  c_size_t, vp]),
         "dflash_token_logprobs": (i, [vp, i, i, i, c_longlong, vp, c_float, i, vp, vp, vp, vp, vp, vp]),
         "dflash_last_error": (ctypes.c_char_p, []),
         "dflash_topk16_noalloc": (i, [vp, i, i, vp, vp, vp]),
@@ -340,6 +353,35 @@ def dflash_cache_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_strid
     return _check(load().dflash_cache_attention(ctypes.byref(heads), ctypes.byref(kv), layer, _p(q), q_stride,
                                                 _p(cu_new), total_new, _p(ctx_len), batch, max_new, window, scale,
                                                 _p(out), _p(lse), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_append_kv_at(heads: dflash_heads, kv: dflash_kv, layer, qkv, row_stride, g_q, g_k, eps, rope_base, cu_new,
+                        total_new, ctx_len, pos, batch, q_out, workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_append_kv_at(ctypes.byref(heads), ctypes.byref(kv), layer, _p(qkv), row_stride, _p(g_q),
+                                             _p(g_k), eps, rope_base, _p(cu_new), total_new, _p(ctx_len), _p(pos), batch,
+                                             _p(q_out), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_add_weights(heads: dflash_heads, kv: dflash_kv, slots: dflash_slots, layer, q, q_stride, lse, cu_new, total_new,
+                       ctx_len, pos, n_commit, batch, max_new, first, scale, workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_add_weights(ctypes.byref(heads), ctypes.byref(kv), ctypes.byref(slots), layer, _p(q),
+                                            q_stride, _p(lse), _p(cu_new), total_new, _p(ctx_len), _p(pos), _p(n_commit),
+                                            batch, max_new, first, scale, _p(workspace), workspace_bytes,
+                                            _stream(stream)))
+
+
+def dflash_plan_eviction(heads: dflash_heads, slots: dflash_slots, layer, n_layers, ctx_len, seq_len, batch, first, recent,
+                         budget, moves, top, counts, ctx_out, workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_plan_eviction(ctypes.byref(heads), ctypes.byref(slots), layer, n_layers, _p(ctx_len),
+                                              _p(seq_len), batch, first, recent, budget, _p(moves), top, _p(counts),
+                                              _p(ctx_out), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def dflash_move_slots(heads: dflash_heads, kv: dflash_kv, slots: dflash_slots, layer, n_layers, moves, top, counts, batch,
+                      workspace, workspace_bytes, stream=None):
+    return _check(load().dflash_move_slots(ctypes.byref(heads), ctypes.byref(kv), ctypes.byref(slots), layer, n_layers,
+                                           _p(moves), top, _p(counts), batch, _p(workspace), workspace_bytes,
+                                           _stream(stream)))
 
 
 def dflash_shared_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_stride, cu_new, total_new, ctx_len, batch,

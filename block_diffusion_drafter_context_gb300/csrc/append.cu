@@ -18,6 +18,7 @@ namespace {
 constexpr int TT = 16;        // tokens per CTA at most
 constexpr int THREADS = 256;
 constexpr int MAX_HPC = 4;    // kv heads per CTA
+constexpr int MAX_POSITION = 1 << 24;
 
 struct AppendArgs {
   const void *qkv;
@@ -26,6 +27,7 @@ struct AppendArgs {
   float eps;
   int rotate;
   const int32_t *cu_new, *ctx_len, *page_table;
+  const int32_t *pos;         // null: a request's first new token is at position ctx_len
   int B, total, max_pages, num_pages;
   int nq, nkv, g, hpc, tt;    // kv heads (with their q heads) and tokens per CTA
   void *k, *v, *q_out;
@@ -154,13 +156,20 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
   {
     int bb[2];
     requests_of(a.cu_new, a.B, t0 + warp, t0 + warp + 8, lane, bb[0], bb[1]);
-    int pos[2], pg[2];
+    int pos[2], turn[2], pg[2];   // slot in the request, position to rotate by, page
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int t = t0 + warp + 8 * k, first = a.cu_new[bb[k]], c = a.ctx_len[bb[k]];
       const long long at = static_cast<long long>(c) + t - first;
-      const bool in = first >= 0 && first <= t && c >= 0 && at < static_cast<long long>(a.max_pages) * PAGE;
+      bool in = first >= 0 && first <= t && c >= 0 && at < static_cast<long long>(a.max_pages) * PAGE;
+      long long rot = at;
+      if (a.pos) {
+        const int p0 = a.pos[bb[k]];
+        rot = static_cast<long long>(p0) + t - first;
+        in = in && p0 >= 0 && rot < MAX_POSITION;
+      }
       pos[k] = in ? static_cast<int>(at) : -1;
+      turn[k] = in ? static_cast<int>(rot) : 0;
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -178,7 +187,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, con
 #pragma unroll
       for (int i = 0; i < HALF / 32; ++i) {
         float co = 1.f, si = 0.f;
-        if (a.rotate) rope_cs(max(pos[k], 0), th_hi[i], th_lo[i], co, si);
+        if (a.rotate) rope_cs(turn[k], th_hi[i], th_lo[i], co, si);
         const int pair = lane + 32 * i;
         cs[j][((pair >> 1 & 1) * LPR + (pair >> 2)) * 2 + (pair & 1)] = make_float2(co, si);
       }
@@ -327,23 +336,21 @@ int current_device(Device *d) {
 
 }  // namespace dflash
 
-extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
-                                           long long row_stride, const float *g_q, const float *g_k, float eps,
-                                           float rope_base, const int32_t *cu_new, int total_new,
-                                           const int32_t *ctx_len, int batch, void *q_out, void *workspace,
-                                           size_t workspace_bytes, dflash_stream_t stream) {
+static int append_kv(const char *who, const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
+                     long long row_stride, const float *g_q, const float *g_k, float eps, float rope_base,
+                     const int32_t *cu_new, int total_new, const int32_t *ctx_len, const int32_t *pos, int batch,
+                     void *q_out, void *workspace, size_t workspace_bytes, dflash_stream_t stream) {
   using namespace dflash;
-  const char *who = "append_kv";
   if (int e = check_heads(who, hs)) return e;
   const int nq = hs->n_q_heads, nkv = hs->n_kv_heads, d = hs->head_dim;
   if (int e = check_target(who, hs, kv, layer, qkv, row_stride, (nq + 2 * nkv) * d, cu_new, total_new, ctx_len, batch,
                            workspace, workspace_bytes, 256))
     return e;
-  if ((g_q == nullptr) != (g_k == nullptr)) return set_error(DFLASH_ERR_ARG, "append_kv: g_q and g_k, both or neither");
+  if ((g_q == nullptr) != (g_k == nullptr)) return set_error(DFLASH_ERR_ARG, "%s: g_q and g_k, both or neither", who);
   if (!(eps >= 0.f) || !(rope_base == 0.f || (rope_base > 1.f && rope_base < 3.0e38f)))
-    return set_error(DFLASH_ERR_ARG, "append_kv: eps / rope_base out of range");
-  if (reinterpret_cast<uintptr_t>(q_out) & 15) return set_error(DFLASH_ERR_ALIGN, "append_kv: q_out not 16-byte aligned");
-  if (off_words(g_q, g_k)) return set_error(DFLASH_ERR_ALIGN, "append_kv: g_q and g_k must be aligned to their elements");
+    return set_error(DFLASH_ERR_ARG, "%s: eps / rope_base out of range", who);
+  if (reinterpret_cast<uintptr_t>(q_out) & 15) return set_error(DFLASH_ERR_ALIGN, "%s: q_out not 16-byte aligned", who);
+  if (off_words(g_q, g_k, pos)) return set_error(DFLASH_ERR_ALIGN, "%s: g_q, g_k and pos must be aligned to their elements", who);
   if (batch == 0 || total_new == 0) return DFLASH_OK;
   Device dev;
   if (int e = current_device(&dev)) return e;
@@ -357,6 +364,7 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
   a.rotate = rope_base != 0.f;
   a.cu_new = cu_new;
   a.ctx_len = ctx_len;
+  a.pos = pos;
   a.page_table = kv->page_table;
   a.B = batch;
   a.total = total_new;
@@ -386,4 +394,23 @@ extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_
     launch_pdl(d == 64 ? append_kernel<__nv_bfloat16, 64> : append_kernel<__nv_bfloat16, 128>, grid, dim3(THREADS), 0,
                s, a, rp);
   return cuda_check(cudaGetLastError(), "append_kv launch");
+}
+
+extern "C" DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
+                                           long long row_stride, const float *g_q, const float *g_k, float eps,
+                                           float rope_base, const int32_t *cu_new, int total_new,
+                                           const int32_t *ctx_len, int batch, void *q_out, void *workspace,
+                                           size_t workspace_bytes, dflash_stream_t stream) {
+  return append_kv("append_kv", hs, kv, layer, qkv, row_stride, g_q, g_k, eps, rope_base, cu_new, total_new, ctx_len, nullptr,
+                   batch, q_out, workspace, workspace_bytes, stream);
+}
+
+extern "C" DFLASH_API int dflash_append_kv_at(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
+                                              long long row_stride, const float *g_q, const float *g_k, float eps,
+                                              float rope_base, const int32_t *cu_new, int total_new,
+                                              const int32_t *ctx_len, const int32_t *pos, int batch, void *q_out,
+                                              void *workspace, size_t workspace_bytes, dflash_stream_t stream) {
+  if (batch > 0 && !pos) return dflash::set_error(DFLASH_ERR_ARG, "append_kv_at: null pos");
+  return append_kv("append_kv_at", hs, kv, layer, qkv, row_stride, g_q, g_k, eps, rope_base, cu_new, total_new, ctx_len, pos,
+                   batch, q_out, workspace, workspace_bytes, stream);
 }

@@ -321,6 +321,33 @@ __device__ __noinline__ void join_parts(Dest p, const float *partials, int cf, i
     join_tile<T, D, PRE, 4, 4>(p, src, np, tile_rows, rows, tid, nthr);
 }
 
+// x = hi + lo, hi of 11 significant bits (to nearest, in integer arithmetic:
+// the conversion instruction runs at a quarter of its rate); the product reads
+// 11 bits of lo
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t &hi, uint32_t &lo) {
+  hi = (x + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += A B from split operands, the small terms in dl (may be d itself).  The
+// tensor cores cut their sums off instead of rounding them, so sums that go on
+// for long are kept short here and added up outside: with O accumulated over
+// all pages the outputs came out 5e-6 too small at 32k positions.
+__device__ __forceinline__ void mma_split(float (&d)[4], float (&dl)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                          uint32_t b0, uint32_t b1) {
+  uint32_t h0, l0, h1, l1;
+  split_tf32(b0, h0, l0);
+  split_tf32(b1, h1, l1);
+  mma_tf32(dl, al, h0, h1);
+  mma_tf32(dl, ah, l0, l1);
+  mma_tf32(d, ah, h0, h1);
+}
+
 // 17..128 query rows per (request, kv head) on tcgen05 (cache_attention_tc.cu).
 // `pages`: the longest list of a (request, kv head) that the call may have.
 int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int pages, const Device &dev, cudaStream_t s);

@@ -1,0 +1,437 @@
+// Cutting a cache down to a budget of tokens by accumulated attention weight
+// (slot_weights.cu): the choice (dflash_plan_eviction) and the moves that
+// follow from it (dflash_move_slots), per (layer, request, kv head).
+//
+// Of the slots first .. ctx-1 those stay whose token is among the `recent`
+// newest, then the heaviest, `budget - first` in all (equal weights: the lower
+// slot).  A cache is a set to the attention over it, so no order has to be
+// kept: the kept tokens above the budget move into the slots that fall free
+// below it, the i-th such token into the i-th such slot, and nothing else
+// moves.  A step that drops 16 of 4 112 tokens moves at most 16, where closing
+// the gaps would move nearly all.  Sources and targets are disjoint, so the
+// moves need no order either.
+#include "target.h"
+#include "common.cuh"
+
+namespace dflash {
+namespace {
+
+// ------------------------------------------------------------------ choice
+// The budget-th largest of a list by radix selection over 32-bit keys (11, 11
+// and 10 bits), the keys in shared memory: weights and positions are read
+// once.  A cluster of CTAs per list where lists are few: each has a stretch of
+// the slots, and they add up each other's counts.
+constexpr int PLAN_THREADS = 512, PLAN_WARPS = PLAN_THREADS / 32;
+constexpr int BINS = 2048;
+constexpr int MAX_CS = 8;
+constexpr uint32_t PROTECTED = 0xffffffffu;   // the key of a recent token, above every weight's
+
+struct PlanArgs {
+  const float *weights;
+  const int32_t *positions;
+  const int32_t *ctx_len, *seq_len;
+  int32_t *moves, *counts, *ctx_out;
+  int batch, batch_rows, nkv, capacity;
+  int first, recent, budget, top;
+  int cs, cached;              // CTAs per list; keys that fit in this CTA's shared memory
+  int *status;
+};
+
+struct __align__(16) PlanCtrl {
+  uint32_t hist[BINS];         // this CTA's counts
+  uint32_t warp_sum[PLAN_WARPS];
+  uint32_t pick[2];            // the digit of the wanted key, and how many lie above it
+  uint32_t ties, holes, movers;   // of this CTA
+  uint32_t warp_a[PLAN_WARPS], warp_b[PLAN_WARPS];
+};
+
+// a weight's place in an unsigned order; NaN lies below every number
+__device__ __forceinline__ uint32_t weight_key(float v) {
+  if (v != v) return 0u;
+  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);   // -0 and +0 are equal
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// exclusive prefix sum over the warps' values in smem (one per warp); every thread calls it
+__device__ __forceinline__ uint32_t before_me(const uint32_t *v, int warp) {
+  uint32_t s = 0;
+  for (int w = 0; w < warp; ++w) s += v[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+  extern __shared__ uint32_t plan_smem[];
+  PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
+  uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(blockIdx.x) % a.cs, h = static_cast<int>(blockIdx.x) / a.cs % a.nkv;
+  const int lb = static_cast<int>(blockIdx.x) / a.cs / a.nkv, layer = lb / a.batch, b = lb % a.batch;
+  auto meet = [&]() {          // the CTAs of the list
+    if (a.cs > 1) {
+      __syncwarp();
+      cluster_sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  pdl_start();
+  const int ctx = a.ctx_len[b];
+  const bool ok = ctx >= 0 && ctx <= a.capacity;
+  if (!ok && rank == 0 && h == 0 && layer == 0 && tid == 0) report(a.status, DFLASH_ERR_DEVICE);
+  const size_t list = (static_cast<size_t>(layer) * a.batch + b) * a.nkv + h;
+  int32_t *into = a.moves + list * 2 * a.top, *source = into + a.top;
+  if (rank == 0 && h == 0 && layer == 0 && tid == 0) a.ctx_out[b] = ok ? min(ctx, a.budget) : ctx;
+  if (!ok || ctx <= a.budget) {            // nothing to drop
+    for (int i = rank * PLAN_THREADS + tid; i < 2 * a.top; i += a.cs * PLAN_THREADS) into[i] = -1;
+    if (rank == 0 && tid == 0) a.counts[list] = 0;
+    return;                                // the whole cluster
+  }
+  const int n = ctx - a.first, per = (n + a.cs - 1) / a.cs;
+  const int lo = a.first + min(n, rank * per), mine = min(n, (rank + 1) * per) - min(n, rank * per);
+  const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity + lo;
+  const float *wt = a.weights + row;
+  const int32_t *ps = a.positions + row;
+  const long long newest = static_cast<long long>(a.seq_len[b]) - a.recent;   // positions from here on stay
+  auto fresh_key = [&](int i) { return ps[i] >= newest ? PROTECTED : weight_key(wt[i]); };
+  const bool cached = mine <= a.cached;
+  auto key_at = [&](int i) { return cached ? keys[i] : fresh_key(i); };
+
+  // ---- radix selection: `want` keys are to stay, those with the found prefix above them already
+  uint32_t want = a.budget - a.first, prefix = 0, ties_all = 0;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, above = shift + bits;
+    for (int i = tid; i < BINS; i += PLAN_THREADS) ct->hist[i] = 0;
+    __syncthreads();
+    uint32_t zeros = 0, prot = 0;          // the two keys that many slots may share, counted without atomics
+    for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
+      const int i = i0 + lane;
+      uint32_t k = 0;
+      bool in = i < mine;
+      if (in) {
+        if (pass == 0) {
+          k = fresh_key(i);
+          if (cached) keys[i] = k;
+        } else {
+          k = key_at(i);
+          in = (k >> above) == prefix;
+        }
+      }
+      const uint32_t z = __ballot_sync(0xffffffffu, in && k == 0x80000000u), p = __ballot_sync(0xffffffffu, in && k == PROTECTED);
+      zeros += __popc(z);
+      prot += __popc(p);
+      if (in && k != 0x80000000u && k != PROTECTED) atomicAdd(&ct->hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    if (lane == 0) {
+      if (zeros) atomicAdd(&ct->hist[(0x80000000u >> shift) & ((1u << bits) - 1)], zeros);
+      if (prot) atomicAdd(&ct->hist[(PROTECTED >> shift) & ((1u << bits) - 1)], prot);
+    }
+    meet();
+    // bins 4t .. 4t + 3 of all CTAs, from the top: the bin that holds the want-th largest key
+    uint32_t c[4] = {0, 0, 0, 0};
+    const int bin0 = BINS - 4 - 4 * tid;
+    for (int r = 0; r < a.cs; ++r)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        c[u] += a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->hist[bin0 + u], r)) : ct->hist[bin0 + u];
+    uint32_t inc = c[0] + c[1] + c[2] + c[3];
+    const uint32_t sum = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) ct->warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t over = before_me(ct->warp_sum, warp) + inc - sum;   // keys above this thread's bins
+    if (over < want && want <= over + sum) {
+#pragma unroll
+      for (int u = 3; u >= 0; --u) {
+        if (over < want && want <= over + c[u]) {
+          ct->pick[0] = bin0 + u;
+          ct->pick[1] = over;
+          ct->ties = c[u];
+          break;
+        }
+        over += c[u];
+      }
+    }
+    meet();                    // and every CTA has read the others' counts
+    prefix = pass == 0 ? ct->pick[0] : (prefix << bits) | ct->pick[0];
+    want -= ct->pick[1];
+    ties_all = ct->ties;
+    __syncthreads();
+  }
+  static_assert(BINS == 4 * PLAN_THREADS, "bins per thread");
+  // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
+  const int seg = ((mine + PLAN_WARPS - 1) / PLAN_WARPS + 31) / 32 * 32;   // slots per warp
+  const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
+  uint32_t tie_base = 0;       // equal keys in slots before this warp's
+  if (want < ties_all) {
+    uint32_t t = 0;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const int i = i0 + lane;
+      t += __popc(__ballot_sync(0xffffffffu, i < s1 && key_at(i) == prefix));
+    }
+    if (lane == 0) ct->warp_a[warp] = t;
+    __syncthreads();
+    if (tid == 0) ct->ties = before_me(ct->warp_a, PLAN_WARPS);
+    meet();
+    tie_base = before_me(ct->warp_a, warp);
+    if (a.cs > 1)
+      for (int r = 0; r < rank; ++r) tie_base += ld_dsmem_u32(dsmem_addr(&ct->ties, r));
+    __syncthreads();
+  }
+  const int keep = a.budget;   // ctx > budget here
+  const uint32_t below = (1u << lane) - 1;
+  auto walk = [&](auto each) {
+    uint32_t t = tie_base;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < s1;
+      const uint32_t k = in ? key_at(i) : 0u;
+      const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix);
+      const bool stays = in && (k > prefix || (k == prefix && t + __popc(eq & below) < want));
+      t += __popc(eq);
+      each(lo + i, in && !stays && lo + i < keep, stays && lo + i >= keep);
+    }
+  };
+  uint32_t holes = 0, movers = 0;
+  walk([&](int, bool hole, bool mover) {
+    holes += __popc(__ballot_sync(0xffffffffu, hole));
+    movers += __popc(__ballot_sync(0xffffffffu, mover));
+  });
+  if (lane == 0) {
+    ct->warp_a[warp] = holes;
+    ct->warp_b[warp] = movers;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    ct->holes = before_me(ct->warp_a, PLAN_WARPS);
+    ct->movers = before_me(ct->warp_b, PLAN_WARPS);
+  }
+  meet();
+  uint32_t hole = before_me(ct->warp_a, warp), mover = before_me(ct->warp_b, warp), count = 0;
+  for (int r = 0; r < a.cs; ++r) {
+    const uint32_t x = a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->holes, r)) : ct->holes;
+    const uint32_t y = a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->movers, r)) : ct->movers;
+    count += x;                // as many as there are movers
+    if (r < rank) {
+      hole += x;
+      mover += y;
+    }
+  }
+  walk([&](int slot, bool is_hole, bool is_mover) {
+    const uint32_t x = __ballot_sync(0xffffffffu, is_hole), y = __ballot_sync(0xffffffffu, is_mover);
+    if (is_hole) into[hole + __popc(x & below)] = slot;
+    if (is_mover) source[mover + __popc(y & below)] = slot;
+    hole += __popc(x);
+    mover += __popc(y);
+  });
+  for (int i = static_cast<int>(count) + rank * PLAN_THREADS + tid; i < a.top; i += a.cs * PLAN_THREADS)
+    into[i] = source[i] = -1;
+  if (rank == 0 && tid == 0) a.counts[list] = static_cast<int32_t>(count);
+  if (a.cs > 1) {
+    __syncwarp();
+    cluster_sync();            // no CTA leaves while its counts are read
+  }
+}
+
+// ------------------------------------------------------------------ moves
+// A CTA takes 32 moves of a list.  K rows are copied 16 bytes a lane; V lies
+// transposed, so a lane is a move and the warps walk the dims: targets and
+// sources ascend, and neighbouring lanes share the sectors of a page's row
+// where they are dense.  Bound by the sectors touched: 32 bytes for a value
+// where the moves are sparse.
+constexpr int MOVE_THREADS = 256, PER_CTA = 32;
+
+struct MoveArgs {
+  void *k, *v;                 // the first layer's
+  long long layer_elems;
+  float *weights;
+  int32_t *positions;
+  const int32_t *moves, *counts, *page_table;
+  int batch, batch_rows, nkv, capacity, top;
+  int max_pages, num_pages;
+  int *status;
+};
+
+template <typename V, int D>   // V: an unsigned integer as wide as the values
+__global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const MoveArgs a) {
+  constexpr int VEC = 16 / sizeof(V), LPR = D / VEC, STEP = MOVE_THREADS / 32;
+  __shared__ long long s_to[PER_CTA], s_of[PER_CTA];   // (page x kv heads + head) x 64 + slot, -1: no move
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int list = blockIdx.x, h = list % a.nkv, b = list / a.nkv % a.batch, layer = list / a.nkv / a.batch;
+  pdl_start();
+  const int count = a.counts[list];
+  if (count < 0 || count > a.top) {
+    if (blockIdx.y == 0 && tid == 0) report(a.status, DFLASH_ERR_DEVICE);
+    return;
+  }
+  V *v = static_cast<V *>(a.v) + layer * a.layer_elems;
+  uint4 *k = reinterpret_cast<uint4 *>(static_cast<V *>(a.k) + layer * a.layer_elems);
+  for (int i0 = blockIdx.y * PER_CTA; i0 < count; i0 += gridDim.y * PER_CTA) {
+    const int n = min(count - i0, PER_CTA);
+    if (warp == 0) {
+      long long to = -1, of = -1;
+      if (lane < n) {
+        const int32_t *m = a.moves + static_cast<size_t>(list) * 2 * a.top + i0 + lane;
+        const int into = m[0], source = m[a.top];
+        const int most = min(a.capacity, a.max_pages * PAGE);
+        bool ok = into >= 0 && into < most && source >= 0 && source < most;
+        if (ok) {
+          const int32_t *table = a.page_table + static_cast<size_t>(b) * a.max_pages;
+          const int p0 = table[into / PAGE], p1 = table[source / PAGE];
+          ok = p0 >= 0 && p0 < a.num_pages && p1 >= 0 && p1 < a.num_pages;
+          if (ok) {
+            to = (static_cast<long long>(p0) * a.nkv + h) * PAGE + into % PAGE;
+            of = (static_cast<long long>(p1) * a.nkv + h) * PAGE + source % PAGE;
+            const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity;
+            a.weights[row + into] = a.weights[row + source];
+            a.positions[row + into] = a.positions[row + source];
+          }
+        }
+        if (!ok) report(a.status, DFLASH_ERR_DEVICE);
+      }
+      s_to[lane] = to;
+      s_of[lane] = of;
+    }
+    __syncthreads();
+    // ---- V [page][head][d][slot]: lane = move
+    const long long to = s_to[lane], of = s_of[lane];
+    if (to >= 0) {
+      const V *src = v + (of / PAGE) * (D * PAGE) + of % PAGE;
+      V *dst = v + (to / PAGE) * (D * PAGE) + to % PAGE;
+      V x[D / STEP];
+#pragma unroll
+      for (int u = 0; u < D / STEP; ++u) x[u] = src[(u * STEP + warp) * PAGE];
+#pragma unroll
+      for (int u = 0; u < D / STEP; ++u) dst[(u * STEP + warp) * PAGE] = x[u];
+    }
+    // ---- K [page][head][slot][d]
+#pragma unroll
+    for (int e0 = 0; e0 < PER_CTA * LPR; e0 += MOVE_THREADS) {
+      const int e = e0 + tid, i = e / LPR, c = e % LPR;
+      if (s_to[i] >= 0) k[s_to[i] * LPR + c] = k[s_of[i] * LPR + c];
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+}  // namespace dflash
+
+using namespace dflash;
+
+extern "C" {
+
+DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *slots, int layer, int n_layers,
+                                    const int32_t *ctx_len, const int32_t *seq_len, int batch, int first, int recent,
+                                    int budget, int32_t *moves, int top, int32_t *counts, int32_t *ctx_out,
+                                    void *workspace, size_t workspace_bytes, dflash_stream_t stream) {
+  const char *who = "plan_eviction";
+  if (int e = check_heads(who, hs)) return e;
+  if (int e = check_slots(who, slots, batch)) return e;
+  if (!workspace || (batch > 0 && (!ctx_len || !seq_len || !ctx_out))) return set_error(DFLASH_ERR_ARG, "%s: null argument", who);
+  if (batch < 0 || layer < 0 || n_layers < 0 || first < 0 || recent < 0 || budget < 1 || budget > (1 << 24) ||
+      static_cast<long long>(first) + recent > budget || first >= budget)
+    return set_error(DFLASH_ERR_ARG, "%s: batch, layers, first, recent or budget out of range (first < budget, first + recent <= budget)", who);
+  const int room = budget - first, over = slots->capacity - budget, most = room < over ? room : over > 0 ? over : 0;
+  if (top < most) return set_error(DFLASH_ERR_SHAPE, "%s: room for %d moves, %d needed", who, top, most);
+  if (batch > 0 && n_layers > 0 && (!counts || (top > 0 && !moves))) return set_error(DFLASH_ERR_ARG, "%s: null argument", who);
+  if (off_words(ctx_len, seq_len, moves, counts, ctx_out) || (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return set_error(DFLASH_ERR_ALIGN, "%s: arrays must be aligned to their elements, the workspace to 16 bytes", who);
+  if (workspace_bytes < 256) return set_error(DFLASH_ERR_SHAPE, "%s: workspace of %zu bytes, 256 needed", who, workspace_bytes);
+  if (batch == 0 || n_layers == 0) return DFLASH_OK;
+  const long long lists = static_cast<long long>(n_layers) * batch * hs->n_kv_heads;
+  if (lists > (1 << 27)) return set_error(DFLASH_ERR_SHAPE, "%s: too many layers x requests x kv heads", who);
+  Device dev;
+  if (int e = current_device(&dev)) return e;
+  const size_t at = static_cast<size_t>(layer) * slots->batch_rows * hs->n_kv_heads * slots->capacity;
+  PlanArgs a = {};
+  a.weights = slots->weights + at;
+  a.positions = slots->positions + at;
+  a.ctx_len = ctx_len;
+  a.seq_len = seq_len;
+  a.moves = moves;
+  a.counts = counts;
+  a.ctx_out = ctx_out;
+  a.batch = batch;
+  a.batch_rows = slots->batch_rows;
+  a.nkv = hs->n_kv_heads;
+  a.capacity = slots->capacity;
+  a.first = first;
+  a.recent = recent;
+  a.budget = budget;
+  a.top = top;
+  a.status = static_cast<int *>(workspace);
+  a.cs = 1;
+  while (a.cs < MAX_CS && lists * a.cs * 2 <= 2LL * dev.sms && slots->capacity / a.cs > 2048) a.cs *= 2;
+  const int room_smem = (200 << 10) - static_cast<int>(sizeof(PlanCtrl)), per = (slots->capacity + a.cs - 1) / a.cs;
+  a.cached = per * 4LL <= room_smem ? per : room_smem / 4;
+  const int smem = static_cast<int>(sizeof(PlanCtrl)) + a.cached * 4;
+  static std::atomic<uint64_t> smem_set;
+  if (int e = allow_smem(smem_set, dev, plan_kernel, 200 << 10)) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(lists * a.cs));
+  cfg.blockDim = dim3(PLAN_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cs > 1 ? 2 : 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, plan_kernel, a), "plan_eviction launch");
+}
+
+DFLASH_API int dflash_move_slots(const dflash_heads *hs, const dflash_kv *kv, const dflash_slots *slots, int layer,
+                                 int n_layers, const int32_t *moves, int top, const int32_t *counts, int batch,
+                                 void *workspace, size_t workspace_bytes, dflash_stream_t stream) {
+  const char *who = "move_slots";
+  if (int e = check_heads(who, hs)) return e;
+  static const int32_t none[2] = {0, 0};   // no rows, no requests: the cache's own checks are what is wanted
+  if (int e = check_target(who, hs, kv, layer, nullptr, 8, 8, none, 0, none, batch, workspace, workspace_bytes, 256)) return e;
+  if (int e = check_slots(who, slots, batch)) return e;
+  if (n_layers < 0 || top < 0 || top > (1 << 24)) return set_error(DFLASH_ERR_ARG, "%s: n_layers or top out of range", who);
+  if (batch > 0 && n_layers > 0 && top > 0 && (!moves || !counts)) return set_error(DFLASH_ERR_ARG, "%s: null argument", who);
+  if (off_words(moves, counts)) return set_error(DFLASH_ERR_ALIGN, "%s: moves and counts must be aligned to their elements", who);
+  const long long lists = static_cast<long long>(n_layers) * batch * hs->n_kv_heads;
+  if (lists > (1 << 27)) return set_error(DFLASH_ERR_SHAPE, "%s: too many layers x requests x kv heads", who);
+  if (batch == 0 || n_layers == 0 || top == 0) return DFLASH_OK;
+  const size_t off = layer_offset(*hs, *kv, layer) * elt_bytes(*hs);
+  const size_t at = static_cast<size_t>(layer) * slots->batch_rows * hs->n_kv_heads * slots->capacity;
+  MoveArgs a = {};
+  a.k = static_cast<char *>(kv->k_cache) + off;
+  a.v = static_cast<char *>(kv->v_cache) + off;
+  a.layer_elems = static_cast<long long>(layer_offset(*hs, *kv, 1));
+  a.weights = slots->weights + at;
+  a.positions = slots->positions + at;
+  a.moves = moves;
+  a.counts = counts;
+  a.page_table = kv->page_table;
+  a.batch = batch;
+  a.batch_rows = slots->batch_rows;
+  a.nkv = hs->n_kv_heads;
+  a.capacity = slots->capacity;
+  a.top = top;
+  a.max_pages = kv->max_pages;
+  a.num_pages = kv->num_pages;
+  a.status = static_cast<int *>(workspace);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto kernel = hs->dtype == DFLASH_F32 ? (hs->head_dim == 64 ? move_kernel<uint32_t, 64> : move_kernel<uint32_t, 128>)
+                                        : (hs->head_dim == 64 ? move_kernel<uint16_t, 64> : move_kernel<uint16_t, 128>);
+  const int parts = (top + PER_CTA - 1) / PER_CTA;
+  const dim3 grid(static_cast<unsigned>(lists), static_cast<unsigned>(parts < 4096 ? parts : 4096));
+  return cuda_check(launch_pdl(kernel, grid, dim3(MOVE_THREADS), 0, s, a), "move_slots launch");
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
 // Host-side checks shared by the target-side operators (append to the paged
-// cache, attention over it).
+// cache, attention over it, its slots' weights and eviction).
 #pragma once
 
 #include <atomic>
@@ -16,6 +16,7 @@ int check_target(const char *who, const dflash_heads *hs, const dflash_kv *kv, i
                  long long row_stride, int row_elems, const int32_t *cu_new, int total_new, const int32_t *ctx_len,
                  int batch, const void *workspace, size_t workspace_bytes, size_t need);
 int check_heads(const char *who, const dflash_heads *hs);
+int check_slots(const char *who, const dflash_slots *slots, int batch);
 // The current device and its SM count, looked up once per device.
 struct Device {
   int index = 0, sms = 0;

@@ -45,6 +45,43 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+class SlotWeights:
+    """What a cache with a budget keeps of every slot, per layer, request and kv
+    head: the attention weight its token received (``add_weights``) and its
+    position.  A new one counts every slot's position as its number and no
+    weight, as after a prompt.  capacity: at least 64 slots per page of the page
+    table's rows."""
+
+    def __init__(self, n_layers, batch, n_kv_heads, capacity, device="cuda"):
+        torch = _torch()
+        shape = (int(n_layers), int(batch), int(n_kv_heads), int(capacity))
+        self.weights = torch.zeros(shape, dtype=torch.float32, device=device)
+        self.positions = torch.arange(shape[3], dtype=torch.int32, device=device).expand(shape).contiguous()
+        self._describe()
+
+    def _describe(self):
+        self.n_layers, self.batch_rows, self.nkv, self.capacity = (int(n) for n in self.weights.shape)
+        self.device = self.weights.device
+        self.struct = B.dflash_slots(self.weights.data_ptr(), self.positions.data_ptr(), self.batch_rows, self.capacity)
+        self.struct_ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def from_tensors(cls, weights, positions):
+        """Over tensors the caller already has: weights fp32 and positions int32
+        [n_layers][batch][n_kv_heads][capacity], contiguous on one CUDA device."""
+        torch = _torch()
+        if weights.dim() != 4 or weights.dtype != torch.float32 or positions.dtype != torch.int32 \
+                or positions.shape != weights.shape:
+            raise ValueError("weights must be fp32 and positions int32, both [layers][batch][n_kv][capacity]")
+        if not (weights.is_contiguous() and positions.is_contiguous() and weights.is_cuda
+                and positions.device == weights.device):
+            raise ValueError("weights and positions must be contiguous on one CUDA device")
+        s = cls.__new__(cls)
+        s.weights, s.positions = weights, positions
+        s._describe()
+        return s
+
+
 class TargetOps:
     """The cache operators for one shape of attention layer: heads, dtype,
     rotation, and the workspace the calls share (ordered on one stream).
@@ -131,16 +168,32 @@ class TargetOps:
                 or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous fp32 [{rows}][{self.nq}] on {self.device}")
 
-    def append_kv(self, kv, layer, qkv, cu_new, ctx_len, g_q=None, g_k=None, q_out=None, stream=None):
+    def _per_request(self, name, x, batch):
+        if x.dtype is not self._i32 or x.shape != (batch,) or x.device != self.device or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 [{batch}] on {self.device}")
+        return x.data_ptr()
+
+    def _slots(self, slots, batch, layer):
+        if slots.nkv != self.nkv or slots.device != self.device or slots.batch_rows < batch:
+            raise ValueError(f"slots of {slots.batch_rows} requests x {slots.nkv} kv heads on {slots.device}: these "
+                             f"operators want {batch} x {self.nkv} on {self.device}")
+        if layer is None:
+            return 0, slots.n_layers
+        if not 0 <= layer < slots.n_layers:
+            raise ValueError(f"layer {layer} of slots with {slots.n_layers}")
+        return layer, 1
+
+    def append_kv(self, kv, layer, qkv, cu_new, ctx_len, g_q=None, g_k=None, q_out=None, stream=None, pos=None):
         """K and V of the rows of qkv ([tokens][(nq + 2 nkv) d], the fused
         projection) into the pages of their requests, K normed (g_k) and
         rotated; returns the normed (g_q) and rotated queries [tokens][nq d].
         Rows before cu_new[0] and from cu_new[batch] on are left alone, in
-        q_out too."""
+        q_out too.  pos (int32 [batch]): the position of each request's first
+        new token, where that is not its slot ctx_len (after an eviction)."""
         torch = self._torch
         if stream is not None or torch.cuda.current_device() != self.device.index:
             with _on(stream, self.device):
-                return self.append_kv(kv, layer, qkv, cu_new, ctx_len, g_q, g_k, q_out)
+                return self.append_kv(kv, layer, qkv, cu_new, ctx_len, g_q, g_k, q_out, pos=pos)
         ld = self._rows("qkv", qkv, (self.nq + 2 * self.nkv) * self.d)
         batch = self._cache(kv, layer, cu_new, ctx_len)
         for g in (g_q, g_k):
@@ -152,10 +205,14 @@ class TargetOps:
             q_out = torch.empty((rows, self.nq * self.d), dtype=self.dtype, device=self.device)
         else:
             self._out(q_out, rows, "q_out")
-        rc = self._lib.dflash_append_kv(
-            self._heads, kv.struct_ref, layer, qkv.data_ptr(), ld, None if g_q is None else g_q.data_ptr(),
-            None if g_k is None else g_k.data_ptr(), self.eps, self.rope_base, cu_new.data_ptr(), rows,
-            ctx_len.data_ptr(), batch, q_out.data_ptr(), self._ws, self.ws_bytes, B.raw_stream(self.device.index))
+        args = (self._heads, kv.struct_ref, layer, qkv.data_ptr(), ld, None if g_q is None else g_q.data_ptr(),
+                None if g_k is None else g_k.data_ptr(), self.eps, self.rope_base, cu_new.data_ptr(), rows,
+                ctx_len.data_ptr())
+        end = (batch, q_out.data_ptr(), self._ws, self.ws_bytes, B.raw_stream(self.device.index))
+        if pos is None:
+            rc = self._lib.dflash_append_kv(*args, *end)
+        else:
+            rc = self._lib.dflash_append_kv_at(*args, self._per_request("pos", pos, batch), *end)
         if rc:
             B._check(rc)
         return q_out
@@ -211,6 +268,92 @@ class TargetOps:
         if rc:
             B._check(rc)
         return out if lse is None else (out, lse)
+
+    def add_weights(self, kv, layer, slots, q, lse, cu_new, ctx_len, pos=None, n_commit=None, max_new=None, first=0,
+                    scale=None, stream=None):
+        """Adds to the slots' weights (a ``SlotWeights``) the attention that the
+        committed new tokens paid to each cached token from slot `first` on.
+        q, cu_new, ctx_len and scale as of the ``attend`` or ``attend_shared``
+        before (without a window), lse what it gave.  n_commit (int32 [batch]):
+        how many of each request's new tokens count, all by default; their own
+        slots start from 0 and get the positions pos[b] ... (default: ctx_len)."""
+        torch = self._torch
+        if stream is not None or torch.cuda.current_device() != self.device.index:
+            with _on(stream, self.device):
+                return self.add_weights(kv, layer, slots, q, lse, cu_new, ctx_len, pos, n_commit, max_new, first, scale)
+        ld = self._rows("q", q, self.nq * self.d)
+        batch = self._cache(kv, layer, cu_new, ctx_len)
+        self._slots(slots, batch, layer)
+        rows = q.shape[0]
+        self._lse(lse, rows)
+        rc = self._lib.dflash_add_weights(
+            self._heads, kv.struct_ref, slots.struct_ref, layer, q.data_ptr(), ld, lse.data_ptr(), cu_new.data_ptr(), rows,
+            ctx_len.data_ptr(), None if pos is None else self._per_request("pos", pos, batch),
+            None if n_commit is None else self._per_request("n_commit", n_commit, batch), batch,
+            self.max_new if max_new is None else max_new, first, self._scale if scale is None else scale, self._ws,
+            self.ws_bytes, B.raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+
+    def plan_eviction(self, slots, ctx_len, seq_len, budget, recent=0, first=0, layer=None, stream=None):
+        """What a cache keeps of requests with more than `budget` tokens, for one
+        layer of `slots` or all: the first `first` slots, the positions from
+        seq_len - recent on, then the heaviest.  Returns (moves
+        [layers][batch][n_kv][2][top], counts [layers][batch][n_kv], ctx
+        [batch]): slots moved into and from (-1 behind the count), and the
+        tokens that are left, min(ctx_len, budget)."""
+        torch = self._torch
+        if stream is not None or torch.cuda.current_device() != self.device.index:
+            with _on(stream, self.device):
+                return self.plan_eviction(slots, ctx_len, seq_len, budget, recent, first, layer)
+        batch = ctx_len.shape[0]
+        layer, n = self._slots(slots, batch, layer)
+        ctx, seq = self._per_request("ctx_len", ctx_len, batch), self._per_request("seq_len", seq_len, batch)
+        top = max(0, min(budget - first, slots.capacity - budget))
+        moves = torch.empty((n, batch, self.nkv, 2, top), dtype=torch.int32, device=self.device)
+        counts = torch.empty((n, batch, self.nkv), dtype=torch.int32, device=self.device)
+        left = torch.empty_like(ctx_len)
+        rc = self._lib.dflash_plan_eviction(
+            self._heads, slots.struct_ref, layer, n, ctx, seq, batch, first, recent, budget, moves.data_ptr(), top,
+            counts.data_ptr(), left.data_ptr(), self._ws, self.ws_bytes, B.raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+        return moves, counts, left
+
+    def move_slots(self, kv, slots, moves, counts, layer=None, stream=None):
+        """Carries out the moves of ``plan_eviction`` on K, V, weights and
+        positions, in the layers that the plan was made for."""
+        torch = self._torch
+        if stream is not None or torch.cuda.current_device() != self.device.index:
+            with _on(stream, self.device):
+                return self.move_slots(kv, slots, moves, counts, layer)
+        if kv.layer_sig != self.layer_sig:
+            raise ValueError(f"the cache holds (dtype, device, kv heads, head dim) {kv.layer_sig}: these operators "
+                             f"want {self.layer_sig}")
+        batch = counts.shape[1] if counts.dim() == 3 else -1
+        layer, n = self._slots(slots, batch, layer)
+        if counts.shape != (n, batch, self.nkv) or moves.dim() != 5 or moves.shape[:4] != (n, batch, self.nkv, 2) \
+                or moves.dtype is not self._i32 or counts.dtype is not self._i32 or moves.device != self.device \
+                or counts.device != self.device or not (moves.is_contiguous() and counts.is_contiguous()):
+            raise ValueError(f"moves and counts must be what plan_eviction gave for {n} layers: contiguous int32 "
+                             "[layers][batch][n_kv][2][top] and [layers][batch][n_kv]")
+        if layer + n > kv.n_layers or batch > kv.batch_rows:
+            raise ValueError(f"{n} layers from {layer} on and {batch} requests, a cache of {kv.n_layers} and "
+                             f"{kv.batch_rows}")
+        rc = self._lib.dflash_move_slots(
+            self._heads, kv.struct_ref, slots.struct_ref, layer, n, moves.data_ptr(), moves.shape[4], counts.data_ptr(),
+            batch, self._ws, self.ws_bytes, B.raw_stream(self.device.index))
+        if rc:
+            B._check(rc)
+
+    def evict(self, kv, slots, ctx_len, seq_len, budget, recent=0, first=0, layer=None, stream=None):
+        """``plan_eviction`` and ``move_slots``: cuts requests with more than
+        `budget` tokens down to it and returns the tokens that are left.  With
+        pages that requests share, `first` is the shared prefix's length."""
+        moves, counts, left = self.plan_eviction(slots, ctx_len, seq_len, budget, recent, first, layer, stream)
+        if moves.shape[4]:
+            self.move_slots(kv, slots, moves, counts, layer, stream)
+        return left
 
 
 def token_logprobs(logits, token_ids, temperature=1.0, n_top=16, stream=None) -> dict:

@@ -495,6 +495,16 @@ DFLASH_API int dflash_append_kv(const dflash_heads *hs, const dflash_kv *kv, int
                      const int32_t *cu_new, int total_new, const int32_t *ctx_len, int batch, void *q_out,
                      void *workspace, size_t workspace_bytes, dflash_stream_t stream);
 
+/* The same with positions of its own for the rotation: token i of request b
+ * goes to slot ctx_len[b] + i and is rotated by pos[b] + i.  For a cache that
+ * tokens were dropped from (dflash_move_slots), where the two differ.
+ *   pos: device int32 [batch], >= 0; positions below 2^24 (else the token is
+ *        not appended, and DFLASH_ERR_DEVICE reported). */
+DFLASH_API int dflash_append_kv_at(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *qkv,
+                     long long row_stride, const float *g_q, const float *g_k, float eps, float rope_base,
+                     const int32_t *cu_new, int total_new, const int32_t *ctx_len, const int32_t *pos, int batch,
+                     void *q_out, void *workspace, size_t workspace_bytes, dflash_stream_t stream);
+
 /* Attention of the newest tokens of each request over its paged cache, which
  * already holds their own K and V.  Token i of request b, at position
  * p = ctx_len[b] + i, sees positions max(0, p - window + 1) .. p:
@@ -556,6 +566,85 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
 /* Bytes of `rows` for at most max_batch requests of at most max_new (1..16)
  * new tokens; 0 for bad arguments.  Host-only. */
 DFLASH_API size_t dflash_shared_rows_bytes(const dflash_heads *hs, int max_batch, int max_new);
+
+/* ----------------------------------------------------------------------
+ * A cache with a budget of tokens.  Each slot of a request's cache has, per
+ * layer and kv head, the attention weight its token received so far and the
+ * token's position.  A step (every call below for all layers or layer by layer):
+ *   append (dflash_append_kv_at), attention with lse, verification;
+ *   dflash_add_weights with the rows that were committed;
+ *   ctx_len += committed, seq_len += committed;
+ *   now and then dflash_plan_eviction and dflash_move_slots, after which the
+ *   requests hold min(ctx_len, budget) tokens in their first slots.
+ * Kv heads drop different tokens; all of a request's heads keep as many.  The
+ * attention over such a cache is the same call (its tokens are a set, the new
+ * ones behind them); a window counts slots, not positions, there. */
+typedef struct dflash_slots {
+  float *weights;        /* device fp32 [layers][batch_rows][nkv][capacity]   */
+  int32_t *positions;    /* device int32, as weights                         */
+  int batch_rows;        /* requests of a layer, >= batch                    */
+  int capacity;          /* slots of a request, <= 2^24                      */
+} dflash_slots;
+
+/* Adds to the weights of layer `layer` what the committed new tokens paid to
+ * each cached token: for slot t >= first of request b and kv head h
+ *   weights[b][h][t] += sum over i < n_commit[b] with t <= ctx_len[b] + i, over
+ *                       the q heads of h: exp(scale * q.k_t - lse).
+ * The slot of a committed token itself (t >= ctx_len[b]) starts from 0 whatever
+ * it held, and its position becomes pos[b] + t - ctx_len[b].  Other slots
+ * (before first, from ctx_len + n_commit on) are left alone.
+ *   q, q_stride, cu_new, total_new, ctx_len, max_new, scale: as of the
+ *              dflash_cache_attention or dflash_shared_attention before, over
+ *              the same cache (no window);
+ *   lse:       device fp32 [total_new][nq], what that call gave.  A row of -inf
+ *              (it saw nothing) adds nothing, a NaN one makes NaN of what its
+ *              token sees.
+ *   pos:       device int32 [batch], or NULL: ctx_len.
+ *   n_commit:  device int32 [batch], 0 .. the request's new tokens, or NULL: all.
+ *   first:     >= 0, e.g. the length of a shared prefix.
+ *   slots->capacity >= 64 max_pages.
+ * Scores and sums are fp32.  A page index outside [0, num_pages) leaves its
+ * slots alone, an invalid request (as in the attention; n_commit out of range)
+ * all of its slots; both are reported as DFLASH_ERR_DEVICE in the status word
+ * of `workspace` (at least 256 bytes).  The same inputs give the same bits. */
+DFLASH_API int dflash_add_weights(const dflash_heads *hs, const dflash_kv *kv, const dflash_slots *slots, int layer,
+                       const void *q, long long q_stride, const float *lse, const int32_t *cu_new, int total_new,
+                       const int32_t *ctx_len, const int32_t *pos, const int32_t *n_commit, int batch, int max_new,
+                       int first, float scale, void *workspace, size_t workspace_bytes, dflash_stream_t stream);
+
+/* Chooses which tokens stay where a request has more than `budget`, for layers
+ * layer .. layer + n_layers - 1.  Of the slots first .. ctx_len[b]-1 of a (layer,
+ * request, kv head) those stay that hold a position >= seq_len[b] - recent, then
+ * the largest weights (equal ones: the lower slot; NaN below every number), in
+ * all budget - first; slots before first stay where they are.  The kept tokens
+ * at and above slot `budget` go into the slots below it that fall free, in
+ * ascending order both; nothing else moves.  first < budget, first + recent <=
+ * budget.
+ *   ctx_len:   device int32 [batch], tokens cached now; seq_len: device int32
+ *              [batch], the next token's position.
+ *   moves:     device int32 [n_layers][batch][nkv][2][top] out: the slots moved
+ *              into, then the slots moved from; -1 behind the list's count.
+ *              top >= min(budget - first, capacity - budget); NULL when 0.
+ *   counts:    device int32 [n_layers][batch][nkv] out;
+ *   ctx_out:   device int32 [batch] out, min(ctx_len, budget); not ctx_len itself.
+ * Reads weights and positions only.  A ctx_len outside 0..capacity is reported
+ * as DFLASH_ERR_DEVICE; that request gets no moves and its ctx_len back.
+ * Of hs only n_kv_heads is used.  workspace: the status word, 256 bytes. */
+DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *slots, int layer, int n_layers,
+                         const int32_t *ctx_len, const int32_t *seq_len, int batch, int first, int recent, int budget,
+                         int32_t *moves, int top, int32_t *counts, int32_t *ctx_out, void *workspace,
+                         size_t workspace_bytes, dflash_stream_t stream);
+
+/* Carries the moves out: K, V, weight and position of moves[..][1][i] to
+ * moves[..][0][i] for i < counts, in layers layer .. layer + n_layers - 1 of the
+ * cache and the slots.  No slot of a list is both a source and a target, or a
+ * target twice.  Pages that requests share must lie before `first` of the plan:
+ * a move into one would be seen by all of them.  A move with a slot outside the
+ * cache or without a valid page is dropped and a count outside 0..top takes its
+ * list with it, both reported as DFLASH_ERR_DEVICE. */
+DFLASH_API int dflash_move_slots(const dflash_heads *hs, const dflash_kv *kv, const dflash_slots *slots, int layer,
+                      int n_layers, const int32_t *moves, int top, const int32_t *counts, int batch, void *workspace,
+                      size_t workspace_bytes, dflash_stream_t stream);
 
 /* Log probabilities of given tokens, with entropy, rank and the most probable
  * alternatives; e.g. of a step's committed tokens under the target logits

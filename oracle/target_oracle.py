@@ -1,5 +1,6 @@
 """fp64 CPU oracle of the target-side operators (append to the paged cache,
-attention over it, token log probabilities).
+attention over it, the weights of its slots and eviction by them, token log
+probabilities).
 
 TEST INFRASTRUCTURE ONLY, like ``dflash_oracle``: plain loops and numpy in
 float64 from the stored inputs, sharing no code with the CUDA path.
@@ -33,23 +34,25 @@ def head_norm_rope(x, gain, eps: float, base: float, pos: int) -> np.ndarray:
     return out
 
 
-def append(k, v, table, qkv, nq, nkv, d, g_q, g_k, eps, base, cu_new, ctx_len):
+def append(k, v, table, qkv, nq, nkv, d, g_q, g_k, eps, base, cu_new, ctx_len, turn=None):
     """K and V pools of one layer (float64 copies, updated) and the rotated
-    queries [tokens][nq d] (NaN where no request owns the row)."""
+    queries [tokens][nq d] (NaN where no request owns the row).  turn: the
+    position that each request's first new token is rotated by (None: ctx_len)."""
     k, v = np.array(k, dtype=np.float64), np.array(v, dtype=np.float64)
     q = np.full((qkv.shape[0], nq * d), np.nan)
     for b in range(len(ctx_len)):
         for t in range(cu_new[b], cu_new[b + 1]):
             pos = int(ctx_len[b]) + t - int(cu_new[b])
+            at = pos if turn is None else int(turn[b]) + t - int(cu_new[b])
             row = np.asarray(qkv[t], dtype=np.float64)
             for h in range(nq):
-                q[t, h * d:(h + 1) * d] = head_norm_rope(row[h * d:(h + 1) * d], g_q, eps, base, pos)
+                q[t, h * d:(h + 1) * d] = head_norm_rope(row[h * d:(h + 1) * d], g_q, eps, base, at)
             page = int(table[b][pos // PAGE]) if pos // PAGE < len(table[b]) else -1
             if not 0 <= page < k.shape[0]:
                 continue
             for h in range(nkv):
                 o = (nq + h) * d
-                k[page, h, pos % PAGE] = head_norm_rope(row[o:o + d], g_k, eps, base, pos)
+                k[page, h, pos % PAGE] = head_norm_rope(row[o:o + d], g_k, eps, base, at)
                 v[page, h, :, pos % PAGE] = row[o + nkv * d:o + (nkv + 1) * d]
     return k, v, q
 
@@ -81,6 +84,46 @@ def attend(k, v, table, q, nq, nkv, d, cu_new, ctx_len, window, scale):
                 spread[t, cols] = (e @ np.abs(vv)) / e.sum()
                 lse[t, h] = m + np.log(e.sum())
     return out, lse, spread
+
+
+def add_weights(w, positions, k, table, q, lse, nq, nkv, d, cu_new, ctx_len, turn, commit, first, scale):
+    """(weights, positions, added) of one layer, [batch][nkv][capacity]: what
+    the committed tokens' attention adds to each slot."""
+    w, positions = np.array(w, dtype=np.float64), np.array(positions)
+    added = np.zeros_like(w)
+    for b in range(len(ctx_len)):
+        c = int(ctx_len[b])
+        for i in range(int(commit[b])):
+            t = int(cu_new[b]) + i
+            for s in range(first, c + int(commit[b])):
+                page = int(table[b][s // PAGE])
+                if not 0 <= page < k.shape[0]:
+                    continue
+                if i == 0 and s >= c:
+                    w[b, :, s] = 0
+                    positions[b, :, s] = int(turn[b]) + s - c
+                if s > c + i:
+                    continue
+                for h in range(nq):
+                    x = scale * float(np.dot(np.asarray(k[page, h // (nq // nkv), s % PAGE], dtype=np.float64),
+                                             np.asarray(q[t, h * d:(h + 1) * d], dtype=np.float64)))
+                    l = float(lse[t, h])
+                    added[b, h // (nq // nkv), s] += 0.0 if l == -np.inf else np.exp(x - l)
+    return w + added, positions, added
+
+
+def plan_eviction(w, positions, ctx: int, seq: int, first: int, recent: int, budget: int):
+    """[(into, from)] of one list of slots."""
+    if ctx <= budget:
+        return []
+
+    def heavier(s):   # sorts what stays to the front
+        x = float(w[s])
+        return (0 if positions[s] >= seq - recent else 1, (1, 0.0) if np.isnan(x) else (0, -x), s)
+
+    keep = set(sorted(range(first, ctx), key=heavier)[:budget - first])
+    into = [s for s in range(first, budget) if s not in keep]
+    return list(zip(into, sorted(s for s in keep if s >= budget)))
 
 
 def token_logprobs(x, token, temperature: float, n_top: int):
