@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build", platform.machine())
 LIB = os.path.join(PKG, "libdflash.so")
 
 SOURCES = ["gemm_tc.cu", "gemm_simt.cu", "attention.cu", "elementwise.cu", "topk.cu",
-           "select_verify.cu", "append.cu", "cache_attention.cu", "cache_attention_tc.cu",
+           "select_verify.cu", "append.cu", "cache_attention.cu", "cache_attention_tc.cu", "shared_prefix.cu",
            "slot_weights.cu", "evict.cu", "logprobs.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // ------------------------------------------------------------ producer (the whole warp walks)
     if (!CL && n == 0) return;
     const T *q = static_cast<const T *>(p.q);
-    const uint64_t pol = policy_evict_first();
+    const uint64_t pol = PRE && p.pre.tile_tokens ? policy_evict_last() : policy_evict_first();
     const Runs runs = ct->runs;
     int cf = 0, cl = 0;
     int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
@@ -444,8 +444,11 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       }
     }
     if (!(ok = csync())) break;
+    const Dest dest = dest_of<PRE>(p, D, c.row0, c.h, c.rt * ROWS);
     for (int e = ctid; e < rows * (D / 4); e += 128) {
       const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
+      Share pre;
+      if (!CL && whole) pre = share_of<D, PRE>(dest, row, c4);
       float M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w * 16 + row]);
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
         *reinterpret_cast<float4 *>(xo + row * D + c4) = acc;
         if (c4 == 0) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * row) = make_float2(M, L);
       } else if (whole) {
-        write_row<T, D, PRE>(dest_of<PRE>(p, D, c.row0, c.h, c.rt * ROWS), row, c4, acc, M, L);
+        write_row<T, D, PRE>(dest, row, c4, acc, M, L, pre);
       } else {
         __stcg(reinterpret_cast<float4 *>(part + row * D + c4), acc);
         if (c4 == 0) {
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       }
       if (!(ok = csync())) break;
       if (ct->merge)
-        join_parts<T, D, PRE>(dest_of<PRE>(p, D, c.row0, c.h, c.rt * ROWS), p.partials, c.cf, c.cl - c.cf + 1, c.slot0,
+        join_parts<T, D, PRE>(dest, p.partials, c.cf, c.cl - c.cf + 1, c.slot0,
                               S::PART, ROWS, rows, ctid, 128);
     } else if (!(ok = csync())) {   // the join's reads of the stage are done
       break;
@@ -513,10 +516,12 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // Each CTA an equal part, all of a column's shares in flight: left to
     // the first CTAs, in two rounds, it took 5200 cycles for 4 rows of 16 shares.
     const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
+    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->h, ct->rt * ROWS);
     auto join = [&](auto in_flight) {
       constexpr int N = decltype(in_flight)::value;
       for (int e = rank * per + ctid; ctid >= 0 && e < end; e += 128) {
         const int row = e / (D / 4), c4 = (e % (D / 4)) * 4;
+        const Share pre = share_of<D, PRE>(dest, row, c4);
         float2 ml[N];
         float4 v[N];
         float M = -INFINITY, L = 0.f;
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
           acc.z = fmaf(w, v[u].z, acc.z);
           acc.w = fmaf(w, v[u].w, acc.w);
         }
-        write_row<T, D, PRE>(dest_of<PRE>(p, D, r.row0, ct->h, ct->rt * ROWS), row, c4, acc, M, L);
+        write_row<T, D, PRE>(dest, row, c4, acc, M, L, pre);
       }
     };
     if (p.cs > 8)
@@ -682,7 +687,8 @@ int row_cap(int total_new, int batch, int max_new) {
   return static_cast<int>(most < total_new ? most : total_new);
 }
 size_t share_bytes(const dflash_heads &h, int rows) {
-  return static_cast<size_t>(rows) * h.n_q_heads * (h.head_dim + 2) * sizeof(float);
+  const size_t shares = static_cast<size_t>(rows) * h.n_q_heads * (h.head_dim + 2) * sizeof(float);
+  return (shares + 15) / 16 * 16 + (h.dtype == DFLASH_F32 ? 0 : PREFIX_PART_BYTES);
 }
 
 }  // namespace
@@ -759,21 +765,20 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
     p.pre.row_cap = most;
     p.pre.pages = pages;
     p.pre.batch = batch;
-    // The prefix.  Tiles of 16 rows (fp32, or all there are): one request with
-    // every row in tiles; of 128 rows: runs of as many whole tokens.
-    Params x = p;
+    // The prefix.  fp32, or no more than 16 rows: one request with every row,
+    // in tiles of 16.
     const bool f32 = hs->dtype == DFLASH_F32;
     const long long all = static_cast<long long>(most) * p.g;
     if (f32 || all <= ROWS) {
+      Params x = p;
       x.B = 1;
       x.pre.tile_tokens = most;
       x.tiles = static_cast<int>((all + ROWS - 1) / ROWS);
-    } else {
-      x.pre.tile_tokens = 128 / p.g;
-      x.B = (most + x.pre.tile_tokens - 1) / x.pre.tile_tokens;
+      // its tiles' counters: at most batch * row_tiles(max_new) for each kv head, as many as the second launch has
+      if (int e = launch_attention(*hs, *kv, x, all, pages, dev, s)) return e;
+    } else if (int e = launch_prefix(*hs, *kv, p, dev, s)) {
+      return e;
     }
-    // its tiles' counters: at most batch * row_tiles(max_new) for each kv head, as many as the second launch has
-    if (int e = launch_attention(*hs, *kv, x, all, pages, dev, s)) return e;
   }
   return launch_attention(*hs, *kv, p, static_cast<long long>(max_new) * p.g, kv->max_pages - pages, dev, s);
 }

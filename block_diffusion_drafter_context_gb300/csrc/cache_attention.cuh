@@ -224,25 +224,45 @@ __device__ __forceinline__ Join2 join_prefix(float &M, float &L, float2 pre) {
   return f;
 }
 
+// The prefix's share of row `row` of the tile: columns c4 .. c4 + 3, its maximum
+// and sum.  Read before the parts that it joins, whose loads do not wait for it.
+struct Share {
+  float4 o;
+  float2 ml;
+};
+template <int D>
+__device__ __forceinline__ size_t share_index(const Dest &p, int row) {
+  row += p.base;
+  return static_cast<size_t>(row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
+}
+template <int D, bool PRE>
+__device__ __forceinline__ Share share_of(const Dest &p, int row, int c4) {
+  Share s = {make_float4(0.f, 0.f, 0.f, 0.f), make_float2(-INFINITY, 0.f)};
+  if (PRE && !p.first) {
+    const size_t i = share_index<D>(p, row);
+    s.o = __ldcg(reinterpret_cast<const float4 *>(p.share + i * D + c4));
+    s.ml = __ldcg(p.share_ml + i);
+  }
+  return s;
+}
+
 // Row `row` of the tile: output columns c4 .. c4 + 3, and its log-sum-exp.
 template <typename T, int D, bool PRE>
-__device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L) {
-  row += p.base;
+__device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L, const Share &share) {
   if (PRE) {
-    const size_t i = static_cast<size_t>(row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
-    float4 *share = reinterpret_cast<float4 *>(p.share + i * D + c4);
     if (p.first) {
-      __stcg(share, o);
+      const size_t i = share_index<D>(p, row);
+      __stcg(reinterpret_cast<float4 *>(p.share + i * D + c4), o);
       if (c4 == 0) __stcg(p.share_ml + i, make_float2(M, L));
       return;
     }
-    const float4 v = __ldcg(share);
-    const Join2 f = join_prefix(M, L, __ldcg(p.share_ml + i));
-    o.x = f.own * o.x + f.pre * v.x;
-    o.y = f.own * o.y + f.pre * v.y;
-    o.z = f.own * o.z + f.pre * v.z;
-    o.w = f.own * o.w + f.pre * v.w;
+    const Join2 f = join_prefix(M, L, share.ml);
+    o.x = f.own * o.x + f.pre * share.o.x;
+    o.y = f.own * o.y + f.pre * share.o.y;
+    o.z = f.own * o.z + f.pre * share.o.z;
+    o.w = f.own * o.w + f.pre * share.o.w;
   }
+  row += p.base;
   const size_t at = static_cast<size_t>(p.row0 + row / p.g) * (p.nkv * p.g) + p.h * p.g + row % p.g;
   const float inv = inverse_sum(M, L);
   T *dst = static_cast<T *>(p.out) + at * D + c4;
@@ -262,6 +282,9 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
   constexpr int PER = D / 4 / NV;   // items per row
   for (int e = tid; e < rows * PER; e += nthr) {
     const int r = e / PER, c = (e % PER) * 4;   // columns c + 4 PER k
+    Share share[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) share[k] = share_of<D, PRE>(p, r, c + 4 * PER * k);
     float M = -INFINITY, L = 0.f;
     float4 acc[NV];
 #pragma unroll
@@ -303,7 +326,7 @@ __device__ __forceinline__ void join_tile(const Dest &p, Src src, int np, int ti
       }
     }
 #pragma unroll
-    for (int k = 0; k < NV; ++k) write_row<T, D, PRE>(p, r, c + 4 * PER * k, acc[k], M, L);
+    for (int k = 0; k < NV; ++k) write_row<T, D, PRE>(p, r, c + 4 * PER * k, acc[k], M, L, share[k]);
   }
 }
 // the same for the runs' partials: np contributors from CTA cf on, a tile's
@@ -351,5 +374,10 @@ __device__ __forceinline__ void mma_split(float (&d)[4], float (&dl)[4], const u
 // 17..128 query rows per (request, kv head) on tcgen05 (cache_attention_tc.cu).
 // `pages`: the longest list of a (request, kv head) that the call may have.
 int launch_verify(const dflash_heads &hs, const dflash_kv &kv, Params &p, int pages, const Device &dev, cudaStream_t s);
+
+// The first launch of dflash_shared_attention, bf16 and more than 16 rows per kv
+// head (shared_prefix.cu).  Its partials lie behind the shares in `rows`.
+constexpr size_t PREFIX_PART_BYTES = 42u << 20;
+int launch_prefix(const dflash_heads &hs, const dflash_kv &kv, const Params &p, const Device &dev, cudaStream_t s);
 
 }  // namespace dflash

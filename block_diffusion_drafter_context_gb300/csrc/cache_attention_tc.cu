@@ -502,26 +502,30 @@ __global__ void __launch_bounds__(NTHR, 1)
       float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
       float Mr = M, Lr = L;   // with PRE: of the row, the prefix in it
       Join2 fr = {1.f, 0.f};
-      const bool keep = PRE && p.pre.tile_tokens;   // the first launch: rows stay shares
-      Dest dest;
-      size_t share_at = 0;
+      const float *share = nullptr;
       if (PRE && whole) {
-        dest = dest_of<true>(p, D, last.row0, last.h);
-        share_at = static_cast<size_t>(live ? tok : 0) * (p.nkv * g) + last.h * g + head;
-        if (!keep) fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + share_at));
+        const Dest dest = dest_of<true>(p, D, last.row0, last.h);
+        const size_t i = share_index<D>(dest, live ? row : 0);
+        share = dest.share + i * D;
+        fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + i));
       }
       const float inv = inverse_sum(Mr, Lr);
+      constexpr int CU = PRE ? 1 : 2;   // blocks of 16 columns in flight: the share's loads want registers too
 #pragma unroll
-      for (int c0 = 0; c0 < D / 16; c0 += 2) {
-        uint32_t a[2][16], b[2][16];
+      for (int c0 = 0; c0 < D / 16; c0 += CU) {
+        uint32_t a[CU][16], b[CU][16];
+        float4 sh[CU][4];
+        if (PRE && whole)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
+          for (int t = 0; t < 4 * CU; ++t) sh[t >> 2][t & 3] = __ldcg(reinterpret_cast<const float4 *>(share + c0 * 16) + t);
+#pragma unroll
+        for (int u = 0; u < CU; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
         if (two)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) tmem_ld16_nw(its_o + (c0 + u) * 16, b[u]);
+          for (int u = 0; u < CU; ++u) tmem_ld16_nw(its_o + (c0 + u) * 16, b[u]);
         tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < CU; ++u) {
           tmem_regs_ready(a[u]);
           float v[16];
 #pragma unroll
@@ -538,22 +542,14 @@ __global__ void __launch_bounds__(NTHR, 1)
               *reinterpret_cast<float4 *>(xo + row * D + ((((c0 + u) * 4 + t) ^ (row & (D / 4 - 1))) << 2)) =
                   make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
           } else if (whole) {
-            if (PRE) {
-              float4 *share = reinterpret_cast<float4 *>(dest.share + share_at * D + (c0 + u) * 16);
-              if (keep) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) __stcg(share + t, make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]));
-                continue;
-              }
+            if (PRE)
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
-                const float4 x = __ldcg(share + t);
-                v[4 * t] = fr.own * v[4 * t] + fr.pre * x.x;
-                v[4 * t + 1] = fr.own * v[4 * t + 1] + fr.pre * x.y;
-                v[4 * t + 2] = fr.own * v[4 * t + 2] + fr.pre * x.z;
-                v[4 * t + 3] = fr.own * v[4 * t + 3] + fr.pre * x.w;
+                v[4 * t] = fr.own * v[4 * t] + fr.pre * sh[u][t].x;
+                v[4 * t + 1] = fr.own * v[4 * t + 1] + fr.pre * sh[u][t].y;
+                v[4 * t + 2] = fr.own * v[4 * t + 2] + fr.pre * sh[u][t].z;
+                v[4 * t + 3] = fr.own * v[4 * t + 3] + fr.pre * sh[u][t].w;
               }
-            }
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
@@ -578,11 +574,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (two) mbar_arrive(&ct->oempty[wg ^ 1]);
       }
       if (whole) {
-        if (keep) {
-          if (live) __stcg(dest.share_ml + share_at, make_float2(M, L));
-        } else if (live && p.lse) {
-          p.lse[at] = log_sum(Mr, Lr);
-        }
+        if (live && p.lse) p.lse[at] = log_sum(Mr, Lr);
         continue;
       }
       if (live) {
@@ -627,6 +619,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int e = rank * per + threadIdx.x; e < end; e += NTHR) {
       const int row = e / (D / 4), c = e % (D / 4);
       const float *at = xo + row * D + ((c ^ (row & (D / 4 - 1))) << 2), *ml_at = xo + MROWS * D + 2 * row;
+      const Share share = share_of<D, PRE>(dest, row, c * 4);
       float2 ml[8];
       float4 v[8];
       float M = -INFINITY, L = 0.f;
@@ -649,7 +642,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         acc.z = fmaf(w, v[u].z, acc.z);
         acc.w = fmaf(w, v[u].w, acc.w);
       }
-      write_row<__nv_bfloat16, D, PRE>(dest, row, c * 4, acc, M, L);
+      write_row<__nv_bfloat16, D, PRE>(dest, row, c * 4, acc, M, L, share);
     }
     __syncwarp();
     cluster_sync();   // no CTA leaves while its share is read

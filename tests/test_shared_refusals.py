@@ -48,7 +48,8 @@ def test_empty_calls_do_nothing():
 
 def test_rows_size():
     h = heads()
-    assert B.dflash_shared_rows_bytes(h, 64, 16) == 64 * 16 * 8 * 130 * 4
+    assert B.dflash_shared_rows_bytes(heads(dtype=1), 64, 16) == 64 * 16 * 8 * 130 * 4
+    assert B.dflash_shared_rows_bytes(h, 64, 16) > 64 * 16 * 8 * 130 * 4      # and the partials of the tiles that are cut
     for batch, new in ((0, 1), (4097, 1), (1, 0), (1, 17)):
         with pytest.raises(B.DflashError):
             B.dflash_shared_rows_bytes(h, batch, new)
