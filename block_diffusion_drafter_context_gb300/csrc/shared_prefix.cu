@@ -7,17 +7,20 @@
 // rows on and by HBM below.  Nothing is masked.
 //
 // A CTA takes 256 rows as two tiles of 128 (one tensor-memory lane a row) that
-// share every block of 128 positions (two pages) in the ring:
-//   warp 0      feeds the ring by TMA, a block's K, then its V^T;
-//   warp 1      issues, block by block, for each tile O += P V of the block before
-//               and S = Q K^T of this one, so that one tile's products run while
-//               the other's scores turn into probabilities;
-//   warps 4-7, 8-11   softmax of tile 0 and 1: one row per thread, online in the
-//               exp2 domain, P in bf16 over the block's S.
-// Tensor memory is full: S (128 columns) and O (128) twice; Q lies in shared
-// memory.  At 64 positions a block, Q in tensor memory, a block's fixed times
-// (barriers, loads, votes) were as long as its work: 1024 tokens x 40 heads on
-// 32768 positions took 850 us.
+// share every K and V^T page of the ring:
+//   warps 0-3, 4-7   softmax of tile 0 and 1: one row per thread, online in the
+//               exp2 domain, P in bf16 over the page's S;
+//   warp 8      feeds the ring by TMA;
+//   warps 9, 10   issue the products, one warp for each tile: S = Q K^T of a page
+//               into one of two buffers, then O += P V of the page before, so that
+//               the next scores are there when a page's probabilities are done.
+// Tensor memory is full: two S (64 columns) and an O (128) for each tile; Q lies
+// in shared memory.
+// For 1024 tokens x 40 heads on 32768 positions (128 positions are 2048 cycles
+// of products for both tiles): 850 us with Q in tensor memory, one S and the
+// products issued by a thread on a branch of its own; 582 with blocks of 128
+// positions; 513 with a converged warp that issues; 475 with two S, which take
+// a tile's products out of the chain from its scores to the next ones.
 //
 // Tiles of a (kv head, 256 rows) go out whole while every CTA gets one, in the
 // order of the heads, so that the CTAs of a head sweep its pages together and
@@ -30,16 +33,16 @@ namespace dflash {
 namespace {
 
 constexpr int MROWS = 128, TILE = 2 * MROWS;
-constexpr int NTHR = 384;
+constexpr int SOFT = 8, NTHR = 32 * (SOFT + 3);   // softmax warps, then the producer and the MMA issuers
 template <int D>
 struct PShape {
-  static constexpr int SLOT = 2 * PAGE * D * 2;                 // K of two pages, [D / 64][128][64], or their V^T, [2][D][64]
-  static constexpr int ST = D == 128 ? 5 : 10;                  // ring depth
+  static constexpr int SLOT = PAGE * D * 2;                     // K of a page, [D / 64][64][64], or its V^T, [D][64]
+  static constexpr int ST = D == 128 ? 10 : 16;                 // ring depth
   static constexpr int QB = MROWS * D * 2;                      // a tile's Q, [D / 64][128][64]
   static constexpr int SMEM = 1024 + ST * SLOT + 2 * QB + 1024;
   static constexpr int PART = TILE * (D + 2);                   // O, then (maximum, sum) of each row
 };
-constexpr uint32_t S_COL = 0, O_COL = 256;                      // of tile w: + 128 w
+constexpr uint32_t S_COL = 0, O_COL = 256;                      // of tile w: + 128 w; S of odd pages: + 64
 
 struct PrefixArgs {
   const __nv_bfloat16 *q;
@@ -47,10 +50,15 @@ struct PrefixArgs {
   const int32_t *pages, *cu_new;   // the first request's row of the page table
   Prefix pre;
   int num_pages, total, nkv, g;
+  uint32_t over_g;                 // 2^32 / g, rounded up: see token_of
   float scale_log2;
   float *partials;                 // [CTA][2][PART]
   int *status;
 };
+
+// r / g for r < 2^20 (65536 tokens of up to 8 heads), g = 1..8: the product is
+// off by r times less than 8 / 2^32, below 1 / g.
+__device__ __forceinline__ int token_of(const PrefixArgs &a, int r) { return a.g == 1 ? r : static_cast<int>(__umulhi(r, a.over_g)); }
 
 // The rows of the batch and how their tiles go out to the CTAs.
 struct Plan {
@@ -101,11 +109,11 @@ struct Segs {
 };
 
 struct __align__(16) PCtrl {
-  uint64_t full[10], empty[10];                    // a slot's data; its last reader (the second tile's product) is done
-  uint64_t qfull[2], sfull[2], pfull[2], pdone[2], oempty[2], drain;   // [2]: of a tile
+  uint64_t full[16], empty[16];                    // a slot's data; both tiles' products are done with it
+  uint64_t qfull[2], sfull[2][2], pfull[2][2], pdone[2], oempty[2], drain[2];   // [2]: of a tile; [2][2]: and of an S
   uint32_t tmem;
   int abort_flag;
-  int bad[10];                                     // pages of the slot that are not there, a bit each
+  int bad[16];                                     // the slot's page is not there
 };
 static_assert(sizeof(PCtrl) <= 1024, "shared memory");
 
@@ -131,35 +139,43 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(NTHR, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PrefixArgs a) {
   using S = PShape<D>;
   constexpr int ST = S::ST, SLOT = S::SLOT;
-  static_assert(S::SMEM <= 232448 && ST <= 10, "shared memory");
+  static_assert(S::SMEM <= 232448 && ST <= 16, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *sq = ring + ST * SLOT;
   PCtrl *ct = reinterpret_cast<PCtrl *>(sq + 2 * S::QB);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform to the compiler
   volatile int *abort_flag = &ct->abort_flag;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&ct->full[i], 1);
-      mbar_init(&ct->empty[i], 1);
+      mbar_init(&ct->empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ct->qfull[i], 4);
-      mbar_init(&ct->sfull[i], 1);
-      mbar_init(&ct->pfull[i], 4);
+      mbar_init(&ct->sfull[i][0], 1);
+      mbar_init(&ct->sfull[i][1], 1);
+      mbar_init(&ct->pfull[i][0], 4);
+      mbar_init(&ct->pfull[i][1], 4);
       mbar_init(&ct->pdone[i], 1);
       mbar_init(&ct->oempty[i], 4);
+      mbar_init(&ct->drain[i], 1);
     }
-    mbar_init(&ct->drain, 1);
     ct->abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == SOFT) {
     tmem_alloc(&ct->tmem, 512);
     tmem_relinquish();
   }
@@ -174,47 +190,41 @@ __global__ void __launch_bounds__(NTHR, 1)
   Segs segs;
   segs.start(plan, blockIdx.x, gridDim.x);
   Seg sg;
-  // the rows of tile w of a segment; its blocks of two pages (the last one may have one)
+  // Whether any of the prefix's pages is missing: only then do the warps ask of each block.
+  int missing = 0;
+  for (int i = threadIdx.x; i < pages; i += NTHR) {
+    const int page = a.pages[i];
+    missing |= page < 0 || page >= a.num_pages;
+  }
+  const bool any_bad = __syncthreads_or(missing) != 0;
+  // the rows of tile w of a segment
   auto rows_of = [&](const Seg &s, int w) { return plan.rows - (s.tile % plan.per_head) * TILE - w * MROWS; };
-  auto blocks_of = [](const Seg &s) { return (s.n + 1) / 2; };
 
-  if (warp == 0) {
+  // A segment's slots in the ring: K of page 0; K of page p, V of page p - 1; V of the last.
+  if (warp == SOFT) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       bool ok = true;
-      int i = 0;                   // slots: K of block j is 2 j, V 2 j + 1
+      int i = 0;
       while (ok && segs.next(plan, pages, sg)) {
         const int h = sg.tile / plan.per_head;
-        for (int k = 0; k < blocks_of(sg) && ok; ++k) {
-          const int have = min(2, sg.n - 2 * k);
-          int page[2], bad = have < 2 ? 2 : 0;
+        for (int k = 0; k < 2 * sg.n; ++k, ++i) {
+          const bool v = k > 0 && (k == 2 * sg.n - 1 || !(k & 1));
+          const int page = a.pages[sg.page + (k == 2 * sg.n - 1 ? sg.n - 1 : v ? k / 2 - 1 : (k + 1) / 2)], st = i % ST;
+          const bool bad = page < 0 || page >= a.num_pages;
+          ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
+          if (!ok) break;
+          if (bad) report(a.status, DFLASH_ERR_DEVICE);
+          ct->bad[st] = bad;
+          mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : SLOT);
+          if (bad) continue;
+          uint8_t *dst = ring + st * SLOT;
+          if (v)
+            tma_load_2d(dst, &tmV, &ct->full[st], 0, (page * a.nkv + h) * D);
+          else
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            page[u] = u < have ? a.pages[sg.page + 2 * k + u] : 0;
-            if (page[u] < 0 || page[u] >= a.num_pages) {
-              bad |= 1 << u;
-              report(a.status, DFLASH_ERR_DEVICE);
-            }
-          }
-          for (int v = 0; v < 2; ++v, ++i) {
-            const int st = i % ST;
-            ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
-            if (!ok) break;
-            ct->bad[st] = bad;
-            mbar_arrive_expect_tx(&ct->full[st], (2 - __popc(bad)) * (SLOT / 2));
-            uint8_t *dst = ring + st * SLOT;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (bad >> u & 1) continue;
-              if (v)
-                tma_load_2d(dst + u * (SLOT / 2), &tmV, &ct->full[st], 0, (page[u] * a.nkv + h) * D);
-              else
-#pragma unroll
-                for (int half = 0; half < D / 64; ++half)
-                  tma_load_2d(dst + half * (MROWS * 128) + u * (PAGE * 128), &tmK, &ct->full[st], half * 64,
-                              (page[u] * a.nkv + h) * PAGE);
-            }
-          }
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_2d(dst + half * (PAGE * 128), &tmK, &ct->full[st], half * 64, (page * a.nkv + h) * PAGE);
         }
       }
       if (!ok) {
@@ -225,257 +235,270 @@ __global__ void __launch_bounds__(NTHR, 1)
       for (int j = max(0, i - ST); j < i; ++j)
         mbar_wait(&ct->full[j % ST], static_cast<uint32_t>((j / ST) & 1), nullptr, WAIT_NS);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(MROWS, 2 * PAGE), idesc_o = idesc_bf16_f32(MROWS, D);
-      bool ok = true, any = false;
-      int j = 0;                                     // block of the CTA
-      int n_tile[2] = {0, 0}, n_block[2] = {0, 0};   // tiles and blocks a tile of the CTA had
-      bool started[2] = {false, false};              // O holds something of the tile
-      auto wait = [&](uint64_t *bar, int n) { return mbar_wait(bar, static_cast<uint32_t>(n & 1), abort_flag, WAIT_NS); };
-      // O += P V of block b of the CTA
-      auto pv = [&](int w, int b, bool frees) -> bool {
-        const int i = 2 * b + 1, st = i % ST;
-        if (!wait(&ct->full[st], i / ST) || !wait(&ct->pfull[w], n_block[w] - 1)) return false;
-        tc_fence_after();
-        const int bad = ct->bad[st];
-        const uint32_t pt = tmem + S_COL + 128 * w, v0 = smem_u32(ring + st * SLOT);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (bad >> u & 1) continue;
-#pragma unroll
-          for (int kk = 0; kk < PAGE / 16; ++kk)
-            umma_bf16_ts(tmem + O_COL + 128 * w, pt + static_cast<uint32_t>(32 * u + kk * 8),
-                         sdesc_k_sw128(v0 + u * (SLOT / 2) + kk * 32), idesc_o, kk > 0 || started[w] ? 1u : 0u);
-          started[w] = true;
+  } else if (warp > SOFT) {
+    // ------------------------------------------------------------ MMA issuers
+    // the whole warp, converged; one lane of it issues
+    constexpr uint32_t idesc_s = idesc_bf16_f32(MROWS, PAGE), idesc_o = idesc_bf16_f32(MROWS, D);
+    const int w = warp - SOFT - 1;
+    const uint32_t s_col = tmem + S_COL + 128 * w, o_col = tmem + O_COL + 128 * w, q0 = smem_u32(sq + w * S::QB);
+    const uint32_t ring0 = smem_u32(ring);
+    bool ok = true, any = false;
+    int n_tile = 0, n_s = 0, n_p = 0;              // tiles of this half of the CTA, pages' S and P V issued
+    int st = 0;                                    // the next slot of the ring, and its parity
+    uint32_t ph = 0;
+    auto wait = [&](uint64_t *bar, uint32_t n) { return mbar_wait(bar, n & 1, abort_flag, WAIT_NS); };
+    auto all = [](bool fine) { return !__any_sync(0xffffffffu, !fine); };
+    auto step = [&] {
+      if (++st == ST) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    while (ok && segs.next(plan, pages, sg)) {
+      if (rows_of(sg, w) <= 0) {                   // the tile is not there: its slots are free as they come
+        for (int i = 0; i < 2 * sg.n && ok; ++i, step()) {
+          ok = all(wait(&ct->full[st], ph));
+          if (ok && lane == 0) mbar_arrive(&ct->empty[st]);
         }
-        umma_commit(&ct->pdone[w]);
-        if (frees) umma_commit(&ct->empty[st]);
-        return true;
-      };
-      // S = Q K^T of block b; a page that is not there gives columns that nobody reads
-      auto qk = [&](int w, int b, bool frees) {
-        const int st = 2 * b % ST;
-        const uint32_t k0 = smem_u32(ring + st * SLOT), q0 = smem_u32(sq + w * S::QB);
-        tc_fence_after();
+        continue;
+      }
+      any = true;
+      bool started = false;                        // O holds something of the tile
+      // S of the next page; a page that is not there gives columns that nobody reads
+      auto scores = [&] {
+        const uint32_t k0 = ring0 + st * SLOT, d = s_col + 64 * (n_s & 1);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16(tmem + S_COL + 128 * w, sdesc_k_sw128(q0 + (kk >> 2) * (MROWS * 128) + (kk & 3) * 32),
-                    sdesc_k_sw128(k0 + (kk >> 2) * (MROWS * 128) + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(&ct->sfull[w]);
-        if (frees) umma_commit(&ct->empty[st]);
-        ++n_block[w];
+          umma_bf16_elect(d, sdesc_k_sw128(q0 + (kk >> 2) * (MROWS * 128) + (kk & 3) * 32),
+                          sdesc_k_sw128(k0 + (kk >> 2) * (PAGE * 128) + (kk & 3) * 32), idesc_s, kk > 0 ? 1u : 0u);
+        umma_commit_elect(&ct->sfull[w][n_s & 1]);
+        umma_commit_elect(&ct->empty[st]);
+        ++n_s;
+        step();
       };
-      while (ok && segs.next(plan, pages, sg)) {
-        const int both = rows_of(sg, 1) > 0 ? 2 : 1, blocks = blocks_of(sg);
-        any = true;
-        for (int k = 0; k <= blocks && ok; ++k) {    // the scores of block k, and P V of the block before
-          if (k < blocks) ok = wait(&ct->full[2 * j % ST], 2 * j / ST);
-          for (int w = 0; w < both && ok; ++w) {
-            if (k == 1) {                            // the tile's first P V: the O of the tile before has been read
-              started[w] = false;
-              if (n_tile[w]++ > 0) ok = wait(&ct->oempty[w], n_tile[w]);
-            }
-            if (ok && k > 0) ok = pv(w, j - 1, w == both - 1);
-            if (ok && k == 0) ok = wait(&ct->qfull[w], n_tile[w]);   // the first S of a tile wants its query rows
-            if (ok && k < blocks) qk(w, j, w == both - 1);
-          }
-          if (k < blocks) ++j;
+      if (!(ok = all(wait(&ct->full[st], ph) && wait(&ct->qfull[w], n_tile++)))) break;
+      tc_fence_after();
+      scores();
+      for (int k = 0; k < sg.n; ++k) {             // S of page k + 1, O += P V of page k
+        if (k + 1 < sg.n) {                        // its buffer is free: P V of page k - 1 was issued before
+          if (!(ok = all(wait(&ct->full[st], ph)))) break;
+          tc_fence_after();
+          scores();
         }
-      }
-      if (!ok) {
-        report(a.status, DFLASH_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      if (any) {
-        umma_commit(&ct->drain);   // every issued MMA retires before TMEM is released
-        mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
+        ok = wait(&ct->full[st], ph);
+        // the first P V of a tile: the O of the tile before has been read
+        if (k == 0 && n_tile > 1) ok = ok && wait(&ct->oempty[w], n_tile);
+        ok = ok && wait(&ct->pfull[w][n_p & 1], n_p >> 1);
+        if (!(ok = all(ok))) break;
+        tc_fence_after();
+        if (!any_bad || !ct->bad[st]) {
+          const uint32_t v0 = ring0 + st * SLOT, p0 = s_col + 64 * (n_p & 1);
+#pragma unroll
+          for (int kk = 0; kk < PAGE / 16; ++kk)
+            umma_bf16_ts_elect(o_col, p0 + static_cast<uint32_t>(kk * 8), sdesc_k_sw128(v0 + kk * 32), idesc_o,
+                               kk > 0 || started ? 1u : 0u);
+          started = true;
+        }
+        umma_commit_elect(&ct->pdone[w]);
+        umma_commit_elect(&ct->empty[st]);
+        ++n_p;
+        step();
       }
     }
-  } else if (warp >= 4) {
+    if (!ok && lane == 0) {
+      report(a.status, DFLASH_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (any) {
+      umma_commit_elect(&ct->drain[w]);   // every issued MMA retires before TMEM is released
+      mbar_wait(&ct->drain[w], 0, nullptr, WAIT_NS);
+    }
+  } else {
     // ------------------------------------------------------------ softmax
-    const int w = (warp >> 2) - 1, quad = warp & 3, row = quad * 32 + lane;   // TMEM lane = query row
+    const int w = warp >> 2, quad = warp & 3, row = quad * 32 + lane;   // tile; TMEM lane = query row
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t my_s = lane_base + S_COL + 128 * w, my_o = lane_base + O_COL + 128 * w;
     const int nq = a.nkv * a.g;
     bool ok = true;
-    int nb = 0, j = 0;               // blocks this tile had; block of the CTA
+    int np = 0;                      // pages this tile had
     float m = -INFINITY, l = 0.f;    // maximum (scaled, log2) and sum of this row
     auto waitw = [&](uint64_t *bar, int n) -> bool {   // warp-uniform bounded wait
       const bool done = mbar_wait(bar, static_cast<uint32_t>(n & 1), abort_flag, WAIT_NS);
       return !__any_sync(0xffffffffu, !done);
     };
-    // this row's query into shared memory, 16-byte chunks XORed by the row as TMA would
-    auto load_q = [&](const Seg &s) {
-      const int r = (s.tile % plan.per_head) * TILE + w * MROWS + row;
-      const bool live = r < plan.rows;
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + static_cast<size_t>(plan.begin + (live ? r / a.g : 0)) * a.ldq +
-                                                         static_cast<size_t>(s.tile / plan.per_head * a.g + r % a.g) * D);
-      uint4 u[D / 8];
+    // the first of this warp's 32 rows of a segment, among the rows of its head
+    auto first_row = [&](const Seg &s) { return (s.tile % plan.per_head) * TILE + w * MROWS + quad * 32; };
+    // This warp's part of the query rows in shared memory: 32 rows of 128 bytes for
+    // each 64 dims, 16-byte chunks XORed by the row as TMA would.
+    auto q_part = [&](int half) { return sq + w * S::QB + half * (MROWS * 128) + quad * (32 * 128); };
+    // Where it pays to be short: code that runs once a tile comes from the
+    // instruction memory, 5 us for this with its loops unrolled and g divided by.
+    auto load_q = [&](const Seg &s) {   // whole rows, 16 bytes a lane
+      constexpr int LPR = D / 8, RPI = 32 / LPR, U = 8;
+      const int c = lane % LPR, h = s.tile / plan.per_head;
+#pragma unroll 1
+      for (int t0 = 0; t0 < 32; t0 += U * RPI) {
+        uint4 u[U];
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
-      uint8_t *dst = sq + w * S::QB + row * 128;
+        for (int t = 0; t < U; ++t) {
+          const int r = first_row(s) + t0 + t * RPI + lane / LPR, tok = token_of(a, r);
+          u[t] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < plan.rows)
+            u[t] = __ldg(reinterpret_cast<const uint4 *>(a.q + (plan.begin + tok) * a.ldq + (h * a.g + r - tok * a.g) * D) + c);
+        }
 #pragma unroll
-      for (int t = 0; t < D / 8; ++t)
-        *reinterpret_cast<uint4 *>(dst + (t >> 3) * (MROWS * 128) + (((t & 7) ^ (row & 7)) << 4)) = u[t];
+        for (int t = 0; t < U; ++t) {
+          const int r = t0 + t * RPI + lane / LPR;
+          *reinterpret_cast<uint4 *>(q_part(c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = u[t];
+        }
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct->qfull[w]);
     };
-    // on to the next segment that has rows for this tile; j moves past the others' blocks
+    // on to the next segment that has rows for this tile
     auto advance = [&](Seg &s) -> bool {
       while (segs.next(plan, pages, s)) {
         if (rows_of(s, w) > 0) return true;
-        j += blocks_of(s);
       }
       return false;
     };
     bool more = advance(sg);
     if (more) load_q(sg);
     while (more && ok) {
-      const int blocks = blocks_of(sg);
-      for (int k = 0; k < blocks; ++k, ++j, ++nb) {
-        // V's slot and its `bad` stay until this block's P V
-        const int vs = (2 * j + 1) % ST;
-        if (!(ok = waitw(&ct->sfull[w], nb) && waitw(&ct->full[vs], (2 * j + 1) / ST))) break;
+      for (int k = 0; k < sg.n; ++k, ++np) {
+        const uint32_t sp = my_s + 64 * (np & 1);
+        if (!(ok = waitw(&ct->sfull[w][np & 1], np >> 1))) break;
         tc_fence_after();
-        const int bad = ct->bad[vs];
-        // ---- the row's maximum over the block
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (bad >> c & 1) continue;
-          uint32_t r[4][16];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) tmem_ld16_nw(my_s + 64 * c + 16 * t, r[t]);
-          tmem_wait_ld();
-          float x0 = -INFINITY, x1 = x0, x2 = x0, x3 = x0;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            tmem_regs_ready(r[t]);
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              x0 = fmaxf(fmaxf(x0, __uint_as_float(r[t][e])), __uint_as_float(r[t][e + 1]));
-              x1 = fmaxf(fmaxf(x1, __uint_as_float(r[t][e + 2])), __uint_as_float(r[t][e + 3]));
-              x2 = fmaxf(fmaxf(x2, __uint_as_float(r[t][e + 4])), __uint_as_float(r[t][e + 5]));
-              x3 = fmaxf(fmaxf(x3, __uint_as_float(r[t][e + 6])), __uint_as_float(r[t][e + 7]));
-            }
-          }
-          mx = fmaxf(mx, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
+        bool bad = false;
+        if (any_bad) {
+          const int page = a.pages[sg.page + k];
+          bad = page < 0 || page >= a.num_pages;
         }
-        mx = fmaxf(mx * a.scale_log2, bad == 3 ? -INFINITY : LOWEST);
+        uint32_t x[4][16];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tmem_ld16_nw(sp + 16 * t, x[t]);
+        tmem_wait_ld();
+        float x0 = -INFINITY, x1 = x0, x2 = x0, x3 = x0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          tmem_regs_ready(x[t]);
+          if (any_bad)   // what a page that is not there left in its columns
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (bad) x[t][e] = __float_as_uint(-INFINITY);
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            x0 = max3(x0, __uint_as_float(x[t][e]), __uint_as_float(x[t][e + 1]));
+            x1 = max3(x1, __uint_as_float(x[t][e + 2]), __uint_as_float(x[t][e + 3]));
+            x2 = max3(x2, __uint_as_float(x[t][e + 4]), __uint_as_float(x[t][e + 5]));
+            x3 = max3(x3, __uint_as_float(x[t][e + 6]), __uint_as_float(x[t][e + 7]));
+          }
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2, bad ? -INFINITY : LOWEST);
+        const bool need = mx > m + RESCALE_LOG2;
         if (k == 0) {
           m = mx;
           l = 0.f;
-        } else {
-          const bool need = mx > m + RESCALE_LOG2;
-          if (__any_sync(0xffffffffu, need)) {   // wait for the P V of the block before, rescale O in TMEM
-            if (!(ok = waitw(&ct->pdone[w], nb - 1))) break;
-            tc_fence_after();
-            const float f = need ? fast_exp2(m - mx) : 1.f;
+        } else if (__any_sync(0xffffffffu, need)) {   // wait for the P V of the page before, rescale O in TMEM
+          if (!(ok = waitw(&ct->pdone[w], np - 1))) break;
+          tc_fence_after();
+          const float f = need ? fast_exp2(m - mx) : 1.f;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t ov[16];
+            tmem_ld16_nw(my_o + c0, ov);
+            tmem_wait_ld();
+            tmem_regs_ready(ov);
 #pragma unroll
-            for (int c0 = 0; c0 < D / 16; c0 += 2) {
-              uint32_t ov[2][16];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, ov[u]);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                tmem_regs_ready(ov[u]);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) ov[u][e] = __float_as_uint(__uint_as_float(ov[u][e]) * f);
-                tmem_st16_nw(my_o + (c0 + u) * 16, ov[u]);
-              }
-            }
-            tmem_wait_st();
-            if (need) {
-              l *= f;
-              m = mx;
-            }
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+            tmem_st16_nw(my_o + c0, ov);
+          }
+          tmem_wait_st();
+          if (need) {
+            l *= f;
+            m = mx;
           }
         }
-        // ---- P over the block's S, rounded to bf16; the sum keeps fp32.  32
-        // columns at a time, read again; their P takes the first half of the columns read before.
+        // P, rounded to bf16, over the page's S; the sum keeps fp32
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t sc2 = pair(a.scale_log2, a.scale_log2), nm2 = pair(nm, nm);
         uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
-        uint32_t r[2][2][16];
-        tmem_ld16_nw(my_s, r[0][0]);
-        tmem_ld16_nw(my_s + 16, r[0][1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c == 2 && (bad & 2)) break;        // the second page is not there: no P V reads it
-          tmem_wait_ld();
-          tmem_regs_ready(r[c & 1][0]);
-          tmem_regs_ready(r[c & 1][1]);
-          if (c < 3 && !(c == 1 && (bad & 2))) {
-            tmem_ld16_nw(my_s + 32 * (c + 1), r[(c + 1) & 1][0]);
-            tmem_ld16_nw(my_s + 32 * (c + 1) + 16, r[(c + 1) & 1][1]);
-          }
-          if (c < 2 && (bad & 1)) continue;
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const uint32_t *x = &r[c & 1][e >> 4][e & 15];
-            const float2 y0 = unpair(fma2(pair(__uint_as_float(x[0]), __uint_as_float(x[1])), sc2, nm2));
-            const float2 y1 = unpair(fma2(pair(__uint_as_float(x[2]), __uint_as_float(x[3])), sc2, nm2));
+            const uint32_t *y = &x[2 * c + (e >> 4)][e & 15];
+            const float2 y0 = unpair(fma2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2, nm2));
+            const float2 y1 = unpair(fma2(pair(__uint_as_float(y[2]), __uint_as_float(y[3])), sc2, nm2));
             const float p0 = fast_exp2(y0.x), p1 = fast_exp2(y0.y), p2 = fast_exp2(y1.x), p3 = fast_exp2(y1.y);
             sum0 = add2(sum0, pair(p0, p1));
             sum1 = add2(sum1, pair(p2, p3));
             pk[e >> 1] = pack_bf16(p0, p1);
             pk[(e >> 1) + 1] = pack_bf16(p2, p3);
           }
-          tmem_st16_nw(my_s + 16 * c, pk);
+          tmem_st16_nw(sp + 16 * c, pk);
         }
         const float2 s0 = unpair(add2(sum0, sum1));
         l += s0.x + s0.y;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ct->pfull[w]);
+        if (lane == 0) mbar_arrive(&ct->pfull[w][np & 1]);
       }
       if (!ok) break;
+      // ---- the tile's rows, as shares or partials, through this warp's part of
+      // the query rows (the last S of the tile is complete, so they are not needed
+      // any more): 32 rows straight from their threads took 4 us of stores a tile
       const Seg last = sg;
-      const int r = (last.tile % plan.per_head) * TILE + w * MROWS + row;
-      more = advance(sg);
-      if (more) load_q(sg);      // the last S of this tile is complete: its query rows are not needed any more
-      // ---- the tile's row, as a share or a partial
-      if (!(ok = waitw(&ct->pdone[w], nb - 1))) break;
+      // (a phase can be waited for once the one before is known to be over, and the
+      // last S tells of the P V two pages before)
+      if (np > 1 && !(ok = waitw(&ct->pdone[w], np - 2))) break;
+      if (!(ok = waitw(&ct->pdone[w], np - 1))) break;
       tc_fence_after();
-      const bool live = r < plan.rows;
-      const size_t at = static_cast<size_t>(live ? r / a.g : 0) * nq + last.tile / plan.per_head * a.g + r % a.g;
-      float *dst, *ml;
-      if (last.slot < 0) {
-        dst = a.pre.rows + at * D;
-        ml = a.pre.rows + static_cast<size_t>(a.pre.row_cap) * nq * D + 2 * at;
-      } else {
-        float *part = a.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
-        dst = part + (w * MROWS + row) * D;
-        ml = part + TILE * D + 2 * (w * MROWS + row);
-      }
+      const int head = last.tile / plan.per_head * a.g;
+      float *part = last.slot < 0 ? nullptr : a.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
+      auto place = [&](int rr) -> size_t {           // of row rr of the warp's 32 among the shares
+        const int r = first_row(last) + rr, tok = token_of(a, r);
+        return static_cast<size_t>(tok) * nq + head + r - tok * a.g;
+      };
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint8_t *stage = q_part(c0 / 32 % (D / 64));
 #pragma unroll
-      for (int c0 = 0; c0 < D / 16; c0 += 2) {
-        uint32_t ov[2][16];
+        for (int u = 0; u < 32; u += 16) {
+          uint32_t ov[16];
+          tmem_ld16_nw(my_o + c0 + u, ov);
+          tmem_wait_ld();
+          tmem_regs_ready(ov);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, ov[u]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          tmem_regs_ready(ov[u]);
-          if (!live) continue;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {   // sum 0: O may never have been written
-            const float4 v = make_float4(__uint_as_float(ov[u][4 * t]), __uint_as_float(ov[u][4 * t + 1]),
-                                         __uint_as_float(ov[u][4 * t + 2]), __uint_as_float(ov[u][4 * t + 3]));
-            __stcg(reinterpret_cast<float4 *>(dst + (c0 + u) * 16 + 4 * t), l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : v);
+          for (int t = 0; t < 4; ++t) {            // sum 0: O may never have been written
+            uint4 v = make_uint4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
+            if (l == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + (((u / 4 + t) ^ (lane & 7)) << 4)) = v;
           }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int t = 0; t < 8; ++t) {
+          const int rr = 4 * t + (lane >> 3), c = lane & 7;
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+          float *dst = part ? part + (w * MROWS + quad * 32 + rr) * D : a.pre.rows + place(rr) * D;
+          if (first_row(last) + rr < plan.rows) __stcg(reinterpret_cast<uint4 *>(dst + c0 + 4 * c), v);
+        }
+        __syncwarp();
       }
-      if (live) __stcg(reinterpret_cast<float2 *>(ml), make_float2(join_max(m, l), l));
+      if (first_row(last) + lane < plan.rows) {
+        float *ml = part ? part + TILE * D + 2 * (w * MROWS + row)
+                         : a.pre.rows + static_cast<size_t>(a.pre.row_cap) * nq * D + 2 * place(lane);
+        __stcg(reinterpret_cast<float2 *>(ml), make_float2(join_max(m, l), l));
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ct->oempty[w]);
+      more = advance(sg);
+      if (more) load_q(sg);
     }
     if (!ok) {
       report(a.status, DFLASH_ERR_TIMEOUT);
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == SOFT) tmem_dealloc(tmem, 512);
 }
 
 // The rows of the tiles that were cut up: D / 4 threads a row, the partials of
@@ -537,7 +560,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const PrefixA
       acc.w = fmaf(e, v[u].w, acc.w);
     }
   }
-  const size_t at = static_cast<size_t>(r / a.g) * nq + h * a.g + r % a.g;
+  const int tok = token_of(a, r);
+  const size_t at = static_cast<size_t>(tok) * nq + h * a.g + r - tok * a.g;
   __stcg(reinterpret_cast<float4 *>(a.pre.rows + at * D + c4), acc);
   if (c4 == 0) __stcg(reinterpret_cast<float2 *>(a.pre.rows + static_cast<size_t>(a.pre.row_cap) * nq * D) + at, make_float2(M, L));
 }
@@ -562,6 +586,7 @@ int launch(const dflash_heads &hs, const dflash_kv &kv, const Params &p, const D
   a.total = p.total;
   a.nkv = p.nkv;
   a.g = p.g;
+  a.over_g = static_cast<uint32_t>((0x100000000ull + p.g - 1) / p.g);
   a.scale_log2 = p.scale_log2;
   a.status = p.status;
   const size_t nq = static_cast<size_t>(p.nkv) * p.g;
