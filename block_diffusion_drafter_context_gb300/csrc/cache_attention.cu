@@ -54,9 +54,8 @@ struct Shape {
 
 struct __align__(16) Ctrl {
   uint64_t full[6], empty[6], cons;
-  long long lo;
   Runs runs;
-  int n_mine, b, h, rt, k;                 // the run's first page: k of tile (b, h, rt)
+  Start run;
   int abort_flag, merge;
   Chunk chunk[6];
 };
@@ -92,13 +91,13 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
   if (CL) {
     if (threadIdx.x == 0) {
       const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs, head = list / p.tiles;
-      ct->b = head / p.nkv;
-      ct->h = head % p.nkv;
-      ct->rt = list % p.tiles;
-      const Req r = request<PRE>(p, ct->b, rank == 0 && ct->h == 0 && ct->rt == 0);
-      const int np = ct->rt < tiles_of(r) ? r.np : 0;
-      ct->k = rank * np / p.cs;
-      ct->n_mine = (rank + 1) * np / p.cs - ct->k;
+      ct->run.b = head / p.nkv;
+      ct->run.h = head % p.nkv;
+      ct->run.rt = list % p.tiles;
+      const Req r = request<PRE>(p, ct->run.b, rank == 0 && ct->run.h == 0 && ct->run.rt == 0);
+      const int np = ct->run.rt < tiles_of(r) ? r.np : 0;
+      ct->run.k = rank * np / p.cs;
+      ct->run.n = (rank + 1) * np / p.cs - ct->run.k;
     }
   } else if (warp == 0) {
     // Lane i sums the pages of a contiguous slice of the requests; a warp
@@ -118,29 +117,14 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     const long long lo = c < runs.G ? runs.lo(c) : 0, hi = c < runs.G ? runs.lo(c + 1) : 0;
     const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
     if (lane == 0) {
-      ct->n_mine = static_cast<int>(hi - lo);
-      ct->lo = lo;
+      if (hi == lo) ct->run.n = 0;
       ct->runs = runs;
     }
-    if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
-      long long pre = ex;
-      for (int b = b0; b < b1; ++b) {
-        const Req r = request<PRE>(p, b, false);
-        const long long np = r.np, head = np * tiles_of(r), span = head * p.nkv;
-        if (lo < pre + span) {
-          const long long h = quotient(lo - pre, head), rt = quotient(lo - pre - h * head, np);
-          ct->b = b;
-          ct->h = static_cast<int>(h);
-          ct->rt = static_cast<int>(rt);
-          ct->k = static_cast<int>(lo - pre - h * head - rt * np);
-          break;
-        }
-        pre += span;
-      }
-    }
+    if (hi > lo && lo >= ex && lo < in)   // exactly one lane
+      find_start<PRE>(p, b0, b1, ex, lo, hi, tiles_of, &ct->run);
   }
   __syncthreads();
-  const int n = ct->n_mine;
+  const int n = ct->run.n;
   if (warp == 0) {
     // ------------------------------------------------------------ producer (the whole warp walks)
     if (!CL && n == 0) return;
@@ -148,12 +132,13 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     const uint64_t pol = PRE && p.pre.tile_tokens ? policy_evict_last() : policy_evict_first();
     const Runs runs = ct->runs;
     int cf = 0, cl = 0;
-    int b = ct->b, h = ct->h, rt = ct->rt, k = ct->k;
-    long long x = ct->lo;
+    int b = ct->run.b, h = ct->run.h, rt = ct->run.rt, k = ct->run.k;
+    long long x0 = ct->run.x0;   // the tile's beginning in the list
+    const int cost = PRE ? p.pre.cost : 0;
     Req r = request<PRE>(p, b, false);
     int issued = 0;
     bool ok = true;
-    for (int i = 0; i < n; ++i, ++x) {
+    for (int i = 0; i < n; ++i) {
       const int st = i % NST;
       ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / NST) & 1) ^ 1), abort_flag, WAIT_NS);
       ok = !__any_sync(0xffffffffu, !ok);
@@ -165,13 +150,13 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       if (lane == 0) {
         if (bad) report(p.status, DFLASH_ERR_DEVICE);
         if (!CL && first) {
-          cf = runs.owner(x - k);
-          cl = runs.owner(x - k + r.np - 1);
+          cf = runs.owner(x0 + cost);
+          cl = runs.owner(x0 + cost + r.np - 1);
         }
         Chunk c;
         c.b = b, c.h = h, c.rt = rt, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
         c.flags = (first ? FIRST : 0) | (last ? LAST : 0) | (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
-        c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
+        c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) >= x0, c.slot = i - k <= 0 ? 0 : 1;
         ct->chunk[st] = c;
         mbar_arrive_expect_tx(&ct->full[st], (bad ? 0 : S::STAGE) + live * D * S::SIZE);
       }
@@ -196,6 +181,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       issued = i + 1;
       if (++k == r.np && !CL) {
         k = 0;
+        x0 += tile_units<PRE>(p, r);
         if (++rt == tiles_of(r)) {
           rt = 0;
           if (++h == p.nkv && i + 1 < n) {
@@ -506,8 +492,8 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
   }
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
-    const Req r = request<PRE>(p, ct->b, false);
-    const int rows = min(ROWS, r.n * p.g - ct->rt * ROWS), rank = static_cast<int>(cluster_ctarank());
+    const Req r = request<PRE>(p, ct->run.b, false);
+    const int rows = min(ROWS, r.n * p.g - ct->run.rt * ROWS), rank = static_cast<int>(cluster_ctarank());
     float *xo = share(share_stage(rows > 0 ? r.np : 0, rank));
     if (n == 0 || !ok)   // nothing to add
       for (int i = ctid; i >= 0 && i < ROWS; i += 128) *reinterpret_cast<float2 *>(xo + ROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
@@ -516,7 +502,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // Each CTA an equal part, all of a column's shares in flight: left to
     // the first CTAs, in two rounds, it took 5200 cycles for 4 rows of 16 shares.
     const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
-    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->h, ct->rt * ROWS);
+    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->run.h, ct->run.rt * ROWS);
     auto join = [&](auto in_flight) {
       constexpr int N = decltype(in_flight)::value;
       for (int e = rank * per + ctid; ctid >= 0 && e < end; e += 128) {
@@ -760,14 +746,15 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
   if (int e = current_device(&dev)) return e;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int pages = shared_len / PAGE;
+  const bool f32 = hs->dtype == DFLASH_F32;
   if (pages > 0) {
     p.pre.rows = static_cast<float *>(rows);
     p.pre.row_cap = most;
     p.pre.pages = pages;
     p.pre.batch = batch;
+    p.pre.cost = 0;
     // The prefix.  fp32, or no more than 16 rows: one request with every row,
     // in tiles of 16.
-    const bool f32 = hs->dtype == DFLASH_F32;
     const long long all = static_cast<long long>(most) * p.g;
     if (f32 || all <= ROWS) {
       Params x = p;
@@ -780,6 +767,10 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
       return e;
     }
   }
+  // What a tile takes beside its pages, in pages (a call of 64 requests: 16 new
+  // tokens of 5 heads on 2..32 own pages 186 us at 0, 122 at 8, 118 at 12 to 16; one
+  // token of 4 heads on 1..16 pages 66.2 at 0, 63.0 at 2, 65.1 at 8).
+  p.pre.cost = !f32 && max_new * p.g > ROWS ? 14 : 3;
   return launch_attention(*hs, *kv, p, static_cast<long long>(max_new) * p.g, kv->max_pages - pages, dev, s);
 }
 

@@ -29,6 +29,7 @@ struct Prefix {
   int pages;           // of the prefix
   int tile_tokens;     // first launch: tokens per run; second: 0
   int batch;           // requests (Params.B counts runs in the first launch)
+  int cost;            // of a tile beside its pages, in pages: see Start
 };
 
 struct Params {
@@ -103,15 +104,21 @@ template <bool PRE>
 __device__ __forceinline__ const int32_t *pages_of(const Params &p, int b) {
   return p.page_table + (PRE && p.pre.tile_tokens ? 0 : static_cast<size_t>(b) * p.max_pages);
 }
-// Pages of requests b0 .. b1-1, each as often as it has row tiles; four
-// requests' loads at a time (one by one, 4096 requests took 45 us).
+// A tile's length in the list that is shared out.
+template <bool PRE>
+__device__ __forceinline__ long long tile_units(const Params &p, const Req &r) {
+  return PRE && r.np > 0 ? r.np + p.pre.cost : r.np;
+}
+// Pages (and `cost` for each tile that has some) of requests b0 .. b1-1, each as
+// often as it has row tiles; four requests' loads at a time (one by one, 4096
+// requests took 45 us).
 template <bool PRE, typename Tiles>
 __device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, bool tell, Tiles tiles_of) {
   long long sum = 0;
   if (PRE && p.pre.tile_tokens) {
     for (int b = b0; b < b1; ++b) {
       const Req r = prefix_run(p, b);
-      sum += static_cast<long long>(r.np) * tiles_of(r);
+      sum += tile_units<PRE>(p, r) * tiles_of(r);
     }
     return sum;
   }
@@ -125,7 +132,7 @@ __device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, 
     for (int i = 0; i < 4; ++i)
       if (b + i < b1) {
         const Req r = make_request<PRE>(p, row0[i], row0[i + 1], ctx[i], tell);
-        sum += static_cast<long long>(r.np) * tiles_of(r);
+        sum += tile_units<PRE>(p, r) * tiles_of(r);
       }
   }
   return sum;
@@ -153,6 +160,54 @@ struct Runs {
     return static_cast<int>(x < big ? quotient(x, base + 1) : rem + quotient(x - big, base));
   }
 };
+
+// A CTA's run: n pages, the first of them k of tile (b, h, rt), which begins at x0
+// in the list.  Each tile is its pages, behind `cost` units that stand for what
+// the tile takes beside them: queries, join, output.  The launch behind a
+// prefix has a cost (short own parts: 64 requests of 2..32 pages; without it
+// the run with the shortest lists took twice the mean), the others 0.
+struct Start {
+  long long x0;
+  int n, b, h, rt, k;
+};
+// The lane whose slice b0 .. b1-1 of the requests, at `pre` in the list, holds
+// the run's first unit lo.
+template <bool PRE, typename Tiles>
+__device__ __forceinline__ void find_start(const Params &p, int b0, int b1, long long pre, long long lo, long long hi,
+                                           Tiles tiles_of, Start *s) {
+  for (int b = b0; b < b1; ++b) {
+    Req r = request<PRE>(p, b, false);
+    const long long tile = tile_units<PRE>(p, r), head = tile * tiles_of(r), span = head * p.nkv;
+    if (lo >= pre + span) {
+      pre += span;
+      continue;
+    }
+    const long long h = quotient(lo - pre, head), rt = quotient(lo - pre - h * head, tile), off = lo - pre - h * head - rt * tile;
+    const int cost = PRE ? p.pre.cost : 0;
+    s->b = b;
+    s->h = static_cast<int>(h);
+    s->rt = static_cast<int>(rt);
+    s->x0 = lo - off;
+    s->k = static_cast<int>(off > cost ? off - cost : 0);
+    long long n = hi - lo;
+    if (PRE && cost > 0) {   // pages alone
+      n = 0;
+      long long x = lo - off, left = (p.nkv - h) * tiles_of(r) - rt;   // a tile's beginning; tiles of the request from there on
+      while (x < hi) {
+        const long long t = tile_units<PRE>(p, r), from = x + cost > lo ? x + cost : lo, to = x + t < hi ? x + t : hi;
+        if (to > from) n += to - from;
+        x += t;
+        if (--left == 0 && x < hi) {
+          do r = request<PRE>(p, ++b, false);   // another request with work follows
+          while (r.np == 0 && b + 1 < p.B);
+          left = static_cast<long long>(p.nkv) * tiles_of(r);
+        }
+      }
+    }
+    s->n = static_cast<int>(n);
+    return;
+  }
+}
 
 // What the consumers need to know of a chunk, written by the producer beside
 // the chunk's data.

@@ -55,9 +55,8 @@ struct __align__(16) Ctrl {
   uint64_t full[MAX_ST], empty[MAX_ST];    // a page's data; its last reader (the PV) is done
   uint64_t sfull[MAX_SB], pfull[MAX_SB], pdone[MAX_SB];   // S written; P written; PV done, the buffer is free
   uint64_t qfull, oempty[2], ml[2], cons[2], drain;       // [2]: of a softmax group
-  long long lo;
   Runs runs;
-  int n_mine, b, h, k;                                   // the run's first page: k of (b, h)
+  Start run;
   uint32_t tmem;
   int abort_flag, merge[2];
   float2 helper[2][MROWS];                 // (maximum, sum) of the group without the tile's last page
@@ -67,12 +66,25 @@ static_assert(sizeof(Ctrl) <= 4096, "shared memory");
 
 // CL: few (request, kv head)s over short capacities: one cluster of p.cs CTAs
 // per tile, joined in distributed shared memory.
+// PRE: what a warp moves whole rows through, 32 rows of 64 bytes.  A thread's row
+// is 256 to 512 bytes away from the next thread's: loads and stores straight
+// from the threads took 8000 cycles of a short tile's 15500.
+constexpr int PATCH = 32 * 64;
+template <int D, bool PRE>
+constexpr int smem_bytes() {
+  return Shape<D>::SMEM + (PRE ? 8 * PATCH : 0);
+}
+// 16 bytes c of row r of a patch: conflict-free by rows and by columns
+__device__ __forceinline__ uint4 *patch_at(uint8_t *patch, int r, int c) {
+  return reinterpret_cast<uint4 *>(patch + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+}
+
 template <int D, bool CL, bool PRE>
 __global__ void __launch_bounds__(NTHR, 1)
     verify_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p) {
   using S = Shape<D>;
   constexpr int ST = S::ST, KB = S::KB, STAGE = S::STAGE, NSB = S::NSB;
-  static_assert(S::SMEM <= 232448, "shared memory");
+  static_assert(smem_bytes<D, PRE>() <= 232448, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Ctrl *ct = reinterpret_cast<Ctrl *>(ring + ST * STAGE);
@@ -112,11 +124,11 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (CL) {
     if (threadIdx.x == 0) {
       const int list = blockIdx.x / p.cs, rank = blockIdx.x % p.cs;
-      ct->b = list / p.nkv;
-      ct->h = list % p.nkv;
-      const int np = request<PRE>(p, ct->b, rank == 0 && ct->h == 0).np;
-      ct->k = rank * np / p.cs;
-      ct->n_mine = (rank + 1) * np / p.cs - ct->k;
+      ct->run.b = list / p.nkv;
+      ct->run.h = list % p.nkv;
+      const int np = request<PRE>(p, ct->run.b, rank == 0 && ct->run.h == 0).np;
+      ct->run.k = rank * np / p.cs;
+      ct->run.n = (rank + 1) * np / p.cs - ct->run.k;
     }
   } else if (warp == 0) {
     // Lane i sums the pages of a contiguous slice of the requests; a warp
@@ -136,27 +148,14 @@ __global__ void __launch_bounds__(NTHR, 1)
     const long long lo = c < runs.G ? runs.lo(c) : 0, hi = c < runs.G ? runs.lo(c + 1) : 0;
     const long long ex = (inc - sum) * p.nkv, in = inc * p.nkv;
     if (lane == 0) {
-      ct->n_mine = static_cast<int>(hi - lo);
-      ct->lo = lo;
+      if (hi == lo) ct->run.n = 0;
       ct->runs = runs;
     }
-    if (hi > lo && lo >= ex && lo < in) {   // exactly one lane
-      long long pre = ex;
-      for (int b = b0; b < b1; ++b) {
-        const long long np = request<PRE>(p, b, false).np, span = np * p.nkv;
-        if (lo < pre + span) {
-          ct->b = b;
-          const long long h = quotient(lo - pre, np);
-          ct->h = static_cast<int>(h);
-          ct->k = static_cast<int>(lo - pre - h * np);
-          break;
-        }
-        pre += span;
-      }
-    }
+    if (hi > lo && lo >= ex && lo < in)   // exactly one lane
+      find_start<PRE>(p, b0, b1, ex, lo, hi, [](const Req &) { return 1; }, &ct->run);
   }
   __syncthreads();
-  const int n = ct->n_mine;
+  const int n = ct->run.n;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -164,11 +163,12 @@ __global__ void __launch_bounds__(NTHR, 1)
       const uint64_t pol = policy_evict_first();
       const Runs runs = ct->runs;
       int cf = 0, cl = 0, i0 = 0, i1 = 0;
-      int b = ct->b, h = ct->h, k = ct->k, issued = 0;
-      long long x = ct->lo;
+      int b = ct->run.b, h = ct->run.h, k = ct->run.k, issued = 0;
+      long long x0 = ct->run.x0;   // the tile's beginning in the list
+      const int cost = PRE ? p.pre.cost : 0;
       Req r = request<PRE>(p, b, false);
       bool ok = true, fresh = true;
-      for (int i = 0; i < n; ++i, ++x) {
+      for (int i = 0; i < n; ++i) {
         const int st = i % ST;
         if (fresh) {
           i0 = i;
@@ -182,13 +182,13 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (lane == 0) {
           if (bad) report(p.status, DFLASH_ERR_DEVICE);
           if (!CL && fresh) {
-            cf = runs.owner(x - k);
-            cl = runs.owner(x - k + r.np - 1);
+            cf = runs.owner(x0 + cost);
+            cl = runs.owner(x0 + cost + r.np - 1);
           }
           Page c;
           c.b = b, c.h = h, c.page = r.p0 + k, c.row0 = r.row0, c.n = r.n, c.ctx = r.ctx;
           c.flags = (bad ? BAD : 0) | (!CL && cf == cl ? WHOLE : 0);
-          c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) == x - k, c.slot = i - k <= 0 ? 0 : 1;
+          c.cf = cf, c.cl = cl, c.slot0 = runs.lo(cf) >= x0, c.slot = i - k <= 0 ? 0 : 1;
           c.i0 = i0, c.i1 = i1, c.pad = 0;
           ct->page[st] = c;
           mbar_arrive_expect_tx(&ct->full[st], bad ? 0 : STAGE);
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         fresh = false;
         if (++k == r.np && !CL) {
           k = 0;
+          x0 += tile_units<PRE>(p, r);
           fresh = true;
           if (++h == p.nkv && i + 1 < n) {
             h = 0;
@@ -298,6 +299,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t my_o = lane_base + S::O_COL + wg * D, its_o = lane_base + S::O_COL + (wg ^ 1) * D;
     const int tok = row / g, head = row % g;
+    // PRE: this warp's patch; lane l moves 16 bytes l % 4 of rows l / 4 + 8 k
+    uint8_t *patch = ring + ST * STAGE + 4096 + (wg * 4 + quad) * PATCH;
+    const int pr = lane >> 2, pc = lane & 3;
     uint32_t cphase = 0;
     int uses = 0, helped = 0;       // tiles this group had a part in; those of them it closed with the other's help
     bool ok = true;
@@ -327,8 +331,29 @@ __global__ void __launch_bounds__(NTHR, 1)
                                                            static_cast<size_t>(c.row0 + (live ? tok : 0)) * p.ldq +
                                                            static_cast<size_t>(c.h * g + head) * D);
         uint4 u[D / 8];
+        if (PRE) {
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < 4; ++k) {
+            const int r = quad * 32 + pr + 8 * k, t = r / g;
+            const uint4 *row_k = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                                 static_cast<size_t>(c.row0 + t) * p.ldq +
+                                                                 static_cast<size_t>(c.h * g + r - t * g) * D) + pc;
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) u[4 * b + k] = t < c.n ? __ldg(row_k + 4 * b) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b) {   // 32 dims at a time, from rows of a lane's quarter to rows of a lane
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *patch_at(patch, pr + 8 * k, pc) = u[4 * b + k];
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[4 * b + k] = *patch_at(patch, lane, k);
+            __syncwarp();
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) u[t] = live ? __ldg(src + t) : make_uint4(0u, 0u, 0u, 0u);
+        }
         if (i > 0 && !(ok = waitw(&ct->sfull[(i - 1) % NSB], static_cast<uint32_t>(((i - 1) / NSB) & 1)))) break;
         tc_fence_after();
 #pragma unroll
@@ -502,22 +527,41 @@ __global__ void __launch_bounds__(NTHR, 1)
       float *part = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
       float Mr = M, Lr = L;   // with PRE: of the row, the prefix in it
       Join2 fr = {1.f, 0.f};
-      const float *share = nullptr;
-      if (PRE && whole) {
-        const Dest dest = dest_of<true>(p, D, last.row0, last.h);
-        const size_t i = share_index<D>(dest, live ? row : 0);
-        share = dest.share + i * D;
-        fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + i));
+      Dest dest;
+      size_t moved[4];        // PRE: the rows pr + 8 k among the shares
+      bool there[4];
+      uint4 sh[4];            // the prefix's share of 16 columns, of those rows
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (there[k]) sh[k] = __ldcg(reinterpret_cast<const uint4 *>(dest.share + moved[k] * D + c * 16) + pc);
+      };
+      if (PRE && !CL) {
+        dest = dest_of<true>(p, D, last.row0, last.h);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = quad * 32 + pr + 8 * k;
+          there[k] = r < rows;
+          moved[k] = share_index<D>(dest, there[k] ? r : 0);
+        }
+        if (whole) {
+          fetch(0);
+          fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + share_index<D>(dest, live ? row : 0)));
+        }
       }
       const float inv = inverse_sum(Mr, Lr);
+      uint32_t kept[2][8];              // two blocks of 16 columns are 64 bytes of a row of bf16
+      // PRE: everything but the sums of products in three factors; a row of nothing
+      // (inverse 0, or a sum of 0 beside a NaN) is 0 or NaN by them
+      const float once = PRE && whole ? inv : 1.f;
+      const uint64_t fa = pair(f0 * fr.own * once, f0 * fr.own * once), fb = pair(f1 * fr.own * once, f1 * fr.own * once),
+                     fc = pair(fr.pre * once, fr.pre * once);
+      const bool unwritten = __any_sync(0xffffffffu, l == 0.f || !two || its.y == 0.f);
+      uint4 *out_row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + static_cast<size_t>(last.row0) * (p.nkv * g) * D) + pc;
       constexpr int CU = PRE ? 1 : 2;   // blocks of 16 columns in flight: the share's loads want registers too
 #pragma unroll
       for (int c0 = 0; c0 < D / 16; c0 += CU) {
         uint32_t a[CU][16], b[CU][16];
-        float4 sh[CU][4];
-        if (PRE && whole)
-#pragma unroll
-          for (int t = 0; t < 4 * CU; ++t) sh[t >> 2][t & 3] = __ldcg(reinterpret_cast<const float4 *>(share + c0 * 16) + t);
 #pragma unroll
         for (int u = 0; u < CU; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
         if (two)
@@ -527,39 +571,89 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
         for (int u = 0; u < CU; ++u) {
           tmem_regs_ready(a[u]);
-          float v[16];
+          if constexpr (PRE && !CL) {
+            // v = fa a + fb b + fc share.  Rows by the lane, then whole rows in and
+            // out; an O that was never written is not read.
+            if (two) tmem_regs_ready(b[u]);
+            if (unwritten) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : f0 * __uint_as_float(a[u][e]);   // sum 0: O was never written
-          if (two) {
-            tmem_regs_ready(b[u]);
+              for (int e = 0; e < 16; ++e) {
+                if (l == 0.f) a[u][e] = 0u;
+                if (!two || its.y == 0.f) b[u][e] = 0u;
+              }
+            }
+            uint64_t v[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = its.y == 0.f ? v[e] : fmaf(f1, __uint_as_float(b[u][e]), v[e]);
-          }
-          if (!live) continue;
-          if (CL) {   // float4s XORed by the row: no bank conflicts
+            for (int e = 0; e < 8; ++e) {
+              v[e] = mul2(pair(__uint_as_float(a[u][2 * e]), __uint_as_float(a[u][2 * e + 1])), fa);
+              if (two) v[e] = fma2(pair(__uint_as_float(b[u][2 * e]), __uint_as_float(b[u][2 * e + 1])), fb, v[e]);
+            }
+            if (whole) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              *reinterpret_cast<float4 *>(xo + row * D + ((((c0 + u) * 4 + t) ^ (row & (D / 4 - 1))) << 2)) =
-                  make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
-          } else if (whole) {
-            if (PRE)
+              for (int k = 0; k < 4; ++k) *patch_at(patch, pr + 8 * k, pc) = sh[k];
+              __syncwarp();
+              if (c0 + 1 < D / 16) fetch(c0 + 1);
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
-                v[4 * t] = fr.own * v[4 * t] + fr.pre * sh[u][t].x;
-                v[4 * t + 1] = fr.own * v[4 * t + 1] + fr.pre * sh[u][t].y;
-                v[4 * t + 2] = fr.own * v[4 * t + 2] + fr.pre * sh[u][t].z;
-                v[4 * t + 3] = fr.own * v[4 * t + 3] + fr.pre * sh[u][t].w;
+                const float4 x = *reinterpret_cast<const float4 *>(patch_at(patch, lane, t));
+                const float2 y = unpair(fma2(pair(x.x, x.y), fc, v[2 * t])), z = unpair(fma2(pair(x.z, x.w), fc, v[2 * t + 1]));
+                kept[c0 & 1][2 * t] = pack_bf16(y.x, y.y);
+                kept[c0 & 1][2 * t + 1] = pack_bf16(z.x, z.y);
               }
-            uint32_t w[8];
+              __syncwarp();
+              if (c0 & 1) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + (c0 + u) * 16);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                for (int t = 0; t < 4; ++t) {
+                  const uint32_t *w = &kept[t >> 1][4 * (t & 1)];
+                  *patch_at(patch, lane, t) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (there[k]) *(out_row + moved[k] * (D / 8) + (c0 - 1) * 2) = *patch_at(patch, pr + 8 * k, pc);
+                __syncwarp();
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const float2 y = unpair(v[2 * t]), z = unpair(v[2 * t + 1]);
+                *reinterpret_cast<float4 *>(patch_at(patch, lane, t)) = make_float4(y.x, y.y, z.x, z.y);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (there[k])
+                  __stcg(reinterpret_cast<uint4 *>(part + (quad * 32 + pr + 8 * k) * D + c0 * 16) + pc,
+                         *patch_at(patch, pr + 8 * k, pc));
+              __syncwarp();
+            }
           } else {
-            float4 *dst = reinterpret_cast<float4 *>(part + row * D + (c0 + u) * 16);
+            float v[16];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) __stcg(dst + t, make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]));
+            for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : f0 * __uint_as_float(a[u][e]);   // sum 0: O was never written
+            if (two) {
+              tmem_regs_ready(b[u]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] = its.y == 0.f ? v[e] : fmaf(f1, __uint_as_float(b[u][e]), v[e]);
+            }
+            if (!live) continue;
+            if (CL) {   // float4s XORed by the row: no bank conflicts
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                *reinterpret_cast<float4 *>(xo + row * D + ((((c0 + u) * 4 + t) ^ (row & (D / 4 - 1))) << 2)) =
+                    make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]);
+            } else if (whole) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pack_bf16(v[2 * e] * inv, v[2 * e + 1] * inv);
+              uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * D + (c0 + u) * 16);
+              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+              float4 *dst = reinterpret_cast<float4 *>(part + row * D + (c0 + u) * 16);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) __stcg(dst + t, make_float4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3]));
+            }
           }
         }
       }
@@ -607,14 +701,14 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
   if constexpr (CL) {
     // ---- the cluster's shares: every CTA finishes a part of the tile's columns
-    const Req r = request<PRE>(p, ct->b, false);
+    const Req r = request<PRE>(p, ct->run.b, false);
     const int rows = r.n * g, rank = static_cast<int>(cluster_ctarank());
     float *xo = reinterpret_cast<float *>(ring);
     if (n == 0 || ct->abort_flag)   // nothing to add
       for (int i = threadIdx.x; i < MROWS; i += NTHR) *reinterpret_cast<float2 *>(xo + MROWS * D + 2 * i) = make_float2(-INFINITY, 0.f);
     __syncwarp();
     cluster_sync();
-    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->h);
+    const Dest dest = dest_of<PRE>(p, D, r.row0, ct->run.h);
     const int items = rows * (D / 4), per = (items + p.cs - 1) / p.cs, end = min(items, (rank + 1) * per);
     for (int e = rank * per + threadIdx.x; e < end; e += NTHR) {
       const int row = e / (D / 4), c = e % (D / 4);
@@ -656,7 +750,8 @@ static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   using S = Shape<D>;
   auto *kernel = verify_kernel<D, CL, PRE>;
   static std::atomic<uint64_t> smem_set;
-  if (int e = allow_smem(smem_set, dev, kernel, S::SMEM)) return e;
+  constexpr int SMEM = smem_bytes<D, PRE>();
+  if (int e = allow_smem(smem_set, dev, kernel, SMEM)) return e;
   const uint64_t pages = static_cast<uint64_t>(kv.num_pages) * hs.n_kv_heads;
   CUtensorMap tk, tv;
   if (int e = make_tmap_2d(&tk, p.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, D, pages * PAGE, D * 2, 64, PAGE)) return e;
@@ -666,7 +761,7 @@ static int launch(const dflash_heads &hs, const dflash_kv &kv, Params &p, const 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CL ? static_cast<unsigned>(p.B * p.nkv * p.cs) : static_cast<unsigned>(dev.sms < most ? dev.sms : most));
   cfg.blockDim = dim3(NTHR);
-  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
