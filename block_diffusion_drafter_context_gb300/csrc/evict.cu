@@ -19,8 +19,10 @@ namespace {
 // ------------------------------------------------------------------ choice
 // The budget-th largest of a list by radix selection over 32-bit keys (11, 11
 // and 10 bits), the keys in shared memory: weights and positions are read
-// once.  A cluster of CTAs per list where lists are few: each has a stretch of
-// the slots, and they add up each other's counts.
+// once, 16 bytes at a time and several loads in flight.  A cluster of CTAs per
+// list where lists are few: each has a stretch of the slots, and they add up
+// each other's counts.  Bound by the passes over the keys in shared memory and
+// the meetings between them; HBM's share is a fifth.
 constexpr int PLAN_THREADS = 512, PLAN_WARPS = PLAN_THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAX_CS = 8;
@@ -39,10 +41,9 @@ struct PlanArgs {
 
 struct __align__(16) PlanCtrl {
   uint32_t hist[BINS];         // this CTA's counts
-  uint32_t warp_sum[PLAN_WARPS];
-  uint32_t pick[2];            // the digit of the wanted key, and how many lie above it
+  uint32_t warp_sum[PLAN_WARPS], warp_a[PLAN_WARPS], warp_b[PLAN_WARPS];
+  uint32_t pick[3];            // the digit of the wanted key, how many keys lie above it, and how many have it
   uint32_t ties, holes, movers;   // of this CTA
-  uint32_t warp_a[PLAN_WARPS], warp_b[PLAN_WARPS];
 };
 
 // a weight's place in an unsigned order; NaN lies below every number
@@ -56,14 +57,21 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// exclusive prefix sum over the warps' values in smem (one per warp); every thread calls it
-__device__ __forceinline__ uint32_t before_me(const uint32_t *v, int warp) {
-  uint32_t s = 0;
-  for (int w = 0; w < warp; ++w) s += v[w];
-  return s;
+__device__ __forceinline__ uint4 ld_dsmem_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// the sum of the first `n` of the warps' values
+__device__ __forceinline__ uint32_t sum_before(const uint32_t *v, int n, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0u);
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+template <int U>
+__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a) {
   extern __shared__ uint32_t plan_smem[];
   PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
   uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
@@ -78,8 +86,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
       __syncthreads();
     }
   };
+  *reinterpret_cast<uint4 *>(&ct->hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
+  static_assert(BINS == 4 * PLAN_THREADS, "bins per thread");
   pdl_start();
-  const int ctx = a.ctx_len[b];
+  const int ctx = a.ctx_len[b], seq = a.seq_len[b];
   const bool ok = ctx >= 0 && ctx <= a.capacity;
   if (!ok && rank == 0 && h == 0 && layer == 0 && tid == 0) report(a.status, DFLASH_ERR_DEVICE);
   const size_t list = (static_cast<size_t>(layer) * a.batch + b) * a.nkv + h;
@@ -90,41 +100,57 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     if (rank == 0 && tid == 0) a.counts[list] = 0;
     return;                                // the whole cluster
   }
-  const int n = ctx - a.first, per = (n + a.cs - 1) / a.cs;
+  // this CTA's stretch of the slots: whole warps' worths
+  const int n = ctx - a.first, per = ((n + a.cs - 1) / a.cs + 31) & ~31;
   const int lo = a.first + min(n, rank * per), mine = min(n, (rank + 1) * per) - min(n, rank * per);
   const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity + lo;
   const float *wt = a.weights + row;
   const int32_t *ps = a.positions + row;
-  const long long newest = static_cast<long long>(a.seq_len[b]) - a.recent;   // positions from here on stay
-  auto fresh_key = [&](int i) { return ps[i] >= newest ? PROTECTED : weight_key(wt[i]); };
+  const long long newest = static_cast<long long>(seq) - a.recent;   // positions from here on stay
   const bool cached = mine <= a.cached;
-  auto key_at = [&](int i) { return cached ? keys[i] : fresh_key(i); };
+  // keys i0 + lane, i0 + lane + PLAN_THREADS, ...: U of them with their loads in flight together
+  auto load_keys = [&](int i0, uint32_t (&k)[U]) {
+    float w[U];
+    int32_t at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * PLAN_THREADS + lane;
+      w[u] = i < mine ? wt[i] : 0.f;
+      at[u] = i < mine ? ps[i] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) k[u] = at[u] >= newest ? PROTECTED : weight_key(w[u]);
+  };
+  auto key_at = [&](int i) { return cached ? keys[i] : ps[i] >= newest ? PROTECTED : weight_key(wt[i]); };
+  __syncthreads();             // the counts are cleared
 
   // ---- radix selection: `want` keys are to stay, those with the found prefix above them already
   uint32_t want = a.budget - a.first, prefix = 0, ties_all = 0;
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, above = shift + bits;
-    for (int i = tid; i < BINS; i += PLAN_THREADS) ct->hist[i] = 0;
-    __syncthreads();
     uint32_t zeros = 0, prot = 0;          // the two keys that many slots may share, counted without atomics
-    for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
-      const int i = i0 + lane;
-      uint32_t k = 0;
-      bool in = i < mine;
-      if (in) {
-        if (pass == 0) {
-          k = fresh_key(i);
-          if (cached) keys[i] = k;
-        } else {
-          k = key_at(i);
-          in = (k >> above) == prefix;
-        }
+    for (int i0 = warp * 32; i0 < mine; i0 += U * PLAN_THREADS) {
+      uint32_t k[U];
+      if (pass == 0 || !cached) {
+        load_keys(i0, k);
+        if (cached)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (i0 + u * PLAN_THREADS + lane < mine) keys[i0 + u * PLAN_THREADS + lane] = k[u];
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) k[u] = i0 + u * PLAN_THREADS + lane < mine ? keys[i0 + u * PLAN_THREADS + lane] : 0u;
       }
-      const uint32_t z = __ballot_sync(0xffffffffu, in && k == 0x80000000u), p = __ballot_sync(0xffffffffu, in && k == PROTECTED);
-      zeros += __popc(z);
-      prot += __popc(p);
-      if (in && k != 0x80000000u && k != PROTECTED) atomicAdd(&ct->hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = i0 + u * PLAN_THREADS + lane < mine && (pass == 0 || (k[u] >> (above & 31)) == prefix);
+        const uint32_t z = __ballot_sync(0xffffffffu, in && k[u] == 0x80000000u);
+        const uint32_t q = __ballot_sync(0xffffffffu, in && k[u] == PROTECTED);
+        zeros += __popc(z);
+        prot += __popc(q);
+        if (in && k[u] != 0x80000000u && k[u] != PROTECTED) atomicAdd(&ct->hist[(k[u] >> shift) & ((1u << bits) - 1)], 1u);
+      }
     }
     if (lane == 0) {
       if (zeros) atomicAdd(&ct->hist[(0x80000000u >> shift) & ((1u << bits) - 1)], zeros);
@@ -132,14 +158,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     }
     meet();
     // bins 4t .. 4t + 3 of all CTAs, from the top: the bin that holds the want-th largest key
-    uint32_t c[4] = {0, 0, 0, 0};
     const int bin0 = BINS - 4 - 4 * tid;
-    for (int r = 0; r < a.cs; ++r)
+    uint4 c = make_uint4(0u, 0u, 0u, 0u);
+    if (a.cs == 1) {
+      c = *reinterpret_cast<const uint4 *>(&ct->hist[bin0]);
+    } else {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        c[u] += a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->hist[bin0 + u], r)) : ct->hist[bin0 + u];
-    uint32_t inc = c[0] + c[1] + c[2] + c[3];
-    const uint32_t sum = inc;
+      for (int r = 0; r < MAX_CS; ++r)
+        if (r < a.cs) {
+          const uint4 x = ld_dsmem_u4(dsmem_addr(&ct->hist[bin0], r));
+          c.x += x.x, c.y += x.y, c.z += x.z, c.w += x.w;
+        }
+    }
+    const uint32_t sum = c.x + c.y + c.z + c.w;
+    uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
@@ -147,26 +179,26 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     }
     if (lane == 31) ct->warp_sum[warp] = inc;
     __syncthreads();
-    uint32_t over = before_me(ct->warp_sum, warp) + inc - sum;   // keys above this thread's bins
+    uint32_t over = sum_before(ct->warp_sum, warp, lane) + inc - sum;   // keys above this thread's bins
     if (over < want && want <= over + sum) {
+      const uint32_t cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
       for (int u = 3; u >= 0; --u) {
-        if (over < want && want <= over + c[u]) {
+        if (over < want && want <= over + cc[u]) {
           ct->pick[0] = bin0 + u;
           ct->pick[1] = over;
-          ct->ties = c[u];
-          break;
+          ct->pick[2] = cc[u];
         }
-        over += c[u];
+        over += cc[u];         // a bin of its own for each `want`: the test holds once
       }
     }
     meet();                    // and every CTA has read the others' counts
+    if (pass < 2) *reinterpret_cast<uint4 *>(&ct->hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
     prefix = pass == 0 ? ct->pick[0] : (prefix << bits) | ct->pick[0];
     want -= ct->pick[1];
-    ties_all = ct->ties;
+    ties_all = ct->pick[2];
     __syncthreads();
   }
-  static_assert(BINS == 4 * PLAN_THREADS, "bins per thread");
   // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
   const int seg = ((mine + PLAN_WARPS - 1) / PLAN_WARPS + 31) / 32 * 32;   // slots per warp
   const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
@@ -179,17 +211,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     }
     if (lane == 0) ct->warp_a[warp] = t;
     __syncthreads();
-    if (tid == 0) ct->ties = before_me(ct->warp_a, PLAN_WARPS);
-    meet();
-    tie_base = before_me(ct->warp_a, warp);
-    if (a.cs > 1)
+    tie_base = sum_before(ct->warp_a, warp, lane);
+    if (a.cs > 1) {
+      const uint32_t all = sum_before(ct->warp_a, PLAN_WARPS, lane);
+      if (tid == 0) ct->ties = all;
+      meet();
       for (int r = 0; r < rank; ++r) tie_base += ld_dsmem_u32(dsmem_addr(&ct->ties, r));
+    }
     __syncthreads();
   }
   const int keep = a.budget;   // ctx > budget here
   const uint32_t below = (1u << lane) - 1;
   auto walk = [&](auto each) {
     uint32_t t = tie_base;
+#pragma unroll 4
     for (int i0 = s0; i0 < s1; i0 += 32) {
       const int i = i0 + lane;
       const bool in = i < s1;
@@ -210,19 +245,23 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     ct->warp_b[warp] = movers;
   }
   __syncthreads();
-  if (tid == 0) {
-    ct->holes = before_me(ct->warp_a, PLAN_WARPS);
-    ct->movers = before_me(ct->warp_b, PLAN_WARPS);
-  }
-  meet();
-  uint32_t hole = before_me(ct->warp_a, warp), mover = before_me(ct->warp_b, warp), count = 0;
-  for (int r = 0; r < a.cs; ++r) {
-    const uint32_t x = a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->holes, r)) : ct->holes;
-    const uint32_t y = a.cs > 1 ? ld_dsmem_u32(dsmem_addr(&ct->movers, r)) : ct->movers;
-    count += x;                // as many as there are movers
-    if (r < rank) {
-      hole += x;
-      mover += y;
+  uint32_t hole = sum_before(ct->warp_a, warp, lane), mover = sum_before(ct->warp_b, warp, lane);
+  uint32_t count = sum_before(ct->warp_a, PLAN_WARPS, lane);   // as many as there are movers
+  if (a.cs > 1) {
+    const uint32_t y = sum_before(ct->warp_b, PLAN_WARPS, lane);
+    if (tid == 0) {
+      ct->holes = count;
+      ct->movers = y;
+    }
+    meet();
+    count = 0;
+    for (int r = 0; r < a.cs; ++r) {
+      const uint32_t x = ld_dsmem_u32(dsmem_addr(&ct->holes, r));
+      count += x;
+      if (r < rank) {
+        hole += x;
+        mover += ld_dsmem_u32(dsmem_addr(&ct->movers, r));
+      }
     }
   }
   walk([&](int slot, bool is_hole, bool is_mover) {
@@ -369,13 +408,17 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.budget = budget;
   a.top = top;
   a.status = static_cast<int *>(workspace);
+  // CTAs per list: 8192 slots each, so that several CTAs' keys fit an SM, and
+  // where lists are few as many as leave 2048 slots
   a.cs = 1;
-  while (a.cs < MAX_CS && lists * a.cs * 2 <= 2LL * dev.sms && slots->capacity / a.cs > 2048) a.cs *= 2;
-  const int room_smem = (200 << 10) - static_cast<int>(sizeof(PlanCtrl)), per = (slots->capacity + a.cs - 1) / a.cs;
+  while (a.cs < MAX_CS && (slots->capacity / a.cs > 8192 || (lists * a.cs * 2 <= 2LL * dev.sms && slots->capacity / a.cs > 2048)))
+    a.cs *= 2;
+  const int room_smem = (200 << 10) - static_cast<int>(sizeof(PlanCtrl)), per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31;
   a.cached = per * 4LL <= room_smem ? per : room_smem / 4;
   const int smem = static_cast<int>(sizeof(PlanCtrl)) + a.cached * 4;
   static std::atomic<uint64_t> smem_set;
-  if (int e = allow_smem(smem_set, dev, plan_kernel, 200 << 10)) return e;
+  auto *kernel = plan_kernel<8>;
+  if (int e = allow_smem(smem_set, dev, kernel, 200 << 10)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(lists * a.cs));
   cfg.blockDim = dim3(PLAN_THREADS);
@@ -390,7 +433,7 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.cs > 1 ? 2 : 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, plan_kernel, a), "plan_eviction launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, a), "plan_eviction launch");
 }
 
 DFLASH_API int dflash_move_slots(const dflash_heads *hs, const dflash_kv *kv, const dflash_slots *slots, int layer,
