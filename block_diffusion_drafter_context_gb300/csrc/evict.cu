@@ -23,8 +23,9 @@ namespace {
 // list where lists are few: each has a stretch of the slots, and they add up
 // each other's counts.  Bound by the passes over the keys in shared memory and
 // the meetings between them; HBM's share is a fifth.
-constexpr int PLAN_THREADS = 512, PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int BINS = 2048;
+constexpr int PLAN_THREADS = 256, PLAN_WARPS = PLAN_THREADS / 32;
+constexpr int BINS = 2048, MINE = BINS / PLAN_THREADS;   // bins of a thread
+constexpr int FEW = 2048;                     // candidates that are kept apart after the first digit
 constexpr int MAX_CS = 8;
 constexpr uint32_t PROTECTED = 0xffffffffu;   // the key of a recent token, above every weight's
 
@@ -35,7 +36,7 @@ struct PlanArgs {
   int32_t *moves, *counts, *ctx_out;
   int batch, batch_rows, nkv, capacity;
   int first, recent, budget, top;
-  int cs, cached;              // CTAs per list; keys that fit in this CTA's shared memory
+  int cs;                      // CTAs per list
   int *status;
 };
 
@@ -44,13 +45,14 @@ struct __align__(16) PlanCtrl {
   uint32_t warp_sum[PLAN_WARPS], warp_a[PLAN_WARPS], warp_b[PLAN_WARPS];
   uint32_t pick[3];            // the digit of the wanted key, how many keys lie above it, and how many have it
   uint32_t ties, holes, movers;   // of this CTA
+  uint32_t found;
+  uint32_t few[FEW];           // this CTA's keys that have the first digit of the wanted one
 };
 
 // a weight's place in an unsigned order; NaN lies below every number
 __device__ __forceinline__ uint32_t weight_key(float v) {
-  if (v != v) return 0u;
-  const uint32_t u = __float_as_uint(v == 0.f ? 0.f : v);   // -0 and +0 are equal
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(v + 0.f);   // -0 and +0 are equal
+  return v != v ? 0u : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
   uint32_t v;
@@ -70,8 +72,10 @@ __device__ __forceinline__ uint32_t sum_before(const uint32_t *v, int n, int lan
   return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0u);
 }
 
-template <int U>
-__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a) {
+// CACHED: a CTA's keys fit its shared memory.
+template <bool CACHED>
+__global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a) {
+  constexpr int U = 4;         // keys of a thread with their loads in flight
   extern __shared__ uint32_t plan_smem[];
   PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
   uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
@@ -86,8 +90,13 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a)
       __syncthreads();
     }
   };
-  *reinterpret_cast<uint4 *>(&ct->hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
-  static_assert(BINS == 4 * PLAN_THREADS, "bins per thread");
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < MINE; i += 4) *reinterpret_cast<uint4 *>(&ct->hist[MINE * tid + i]) = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear();
+  if (tid == 0) ct->found = 0;
+  static_assert(MINE % 4 == 0, "bins per thread");
   pdl_start();
   const int ctx = a.ctx_len[b], seq = a.seq_len[b];
   const bool ok = ctx >= 0 && ctx <= a.capacity;
@@ -106,71 +115,79 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a)
   const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity + lo;
   const float *wt = a.weights + row;
   const int32_t *ps = a.positions + row;
-  const long long newest = static_cast<long long>(seq) - a.recent;   // positions from here on stay
-  const bool cached = mine <= a.cached;
-  // keys i0 + lane, i0 + lane + PLAN_THREADS, ...: U of them with their loads in flight together
-  auto load_keys = [&](int i0, uint32_t (&k)[U]) {
-    float w[U];
-    int32_t at[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * PLAN_THREADS + lane;
-      w[u] = i < mine ? wt[i] : 0.f;
-      at[u] = i < mine ? ps[i] : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) k[u] = at[u] >= newest ? PROTECTED : weight_key(w[u]);
-  };
-  auto key_at = [&](int i) { return cached ? keys[i] : ps[i] >= newest ? PROTECTED : weight_key(wt[i]); };
+  // positions from here on stay
+  const int newest = static_cast<int>(max(static_cast<long long>(seq) - a.recent, -0x80000000ll));
+  auto make_key = [&](float w, int32_t at) { return at >= newest ? PROTECTED : weight_key(w); };
+  auto key_at = [&](int i) { return CACHED ? keys[i] : make_key(wt[i], ps[i]); };
   __syncthreads();             // the counts are cleared
 
   // ---- radix selection: `want` keys are to stay, those with the found prefix above them already
   uint32_t want = a.budget - a.first, prefix = 0, ties_all = 0;
+  int n_few = -1;              // keys with the first digit, where they were few enough to be set apart
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, above = shift + bits;
     uint32_t zeros = 0, prot = 0;          // the two keys that many slots may share, counted without atomics
-    for (int i0 = warp * 32; i0 < mine; i0 += U * PLAN_THREADS) {
-      uint32_t k[U];
-      if (pass == 0 || !cached) {
-        load_keys(i0, k);
-        if (cached)
+    auto count = [&](uint32_t k, bool in) {
+      if (pass > 0) in = in && (k >> (above & 31)) == prefix;
+      zeros += in && k == 0x80000000u;
+      prot += in && k == PROTECTED;
+      if (in && k != 0x80000000u && k != PROTECTED) atomicAdd(&ct->hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+    };
+    if (pass > 0 && n_few >= 0) {
+      for (int i = tid; i < n_few; i += PLAN_THREADS) count(ct->few[i], true);
+    } else if (pass > 0 && CACHED) {
+#pragma unroll 4
+      for (int i = tid; i < mine; i += PLAN_THREADS) count(keys[i], true);
+    } else {
+      int i = tid;
+      for (; i + (U - 1) * PLAN_THREADS < mine; i += U * PLAN_THREADS) {
+        float w[U];
+        int32_t at[U];
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (i0 + u * PLAN_THREADS + lane < mine) keys[i0 + u * PLAN_THREADS + lane] = k[u];
-      } else {
+        for (int u = 0; u < U; ++u) {
+          w[u] = wt[i + u * PLAN_THREADS];
+          at[u] = ps[i + u * PLAN_THREADS];
+        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) k[u] = i0 + u * PLAN_THREADS + lane < mine ? keys[i0 + u * PLAN_THREADS + lane] : 0u;
+        for (int u = 0; u < U; ++u) {
+          const uint32_t k = make_key(w[u], at[u]);
+          if (CACHED) keys[i + u * PLAN_THREADS] = k;
+          count(k, true);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = i0 + u * PLAN_THREADS + lane < mine && (pass == 0 || (k[u] >> (above & 31)) == prefix);
-        const uint32_t z = __ballot_sync(0xffffffffu, in && k[u] == 0x80000000u);
-        const uint32_t q = __ballot_sync(0xffffffffu, in && k[u] == PROTECTED);
-        zeros += __popc(z);
-        prot += __popc(q);
-        if (in && k[u] != 0x80000000u && k[u] != PROTECTED) atomicAdd(&ct->hist[(k[u] >> shift) & ((1u << bits) - 1)], 1u);
+      for (; i < mine; i += PLAN_THREADS) {
+        const uint32_t k = make_key(wt[i], ps[i]);
+        if (CACHED) keys[i] = k;
+        count(k, true);
       }
     }
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    prot = __reduce_add_sync(0xffffffffu, prot);
     if (lane == 0) {
       if (zeros) atomicAdd(&ct->hist[(0x80000000u >> shift) & ((1u << bits) - 1)], zeros);
       if (prot) atomicAdd(&ct->hist[(PROTECTED >> shift) & ((1u << bits) - 1)], prot);
     }
     meet();
-    // bins 4t .. 4t + 3 of all CTAs, from the top: the bin that holds the want-th largest key
-    const int bin0 = BINS - 4 - 4 * tid;
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    if (a.cs == 1) {
-      c = *reinterpret_cast<const uint4 *>(&ct->hist[bin0]);
-    } else {
+    // MINE bins of all CTAs, from the top: the bin that holds the want-th largest key
+    const int bin0 = BINS - MINE * (tid + 1);
+    uint32_t c[MINE], sum = 0;
 #pragma unroll
-      for (int r = 0; r < MAX_CS; ++r)
-        if (r < a.cs) {
-          const uint4 x = ld_dsmem_u4(dsmem_addr(&ct->hist[bin0], r));
-          c.x += x.x, c.y += x.y, c.z += x.z, c.w += x.w;
-        }
+    for (int i = 0; i < MINE; i += 4) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (a.cs == 1) {
+        x = *reinterpret_cast<const uint4 *>(&ct->hist[bin0 + i]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < MAX_CS; ++r)
+          if (r < a.cs) {
+            const uint4 y = ld_dsmem_u4(dsmem_addr(&ct->hist[bin0 + i], r));
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+      }
+      c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+      sum += x.x + x.y + x.z + x.w;
     }
-    const uint32_t sum = c.x + c.y + c.z + c.w;
     uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -181,23 +198,42 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a)
     __syncthreads();
     uint32_t over = sum_before(ct->warp_sum, warp, lane) + inc - sum;   // keys above this thread's bins
     if (over < want && want <= over + sum) {
-      const uint32_t cc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-      for (int u = 3; u >= 0; --u) {
-        if (over < want && want <= over + cc[u]) {
+      for (int u = MINE - 1; u >= 0; --u) {
+        if (over < want && want <= over + c[u]) {
           ct->pick[0] = bin0 + u;
           ct->pick[1] = over;
-          ct->pick[2] = cc[u];
+          ct->pick[2] = c[u];
         }
-        over += cc[u];         // a bin of its own for each `want`: the test holds once
+        over += c[u];          // a bin of its own for each `want`: the test holds once
       }
     }
     meet();                    // and every CTA has read the others' counts
-    if (pass < 2) *reinterpret_cast<uint4 *>(&ct->hist[4 * tid]) = make_uint4(0u, 0u, 0u, 0u);
     prefix = pass == 0 ? ct->pick[0] : (prefix << bits) | ct->pick[0];
     want -= ct->pick[1];
     ties_all = ct->pick[2];
+    if (pass == 0 && CACHED) {
+      // most keys are decided by their first digit: set the others apart
+      n_few = static_cast<int>(ct->hist[prefix]);
+      if (n_few > FEW) n_few = -1;
+      if (n_few >= 0)
+#pragma unroll 4
+        for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
+          const uint32_t k = i0 + lane < mine ? keys[i0 + lane] : 0u;
+          const bool in = i0 + lane < mine && k >> 21 == prefix;
+          const uint32_t v = __ballot_sync(0xffffffffu, in);
+          if (!v) continue;
+          uint32_t at = 0;
+          if (lane == 0) at = atomicAdd(&ct->found, __popc(v));
+          at = __shfl_sync(0xffffffffu, at, 0);
+          if (in) ct->few[at + __popc(v & ((1u << lane) - 1))] = k;
+        }
+    }
     __syncthreads();
+    if (pass < 2) {
+      clear();
+      __syncthreads();
+    }
   }
   // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
   const int seg = ((mine + PLAN_WARPS - 1) / PLAN_WARPS + 31) / 32 * 32;   // slots per warp
@@ -222,24 +258,32 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a)
   }
   const int keep = a.budget;   // ctx > budget here
   const uint32_t below = (1u << lane) - 1;
-  auto walk = [&](auto each) {
-    uint32_t t = tie_base;
-#pragma unroll 4
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < s1;
-      const uint32_t k = in ? key_at(i) : 0u;
+  // Of 32 slots from i0 on, those that fall free below `keep` and those kept from
+  // it on, a bit each; `tie` counts the equal keys before.
+  auto flags = [&](int i0, uint32_t &tie) {
+    const int i = i0 + lane;
+    const bool in = i < s1;
+    const uint32_t k = in ? key_at(i) : 0u;
+    bool stays = k >= prefix;
+    if (want < ties_all) {
       const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix);
-      const bool stays = in && (k > prefix || (k == prefix && t + __popc(eq & below) < want));
-      t += __popc(eq);
-      each(lo + i, in && !stays && lo + i < keep, stays && lo + i >= keep);
+      stays = k > prefix || (k == prefix && tie + __popc(eq & below) < want);
+      tie += __popc(eq);
     }
+    return __ballot_sync(0xffffffffu, in && stays == (lo + i >= keep));
   };
-  uint32_t holes = 0, movers = 0;
-  walk([&](int, bool hole, bool mover) {
-    holes += __popc(__ballot_sync(0xffffffffu, hole));
-    movers += __popc(__ballot_sync(0xffffffffu, mover));
-  });
+  auto under = [&](int i0) {   // of 32 slots from i0 on, those below `keep`
+    const int m = keep - lo - i0;
+    return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1;
+  };
+  uint32_t holes = 0, movers = 0, tie = tie_base;
+#pragma unroll 4
+  for (int i0 = s0; i0 < s1; i0 += 32) {
+    const uint32_t f = flags(i0, tie), u = under(i0);
+    holes += __popc(f & u);
+    movers += __popc(f & ~u);
+    if (CACHED && lane == 0) keys[i0] = f;   // in the place of the first key, which nobody asks for again
+  }
   if (lane == 0) {
     ct->warp_a[warp] = holes;
     ct->warp_b[warp] = movers;
@@ -264,13 +308,30 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const PlanArgs a)
       }
     }
   }
-  walk([&](int slot, bool is_hole, bool is_mover) {
-    const uint32_t x = __ballot_sync(0xffffffffu, is_hole), y = __ballot_sync(0xffffffffu, is_mover);
-    if (is_hole) into[hole + __popc(x & below)] = slot;
-    if (is_mover) source[mover + __popc(y & below)] = slot;
-    hole += __popc(x);
-    mover += __popc(y);
-  });
+  __syncwarp();
+  tie = tie_base;
+  for (int g0 = s0; g0 < s1; g0 += 1024) {   // 32 times 32 slots, those that have something to write
+    uint32_t mine_f = 0, some;
+    if (CACHED) {
+      if (g0 + 32 * lane < s1) mine_f = keys[g0 + 32 * lane];
+      some = __ballot_sync(0xffffffffu, mine_f != 0);
+    } else {
+      const int groups = (min(s1, g0 + 1024) - g0 + 31) / 32;
+      some = groups == 32 ? 0xffffffffu : (1u << groups) - 1;
+    }
+    for (; some; some &= some - 1) {
+      const int g = __ffs(some) - 1, i0 = g0 + 32 * g;
+      const uint32_t f = CACHED ? __shfl_sync(0xffffffffu, mine_f, g) : flags(i0, tie), u = under(i0);
+      if (f >> lane & 1) {
+        if (u >> lane & 1)
+          into[hole + __popc(f & u & below)] = lo + i0 + lane;
+        else
+          source[mover + __popc(f & ~u & below)] = lo + i0 + lane;
+      }
+      hole += __popc(f & u);
+      mover += __popc(f & ~u);
+    }
+  }
   for (int i = static_cast<int>(count) + rank * PLAN_THREADS + tid; i < a.top; i += a.cs * PLAN_THREADS)
     into[i] = source[i] = -1;
   if (rank == 0 && tid == 0) a.counts[list] = static_cast<int32_t>(count);
@@ -413,12 +474,21 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.cs = 1;
   while (a.cs < MAX_CS && (slots->capacity / a.cs > 8192 || (lists * a.cs * 2 <= 2LL * dev.sms && slots->capacity / a.cs > 2048)))
     a.cs *= 2;
-  const int room_smem = (200 << 10) - static_cast<int>(sizeof(PlanCtrl)), per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31;
-  a.cached = per * 4LL <= room_smem ? per : room_smem / 4;
-  const int smem = static_cast<int>(sizeof(PlanCtrl)) + a.cached * 4;
-  static std::atomic<uint64_t> smem_set;
-  auto *kernel = plan_kernel<8>;
-  if (int e = allow_smem(smem_set, dev, kernel, 200 << 10)) return e;
+  const int per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31, limit = 200 << 10;
+  const bool cached = static_cast<int>(sizeof(PlanCtrl)) + per * 4LL <= limit;
+  const int smem = static_cast<int>(sizeof(PlanCtrl)) + (cached ? per * 4 : 0);
+  static std::atomic<uint64_t> smem_set[2];
+  auto *kernel = cached ? plan_kernel<true> : plan_kernel<false>;
+  if (int e = allow_smem(smem_set[cached], dev, kernel, limit)) return e;
+  // as many CTAs on an SM as its shared memory holds, not a default split with L1
+  static std::atomic<uint64_t> carved[2];
+  const uint64_t bit = dev.index < 64 ? 1ull << dev.index : 0;
+  if (!(carved[cached].load(std::memory_order_relaxed) & bit)) {
+    if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared),
+                           "shared memory carveout"))
+      return e;
+    carved[cached].fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(lists * a.cs));
   cfg.blockDim = dim3(PLAN_THREADS);
