@@ -13,19 +13,22 @@
 #include "target.h"
 #include "common.cuh"
 
+#include <type_traits>
+
 namespace dflash {
 namespace {
 
 // ------------------------------------------------------------------ choice
 // The budget-th largest of a list by radix selection over 32-bit keys (11, 11
 // and 10 bits), the keys in shared memory: weights and positions are read
-// once, 16 bytes at a time and several loads in flight.  A cluster of CTAs per
-// list where lists are few: each has a stretch of the slots, and they add up
-// each other's counts.  Bound by the passes over the keys in shared memory and
-// the meetings between them; HBM's share is a fifth.
-constexpr int PLAN_THREADS = 256, PLAN_WARPS = PLAN_THREADS / 32;
-constexpr int BINS = 2048, MINE = BINS / PLAN_THREADS;   // bins of a thread
-constexpr int FEW = 2048;                     // candidates that are kept apart after the first digit
+// once.  The first digit decides nearly all keys, the few others are set apart
+// for the next two.  What stays is marked 32 slots to a word, and the words
+// that have something to write are written.  Where lists are long or few, a
+// cluster of CTAs shares one: each has a stretch of the slots and sends the
+// counts that are not 0 to the first, which finds the digit for all.  Bound by
+// instructions: some 60 per 32 slots, and HBM's share a quarter.
+constexpr int BINS = 2048;
+constexpr int FEW = 2048;                     // keys set apart at most
 constexpr int MAX_CS = 8;
 constexpr uint32_t PROTECTED = 0xffffffffu;   // the key of a recent token, above every weight's
 
@@ -42,7 +45,7 @@ struct PlanArgs {
 
 struct __align__(16) PlanCtrl {
   uint32_t hist[BINS];         // this CTA's counts
-  uint32_t warp_sum[PLAN_WARPS], warp_a[PLAN_WARPS], warp_b[PLAN_WARPS];
+  uint32_t warp_sum[32], warp_a[32], warp_b[32];
   uint32_t pick[3];            // the digit of the wanted key, how many keys lie above it, and how many have it
   uint32_t ties, holes, movers;   // of this CTA
   uint32_t found;
@@ -59,23 +62,22 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 ld_dsmem_u4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_dsmem_u32(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 // the sum of the first `n` of the warps' values
 __device__ __forceinline__ uint32_t sum_before(const uint32_t *v, int n, int lane) {
   return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0u);
 }
 
-// CACHED: a CTA's keys fit its shared memory.
-template <bool CACHED>
-__global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a) {
-  constexpr int U = 4;         // keys of a thread with their loads in flight
+// T threads; CACHED: a CTA's keys fit its shared memory.
+template <int T, bool CACHED>
+__global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArgs a) {
+  constexpr int PLAN_THREADS = T, PLAN_WARPS = T / 32, MINE = BINS / T;   // MINE: bins of a thread
+  constexpr int U = T == 256 ? 4 : 8;   // keys of a thread with their loads in flight
   extern __shared__ uint32_t plan_smem[];
   PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
   uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
@@ -90,13 +92,18 @@ __global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a)
       __syncthreads();
     }
   };
+  // this thread's bins, the highest first
+  const int bin0 = BINS - MINE * (tid + 1);
+  using Word = typename std::conditional<MINE % 4 == 0, uint4, uint2>::type;
+  constexpr int W = sizeof(Word) / 4;
+  static_assert(MINE % W == 0, "bins per thread");
   auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < MINE; i += 4) *reinterpret_cast<uint4 *>(&ct->hist[MINE * tid + i]) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < MINE; i += W) *reinterpret_cast<Word *>(&ct->hist[bin0 + i]) = Word();
   };
   clear();
   if (tid == 0) ct->found = 0;
-  static_assert(MINE % 4 == 0, "bins per thread");
+  if (a.cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the counts are cleared
   pdl_start();
   const int ctx = a.ctx_len[b], seq = a.seq_len[b];
   const bool ok = ctx >= 0 && ctx <= a.capacity;
@@ -107,6 +114,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a)
   if (!ok || ctx <= a.budget) {            // nothing to drop
     for (int i = rank * PLAN_THREADS + tid; i < 2 * a.top; i += a.cs * PLAN_THREADS) into[i] = -1;
     if (rank == 0 && tid == 0) a.counts[list] = 0;
+    if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;                                // the whole cluster
   }
   // this CTA's stretch of the slots: whole warps' worths
@@ -119,7 +127,10 @@ __global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a)
   const int newest = static_cast<int>(max(static_cast<long long>(seq) - a.recent, -0x80000000ll));
   auto make_key = [&](float w, int32_t at) { return at >= newest ? PROTECTED : weight_key(w); };
   auto key_at = [&](int i) { return CACHED ? keys[i] : make_key(wt[i], ps[i]); };
-  __syncthreads();             // the counts are cleared
+  if (a.cs > 1)                // the counts are cleared
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
 
   // ---- radix selection: `want` keys are to stay, those with the found prefix above them already
   uint32_t want = a.budget - a.first, prefix = 0, ties_all = 0;
@@ -168,71 +179,80 @@ __global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a)
       if (zeros) atomicAdd(&ct->hist[(0x80000000u >> shift) & ((1u << bits) - 1)], zeros);
       if (prot) atomicAdd(&ct->hist[(PROTECTED >> shift) & ((1u << bits) - 1)], prot);
     }
-    meet();
-    // MINE bins of all CTAs, from the top: the bin that holds the want-th largest key
-    const int bin0 = BINS - MINE * (tid + 1);
     uint32_t c[MINE], sum = 0;
+    auto take = [&] {          // this thread's counts, cleared for the next pass
 #pragma unroll
-    for (int i = 0; i < MINE; i += 4) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (a.cs == 1) {
-        x = *reinterpret_cast<const uint4 *>(&ct->hist[bin0 + i]);
-      } else {
+      for (int i = 0; i < MINE; i += W) {
+        *reinterpret_cast<Word *>(&c[i]) = *reinterpret_cast<const Word *>(&ct->hist[bin0 + i]);
+        *reinterpret_cast<Word *>(&ct->hist[bin0 + i]) = Word();
+      }
+    };
+    if (a.cs > 1) {
+      if (rank > 0) {
+        __syncthreads();
+        take();
 #pragma unroll
-        for (int r = 0; r < MAX_CS; ++r)
-          if (r < a.cs) {
-            const uint4 y = ld_dsmem_u4(dsmem_addr(&ct->hist[bin0 + i], r));
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        for (int i = 0; i < MINE; ++i)
+          if (c[i]) add_dsmem_u32(dsmem_addr(&ct->hist[bin0 + i], 0), c[i]);
+      }
+      meet();
+    } else {
+      __syncthreads();
+    }
+    if (rank == 0) {           // the bin that holds the want-th largest key
+      take();
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) sum += c[i];
+      uint32_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += t;
+      }
+      if (lane == 31) ct->warp_sum[warp] = inc;
+      __syncthreads();
+      uint32_t over = sum_before(ct->warp_sum, warp, lane) + inc - sum;   // keys above this thread's bins
+      if (over < want && want <= over + sum) {
+        int bin = bin0;        // this thread's, from the top down
+        uint32_t has = 0;
+#pragma unroll
+        for (int u = MINE - 1; u >= 0; --u)
+          if (has == 0) {
+            if (want <= over + c[u])
+              has = c[u], bin = bin0 + u;
+            else
+              over += c[u];
           }
-      }
-      c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-      sum += x.x + x.y + x.z + x.w;
-    }
-    uint32_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    if (lane == 31) ct->warp_sum[warp] = inc;
-    __syncthreads();
-    uint32_t over = sum_before(ct->warp_sum, warp, lane) + inc - sum;   // keys above this thread's bins
-    if (over < want && want <= over + sum) {
-#pragma unroll
-      for (int u = MINE - 1; u >= 0; --u) {
-        if (over < want && want <= over + c[u]) {
-          ct->pick[0] = bin0 + u;
-          ct->pick[1] = over;
-          ct->pick[2] = c[u];
+        if (a.cs == 1) {
+          ct->pick[0] = bin, ct->pick[1] = over, ct->pick[2] = has;
+        } else {
+          for (int r = 0; r < a.cs; ++r) {
+            const uint32_t to = dsmem_addr(ct->pick, r);
+            st_dsmem_u32(to, bin);
+            st_dsmem_u32(to + 4, over);
+            st_dsmem_u32(to + 8, has);
+          }
         }
-        over += c[u];          // a bin of its own for each `want`: the test holds once
       }
     }
-    meet();                    // and every CTA has read the others' counts
+    meet();
     prefix = pass == 0 ? ct->pick[0] : (prefix << bits) | ct->pick[0];
     want -= ct->pick[1];
     ties_all = ct->pick[2];
     if (pass == 0 && CACHED) {
-      // most keys are decided by their first digit: set the others apart
-      n_few = static_cast<int>(ct->hist[prefix]);
-      if (n_few > FEW) n_few = -1;
-      if (n_few >= 0)
 #pragma unroll 4
-        for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
-          const uint32_t k = i0 + lane < mine ? keys[i0 + lane] : 0u;
-          const bool in = i0 + lane < mine && k >> 21 == prefix;
-          const uint32_t v = __ballot_sync(0xffffffffu, in);
-          if (!v) continue;
-          uint32_t at = 0;
-          if (lane == 0) at = atomicAdd(&ct->found, __popc(v));
-          at = __shfl_sync(0xffffffffu, at, 0);
-          if (in) ct->few[at + __popc(v & ((1u << lane) - 1))] = k;
-        }
-    }
-    __syncthreads();
-    if (pass < 2) {
-      clear();
+      for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
+        const uint32_t k = i0 + lane < mine ? keys[i0 + lane] : 0u;
+        const bool in = i0 + lane < mine && k >> 21 == prefix;
+        const uint32_t v = __ballot_sync(0xffffffffu, in);
+        if (!v) continue;
+        uint32_t at = 0;
+        if (lane == 0) at = atomicAdd(&ct->found, __popc(v));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(v & ((1u << lane) - 1));
+        if (in && at < FEW) ct->few[at] = k;
+      }
       __syncthreads();
+      if (ct->found <= FEW) n_few = static_cast<int>(ct->found);
     }
   }
   // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
@@ -345,8 +365,10 @@ __global__ void __launch_bounds__(PLAN_THREADS, 5) plan_kernel(const PlanArgs a)
 // A CTA takes 32 moves of a list.  K rows are copied 16 bytes a lane; V lies
 // transposed, so a lane is a move and the warps walk the dims: targets and
 // sources ascend, and neighbouring lanes share the sectors of a page's row
-// where they are dense.  Bound by the sectors touched: 32 bytes for a value
-// where the moves are sparse.
+// where they are dense.  Bound by the sectors touched, 32 bytes for a value
+// where the moves are sparse, and with few moves by the way to them (count and
+// moves, then pages, then the values): the loads of K and V are all in flight
+// before the first store.
 constexpr int MOVE_THREADS = 256, PER_CTA = 32;
 
 struct MoveArgs {
@@ -364,23 +386,29 @@ template <typename V, int D>   // V: an unsigned integer as wide as the values
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const MoveArgs a) {
   constexpr int VEC = 16 / sizeof(V), LPR = D / VEC, STEP = MOVE_THREADS / 32;
   __shared__ long long s_to[PER_CTA], s_of[PER_CTA];   // (page x kv heads + head) x 64 + slot, -1: no move
+  __shared__ int2 s_slot[PER_CTA];                     // the request's slots
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int list = blockIdx.x, h = list % a.nkv, b = list / a.nkv % a.batch, layer = list / a.nkv / a.batch;
   pdl_start();
-  const int count = a.counts[list];
-  if (count < 0 || count > a.top) {
-    if (blockIdx.y == 0 && tid == 0) report(a.status, DFLASH_ERR_DEVICE);
-    return;
-  }
   V *v = static_cast<V *>(a.v) + layer * a.layer_elems;
   uint4 *k = reinterpret_cast<uint4 *>(static_cast<V *>(a.k) + layer * a.layer_elems);
-  for (int i0 = blockIdx.y * PER_CTA; i0 < count; i0 += gridDim.y * PER_CTA) {
-    const int n = min(count - i0, PER_CTA);
+  const int32_t *moves = a.moves + static_cast<size_t>(list) * 2 * a.top;
+  const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity;
+  for (int i0 = blockIdx.y * PER_CTA; i0 < a.top; i0 += gridDim.y * PER_CTA) {
+    const int count = a.counts[list];
+    if (count < 0 || count > a.top) {
+      if (blockIdx.y == 0 && tid == 0) report(a.status, DFLASH_ERR_DEVICE);
+      return;
+    }
+    if (i0 >= count) return;
     if (warp == 0) {
       long long to = -1, of = -1;
-      if (lane < n) {
-        const int32_t *m = a.moves + static_cast<size_t>(list) * 2 * a.top + i0 + lane;
-        const int into = m[0], source = m[a.top];
+      int into = 0, source = 0;
+      if (i0 + lane < a.top) {   // whether it counts or not: the loads need not wait for the count
+        into = moves[i0 + lane];
+        source = moves[a.top + i0 + lane];
+      }
+      if (i0 + lane < count) {
         const int most = min(a.capacity, a.max_pages * PAGE);
         bool ok = into >= 0 && into < most && source >= 0 && source < most;
         if (ok) {
@@ -390,33 +418,50 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const MoveArgs a) {
           if (ok) {
             to = (static_cast<long long>(p0) * a.nkv + h) * PAGE + into % PAGE;
             of = (static_cast<long long>(p1) * a.nkv + h) * PAGE + source % PAGE;
-            const size_t row = ((static_cast<size_t>(layer) * a.batch_rows + b) * a.nkv + h) * a.capacity;
-            a.weights[row + into] = a.weights[row + source];
-            a.positions[row + into] = a.positions[row + source];
           }
         }
         if (!ok) report(a.status, DFLASH_ERR_DEVICE);
       }
       s_to[lane] = to;
       s_of[lane] = of;
+      s_slot[lane] = make_int2(into, source);
     }
     __syncthreads();
-    // ---- V [page][head][d][slot]: lane = move
+    // K [page][head][slot][d]
+    constexpr int KN = PER_CTA * LPR / MOVE_THREADS;
+    uint4 kx[KN];
+#pragma unroll
+    for (int u = 0; u < KN; ++u) {
+      const int e = u * MOVE_THREADS + tid, i = e / LPR, c = e % LPR;
+      if (s_to[i] >= 0) kx[u] = k[s_of[i] * LPR + c];
+    }
+    // V [page][head][d][slot]: lane = move
     const long long to = s_to[lane], of = s_of[lane];
+    const V *src = v + (of / PAGE) * (D * PAGE) + of % PAGE;
+    V *dst = v + (to / PAGE) * (D * PAGE) + to % PAGE;
+    V x[D / STEP];
+    float wt = 0.f;
+    int32_t at = 0;
     if (to >= 0) {
-      const V *src = v + (of / PAGE) * (D * PAGE) + of % PAGE;
-      V *dst = v + (to / PAGE) * (D * PAGE) + to % PAGE;
-      V x[D / STEP];
 #pragma unroll
       for (int u = 0; u < D / STEP; ++u) x[u] = src[(u * STEP + warp) * PAGE];
+      if (warp == 0) {
+        wt = a.weights[row + s_slot[lane].y];
+        at = a.positions[row + s_slot[lane].y];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < KN; ++u) {
+      const int e = u * MOVE_THREADS + tid, i = e / LPR, c = e % LPR;
+      if (s_to[i] >= 0) k[s_to[i] * LPR + c] = kx[u];
+    }
+    if (to >= 0) {
 #pragma unroll
       for (int u = 0; u < D / STEP; ++u) dst[(u * STEP + warp) * PAGE] = x[u];
-    }
-    // ---- K [page][head][slot][d]
-#pragma unroll
-    for (int e0 = 0; e0 < PER_CTA * LPR; e0 += MOVE_THREADS) {
-      const int e = e0 + tid, i = e / LPR, c = e % LPR;
-      if (s_to[i] >= 0) k[s_to[i] * LPR + c] = k[s_of[i] * LPR + c];
+      if (warp == 0) {
+        a.weights[row + s_slot[lane].x] = wt;
+        a.positions[row + s_slot[lane].x] = at;
+      }
     }
     __syncthreads();
   }
@@ -469,29 +514,34 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.budget = budget;
   a.top = top;
   a.status = static_cast<int *>(workspace);
-  // CTAs per list: 8192 slots each, so that several CTAs' keys fit an SM, and
-  // where lists are few as many as leave 2048 slots
+  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 101 us
+  // on 1024 threads each, 139 on clusters of two, whose meetings cost more than
+  // the emptier SM), 256 threads up to 8192 slots; where lists are few, a
+  // cluster (8 lists of 131071: 24 us on eight CTAs each).
   a.cs = 1;
-  while (a.cs < MAX_CS && (slots->capacity / a.cs > 8192 || (lists * a.cs * 2 <= 2LL * dev.sms && slots->capacity / a.cs > 2048)))
+  const int short_list = 8192, longest = 49152;
+  while (a.cs < MAX_CS && (slots->capacity / a.cs > longest || (lists * a.cs * 2 <= dev.sms && slots->capacity / a.cs > 4096)))
     a.cs *= 2;
   const int per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31, limit = 200 << 10;
   const bool cached = static_cast<int>(sizeof(PlanCtrl)) + per * 4LL <= limit;
   const int smem = static_cast<int>(sizeof(PlanCtrl)) + (cached ? per * 4 : 0);
-  static std::atomic<uint64_t> smem_set[2];
-  auto *kernel = cached ? plan_kernel<true> : plan_kernel<false>;
-  if (int e = allow_smem(smem_set[cached], dev, kernel, limit)) return e;
+  const bool wide = per > short_list;
+  static std::atomic<uint64_t> smem_set[3];
+  auto *kernel = !cached ? plan_kernel<1024, false> : wide ? plan_kernel<1024, true> : plan_kernel<256, true>;
+  const int which = !cached ? 0 : wide ? 1 : 2;
+  if (int e = allow_smem(smem_set[which], dev, kernel, limit)) return e;
   // as many CTAs on an SM as its shared memory holds, not a default split with L1
-  static std::atomic<uint64_t> carved[2];
+  static std::atomic<uint64_t> carved[3];
   const uint64_t bit = dev.index < 64 ? 1ull << dev.index : 0;
-  if (!(carved[cached].load(std::memory_order_relaxed) & bit)) {
+  if (!(carved[which].load(std::memory_order_relaxed) & bit)) {
     if (int e = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared),
                            "shared memory carveout"))
       return e;
-    carved[cached].fetch_or(bit, std::memory_order_relaxed);
+    carved[which].fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(lists * a.cs));
-  cfg.blockDim = dim3(PLAN_THREADS);
+  cfg.blockDim = dim3(cached && !wide ? 256 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
