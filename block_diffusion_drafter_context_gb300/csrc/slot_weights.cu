@@ -142,9 +142,11 @@ __device__ __forceinline__ float row_bias(float lse) { return lse == -INFINITY ?
 // ------------------------------------------------------------------ bf16: tcgen05
 // warp 0 feeds the ring with page pairs by TMA, warp 1 issues S^T = K Q^T,
 // warps 2-3 bring each tile's query rows (swizzled as TMA would) and biases
-// into one of two buffers, warps 4-7 turn scores into weights.  At 80 rows a
-// chunk keeps those four warps busy for about half of its share of HBM's time.
-constexpr int NTHR = 256;
+// into one of two buffers, warps 4-7 and 8-11 turn the scores of even and odd
+// chunks into weights.  At 80 rows a chunk keeps four warps busy for as long as
+// its share of HBM's time: 64 requests x 16 tokens x 5 heads at 16k..32k took 553
+// us with four of them, 487 with eight (the copy rate).
+constexpr int NTHR = 384;
 constexpr int NSB = 4;           // S^T buffers of up to 128 columns: all of tensor memory
 template <int D>
 struct WShape {
@@ -159,7 +161,7 @@ struct WChunk {
   int seg;                       // tiles before this one in the run
   int rows;
 };
-enum { NEW_TILE = 1, END_TILE = 2, DROP0 = 4, DROP1 = 8 };   // DROP: a page that is not there
+enum { NEW_TILE = 1, END_TILE = 2, DROP0 = 4, DROP1 = 8, NEXT_END = 16 };   // DROP: a page that is not there; NEXT_END: the next chunk ends the tile
 struct __align__(16) WCtrl {
   uint64_t full[8], empty[8], ready[NSB], sfull[NSB], sempty[NSB], qfull[2], qempty[2], drain;   // ready: sfull will come
   Run run;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
   uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t *sq = ring + ST * S::STAGE;
   WCtrl *ct = reinterpret_cast<WCtrl *>(sq + 2 * S::QB);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp: uniform to the compiler
   volatile int *abort_flag = &ct->abort_flag;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ct->qfull[i], 2);
-      mbar_init(&ct->qempty[i], 4);
+      mbar_init(&ct->qempty[i], 8);
     }
     mbar_init(&ct->drain, 1);
     ct->abort_flag = 0;
@@ -237,8 +239,8 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
         if (lane == 0) {
           WChunk c;
           c.b = w.b, c.h = w.h, c.t0 = (w.r.p0 + 2 * w.k) * PAGE, c.m = w.r.m, c.ctx = w.r.ctx;
-          c.flags = (w.fresh ? NEW_TILE : 0) | (i == run.n - 1 || w.k == w.r.chunks - 1 ? END_TILE : 0) |
-                    static_cast<int>(drop) * DROP0;
+          const int left = min(run.n - i, w.r.chunks - w.k);   // of the tile, this one among them
+          c.flags = (w.fresh ? NEW_TILE : 0) | (left == 1 ? END_TILE : left == 2 ? NEXT_END : 0) | static_cast<int>(drop) * DROP0;
           c.seg = seg, c.rows = w.r.m * a.g;
           ct->chunk[i % NI] = c;
           mbar_arrive_expect_tx(&ct->full[st], (2 - __popc(drop)) * (S::STAGE / 2));
@@ -263,34 +265,43 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && run.n > 0) {
-      bool ok = true;
-      for (int i = 0; i < run.n && ok; ++i) {
-        const int st = i % ST, sb = i % NSB;
-        ok = mbar_wait(&ct->full[st], static_cast<uint32_t>((i / ST) & 1), abort_flag, WAIT_NS);
-        if (!ok) break;
-        const WChunk &c = ct->chunk[i % NI];
-        const int qb = c.seg & 1;
-        if (c.flags & NEW_TILE) ok = mbar_wait(&ct->qfull[qb], static_cast<uint32_t>((c.seg >> 1) & 1), abort_flag, WAIT_NS);
-        ok = ok && mbar_wait(&ct->sempty[sb], static_cast<uint32_t>(((i / NSB) & 1) ^ 1), abort_flag, WAIT_NS);
-        if (!ok) break;
-        tc_fence_after();
-        const int n = (c.rows + 15) & ~15;
-        const uint32_t idesc = idesc_bf16_f32(PAIR, n), k0 = smem_u32(ring + st * S::STAGE), q0 = smem_u32(sq + qb * S::QB);
-        // a page that is not there leaves what the stage held: its lanes are dropped
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16(tmem + sb * 128, sdesc_k_sw128(k0 + (kk >> 2) * S::HALF + (kk & 3) * 32),
-                    sdesc_k_sw128(q0 + (kk >> 2) * (n * 128) + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-        umma_commit(&ct->sfull[sb]);
-        umma_commit(&ct->empty[st]);
-        mbar_arrive(&ct->ready[sb]);
+    // (the whole warp, converged; one lane of it issues)
+    bool ok = true;
+    int st = 0;
+    uint32_t ph = 0;
+    const uint32_t ring0 = smem_u32(ring), sq0 = smem_u32(sq);
+    for (int i = 0; i < run.n; ++i) {
+      const int sb = i % NSB;
+      ok = mbar_wait(&ct->full[st], ph, abort_flag, WAIT_NS) &&
+           mbar_wait(&ct->sempty[sb], static_cast<uint32_t>(((i / NSB) & 1) ^ 1), abort_flag, WAIT_NS);
+      if (!(ok = !__any_sync(0xffffffffu, !ok))) break;
+      const WChunk &c = ct->chunk[i % NI];
+      const int qb = c.seg & 1, n = (c.rows + 15) & ~15;
+      if (c.flags & NEW_TILE) {
+        ok = mbar_wait(&ct->qfull[qb], static_cast<uint32_t>((c.seg >> 1) & 1), abort_flag, WAIT_NS);
+        if (!(ok = !__any_sync(0xffffffffu, !ok))) break;
       }
-      if (!ok) {
+      tc_fence_after();
+      const uint32_t idesc = idesc_bf16_f32(PAIR, n), k0 = ring0 + st * S::STAGE, q0 = sq0 + qb * S::QB;
+      // a page that is not there leaves what the stage held: its lanes are dropped
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        umma_bf16_elect(tmem + sb * 128, sdesc_k_sw128(k0 + (kk >> 2) * S::HALF + (kk & 3) * 32),
+                        sdesc_k_sw128(q0 + (kk >> 2) * (n * 128) + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+      umma_commit_elect(&ct->sfull[sb]);
+      umma_commit_elect(&ct->empty[st]);
+      if (lane == 0) mbar_arrive(&ct->ready[sb]);
+      if (++st == ST) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    if (run.n > 0) {
+      if (!ok && lane == 0) {
         report(a.status, DFLASH_ERR_TIMEOUT);
         *abort_flag = 1;
       }
-      umma_commit(&ct->drain);   // every issued MMA retires before TMEM is released
+      umma_commit_elect(&ct->drain);   // every issued MMA retires before TMEM is released
       mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
     }
   } else if (warp < 4) {
@@ -340,14 +351,14 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
     }
   } else if (run.n > 0) {
     // ------------------------------------------------------------ weights
-    const int quad = warp & 3, key = quad * 32 + lane;   // TMEM lane = key of the chunk
+    const int wg = (warp >> 2) - 1, quad = warp & 3, key = quad * 32 + lane;   // TMEM lane = key of the chunk
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     bool ok = true;
     auto waitw = [&](uint64_t *bar, uint32_t par) -> bool {   // warp-uniform bounded wait
       const bool done = mbar_wait(bar, par, abort_flag, WAIT_NS);
       return !__any_sync(0xffffffffu, !done);
     };
-    for (int i = 0; i < run.n; ++i) {
+    for (int i = wg; i < run.n; i += 2) {
       const int sb = i % NSB;
       // not on `full`: the ring may have come round by now
       if (!(ok = waitw(&ct->ready[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;
@@ -361,36 +372,50 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
       if (!(ok = waitw(&ct->sfull[sb], static_cast<uint32_t>((i / NSB) & 1)))) break;
       tc_fence_after();
       const float *bias = ct->bias[c.seg & 1];
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-      for (int c0 = 0; c0 < n; c0 += 16) {
-        uint32_t r[16];
-        tmem_ld16_nw(lane_base + sb * 128 + c0, r);
-        tmem_wait_ld();
-        tmem_regs_ready(r);
+      // 16 rows at a time, the next ones on their way
+      const uint64_t sc2 = pair(a.scale_log2, a.scale_log2);
+      uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
+      auto add = [&](const uint32_t (&r)[16], int c0) {
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           const float4 bi = *reinterpret_cast<const float4 *>(bias + c0 + e);
-          float p0 = fast_exp2(fmaf(__uint_as_float(r[e]), a.scale_log2, bi.x));
-          float p1 = fast_exp2(fmaf(__uint_as_float(r[e + 1]), a.scale_log2, bi.y));
-          float p2 = fast_exp2(fmaf(__uint_as_float(r[e + 2]), a.scale_log2, bi.z));
-          float p3 = fast_exp2(fmaf(__uint_as_float(r[e + 3]), a.scale_log2, bi.w));
+          const float2 y = unpair(fma2(pair(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, pair(bi.x, bi.y)));
+          const float2 z = unpair(fma2(pair(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2, pair(bi.z, bi.w)));
+          float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y), p2 = fast_exp2(z.x), p3 = fast_exp2(z.y);
           if (edge) {
             if (c0 + e < hidden) p0 = 0.f;
             if (c0 + e + 1 < hidden) p1 = 0.f;
             if (c0 + e + 2 < hidden) p2 = 0.f;
             if (c0 + e + 3 < hidden) p3 = 0.f;
           }
-          s0 += p0, s1 += p1, s2 += p2, s3 += p3;
+          sum0 = add2(sum0, pair(p0, p1));
+          sum1 = add2(sum1, pair(p2, p3));
         }
+      };
+      uint32_t r0[16], r1[16];
+      tmem_ld16_nw(lane_base + sb * 128, r0);
+      for (int c0 = 0; c0 < n; c0 += 32) {
+        tmem_wait_ld();
+        tmem_regs_ready(r0);
+        if (c0 + 16 < n) tmem_ld16_nw(lane_base + sb * 128 + c0 + 16, r1);
+        add(r0, c0);
+        if (c0 + 16 >= n) break;
+        tmem_wait_ld();
+        tmem_regs_ready(r1);
+        if (c0 + 32 < n) tmem_ld16_nw(lane_base + sb * 128 + c0 + 32, r0);
+        add(r1, c0 + 16);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ct->sempty[sb]);
-        if (c.flags & END_TILE) mbar_arrive(&ct->qempty[c.seg & 1]);
+        // each group once a tile, at its last chunk of it; both at the only one
+        if (c.flags & (END_TILE | NEXT_END)) mbar_arrive(&ct->qempty[c.seg & 1]);
+        if ((c.flags & NEW_TILE) && (c.flags & END_TILE)) mbar_arrive(&ct->qempty[c.seg & 1]);
       }
       if (mine) {
-        a.weights[at] = old + ((s0 + s1) + (s2 + s3));
+        const float2 sum = unpair(add2(sum0, sum1));
+        a.weights[at] = old + (sum.x + sum.y);
         if (t >= c.ctx) a.positions[at] = (a.pos ? a.pos[c.b] : c.ctx) + (t - c.ctx);
       }
     }
