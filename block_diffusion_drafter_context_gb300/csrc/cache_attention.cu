@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
     // ------------------------------------------------------------ producer (the whole warp walks)
     if (!CL && n == 0) return;
     const T *q = static_cast<const T *>(p.q);
-    const uint64_t pol = PRE && p.pre.tile_tokens ? policy_evict_last() : policy_evict_first();
+    const uint64_t pol = PRE && p.pre.form == PREFIX ? policy_evict_last() : policy_evict_first();
     const Runs runs = ct->runs;
     int cf = 0, cl = 0;
     int b = ct->run.b, h = ct->run.h, rt = ct->run.rt, k = ct->run.k;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
       ok = !__any_sync(0xffffffffu, !ok);
       if (!ok) break;
       const bool first = i == 0 || (!CL && k == 0), last = i == n - 1 || (!CL && k == r.np - 1);
-      const int page = pages_of<PRE>(p, b)[r.p0 + k];
+      const int page = page_of<PRE>(p, b, r.p0 + k);
       const bool bad = page < 0 || page >= p.num_pages;
       const int live = first ? min(ROWS, r.n * p.g - rt * ROWS) : 0;   // query rows to load
       if (lane == 0) {
@@ -747,31 +747,44 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int pages = shared_len / PAGE;
   const bool f32 = hs->dtype == DFLASH_F32;
-  if (pages > 0) {
-    p.pre.rows = static_cast<float *>(rows);
-    p.pre.row_cap = most;
-    p.pre.pages = pages;
-    p.pre.batch = batch;
-    p.pre.cost = 0;
-    // The prefix.  fp32, or no more than 16 rows: one request with every row,
-    // in tiles of 16.
-    const long long all = static_cast<long long>(most) * p.g;
-    if (f32 || all <= ROWS) {
-      Params x = p;
-      x.B = 1;
-      x.pre.tile_tokens = most;
-      x.tiles = static_cast<int>((all + ROWS - 1) / ROWS);
-      // its tiles' counters: at most batch * row_tiles(max_new) for each kv head, as many as the second launch has
-      if (int e = launch_attention(*hs, *kv, x, all, pages, dev, s)) return e;
-    } else if (int e = launch_prefix(*hs, *kv, p, dev, s)) {
-      return e;
-    }
+  const long long rows_each = static_cast<long long>(max_new) * p.g, all = static_cast<long long>(most) * p.g;
+  p.pre.rows = static_cast<float *>(rows);
+  p.pre.row_cap = most;
+  p.pre.pages = pages;
+  p.pre.batch = batch;
+  // One launch while what it reads of the prefix beyond two launches is little:
+  // once per request (fp32: per tile of 16 rows) instead of once (per 16 of all
+  // rows).  Two launches against one, us, at
+  //   32 / 8 heads x 1 token, 4 requests on 1024: 15.9, 10.1; 16 on 1024 (60 MB):
+  //     21.5, 19.4; 32 on 1024 (130 MB): 22.3, 26.4;
+  //   40 / 8 heads x 16 tokens, 8 on 4096 (117 MB): 47, 45; 16 on 4096 (250 MB): 58, 61.5;
+  //   fp32, 16 / 8 heads x 1 token, 16 on 256 (29 MB): 23, 21; 64 on 256 (115 MB): 59, 65.
+  const long long tiles_each = f32 ? (rows_each + ROWS - 1) / ROWS : 1;
+  const long long passes = batch * tiles_each - (f32 ? (all + ROWS - 1) / ROWS : 1);
+  const long long again = passes * hs->n_kv_heads * pages * 2 * PAGE * hs->head_dim * elt_bytes(*hs);
+  if (again <= (f32 ? 48ll << 20 : rows_each > ROWS ? 192ll << 20 : 96ll << 20)) {
+    p.pre.form = ONE;
+    return launch_attention(*hs, *kv, p, rows_each, kv->max_pages, dev, s);
+  }
+  // The prefix.  fp32, or no more than 16 rows: one request with every row, in
+  // tiles of 16, whose counters are at most batch * row_tiles(max_new) for each
+  // kv head, as many as the second launch has.
+  if (f32 || all <= ROWS) {
+    Params x = p;
+    x.B = 1;
+    x.pre.form = PREFIX;
+    x.pre.tile_tokens = most;
+    x.tiles = static_cast<int>((all + ROWS - 1) / ROWS);
+    if (int e = launch_attention(*hs, *kv, x, all, pages, dev, s)) return e;
+  } else if (int e = launch_prefix(*hs, *kv, p, dev, s)) {
+    return e;
   }
   // What a tile takes beside its pages, in pages (a call of 64 requests: 16 new
   // tokens of 5 heads on 2..32 own pages 186 us at 0, 122 at 8, 118 at 12 to 16; one
   // token of 4 heads on 1..16 pages 66.2 at 0, 63.0 at 2, 65.1 at 8).
-  p.pre.cost = !f32 && max_new * p.g > ROWS ? 14 : 3;
-  return launch_attention(*hs, *kv, p, static_cast<long long>(max_new) * p.g, kv->max_pages - pages, dev, s);
+  p.pre.form = OWN;
+  p.pre.cost = !f32 && rows_each > ROWS ? 14 : 3;
+  return launch_attention(*hs, *kv, p, rows_each, kv->max_pages - pages, dev, s);
 }
 
 }  // extern "C"

@@ -22,13 +22,16 @@ constexpr size_t PART_TOTAL = PART_BYTES / sizeof(float);
 // batch shares for one request: its "requests" are runs of `tile_tokens` tokens,
 // whosever they are, that see every position of the prefix, and a row's
 // (O, maximum, sum) go to `rows`.  The second takes each request's own pages,
-// and joins them where it writes a row.
+// and joins them where it writes a row.  Where the prefix is short, one launch
+// reads it once for each request, from the first request's row of the table.
+enum Form { PREFIX, OWN, ONE };
 struct Prefix {
   float *rows;         // [row_cap][nq][D] O, then [row_cap][nq] (maximum, sum); row 0 is the batch's first
   int row_cap;         // rows a valid batch has at most
   int pages;           // of the prefix
-  int tile_tokens;     // first launch: tokens per run; second: 0
-  int batch;           // requests (Params.B counts runs in the first launch)
+  Form form;
+  int tile_tokens;     // PREFIX: tokens per run
+  int batch;           // requests (Params.B counts runs in PREFIX)
   int cost;            // of a tile beside its pages, in pages: see Start
 };
 
@@ -76,13 +79,13 @@ __device__ __forceinline__ Req make_request(const Params &p, int row0, int next,
   r.np = 0;
   if (r.n > 0) {
     const int lo = p.window > 0 ? max(0, r.ctx - p.window + 1) : 0;
-    r.p0 = PRE ? p.pre.pages : lo / PAGE;
+    r.p0 = !PRE ? lo / PAGE : p.pre.form == OWN ? p.pre.pages : 0;
     r.np = (r.ctx + r.n - 1) / PAGE - r.p0 + 1;
   }
   return r;
 }
 
-// Run j of the first launch: the prefix lies before all of its tokens.
+// Run j of PREFIX: the prefix lies before all of its tokens.
 __device__ __forceinline__ Req prefix_run(const Params &p, int j) {
   const int begin = min(max(0, p.cu_new[0]), p.total);
   const int end = min(p.cu_new[p.pre.batch], begin + min(p.total - begin, p.pre.row_cap));   // `rows` holds no more
@@ -96,13 +99,13 @@ __device__ __forceinline__ Req prefix_run(const Params &p, int j) {
 }
 template <bool PRE>
 __device__ __forceinline__ Req request(const Params &p, int b, bool tell) {
-  if (PRE && p.pre.tile_tokens) return prefix_run(p, b);
+  if (PRE && p.pre.form == PREFIX) return prefix_run(p, b);
   return make_request<PRE>(p, p.cu_new[b], p.cu_new[b + 1], p.ctx_len[b], tell);
 }
-// its row of the page table: the first request's holds the prefix
+// page k of request b: the first request's row of the table holds the prefix
 template <bool PRE>
-__device__ __forceinline__ const int32_t *pages_of(const Params &p, int b) {
-  return p.page_table + (PRE && p.pre.tile_tokens ? 0 : static_cast<size_t>(b) * p.max_pages);
+__device__ __forceinline__ int page_of(const Params &p, int b, int k) {
+  return p.page_table[k + (PRE && k < p.pre.pages ? 0 : static_cast<size_t>(b) * p.max_pages)];
 }
 // A tile's length in the list that is shared out.
 template <bool PRE>
@@ -115,7 +118,7 @@ __device__ __forceinline__ long long tile_units(const Params &p, const Req &r) {
 template <bool PRE, typename Tiles>
 __device__ __forceinline__ long long sum_pages(const Params &p, int b0, int b1, bool tell, Tiles tiles_of) {
   long long sum = 0;
-  if (PRE && p.pre.tile_tokens) {
+  if (PRE && p.pre.form == PREFIX) {
     for (int b = b0; b < b1; ++b) {
       const Req r = prefix_run(p, b);
       sum += tile_units<PRE>(p, r) * tiles_of(r);
@@ -233,16 +236,16 @@ struct Dest {
   int base;                // the tile's first query row
   float *share;            // PRE: the prefix's share of the request's first row, its maximum and sum
   float2 *share_ml;
-  bool first;              // PRE: the first launch
+  Form form;               // PRE
 };
 template <bool PRE>
 __device__ __forceinline__ Dest dest_of(const Params &p, int D, int row0, int h, int base = 0) {
-  Dest d = {p.out, p.lse, row0, h, p.nkv, p.g, base, nullptr, nullptr, false};
+  Dest d = {p.out, p.lse, row0, h, p.nkv, p.g, base, nullptr, nullptr, OWN};
   if (PRE) {
     const size_t nq = static_cast<size_t>(p.nkv) * p.g, at = (row0 - max(0, p.cu_new[0])) * nq;
     d.share = p.pre.rows + at * D;
     d.share_ml = reinterpret_cast<float2 *>(p.pre.rows + static_cast<size_t>(p.pre.row_cap) * nq * D) + at;
-    d.first = p.pre.tile_tokens > 0;
+    d.form = p.pre.form;
   }
   return d;
 }
@@ -293,7 +296,7 @@ __device__ __forceinline__ size_t share_index(const Dest &p, int row) {
 template <int D, bool PRE>
 __device__ __forceinline__ Share share_of(const Dest &p, int row, int c4) {
   Share s = {make_float4(0.f, 0.f, 0.f, 0.f), make_float2(-INFINITY, 0.f)};
-  if (PRE && !p.first) {
+  if (PRE && p.form == OWN) {
     const size_t i = share_index<D>(p, row);
     s.o = __ldcg(reinterpret_cast<const float4 *>(p.share + i * D + c4));
     s.ml = __ldcg(p.share_ml + i);
@@ -305,7 +308,7 @@ __device__ __forceinline__ Share share_of(const Dest &p, int row, int c4) {
 template <typename T, int D, bool PRE>
 __device__ __forceinline__ void write_row(const Dest &p, int row, int c4, float4 o, float M, float L, const Share &share) {
   if (PRE) {
-    if (p.first) {
+    if (p.form == PREFIX) {
       const size_t i = share_index<D>(p, row);
       __stcg(reinterpret_cast<float4 *>(p.share + i * D + c4), o);
       if (c4 == 0) __stcg(p.share_ml + i, make_float2(M, L));

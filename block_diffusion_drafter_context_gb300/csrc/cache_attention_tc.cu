@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         ok = mbar_wait(&ct->empty[st], static_cast<uint32_t>(((i / ST) & 1) ^ 1), abort_flag, WAIT_NS);
         ok = !__any_sync(0xffffffffu, !ok);
         if (!ok) break;
-        const int page = pages_of<PRE>(p, b)[r.p0 + k];
+        const int page = page_of<PRE>(p, b, r.p0 + k);
         const bool bad = page < 0 || page >= p.num_pages;
         if (lane == 0) {
           if (bad) report(p.status, DFLASH_ERR_DEVICE);
@@ -530,11 +530,11 @@ __global__ void __launch_bounds__(NTHR, 1)
       Dest dest;
       size_t moved[4];        // PRE: the rows pr + 8 k among the shares
       bool there[4];
-      uint4 sh[4];            // the prefix's share of 16 columns, of those rows
+      uint4 sh[4] = {};       // the prefix's share of 16 columns, of those rows (none in ONE)
       auto fetch = [&](int c) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (there[k]) sh[k] = __ldcg(reinterpret_cast<const uint4 *>(dest.share + moved[k] * D + c * 16) + pc);
+          if (there[k] && dest.form == OWN) sh[k] = __ldcg(reinterpret_cast<const uint4 *>(dest.share + moved[k] * D + c * 16) + pc);
       };
       if (PRE && !CL) {
         dest = dest_of<true>(p, D, last.row0, last.h);
@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
         if (whole) {
           fetch(0);
-          fr = join_prefix(Mr, Lr, __ldcg(dest.share_ml + share_index<D>(dest, live ? row : 0)));
+          fr = join_prefix(Mr, Lr, dest.form == OWN ? __ldcg(dest.share_ml + share_index<D>(dest, live ? row : 0))
+                                                    : make_float2(-INFINITY, 0.f));
         }
       }
       const float inv = inverse_sum(Mr, Lr);
