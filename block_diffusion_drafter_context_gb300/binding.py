@@ -30,7 +30,7 @@ EXPORTS = (
     "dflash_debug_gemm_pair_clusters", "dflash_set_fused_topk",
     "dflash_target_workspace_bytes", "dflash_append_kv", "dflash_cache_attention", "dflash_token_logprobs",
     "dflash_shared_attention", "dflash_shared_rows_bytes", "dflash_append_kv_at", "dflash_add_weights",
-    "dflash_plan_eviction", "dflash_move_slots",
+    "dflash_plan_eviction", "dflash_move_slots", "dflash_debug_shared_launches",
 )
 
 
@@ -131,6 +131,7 @@ def load(path: str = LIB_PATH):
                                        c_float, vp, vp, vp, c_size_t, vp]),
         "dflash_shared_attention": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, i, vp, i, i, i,
                                         c_float, vp, vp, vp, c_size_t, vp, c_size_t, vp]),
+        "dflash_debug_shared_launches": (i, [i]),
         "dflash_shared_rows_bytes": (c_size_t, [POINTER(dflash_heads), i, i]),
         "dflash_append_kv_at": (i, [POINTER(dflash_heads), POINTER(dflash_kv), i, vp, c_longlong, vp, vp, c_float, c_float,
                                     vp, i, vp, vp, i, vp, vp, c_size_t, vp]),
@@ -391,6 +392,10 @@ def dflash_shared_attention(heads: dflash_heads, kv: dflash_kv, layer, q, q_stri
                                                  _p(cu_new), total_new, _p(ctx_len), batch, max_new, shared_len, scale,
                                                  _p(out), _p(lse), _p(rows), rows_bytes, _p(workspace),
                                                  workspace_bytes, _stream(stream)))
+
+
+def dflash_debug_shared_launches(n: int) -> int:
+    return _check(load().dflash_debug_shared_launches(n))
 
 
 def dflash_shared_rows_bytes(heads: dflash_heads, max_batch: int, max_new: int) -> int:

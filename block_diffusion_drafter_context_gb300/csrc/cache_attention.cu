@@ -667,6 +667,8 @@ int take(const char *who, const dflash_heads *hs, const dflash_kv *kv, int layer
   return DFLASH_OK;
 }
 
+std::atomic<int> forced_launches{0};   // dflash_debug_shared_launches
+
 // rows of a valid batch: each of its requests has at most max_new
 int row_cap(int total_new, int batch, int max_new) {
   const long long most = static_cast<long long>(batch) * max_new;
@@ -722,6 +724,12 @@ DFLASH_API size_t dflash_shared_rows_bytes(const dflash_heads *hs, int max_batch
   return share_bytes(*hs, max_batch * max_new);
 }
 
+DFLASH_API int dflash_debug_shared_launches(int n) {
+  if (n < 0 || n > 2) return set_error(DFLASH_ERR_ARG, "debug_shared_launches: 0, 1 or 2");
+  forced_launches.store(n, std::memory_order_relaxed);
+  return DFLASH_OK;
+}
+
 DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *kv, int layer, const void *q,
                                        long long q_stride, const int32_t *cu_new, int total_new,
                                        const int32_t *ctx_len, int batch, int max_new, int shared_len, float scale,
@@ -762,7 +770,8 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
   const long long tiles_each = f32 ? (rows_each + ROWS - 1) / ROWS : 1;
   const long long passes = batch * tiles_each - (f32 ? (all + ROWS - 1) / ROWS : 1);
   const long long again = passes * hs->n_kv_heads * pages * 2 * PAGE * hs->head_dim * elt_bytes(*hs);
-  if (again <= (f32 ? 48ll << 20 : rows_each > ROWS ? 192ll << 20 : 96ll << 20)) {
+  const int forced = forced_launches.load(std::memory_order_relaxed);
+  if (pages == 0 || (forced ? forced == 1 : again <= (f32 ? 48ll << 20 : rows_each > ROWS ? 192ll << 20 : 96ll << 20))) {
     p.pre.form = ONE;
     return launch_attention(*hs, *kv, p, rows_each, kv->max_pages, dev, s);
   }

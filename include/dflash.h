@@ -646,6 +646,11 @@ DFLASH_API int dflash_move_slots(const dflash_heads *hs, const dflash_kv *kv, co
                       int n_layers, const int32_t *moves, int top, const int32_t *counts, int batch, void *workspace,
                       size_t workspace_bytes, dflash_stream_t stream);
 
+/* How dflash_shared_attention proceeds, in every thread of the process: 0 (the
+ * default) by the prefix's length, 1 in one launch that reads the prefix once
+ * per request, 2 with a launch for the prefix.  For tests. */
+DFLASH_API int dflash_debug_shared_launches(int n);
+
 /* Log probabilities of given tokens, with entropy, rank and the most probable
  * alternatives; e.g. of a step's committed tokens under the target logits
  * they were verified with.  Per row, y = logits / temperature:

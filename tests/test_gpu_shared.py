@@ -16,6 +16,15 @@ def built():
     build()
 
 
+@pytest.fixture(autouse=True, params=[1, 2], ids=["one launch", "prefix apart"])
+def launches(request, built):
+    """Every test in both forms, whatever the prefix's length would choose."""
+    from block_diffusion_drafter_context_gb300 import binding as B
+    B.dflash_debug_shared_launches(request.param)
+    yield request.param
+    B.dflash_debug_shared_launches(0)
+
+
 class Shared(Batch):
     """A Batch whose requests share their first `pages` pages: the kernels get
     them in the first request's row alone (the other rows hold -1 there)."""
@@ -114,6 +123,88 @@ def test_a_page_multiple_of_zero_is_plain_attention():
     out, lse = c.attend()
     out2, lse2 = c.ops.attend(c.kv, 1, c.q, c.cu_d, c.ctx_d, want_lse=True)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def exact(c):
+    """(out, lse, sum p |v|) in fp64 on the device."""
+    import torch
+    table = torch.from_numpy(c.table).cuda().long()
+    out = torch.empty(c.T, c.nq, c.d, dtype=torch.float64, device="cuda")
+    lse, spread = torch.empty(c.T, c.nq, dtype=torch.float64, device="cuda"), torch.empty_like(out)
+    g = c.nq // c.nkv
+    for b in range(len(c.ctx)):
+        n, L = c.new[b], c.ctx[b] + c.new[b]
+        if n == 0:
+            continue
+        pages = table[b, :-(-L // PAGE)]
+        rows = slice(int(c.cu[b]), int(c.cu[b + 1]))
+        for h in range(c.nkv):
+            k = c.k[1, pages, h].double().reshape(-1, c.d)[:L]
+            v = c.v[1, pages, h].double().permute(0, 2, 1).reshape(-1, c.d)[:L]
+            q = c.q[rows].double().view(n, c.nq, c.d)[:, h * g:(h + 1) * g]
+            s = torch.einsum("igd,td->igt", q, k) * c.d ** -0.5
+            hide = torch.arange(L, device="cuda") > c.ctx[b] + torch.arange(n, device="cuda")[:, None]
+            s.masked_fill_(hide[:, None], -float("inf"))
+            l = torch.logsumexp(s, -1)
+            p = (s - l[..., None]).exp()
+            out[rows, h * g:(h + 1) * g], spread[rows, h * g:(h + 1) * g] = p @ v, p @ v.abs()
+            lse[rows, h * g:(h + 1) * g] = l
+    return out, lse, spread
+
+
+@pytest.mark.parametrize("nq,nkv,d,dtype,batch,pages,new", [
+    (40, 8, 128, "bf16", 64, 33, 16),     # 160 tiles of 256 rows: one each and 8 that are cut, an odd number of pages
+    (32, 8, 128, "bf16", 64, 128, 1),     # a tile per head, cut into 19
+    (8, 8, 64, "bf16", 50, 300, 1),       # rows for less than a tile
+    (8, 1, 128, "bf16", 21, 511, 7),      # one head, tiles that end inside
+    (16, 2, 64, "bf16", 200, 16, 16),     # many tiles of few pages
+    (6, 1, 128, "bf16", 3, 1025, 16),     # few rows on a long prefix
+    (3, 3, 64, "bf16", 5, 40, 1),         # 16-row tiles
+    (16, 8, 128, "f32", 40, 60, 1), (4, 1, 64, "f32", 12, 201, 16)])
+def test_long_prefixes(nq, nkv, d, dtype, batch, pages, new):
+    """Against fp64 on the device, tolerances as in Shared.check; three calls
+    with the same bits."""
+    import torch
+    own = [(b * 61) % 300 for b in range(batch)]
+    c = Shared(nq, nkv, d, dtype, pages, own, [1 + (b * 7) % new for b in range(batch)], seed=pages, stale=0.0)
+    out, lse = c.attend()
+    for _ in range(2):
+        again = c.attend()
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert c.ops.status() == 0
+    ref, rlse, spread = exact(c)
+    size = float(c.q.double().abs().view(c.T, nq, d).sum(-1).max() * c.k[1].abs().max()) * d ** -0.5
+    e = 2 * d * 2.0 ** -24 * size + (max(c.ctx) + 16) * 2.0 ** -24 + 2.0 ** -19
+    tol = ((U["bf16"] if dtype == "bf16" else 0) + e) * spread + U[dtype] * ref.abs() + 1e-30
+    got = out.double().view(c.T, nq, d)
+    assert ((got - ref).abs() <= tol).all(), float(((got - ref).abs() / tol).max())
+    assert ((lse.double() - rlse).abs() <= e + 2.0 ** -22 * (1 + rlse.abs())).all()
+
+
+def test_missing_pages_at_both_ends_of_a_long_prefix():
+    """The first, the last and a pair of pages in between are not there, for rows
+    of several tiles."""
+    import torch
+    from block_diffusion_drafter_context_gb300.drafter import PagedKV
+    c = Shared(8, 1, 128, "bf16", 31, [10 * b for b in range(40)], [9] * 40, seed=12, stale=0.0)
+    for hole in (0, 12, 13, 30):
+        c.table[:, hole] = -1
+    c.kv = PagedKV.from_tensors(c.k, c.v, torch.from_numpy(c.table).cuda())
+    out, lse = c.attend()
+    assert c.ops.status() == -7
+    c.check(out, lse)
+
+
+def test_the_choice_by_length():
+    """What the library chooses by itself agrees with both forms."""
+    from block_diffusion_drafter_context_gb300 import binding as B
+    B.dflash_debug_shared_launches(0)
+    for pages, batch in ((2, 4), (400, 30)):
+        c = Shared(8, 1, 128, "bf16", pages, [40] * batch, [2] * batch, seed=3, stale=0.0)
+        out, lse = c.attend()
+        ref, rlse, spread = exact(c)
+        assert c.ops.status() == 0
+        assert ((out.double().view(c.T, 8, 128) - ref).abs() <= 2.0 ** -7 * (spread + ref.abs())).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

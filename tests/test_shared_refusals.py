@@ -54,3 +54,10 @@ def test_rows_size():
         with pytest.raises(B.DflashError):
             B.dflash_shared_rows_bytes(h, batch, new)
     assert B.load().dflash_shared_rows_bytes(None, 1, 1) == 0 and ctypes.sizeof(B.dflash_heads) == 16
+
+
+def test_debug_launches():
+    for bad in (-1, 3):
+        with pytest.raises(B.DflashError):
+            B.dflash_debug_shared_launches(bad)
+    assert B.dflash_debug_shared_launches(0) == 0
