@@ -551,7 +551,6 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
       }
       const float inv = inverse_sum(Mr, Lr);
-      uint32_t kept[2][8];              // two blocks of 16 columns are 64 bytes of a row of bf16
       // PRE: everything but the sums of products in three factors; a row of nothing
       // (inverse 0, or a sum of 0 beside a NaN) is 0 or NaN by them
       const float once = PRE && whole ? inv : 1.f;
@@ -559,61 +558,48 @@ __global__ void __launch_bounds__(NTHR, 1)
                      fc = pair(fr.pre * once, fr.pre * once);
       const bool unwritten = __any_sync(0xffffffffu, l == 0.f || !two || its.y == 0.f);
       uint4 *out_row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + static_cast<size_t>(last.row0) * (p.nkv * g) * D) + pc;
-      constexpr int CU = PRE ? 1 : 2;   // blocks of 16 columns in flight: the share's loads want registers too
+      if constexpr (PRE && !CL) {
+        // v = fa a + fb b + fc share, 32 columns at a time, rows by the lane, then
+        // whole rows in and out; an O that was never written is not read.  The loop
+        // stays one: unrolled, its instructions came from L2 for every tile, 2000 to
+        // 4000 cycles for 16 columns.
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t kept[2][8];
 #pragma unroll
-      for (int c0 = 0; c0 < D / 16; c0 += CU) {
-        uint32_t a[CU][16], b[CU][16];
-#pragma unroll
-        for (int u = 0; u < CU; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
-        if (two)
-#pragma unroll
-          for (int u = 0; u < CU; ++u) tmem_ld16_nw(its_o + (c0 + u) * 16, b[u]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < CU; ++u) {
-          tmem_regs_ready(a[u]);
-          if constexpr (PRE && !CL) {
-            // v = fa a + fb b + fc share.  Rows by the lane, then whole rows in and
-            // out; an O that was never written is not read.
-            if (two) tmem_regs_ready(b[u]);
+          for (int u = 0; u < 2; ++u) {
+            uint32_t a[16], b[16];
+            tmem_ld16_nw(my_o + c0 + 16 * u, a);
+            if (two) tmem_ld16_nw(its_o + c0 + 16 * u, b);
+            tmem_wait_ld();
+            tmem_regs_ready(a);
+            if (two) tmem_regs_ready(b);
             if (unwritten) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                if (l == 0.f) a[u][e] = 0u;
-                if (!two || its.y == 0.f) b[u][e] = 0u;
+                if (l == 0.f) a[e] = 0u;
+                if (!two || its.y == 0.f) b[e] = 0u;
               }
             }
             uint64_t v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              v[e] = mul2(pair(__uint_as_float(a[u][2 * e]), __uint_as_float(a[u][2 * e + 1])), fa);
-              if (two) v[e] = fma2(pair(__uint_as_float(b[u][2 * e]), __uint_as_float(b[u][2 * e + 1])), fb, v[e]);
+              v[e] = mul2(pair(__uint_as_float(a[2 * e]), __uint_as_float(a[2 * e + 1])), fa);
+              if (two) v[e] = fma2(pair(__uint_as_float(b[2 * e]), __uint_as_float(b[2 * e + 1])), fb, v[e]);
             }
             if (whole) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) *patch_at(patch, pr + 8 * k, pc) = sh[k];
               __syncwarp();
-              if (c0 + 1 < D / 16) fetch(c0 + 1);
+              if (c0 + 16 * u + 16 < D) fetch(c0 / 16 + u + 1);
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
                 const float4 x = *reinterpret_cast<const float4 *>(patch_at(patch, lane, t));
                 const float2 y = unpair(fma2(pair(x.x, x.y), fc, v[2 * t])), z = unpair(fma2(pair(x.z, x.w), fc, v[2 * t + 1]));
-                kept[c0 & 1][2 * t] = pack_bf16(y.x, y.y);
-                kept[c0 & 1][2 * t + 1] = pack_bf16(z.x, z.y);
+                kept[u][2 * t] = pack_bf16(y.x, y.y);
+                kept[u][2 * t + 1] = pack_bf16(z.x, z.y);
               }
               __syncwarp();
-              if (c0 & 1) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                  const uint32_t *w = &kept[t >> 1][4 * (t & 1)];
-                  *patch_at(patch, lane, t) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (there[k]) *(out_row + moved[k] * (D / 8) + (c0 - 1) * 2) = *patch_at(patch, pr + 8 * k, pc);
-                __syncwarp();
-              }
             } else {
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
@@ -624,11 +610,37 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (there[k])
-                  __stcg(reinterpret_cast<uint4 *>(part + (quad * 32 + pr + 8 * k) * D + c0 * 16) + pc,
+                  __stcg(reinterpret_cast<uint4 *>(part + (quad * 32 + pr + 8 * k) * D + c0 + 16 * u) + pc,
                          *patch_at(patch, pr + 8 * k, pc));
               __syncwarp();
             }
-          } else {
+          }
+          if (whole) {   // 64 bytes of a row of bf16
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t *w = &kept[t >> 1][4 * (t & 1)];
+              *patch_at(patch, lane, t) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (there[k]) *(out_row + moved[k] * (D / 8) + c0 / 8) = *patch_at(patch, pr + 8 * k, pc);
+            __syncwarp();
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c0 = 0; c0 < D / 16; c0 += 2) {
+          uint32_t a[2][16], b[2][16];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) tmem_ld16_nw(my_o + (c0 + u) * 16, a[u]);
+          if (two)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) tmem_ld16_nw(its_o + (c0 + u) * 16, b[u]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            tmem_regs_ready(a[u]);
             float v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = l == 0.f ? 0.f : f0 * __uint_as_float(a[u][e]);   // sum 0: O was never written
