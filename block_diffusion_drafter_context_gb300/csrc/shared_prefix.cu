@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       any = true;
       bool started = false;                        // O holds something of the tile
-      // S of the next page; a page that is not there gives columns that nobody reads
+      // S of the next page; one that is not there gives columns that nobody reads
       auto scores = [&] {
         const uint32_t k0 = ring0 + st * SLOT, d = s_col + 64 * (n_s & 1);
 #pragma unroll
@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       report(a.status, DFLASH_ERR_TIMEOUT);
       *abort_flag = 1;
     }
+    __syncwarp();
     if (any) {
       umma_commit_elect(&ct->drain[w]);   // every issued MMA retires before TMEM is released
       mbar_wait(&ct->drain[w], 0, nullptr, WAIT_NS);

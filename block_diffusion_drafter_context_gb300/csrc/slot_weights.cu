@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(NTHR, 1) weights_kernel(const __grid_constant_
         report(a.status, DFLASH_ERR_TIMEOUT);
         *abort_flag = 1;
       }
+      __syncwarp();
       umma_commit_elect(&ct->drain);   // every issued MMA retires before TMEM is released
       mbar_wait(&ct->drain, 0, nullptr, WAIT_NS);
     }
