@@ -26,7 +26,8 @@ namespace {
 // that have something to write are written.  Where lists are long or few, a
 // cluster of CTAs shares one: each has a stretch of the slots and sends the
 // counts that are not 0 to the first, which finds the digit for all.  Bound by
-// instructions: some 60 per 32 slots, and HBM's share a quarter.
+// instructions and by the dependent steps of a list (loads, two selections, two
+// walks): 36 layers of 4 x 8 lists of 4.1k take 37 us, 11 of them HBM's.
 constexpr int BINS = 2048;
 constexpr int FEW = 2048;                     // keys set apart at most
 constexpr int MAX_CS = 8;
@@ -77,7 +78,7 @@ __device__ __forceinline__ uint32_t sum_before(const uint32_t *v, int n, int lan
 template <int T, bool CACHED>
 __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArgs a) {
   constexpr int PLAN_THREADS = T, PLAN_WARPS = T / 32, MINE = BINS / T;   // MINE: bins of a thread
-  constexpr int U = T == 256 ? 4 : 8;   // keys of a thread with their loads in flight
+  constexpr int U = 8;         // keys of a thread with their loads in flight
   extern __shared__ uint32_t plan_smem[];
   PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
   uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
@@ -151,26 +152,23 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
 #pragma unroll 4
       for (int i = tid; i < mine; i += PLAN_THREADS) count(keys[i], true);
     } else {
-      int i = tid;
-      for (; i + (U - 1) * PLAN_THREADS < mine; i += U * PLAN_THREADS) {
+      // (the last ones with the others in one batch: a loop of their own is a latency of its own)
+      for (int i = tid; i < mine; i += U * PLAN_THREADS) {
         float w[U];
         int32_t at[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          w[u] = wt[i + u * PLAN_THREADS];
-          at[u] = ps[i + u * PLAN_THREADS];
-        }
+        for (int u = 0; u < U; ++u)
+          if (i + u * PLAN_THREADS < mine) {
+            w[u] = wt[i + u * PLAN_THREADS];
+            at[u] = ps[i + u * PLAN_THREADS];
+          }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t k = make_key(w[u], at[u]);
-          if (CACHED) keys[i + u * PLAN_THREADS] = k;
-          count(k, true);
-        }
-      }
-      for (; i < mine; i += PLAN_THREADS) {
-        const uint32_t k = make_key(wt[i], ps[i]);
-        if (CACHED) keys[i] = k;
-        count(k, true);
+        for (int u = 0; u < U; ++u)
+          if (i + u * PLAN_THREADS < mine) {
+            const uint32_t k = make_key(w[u], at[u]);
+            if (CACHED) keys[i + u * PLAN_THREADS] = k;
+            count(k, true);
+          }
       }
     }
     zeros = __reduce_add_sync(0xffffffffu, zeros);
@@ -253,6 +251,31 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
       }
       __syncthreads();
       if (ct->found <= FEW) n_few = static_cast<int>(ct->found);
+      if (a.cs == 1 && n_few >= 0 && n_few <= 256) {
+        // each compared with all of them, by the warps that hold one; with the loads above in
+        // one batch the 36 layers take 38 us for 45. All 1024 threads against as many
+        // candidates took 171 us for 101 on 64 prompts
+        const bool holds = (tid & ~31) < n_few;
+        const uint32_t k = tid < n_few ? ct->few[tid] : 0u;
+        uint32_t more = 0, same = 0;
+#pragma unroll 4
+        for (int i = 0; i < (holds ? n_few : 0); ++i) {
+          const uint32_t x = ct->few[i];
+          more += x > k;
+          same += x == k;
+        }
+        __syncthreads();       // everybody has read what the first digit's pick says
+        if (tid < n_few && more < want && want <= more + same) {   // equal keys write the same
+          ct->pick[0] = k;
+          ct->pick[1] = more;
+          ct->pick[2] = same;
+        }
+        __syncthreads();
+        prefix = ct->pick[0];
+        want -= ct->pick[1];
+        ties_all = ct->pick[2];
+        break;
+      }
     }
   }
   // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
@@ -514,10 +537,10 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.budget = budget;
   a.top = top;
   a.status = static_cast<int *>(workspace);
-  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 101 us
+  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 94 us
   // on 1024 threads each, 139 on clusters of two, whose meetings cost more than
   // the emptier SM), 256 threads up to 8192 slots; where lists are few, a
-  // cluster (8 lists of 131071: 24 us on eight CTAs each).
+  // cluster (8 lists of 131071: 23 us on eight CTAs each).
   a.cs = 1;
   const int short_list = 8192, longest = 49152;
   while (a.cs < MAX_CS && (slots->capacity / a.cs > longest || (lists * a.cs * 2 <= dev.sms && slots->capacity / a.cs > 4096)))
