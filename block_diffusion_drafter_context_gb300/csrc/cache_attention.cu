@@ -382,6 +382,17 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
         // form pays 12 % for it: both keep the one product.
         const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
                                 pack_bf16(s[1][2], s[1][3])};
+        // With a shared prefix the rest has its product: over few rows the error
+        // of a call's outputs was up to 1.57 times that of their own rounding
+        // (1.37 over many rows), and is 1.0 times with it; 64 x 1 on 8k 63.4 us
+        // without, 64.6 with it.
+        uint32_t pr[4];
+        if constexpr (PRE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            pr[i] = pack_bf16(s[i >> 1][(i & 1) * 2] - __uint_as_float(pa[i] << 16),
+                              s[i >> 1][(i & 1) * 2 + 1] - __uint_as_float(pa[i] & 0xffff0000u));
+        }
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (stale) {
           keep0 = mine + 1 <= newest ? 0xffffffffu : mine <= newest ? 0xffffu : 0u;
@@ -395,6 +406,10 @@ __global__ void __launch_bounds__(160, Shape<T, D>::CTAS)
           if (stale) b0 &= keep0, b1 &= keep1, b2 &= keep0, b3 &= keep1;
           mma_bf16_16816(o[t], pa, b0, b1);
           mma_bf16_16816(o[t + 1], pa, b2, b3);
+          if constexpr (PRE) {
+            mma_bf16_16816(o[t], pr, b0, b1);
+            mma_bf16_16816(o[t + 1], pr, b2, b3);
+          }
         }
       }
     }
@@ -789,8 +804,9 @@ DFLASH_API int dflash_shared_attention(const dflash_heads *hs, const dflash_kv *
     return e;
   }
   // What a tile takes beside its pages, in pages (a call of 64 requests: 16 new
-  // tokens of 5 heads on 2..32 own pages 186 us at 0, 122 at 8, 118 at 12 to 16; one
-  // token of 4 heads on 1..16 pages 66.2 at 0, 63.0 at 2, 65.1 at 8).
+  // tokens of 5 heads on 2..32 own pages behind 2048 positions 206 us at 0, 147 at 8,
+  // 145 at 12, 147 at 16; one token of 4 heads on 1..16 pages behind 8192 67.2 at 0,
+  // 63.3 at 3, 65.0 at 8).
   p.pre.form = OWN;
   p.pre.cost = !f32 && rows_each > ROWS ? 14 : 3;
   return launch_attention(*hs, *kv, p, rows_each, kv->max_pages - pages, dev, s);

@@ -541,7 +541,10 @@ DFLASH_API int dflash_cache_attention(const dflash_heads *hs, const dflash_kv *k
  * positions 0 .. shared_len-1 are read and multiplied once for the rows of all
  * requests, and joined with each request's own positions
  * shared_len .. ctx_len[b]+i.  Results as dflash_cache_attention's without a
- * window, up to the order of the sums.
+ * window, up to the order of the sums and in bf16 the probabilities: with at
+ * most 16 rows (max_new * nq / nkv) they are good to 2^-16 over the requests' own
+ * positions, and over the prefix where it is so short that each request reads
+ * it, or the whole batch has at most 16.
  *   shared_len: tokens of the prefix, whole pages (a multiple of 64; 0: the
  *              call is dflash_cache_attention).  Its pages are those of the
  *              first request's row of the page table; the other rows' first

@@ -7,7 +7,7 @@ import pytest
 from block_diffusion_drafter_context_gb300 import binding as B
 from tests.test_gpu_shared import Shared
 from tests.test_gpu_slots import Weighed, i32, np32, ops_for, plan_on_device, some_slots
-from tests.test_gpu_target import PAGE
+from tests.test_gpu_target import PAGE, U, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -51,6 +51,25 @@ def test_plan_with_keys_that_lie_close(nkv, batch, cap, near, ties):
         assert torch.equal(got[..., 0, :].long(), into[..., :top]) and torch.equal(got[..., 1, :].long(), source[..., :top])
         assert torch.equal(counts.long(), (source < cap).sum(-1)) and torch.equal(left, ctx.clamp(max=keep))
     assert ops.status() == 0
+
+
+@pytest.mark.parametrize("nq,nkv,d,ctx,new,launches", [
+    (2, 2, 64, [40, 3, 0, 70], [1, 1, 1, 1], 1), (8, 2, 128, [9, 300], [3, 1], 1), (8, 1, 64, [0, 1], [1, 1], 2),
+    (12, 4, 128, [5], [5], 2)])
+def test_few_rows_have_exact_probabilities(nq, nkv, d, ctx, new, launches):
+    """bf16, up to 16 rows per kv head: P as two bf16 parts, each off by half a
+    step, 2^-8 of 2^-8.  The other terms as in Shared.check."""
+    c = Shared(nq, nkv, d, "bf16", 5, ctx, new, seed=d + nq)
+    B.dflash_debug_shared_launches(launches)
+    try:
+        out = np64(c.attend()[0])
+    finally:
+        B.dflash_debug_shared_launches(0)
+    ref, _, spread = c.attend_ref()
+    size = np.abs(np64(c.q)).reshape(c.T, nq, d).sum(-1).max() * np.nanmax(np.abs(np64(c.k[1]))) * d ** -0.5
+    e = 2 * d * 2.0 ** -24 * size + max(a + b for a, b in zip(c.ctx, c.new)) * 2.0 ** -24 + 2.0 ** -19
+    assert c.ops.status() == 0
+    assert (np.abs(out - ref) <= (2.0 ** -16 + e) * spread + U["bf16"] * np.abs(ref) + 1e-30).all()
 
 
 def far(c, pages, used):
