@@ -77,9 +77,9 @@ __device__ __forceinline__ uint32_t sum_before(const uint32_t *v, int n, int lan
 
 // T threads; CACHED: a CTA's keys fit its shared memory.
 template <int T, bool CACHED>
-__global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArgs a) {
   constexpr int PLAN_THREADS = T, PLAN_WARPS = T / 32, MINE = BINS / T;   // MINE: bins of a thread
-  constexpr int U = 8;         // keys of a thread with their loads in flight
+  constexpr int U = T == 256 ? 6 : 8;   // keys of a thread with their loads in flight
   extern __shared__ uint32_t plan_smem[];
   PlanCtrl *ct = reinterpret_cast<PlanCtrl *>(plan_smem);
   uint32_t *keys = plan_smem + sizeof(PlanCtrl) / 4;
@@ -133,6 +133,43 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   else
     __syncthreads();
+
+  // Each lane looks after 32 neighbouring slots of its warp's stretch (8 or 16 where it
+  // is short), GW times, a bit each, and reads its keys in an order that keeps the
+  // lanes on banks of their own.  Against 32 slots to a warp, whose masks are ballots
+  // and whose moves leave from where they are found, 64 prompts took 70 us for 94.
+  constexpr int GW = T == 256 ? 1 : 2;
+  const int seg = ((mine + PLAN_WARPS - 1) / PLAN_WARPS + 31) / 32 * 32;   // slots per warp, at most 1024 GW where they are cached
+  const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
+  const int log_w = seg <= 256 ? 3 : seg <= 512 ? 4 : 5, width = 1 << log_w;
+  auto slot_of = [&](int w) { return s0 + ((32 * w + lane) << log_w); };
+  auto mask = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1; };   // the lowest n bits
+  uint32_t up[GW], eq[GW];     // slots whose key's bits from `shift` on lie above `value`, and those that equal it
+  auto look = [&](int shift, uint32_t value) {
+#pragma unroll
+    for (int w = 0; w < GW; ++w) {
+      const int g = slot_of(w);
+      up[w] = eq[w] = 0;
+      if (g >= s1) continue;
+#pragma unroll 8
+      for (int j = 0; j < width; ++j) {
+        const int r = (j + (lane >> (5 - log_w))) & (width - 1);
+        const uint32_t k = keys[g + r] >> shift;
+        if (k > value) up[w] |= 1u << r;
+        if (k == value) eq[w] |= 1u << r;
+      }
+      up[w] &= mask(s1 - g);
+      eq[w] &= mask(s1 - g);
+    }
+  };
+  auto scan = [&](uint32_t v) {   // of the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += t;
+    }
+    return v;
+  };
 
   // ---- radix selection: `want` keys are to stay, those with the found prefix above them already
   uint32_t want = a.budget - a.first, prefix = 0, ties_all = 0;
@@ -239,17 +276,17 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
     want -= ct->pick[1];
     ties_all = ct->pick[2];
     if (pass == 0 && CACHED) {
-#pragma unroll 4
-      for (int i0 = warp * 32; i0 < mine; i0 += PLAN_THREADS) {
-        const uint32_t k = i0 + lane < mine ? keys[i0 + lane] : 0u;
-        const bool in = i0 + lane < mine && k >> 21 == prefix;
-        const uint32_t v = __ballot_sync(0xffffffffu, in);
-        if (!v) continue;
-        uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&ct->found, __popc(v));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(v & ((1u << lane) - 1));
-        if (in && at < FEW) ct->few[at] = k;
-      }
+      look(21, prefix);
+      uint32_t have = 0;
+#pragma unroll
+      for (int w = 0; w < GW; ++w) have += __popc(eq[w]);
+      const uint32_t inc = scan(have);
+      uint32_t at = 0;
+      if (lane == 31 && inc) at = atomicAdd(&ct->found, inc);
+      at = __shfl_sync(0xffffffffu, at, 31) + inc - have;
+#pragma unroll
+      for (int w = 0; w < GW; ++w)
+        for (uint32_t e = eq[w]; e && at < FEW; e &= e - 1, ++at) ct->few[at] = keys[slot_of(w) + __ffs(e) - 1];
       __syncthreads();
       if (ct->found <= FEW) n_few = static_cast<int>(ct->found);
       if (a.cs == 1 && n_few >= 0 && n_few <= 256) {
@@ -280,15 +317,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
     }
   }
   // keys above `prefix` stay, and `want` of the ties_all that equal it: the lowest slots
-  const int seg = ((mine + PLAN_WARPS - 1) / PLAN_WARPS + 31) / 32 * 32;   // slots per warp
-  const int s0 = min(mine, warp * seg), s1 = min(mine, s0 + seg);
   uint32_t tie_base = 0;       // equal keys in slots before this warp's
-  if (want < ties_all) {
-    uint32_t t = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-      const int i = i0 + lane;
-      t += __popc(__ballot_sync(0xffffffffu, i < s1 && key_at(i) == prefix));
-    }
+  auto count_ties = [&](uint32_t t) {   // t: this warp's
     if (lane == 0) ct->warp_a[warp] = t;
     __syncthreads();
     tie_base = sum_before(ct->warp_a, warp, lane);
@@ -299,73 +329,130 @@ __global__ void __launch_bounds__(T, T == 256 ? 5 : 1) plan_kernel(const PlanArg
       for (int r = 0; r < rank; ++r) tie_base += ld_dsmem_u32(dsmem_addr(&ct->ties, r));
     }
     __syncthreads();
-  }
+  };
   const int keep = a.budget;   // ctx > budget here
-  const uint32_t below = (1u << lane) - 1;
-  // Of 32 slots from i0 on, those that fall free below `keep` and those kept from
-  // it on, a bit each; `tie` counts the equal keys before.
-  auto flags = [&](int i0, uint32_t &tie) {
-    const int i = i0 + lane;
-    const bool in = i < s1;
-    const uint32_t k = in ? key_at(i) : 0u;
-    bool stays = k >= prefix;
-    if (want < ties_all) {
-      const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix);
-      stays = k > prefix || (k == prefix && tie + __popc(eq & below) < want);
-      tie += __popc(eq);
+  auto under = [&](int i0) { return mask(keep - lo - i0); };   // of 32 slots from i0 on, those below `keep`
+  uint32_t hole0 = 0, mover0 = 0, count = 0;   // of the CTAs before this one; in all: as many holes as movers
+  auto count_moves = [&](uint32_t holes, uint32_t movers) {    // this warp's
+    if (lane == 0) {
+      ct->warp_a[warp] = holes;
+      ct->warp_b[warp] = movers;
     }
-    return __ballot_sync(0xffffffffu, in && stays == (lo + i >= keep));
-  };
-  auto under = [&](int i0) {   // of 32 slots from i0 on, those below `keep`
-    const int m = keep - lo - i0;
-    return m >= 32 ? 0xffffffffu : m <= 0 ? 0u : (1u << m) - 1;
-  };
-  uint32_t holes = 0, movers = 0, tie = tie_base;
-#pragma unroll 4
-  for (int i0 = s0; i0 < s1; i0 += 32) {
-    const uint32_t f = flags(i0, tie), u = under(i0);
-    holes += __popc(f & u);
-    movers += __popc(f & ~u);
-    if (CACHED && lane == 0) keys[i0] = f;   // in the place of the first key, which nobody asks for again
-  }
-  if (lane == 0) {
-    ct->warp_a[warp] = holes;
-    ct->warp_b[warp] = movers;
-  }
-  __syncthreads();
-  uint32_t hole = sum_before(ct->warp_a, warp, lane), mover = sum_before(ct->warp_b, warp, lane);
-  uint32_t count = sum_before(ct->warp_a, PLAN_WARPS, lane);   // as many as there are movers
-  if (a.cs > 1) {
-    const uint32_t y = sum_before(ct->warp_b, PLAN_WARPS, lane);
-    if (tid == 0) {
-      ct->holes = count;
-      ct->movers = y;
-    }
-    meet();
-    count = 0;
-    for (int r = 0; r < a.cs; ++r) {
-      const uint32_t x = ld_dsmem_u32(dsmem_addr(&ct->holes, r));
-      count += x;
-      if (r < rank) {
-        hole += x;
-        mover += ld_dsmem_u32(dsmem_addr(&ct->movers, r));
+    __syncthreads();
+    count = sum_before(ct->warp_a, PLAN_WARPS, lane);
+    if (a.cs > 1) {
+      const uint32_t y = sum_before(ct->warp_b, PLAN_WARPS, lane);
+      if (tid == 0) {
+        ct->holes = count;
+        ct->movers = y;
+      }
+      meet();
+      count = 0;
+      for (int r = 0; r < a.cs; ++r) {
+        const uint32_t x = ld_dsmem_u32(dsmem_addr(&ct->holes, r));
+        count += x;
+        if (r < rank) {
+          hole0 += x;
+          mover0 += ld_dsmem_u32(dsmem_addr(&ct->movers, r));
+        }
       }
     }
-  }
-  __syncwarp();
-  tie = tie_base;
-  for (int g0 = s0; g0 < s1; g0 += 1024) {   // 32 times 32 slots, those that have something to write
-    uint32_t mine_f = 0, some;
-    if (CACHED) {
-      if (g0 + 32 * lane < s1) mine_f = keys[g0 + 32 * lane];
-      some = __ballot_sync(0xffffffffu, mine_f != 0);
+    __syncwarp();
+  };
+  if constexpr (CACHED) {
+    uint32_t tie[GW];
+    if (n_few >= 0) {          // what the first digit left open
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        tie[w] = 0;
+        for (uint32_t e = eq[w]; e; e &= e - 1) {
+          const uint32_t k = keys[slot_of(w) + __ffs(e) - 1], bit = e & (0u - e);
+          if (k > prefix) up[w] |= bit;
+          if (k == prefix) tie[w] |= bit;
+        }
+      }
     } else {
-      const int groups = (min(s1, g0 + 1024) - g0 + 31) / 32;
-      some = groups == 32 ? 0xffffffffu : (1u << groups) - 1;
+      look(0, prefix);
+#pragma unroll
+      for (int w = 0; w < GW; ++w) tie[w] = eq[w];
     }
-    for (; some; some &= some - 1) {
-      const int g = __ffs(some) - 1, i0 = g0 + 32 * g;
-      const uint32_t f = CACHED ? __shfl_sync(0xffffffffu, mine_f, g) : flags(i0, tie), u = under(i0);
+    if (want < ties_all) {
+      uint32_t t = 0;
+#pragma unroll
+      for (int w = 0; w < GW; ++w) t += __popc(tie[w]);
+      count_ties(__reduce_add_sync(0xffffffffu, t));
+#pragma unroll
+      for (int w = 0; w < GW; ++w) {
+        const uint32_t n = __popc(tie[w]), inc = scan(n), before = tie_base + inc - n;
+        const uint32_t some = before < want ? want - before : 0;
+        if (some < n) {        // the lowest of them
+          uint32_t rest = tie[w];
+          for (uint32_t i = 0; i < some; ++i) rest &= rest - 1;
+          tie[w] ^= rest;
+        }
+        tie_base += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    // what falls free below `keep` and what is kept from it on; both counts in one sum
+    uint32_t hole[GW], mover[GW], off[GW], sum = 0;
+#pragma unroll
+    for (int w = 0; w < GW; ++w) {
+      const uint32_t in = mask(min(width, s1 - slot_of(w))), low = under(slot_of(w)), stays = up[w] | tie[w];
+      hole[w] = ~stays & low & in;
+      mover[w] = stays & ~low & in;
+      const uint32_t n = __popc(hole[w]) | __popc(mover[w]) << 16, inc = scan(n);
+      off[w] = sum + inc - n;
+      sum += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    count_moves(sum & 0xffffu, sum >> 16);
+    // the slots in their order, in the keys' place, which everybody has read
+    const uint32_t holes = sum_before(ct->warp_a, PLAN_WARPS, lane), movers = sum_before(ct->warp_b, PLAN_WARPS, lane);
+    const uint32_t h0 = sum_before(ct->warp_a, warp, lane), m0 = holes + sum_before(ct->warp_b, warp, lane);
+#pragma unroll
+    for (int w = 0; w < GW; ++w) {
+      uint32_t *to = keys + h0 + (off[w] & 0xffffu);
+      for (uint32_t e = hole[w]; e; e &= e - 1) *to++ = lo + slot_of(w) + __ffs(e) - 1;
+      to = keys + m0 + (off[w] >> 16);
+      for (uint32_t e = mover[w]; e; e &= e - 1) *to++ = lo + slot_of(w) + __ffs(e) - 1;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = tid; i < holes; i += PLAN_THREADS) into[hole0 + i] = keys[i];
+#pragma unroll 4
+    for (uint32_t i = tid; i < movers; i += PLAN_THREADS) source[mover0 + i] = keys[holes + i];
+  } else {
+    if (want < ties_all) {
+      uint32_t t = 0;
+      for (int i0 = s0; i0 < s1; i0 += 32)
+        t += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && key_at(i0 + lane) == prefix));
+      count_ties(t);
+    }
+    const uint32_t below = (1u << lane) - 1;
+    // Of 32 slots from i0 on, those that fall free below `keep` and those kept from
+    // it on, a bit each; `tie` counts the equal keys before.
+    auto flags = [&](int i0, uint32_t &tie) {
+      const int i = i0 + lane;
+      const bool in = i < s1;
+      const uint32_t k = in ? key_at(i) : 0u;
+      bool stays = k >= prefix;
+      if (want < ties_all) {
+        const uint32_t eq = __ballot_sync(0xffffffffu, in && k == prefix);
+        stays = k > prefix || (k == prefix && tie + __popc(eq & below) < want);
+        tie += __popc(eq);
+      }
+      return __ballot_sync(0xffffffffu, in && stays == (lo + i >= keep));
+    };
+    uint32_t holes = 0, movers = 0, tie = tie_base;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const uint32_t f = flags(i0, tie), u = under(i0);
+      holes += __popc(f & u);
+      movers += __popc(f & ~u);
+    }
+    count_moves(holes, movers);
+    uint32_t hole = hole0 + sum_before(ct->warp_a, warp, lane), mover = mover0 + sum_before(ct->warp_b, warp, lane);
+    tie = tie_base;
+    for (int i0 = s0; i0 < s1; i0 += 32) {
+      const uint32_t f = flags(i0, tie), u = under(i0);
       if (f >> lane & 1) {
         if (u >> lane & 1)
           into[hole + __popc(f & u & below)] = lo + i0 + lane;
@@ -546,7 +633,7 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   const int short_list = 8192, longest = 49152;
   while (a.cs < MAX_CS && (slots->capacity / a.cs > longest || (lists * a.cs * 2 <= dev.sms && slots->capacity / a.cs > 4096)))
     a.cs *= 2;
-  const int per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31, limit = 200 << 10;
+  const int per = ((slots->capacity + a.cs - 1) / a.cs + 31) & ~31, limit = 227 << 10;
   const bool cached = static_cast<int>(sizeof(PlanCtrl)) + per * 4LL <= limit;
   const int smem = static_cast<int>(sizeof(PlanCtrl)) + (cached ? per * 4 : 0);
   const bool wide = per > short_list;
