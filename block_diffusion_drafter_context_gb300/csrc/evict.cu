@@ -21,17 +21,20 @@ namespace {
 // ------------------------------------------------------------------ choice
 // The budget-th largest of a list by radix selection over 32-bit keys (11, 11
 // and 10 bits), the keys in shared memory: weights and positions are read
-// once.  The first digit decides nearly all keys, the few others are set apart
-// for the next two.  What stays is marked 32 slots to a word, and the words
-// that have something to write are written.  Where lists are long or few, a
-// cluster of CTAs shares one: each has a stretch of the slots and sends the
-// counts that are not 0 to the first, which finds the digit for all.  Bound by
-// instructions and by the dependent steps of a list (loads, two selections, two
-// walks): 36 layers of 8 x 8 lists of 4.1k take 37 us, 11 of them HBM's.  Counts
-// kept two or four times over, for lanes that meet in a bin, were slower (45 us).
+// once.  The first digit decides nearly all keys, the few others are set apart:
+// compared with each other, or counted by the next two digits.  What stays is a
+// bit per slot in a lane's registers, and the moves leave in one piece through
+// the keys' place.  Where lists are long or few, a cluster of CTAs shares one:
+// each has a stretch of the slots and sends the counts that are not 0 to the
+// first, which finds the digit for all.  Bound by instructions and by the
+// dependent steps of a list (loads, digits, counts of what moves): 36 layers of
+// 8 x 8 lists of 4.1k take 31 us, 11 of them HBM's.  Counts kept two or four
+// times over, for lanes that meet in a bin, were slower (45 us against 37), and
+// so were weights that came by asynchronous copies (34 against 31).
 constexpr int BINS = 2048;
 constexpr int FEW = 2048;                     // keys set apart at most
 constexpr int MAX_CS = 8;
+constexpr uint32_t ZERO = 0x80000000u;        // the key of a weight of 0
 constexpr uint32_t PROTECTED = 0xffffffffu;   // the key of a recent token, above every weight's
 
 struct PlanArgs {
@@ -48,9 +51,9 @@ struct PlanArgs {
 struct __align__(16) PlanCtrl {
   uint32_t hist[BINS];         // this CTA's counts
   uint32_t warp_sum[32], warp_a[32], warp_b[32];
-  uint32_t pick[3];            // the digit of the wanted key, how many keys lie above it, and how many have it
+  uint32_t pick[4];            // the digit of the wanted key, how many keys lie above it, how many have it, and whether those are all 0
   uint32_t ties, holes, movers;   // of this CTA
-  uint32_t found;
+  uint32_t found, zeros;
   uint32_t few[FEW];           // this CTA's keys that have the first digit of the wanted one
 };
 
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
     for (int i = 0; i < MINE; i += W) *reinterpret_cast<Word *>(&ct->hist[bin0 + i]) = Word();
   };
   clear();
-  if (tid == 0) ct->found = 0;
+  if (tid == 0) ct->found = ct->zeros = 0;
   if (a.cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the counts are cleared
   pdl_start();
   const int ctx = a.ctx_len[b], seq = a.seq_len[b];
@@ -180,9 +183,9 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
     uint32_t zeros = 0, prot = 0;          // the two keys that many slots may share, counted without atomics
     auto count = [&](uint32_t k, bool in) {
       if (pass > 0) in = in && (k >> (above & 31)) == prefix;
-      zeros += in && k == 0x80000000u;
+      zeros += in && k == ZERO;
       prot += in && k == PROTECTED;
-      if (in && k != 0x80000000u && k != PROTECTED) atomicAdd(&ct->hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+      if (in && k != ZERO && k != PROTECTED) atomicAdd(&ct->hist[(k >> shift) & ((1u << bits) - 1)], 1u);
     };
     if (pass > 0 && n_few >= 0) {
       for (int i = tid; i < n_few; i += PLAN_THREADS) count(ct->few[i], true);
@@ -212,7 +215,13 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
     zeros = __reduce_add_sync(0xffffffffu, zeros);
     prot = __reduce_add_sync(0xffffffffu, prot);
     if (lane == 0) {
-      if (zeros) atomicAdd(&ct->hist[(0x80000000u >> shift) & ((1u << bits) - 1)], zeros);
+      if (zeros && pass == 0) {
+        if (a.cs > 1)
+          add_dsmem_u32(dsmem_addr(&ct->zeros, 0), zeros);
+        else
+          atomicAdd(&ct->zeros, zeros);
+      }
+      if (zeros) atomicAdd(&ct->hist[(ZERO >> shift) & ((1u << bits) - 1)], zeros);
       if (prot) atomicAdd(&ct->hist[(PROTECTED >> shift) & ((1u << bits) - 1)], prot);
     }
     uint32_t c[MINE], sum = 0;
@@ -259,14 +268,16 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
             else
               over += c[u];
           }
+        const uint32_t all_zero = pass == 0 && bin == static_cast<int>(ZERO >> 21) && has == ct->zeros;
         if (a.cs == 1) {
-          ct->pick[0] = bin, ct->pick[1] = over, ct->pick[2] = has;
+          ct->pick[0] = bin, ct->pick[1] = over, ct->pick[2] = has, ct->pick[3] = all_zero;
         } else {
           for (int r = 0; r < a.cs; ++r) {
             const uint32_t to = dsmem_addr(ct->pick, r);
             st_dsmem_u32(to, bin);
             st_dsmem_u32(to + 4, over);
             st_dsmem_u32(to + 8, has);
+            st_dsmem_u32(to + 12, all_zero);
           }
         }
       }
@@ -275,6 +286,12 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
     prefix = pass == 0 ? ct->pick[0] : (prefix << bits) | ct->pick[0];
     want -= ct->pick[1];
     ties_all = ct->pick[2];
+    // Tokens that nobody attended to may be many: their key needs no more digits (36
+    // layers, a third of the weights 0: 31 us, 50 with them).
+    if (pass == 0 && ct->pick[3]) {
+      prefix = ZERO;
+      break;
+    }
     if (pass == 0 && CACHED) {
       look(21, prefix);
       uint32_t have = 0;
@@ -625,10 +642,10 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.budget = budget;
   a.top = top;
   a.status = static_cast<int *>(workspace);
-  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 94 us
-  // on 1024 threads each, 139 on clusters of two, whose meetings cost more than
+  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 69 us
+  // on 1024 threads each; 139 for 101 on clusters of two, whose meetings cost more than
   // the emptier SM), 256 threads up to 8192 slots; where lists are few, a
-  // cluster (8 lists of 131071: 23 us on eight CTAs each).
+  // cluster (8 lists of 131071: 19 us on eight CTAs each).
   a.cs = 1;
   const int short_list = 8192, longest = 49152;
   while (a.cs < MAX_CS && (slots->capacity / a.cs > longest || (lists * a.cs * 2 <= dev.sms && slots->capacity / a.cs > 4096)))
