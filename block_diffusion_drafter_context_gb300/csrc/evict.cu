@@ -642,9 +642,9 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   a.budget = budget;
   a.top = top;
   a.status = static_cast<int *>(workspace);
-  // A CTA per list as long as its keys fit (64 x 8 lists of 16k..32k slots: 69 us
-  // on 1024 threads each; 139 for 101 on clusters of two, whose meetings cost more than
-  // the emptier SM), 256 threads up to 8192 slots; where lists are few, a
+  // A CTA per list as long as its keys fit, 256 threads up to 8192 slots and 1024
+  // beyond (64 x 8 lists of 16k..32k slots 69 us; on clusters of two, whose meetings
+  // cost more than the emptier SM, 139 when it was 101); where lists are few, a
   // cluster (8 lists of 131071: 19 us on eight CTAs each).
   a.cs = 1;
   const int short_list = 8192, longest = 49152;

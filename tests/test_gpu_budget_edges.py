@@ -53,6 +53,26 @@ def test_plan_with_keys_that_lie_close(nkv, batch, cap, near, ties):
     assert ops.status() == 0
 
 
+@pytest.mark.parametrize("kind", ["any", "ties", "zeros", "same"])
+@pytest.mark.parametrize("B,nkv,cap,budget,recent,first", [
+    (20, 8, 45000, 40000, 100, 5),       # a CTA per list, more than 1024 slots for each of its warps
+    (1, 2, 300001, 150000, 3000, 0),     # the same in clusters
+    (1, 2, 49153, 20000, 0, 64),         # clusters of two or more by length
+    (2, 2, 1500, 900, 0, 0), (2, 1, 3000, 2500, 7, 1), (1, 1, 2048, 1, 0, 0)])   # 8 and 16 slots to a lane
+def test_plan_of_every_stretch(kind, B, nkv, cap, budget, recent, first):
+    import torch
+    s = some_slots(1, B, nkv, cap, budget, 11, kind)
+    ctx = i32([cap - 13 * b for b in range(B)])
+    ops = ops_for(nkv)
+    moves, counts, left = ops.plan_eviction(s, ctx, ctx + 10, budget, recent=recent, first=first)
+    into, source = plan_on_device(s, ctx, ctx + 10, first, recent, budget)
+    top = moves.shape[-1]
+    got = torch.where(moves >= 0, moves, cap)
+    assert torch.equal(got[..., 0, :].long(), into[..., :top]) and torch.equal(got[..., 1, :].long(), source[..., :top])
+    assert torch.equal(counts.long(), (source < cap).sum(-1)) and torch.equal(left, ctx.clamp(max=budget))
+    assert ops.status() == 0
+
+
 @pytest.mark.parametrize("nq,nkv,d,ctx,new,launches", [
     (2, 2, 64, [40, 3, 0, 70], [1, 1, 1, 1], 1), (8, 2, 128, [9, 300], [3, 1], 1), (8, 1, 64, [0, 1], [1, 1], 2),
     (12, 4, 128, [5], [5], 2)])
