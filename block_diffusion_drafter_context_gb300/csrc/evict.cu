@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
       if (ct->found <= FEW) n_few = static_cast<int>(ct->found);
       if (a.cs == 1 && n_few >= 0 && n_few <= 256) {
         // each compared with all of them, by the warps that hold one; with the loads above in
-        // one batch the 36 layers take 38 us for 45. All 1024 threads against as many
+        // one batch the 36 layers took 38 us for 45. All 1024 threads against as many
         // candidates took 171 us for 101 on 64 prompts
         const bool holds = (tid & ~31) < n_few;
         const uint32_t k = tid < n_few ? ct->few[tid] : 0u;
