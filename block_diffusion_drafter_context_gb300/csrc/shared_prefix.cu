@@ -28,6 +28,7 @@
 // pages, whose (O, maximum, sum) partials a second kernel joins row by row over
 // the whole GPU, in the order of the pages: the same bits on every call.
 #include "cache_attention.cuh"
+#include "pv_done.h"
 
 namespace dflash {
 namespace {
@@ -110,7 +111,8 @@ struct Segs {
 
 struct __align__(16) PCtrl {
   uint64_t full[16], empty[16];                    // a slot's data; both tiles' products are done with it
-  uint64_t qfull[2], sfull[2][2], pfull[2][2], pdone[2], oempty[2], drain[2];   // [2]: of a tile; [2][2]: and of an S
+  uint64_t qfull[2], sfull[2][2], pfull[2][2], oempty[2], drain[2];   // [2]: of a tile; [2][2]: and of an S
+  uint64_t pdone[2][PV_BARS];                      // P V of a tile's page (pv_done.h)
   uint32_t tmem;
   int abort_flag;
   int bad[16];                                     // the slot's page is not there
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       mbar_init(&ct->sfull[i][1], 1);
       mbar_init(&ct->pfull[i][0], 4);
       mbar_init(&ct->pfull[i][1], 4);
-      mbar_init(&ct->pdone[i], 1);
+      for (int k = 0; k < PV_BARS; ++k) mbar_init(&ct->pdone[i][k], 1);
       mbar_init(&ct->oempty[i], 4);
       mbar_init(&ct->drain[i], 1);
     }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(NTHR, 1)
                                kk > 0 || started ? 1u : 0u);
           started = true;
         }
-        umma_commit_elect(&ct->pdone[w]);
+        umma_commit_elect(&ct->pdone[w][pv_bar(n_p)]);
         umma_commit_elect(&ct->empty[st]);
         ++n_p;
         step();
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           m = mx;
           l = 0.f;
         } else if (__any_sync(0xffffffffu, need)) {   // wait for the P V of the page before, rescale O in TMEM
-          if (!(ok = waitw(&ct->pdone[w], np - 1))) break;
+          if (!(ok = waitw(&ct->pdone[w][pv_bar(np - 1)], pv_phase(np - 1)))) break;
           tc_fence_after();
           const float f = need ? fast_exp2(m - mx) : 1.f;
 #pragma unroll 1
@@ -431,10 +433,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       // the query rows (the last S of the tile is complete, so they are not needed
       // any more): 32 rows straight from their threads took 4 us of stores a tile
       const Seg last = sg;
-      // (a phase can be waited for once the one before is known to be over, and the
-      // last S tells of the P V two pages before)
-      if (np > 1 && !(ok = waitw(&ct->pdone[w], np - 2))) break;
-      if (!(ok = waitw(&ct->pdone[w], np - 1))) break;
+      if (!(ok = waitw(&ct->pdone[w][pv_bar(np - 1)], pv_phase(np - 1)))) break;   // and with it every P V before
       tc_fence_after();
       const int head = last.tile / plan.per_head * a.g;
       float *part = last.slot < 0 ? nullptr : a.partials + (static_cast<size_t>(blockIdx.x) * 2 + last.slot) * S::PART;
