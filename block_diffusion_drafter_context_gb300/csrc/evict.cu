@@ -613,6 +613,8 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   if (batch < 0 || layer < 0 || n_layers < 0 || first < 0 || recent < 0 || budget < 1 || budget > (1 << 24) ||
       static_cast<long long>(first) + recent > budget || first >= budget)
     return set_error(DFLASH_ERR_ARG, "%s: batch, layers, first, recent or budget out of range (first < budget, first + recent <= budget)", who);
+  if (top > (1 << 24))   // no list has as many slots
+    return set_error(DFLASH_ERR_ARG, "%s: top must be at most 2^24", who);
   const int room = budget - first, over = slots->capacity - budget, most = room < over ? room : over > 0 ? over : 0;
   if (top < most) return set_error(DFLASH_ERR_SHAPE, "%s: room for %d moves, %d needed", who, top, most);
   if (batch > 0 && n_layers > 0 && (!counts || (top > 0 && !moves))) return set_error(DFLASH_ERR_ARG, "%s: null argument", who);

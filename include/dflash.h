@@ -627,7 +627,7 @@ DFLASH_API int dflash_add_weights(const dflash_heads *hs, const dflash_kv *kv, c
  *              [batch], the next token's position.
  *   moves:     device int32 [n_layers][batch][nkv][2][top] out: the slots moved
  *              into, then the slots moved from; -1 behind the list's count.
- *              top >= min(budget - first, capacity - budget); NULL when 0.
+ *              min(budget - first, capacity - budget) <= top <= 2^24; NULL when 0.
  *   counts:    device int32 [n_layers][batch][nkv] out;
  *   ctx_out:   device int32 [batch] out, min(ctx_len, budget); not ctx_len itself.
  * Reads weights and positions only.  A ctx_len outside 0..capacity is reported
