@@ -624,6 +624,12 @@ DFLASH_API int dflash_plan_eviction(const dflash_heads *hs, const dflash_slots *
   if (batch == 0 || n_layers == 0) return DFLASH_OK;
   const long long lists = static_cast<long long>(n_layers) * batch * hs->n_kv_heads;
   if (lists > (1 << 27)) return set_error(DFLASH_ERR_SHAPE, "%s: too many layers x requests x kv heads", who);
+  // one CTA writes a request's length while those of other lists may not have read it yet
+  auto over_it = [&](const int32_t *in) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(in), y = reinterpret_cast<uintptr_t>(ctx_out);
+    return (x < y ? y - x : x - y) < batch * sizeof(int32_t);
+  };
+  if (over_it(ctx_len) || over_it(seq_len)) return set_error(DFLASH_ERR_ARG, "%s: ctx_out lies over ctx_len or seq_len", who);
   Device dev;
   if (int e = current_device(&dev)) return e;
   const size_t at = static_cast<size_t>(layer) * slots->batch_rows * hs->n_kv_heads * slots->capacity;

@@ -629,7 +629,8 @@ DFLASH_API int dflash_add_weights(const dflash_heads *hs, const dflash_kv *kv, c
  *              into, then the slots moved from; -1 behind the list's count.
  *              min(budget - first, capacity - budget) <= top <= 2^24; NULL when 0.
  *   counts:    device int32 [n_layers][batch][nkv] out;
- *   ctx_out:   device int32 [batch] out, min(ctx_len, budget); not ctx_len itself.
+ *   ctx_out:   device int32 [batch] out, min(ctx_len, budget); not over ctx_len
+ *              or seq_len (refused).
  * Reads weights and positions only.  A ctx_len outside 0..capacity is reported
  * as DFLASH_ERR_DEVICE; that request gets no moves and its ctx_len back.
  * Of hs only n_kv_heads is used.  workspace: the status word, 256 bytes. */
