@@ -108,6 +108,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
   };
   clear();
   if (tid == 0) ct->found = ct->zeros = 0;
+  // a warp's lanes meet before each half of the barrier: `aligned` wants all of them there
+  __syncwarp();
   if (a.cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // the counts are cleared
   pdl_start();
   const int ctx = a.ctx_len[b], seq = a.seq_len[b];
@@ -119,6 +121,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
   if (!ok || ctx <= a.budget) {            // nothing to drop
     for (int i = rank * PLAN_THREADS + tid; i < 2 * a.top; i += a.cs * PLAN_THREADS) into[i] = -1;
     if (rank == 0 && tid == 0) a.counts[list] = 0;
+    __syncwarp();
     if (a.cs > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     return;                                // the whole cluster
   }
@@ -132,6 +135,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1) plan_kernel(const PlanArg
   const int newest = static_cast<int>(max(static_cast<long long>(seq) - a.recent, -0x80000000ll));
   auto make_key = [&](float w, int32_t at) { return at >= newest ? PROTECTED : weight_key(w); };
   auto key_at = [&](int i) { return CACHED ? keys[i] : make_key(wt[i], ps[i]); };
+  __syncwarp();
   if (a.cs > 1)                // the counts are cleared
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   else
