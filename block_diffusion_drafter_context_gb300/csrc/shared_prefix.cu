@@ -350,6 +350,8 @@ __global__ void __launch_bounds__(NTHR, 1)
       for (int k = 0; k < sg.n; ++k, ++np) {
         const uint32_t sp = my_s + 64 * (np & 1);
         if (!(ok = waitw(&ct->sfull[w][np & 1], np >> 1))) break;
+        // no phase of P V goes by unseen: the waits below rest on it (pv_done.h)
+        if (np > 1 && !(ok = waitw(&ct->pdone[w][pv_bar(np - 2)], pv_phase(np - 2)))) break;
         tc_fence_after();
         bool bad = false;
         if (any_bad) {

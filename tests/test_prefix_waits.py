@@ -37,33 +37,33 @@ def places(tmp_path_factory):
     return [tuple(int(x) for x in line.split()) for line in lines if line]
 
 
-def faults(place, at_end, tiles):
+def faults(place, lag, at_end, tiles):
     """What can go wrong over tiles of so many pages: waits that pass before the
-    page's P V is complete, and waits that nothing can end.  at_end(n): the pages
-    whose P V is waited for when n was a tile's last."""
-    found, page, known = set(), 0, 0       # known: P V complete whatever the timing
+    page's P V is complete, and waits that nothing can end.  lag: each page waits
+    for the page so many before it (None: it does not); at_end(n): the pages that
+    are waited for one after the other when n was a tile's last.  Nothing but a wait
+    tells of P V."""
+    found, page = set(), 0
+    low = 0                                # P V known to be complete
     for length in tiles:
         for k in range(length):
-            if k > 0:                      # S of this page was issued behind P V of page - 2
-                known = max(known, page - 1)
-            waits = [[page - 1]] if k > 0 else []          # where O is rescaled, before P goes out
+            # (for which page, P handed over by then, whether it is made every time)
+            waits = [(page - lag, page, True)] if lag and page >= lag else []
+            if k > 0:
+                waits.append((page - 1, page, False))      # where O is rescaled
             if k == length - 1:
-                waits.append(at_end(page))
-            for i, pages in enumerate(waits):
-                most = page + 1 if k == length - 1 and i == len(waits) - 1 else page   # P handed over so far
-                low = known
-                for w in pages:
-                    bar, phase = place(w)
-                    for done in range(low, most + 1):
-                        count = sum(place(n)[0] == bar for n in range(done))
-                        passes = count % 2 != phase % 2
-                        if passes and done <= w:
-                            found.add("early")
-                        if not passes and done == most:
-                            found.add("stuck")
-                    low = max(low, w + 1)
+                waits += [(n, page + 1, True) for n in at_end(page)]
+            for n, most, always in waits:
+                bar, phase = place(n)
+                for done in range(low, most + 1):
+                    passes = sum(place(m)[0] == bar for m in range(done)) % 2 != phase % 2
+                    if passes and done <= n:
+                        found.add("early")
+                    if not passes and done == most:
+                        found.add("stuck")
+                if always:
+                    low = max(low, n + 1)
             page += 1
-        known = page                       # the tile's end waited for all of them
     return found
 
 
@@ -72,12 +72,14 @@ TILES = [t for n in (1, 2, 3, 4) for t in itertools.product((1, 2, 3, 4, 7), rep
 
 def test_every_wait_ends_and_none_ends_early(places):
     for tiles in TILES:
-        assert not faults(lambda n: places[n], lambda n: [n], tiles), tiles
+        assert not faults(lambda n: places[n], 2, lambda n: [n], tiles), tiles
 
 
-def test_a_single_barrier_would_not_do():
-    """The walk tells: waits for the last two pages in turn on one barrier can
-    miss the first of them, and one wait alone can pass early."""
+def test_other_rules_would_not_do(places):
+    """The walk tells: on one barrier, waits for the last two pages in turn can
+    miss the first of them; without a wait for every page, one can pass early on
+    a phase that nobody saw."""
     one = lambda n: (0, n)   # noqa: E731
-    assert "stuck" in faults(one, lambda n: [n - 1, n] if n else [n], (3,))
-    assert "early" in faults(one, lambda n: [n], (3,))
+    assert "stuck" in faults(one, None, lambda n: [n - 1, n] if n else [n], (3,))
+    assert "early" in faults(one, None, lambda n: [n], (3,))
+    assert "early" in faults(lambda n: places[n], None, lambda n: [n], (4,))
