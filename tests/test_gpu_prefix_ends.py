@@ -77,3 +77,23 @@ def without(c, hole):
         spread[rows] = torch.einsum("ihgt,htd->ihgd", p, v.abs()).reshape(n, c.nq, c.d)
         lse[rows] = l.reshape(n, c.nq)
     return out, lse, spread
+
+
+def test_the_largest_batch():
+    """4096 requests behind one prefix, in both forms; tolerances as above."""
+    import torch
+    from block_diffusion_drafter_context_gb300 import binding as B
+    nq, nkv, d, batch = 8, 1, 128, 4096
+    c = Shared(nq, nkv, d, "bf16", 2, [(b * 37) % 90 for b in range(batch)], [1 + b % 2 for b in range(batch)], seed=1,
+               stale=0.0)
+    ref, rlse, spread = without(c, range(0))
+    size = float(c.q.double().abs().view(c.T, nq, d).sum(-1).max() * c.k[1].abs().max()) * d ** -0.5
+    e = 2 * d * 2.0 ** -24 * size + (max(c.ctx) + 16) * 2.0 ** -24 + 2.0 ** -19
+    tol = (U["bf16"] + e) * spread + U["bf16"] * ref.abs() + 1e-30
+    for launches in (1, 2):
+        B.dflash_debug_shared_launches(launches)
+        out, lse = c.attend()
+        assert c.ops.status() == 0
+        assert ((out.double().view(c.T, nq, d) - ref).abs() <= tol).all()
+        assert ((lse.double() - rlse).abs() <= e + 2.0 ** -22 * (1 + rlse.abs())).all()
+        assert torch.equal(c.attend()[0], out)
