@@ -20,7 +20,8 @@
 // of products for both tiles): 850 us with Q in tensor memory, one S and the
 // products issued by a thread on a branch of its own; 582 with blocks of 128
 // positions; 513 with a converged warp that issues; 475 with two S, which take
-// a tile's products out of the chain from its scores to the next ones.
+// a tile's products out of the chain from its scores to the next ones; 450 with a
+// wait for every page's P V (pv_done.h).
 //
 // Tiles of a (kv head, 256 rows) go out whole while every CTA gets one, in the
 // order of the heads, so that the CTAs of a head sweep its pages together and
